@@ -456,6 +456,140 @@ void mk_sched_destroy(mk_sched* s);
 int mk_serve_step(mk_sched* s, mk_plan** plan, const mk_model_dims* dims, const mk_weights* w, const mk_kv* kv,
                   const mk_plan_opts* opts, mk_stream stream);
 
+/* ---- Operators over a chunk of new tokens of each request ----
+ *
+ * The decode step appends, attends and samples inside its own launch, at most
+ * 8 rows at a time.  These calls do the same pieces by themselves for chunks
+ * of any length (a whole prompt, a part of one, a single next token, a few
+ * drafted tokens to be checked), on the same paged cache and logits.  They
+ * are enqueued on `stream` and can be captured into a graph, except where
+ * said otherwise. */
+
+/* What a pool holds.
+ *   MK_KV_BF16  the pool of mk_kv: bf16 [num_pages, n_kv_heads, 2, head_dim,
+ *               page_size]
+ *   MK_KV_E4M3  8 bits: bytes [num_pages, n_kv_heads, 2, head_dim + 1,
+ *               page_size]: a block's first head_dim rows are e4m3 codes (one
+ *               row of page_size slots per dimension, as in bf16), its last
+ *               row each slot's scale as E8M0, the biased exponent k + 127 of
+ *               a power of two: a value is code * 2^k.  A token's scale in a
+ *               head's K or V is the smallest power of two with
+ *               |value| <= 448 * 2^k for the whole vector (k = -127 for a
+ *               vector of zeros), so reading back is exact in bf16 unless the
+ *               value underflows or overflows there */
+enum { MK_KV_BF16 = 0, MK_KV_E4M3 = 1 };
+enum { MK_ROWS_BF16 = 0, MK_ROWS_F32 = 1 };
+
+/* A chunk: `batch` requests, request b with seq_lens[b] >= 0 cached tokens and
+ * new_lens[b] >= 0 new ones at positions seq_lens[b] .. seq_lens[b] +
+ * new_lens[b] - 1.  Rows of new tokens are packed: request 0's, then request
+ * 1's, and so on.  One chunk serves every layer of a model. */
+typedef struct mk_chunk mk_chunk;
+
+/* Builds a chunk for `batch` requests (at most 65535).  Of dims only
+ * n_q_heads, n_kv_heads, head_dim, page_size and rope_theta are read, with the
+ * limits of mk_model_dims; rope_theta 0 appends without rotation, and
+ * n_q_heads 0 makes a chunk of keys and values alone (no mk_chunk_attend).
+ * Host arrays seq_lens, new_lens [batch], page_table [batch,
+ * max_pages_per_seq] are copied.  Every page that covers a position below
+ * seq_lens[b] + new_lens[b] must be there, in [0, num_pages)
+ * (MK_ERR_CAPACITY beyond max_pages_per_seq); a page that receives new tokens
+ * belongs to one request, others may be shared.  Device memory (tables, the
+ * rotation's angles and the space for split rows) is allocated on the current
+ * device, where all later calls must run (MK_ERR_INVALID elsewhere). */
+int mk_chunk_create(const mk_model_dims* dims, int kv_type, int num_pages, int batch, const int* seq_lens,
+                    const int* new_lens, const int* page_table, int max_pages_per_seq, mk_chunk** out);
+
+/* Another batch for the same chunk object, checked like mk_chunk_create's;
+ * uploaded on `stream`.  Work already enqueued on other streams must be
+ * ordered before it.  On an error the chunk keeps its batch, except after
+ * MK_ERR_CUDA.  Not during a stream capture (MK_ERR_INVALID). */
+int mk_chunk_update(mk_chunk* c, int batch, const int* seq_lens, const int* new_lens, const int* page_table,
+                    int max_pages_per_seq, mk_stream stream);
+
+/* Append the chunk's rows to the cache of one layer.  qkv (device, MK_ROWS_*)
+ * holds a row per new token, row_stride elements apart, laid out as the QKV
+ * projection of mk_weights gives it: per KV head its G query heads, its key,
+ * its value ([n_kv_heads, G + 2, head_dim]).  Queries and keys are rotated at
+ * their positions (angles and sums in fp32 or better); queries are written to
+ * q (device bf16 [rows, n_q_heads, head_dim]; NULL when n_q_heads is 0), keys
+ * and values into kv_pool at their tokens' slots, rounded to the pool's type.
+ * Nothing else of the pool is written.  qkv, q and kv_pool 16-byte aligned,
+ * row_stride * element size a multiple of 16. */
+int mk_chunk_append(mk_chunk* c, const void* qkv, int rows_type, long long row_stride, void* kv_pool, void* q,
+                    mk_stream stream);
+
+/* Causal attention of the chunk's rows over the paged cache, which must hold
+ * their own keys and values already (mk_chunk_append): row i of request b sees
+ * positions 0 .. seq_lens[b] + i.  q, out: device bf16 [rows, n_q_heads,
+ * head_dim], 16-byte aligned; scores are scaled by 1 / sqrt(head_dim), softmax
+ * statistics and sums are fp32.  The cached values of the positions below
+ * seq_lens[b] + new_lens[b] must be finite; slots behind them may hold
+ * anything.  Calls on one chunk share its space for split rows: enqueue them
+ * on one stream, or one after another, replays of graphs that captured them
+ * among them (chunks of their own run at the same time). */
+int mk_chunk_attend(mk_chunk* c, const void* q, const void* kv_pool, void* out, mk_stream stream);
+
+/* Read the cache back: every position below seq_lens[b] + new_lens[b] of every
+ * request, packed (request 0's first), as bf16 [tokens, n_kv_heads, 2,
+ * head_dim] (K, then V; 16-byte aligned).  A chunk with n_q_heads 0 and
+ * rope_theta 0 appends such rows to another pool. */
+int mk_chunk_read(mk_chunk* c, const void* kv_pool, void* out, mk_stream stream);
+
+/* Wait for `stream`, then return the device status: MK_OK, or
+ * MK_ERR_DEP_TIMEOUT when a bounded wait inside mk_chunk_attend ran out (its
+ * output is then void).  mk_chunk_update clears it. */
+int mk_chunk_sync(mk_chunk* c, mk_stream stream);
+
+/* [batch, rows, cached + new tokens, attention tasks, tasks that write split
+ * rows, rows to join, CTAs planned for]: writes up to n ints. */
+int mk_chunk_info(const mk_chunk* c, int* out, int n);
+
+void mk_chunk_destroy(mk_chunk* c);
+
+/* Host only (no CUDA call): the attention tasks a chunk of these lengths would
+ * run on num_ctas CTAs, 8 ints each (request, KV head, first new row, rows,
+ * first 128-key tile, tiles, first split row or -1, 0).  Writes up to
+ * max_tasks tasks and returns their number, or an error. */
+int mk_chunk_inspect(const mk_model_dims* dims, int batch, const int* seq_lens, const int* new_lens, int num_ctas,
+                     int* tasks, int max_tasks);
+
+/* Probabilities from logits: probs[r, v] = softmax(logits[r, :] / temperature)
+ * of fp32 rows (logits row_stride elements apart, probs packed [rows, vocab]),
+ * the distribution that mk_plan_set_sampling draws from; temperature 0 gives
+ * the greedy one, 1 at the largest logit (the lowest index of equal ones) and
+ * 0 elsewhere.  A logit of -infinity has probability 0; a row of nothing else
+ * is all 0.  A row with a NaN or +infinity is all NaN.  probs may be the
+ * logits' own packed buffer, but may not overlap them otherwise.  rows 0 is
+ * allowed; vocab at most 393216 (MK_ERR_UNSUPPORTED); temperature as
+ * mk_plan_set_sampling. */
+int mk_probs(const float* logits, int rows, int vocab, long long row_stride, float temperature, float* probs,
+             mk_stream stream);
+
+/* Verification of drafted tokens: request b drafted n = n_draft[b] tokens
+ * (device int32, NULL: max_draft each; taken as 0 .. max_draft) drafts[b, i].
+ * target[b, i, :] (device fp32 [batch, max_draft + 1, vocab]) is the target's
+ * distribution for the token after i drafted ones, draft[b, i, :] (device
+ * fp32 [batch, max_draft, vocab]) the one that drafts[b, i] was drawn from;
+ * draft NULL: drafts without one, each taken as certain.  Draft i is accepted
+ * when every earlier one is and u[b, i] * draft[b, i, x] < target[b, i, x]
+ * for its token x (compared exactly; an x outside the vocabulary or a NaN is
+ * refused).  The next token is drawn at the first refused place i from
+ * max(target[b, i] - draft[b, i], 0), after n accepted ones from target[b,
+ * n], so that the tokens follow the target's distribution whatever the drafts
+ * were.
+ * The draw is exact: a weight w counts as round(min(w, 1) * 2^40) (0 for a
+ * negative or NaN one), and with r = r[b] clamped to [0, 1) the token is the
+ * lowest one where the running sum passes floor(total * floor(r * 2^24) /
+ * 2^24).  Where the difference's total is 0 the target's row is drawn from;
+ * where that is 0 too the token is -1.
+ * tokens[b, :] (device int32 [batch, max_draft + 1]) = the accepted drafts,
+ * the drawn token, then -1; accepted[b] (device int32) their number.
+ * max_draft >= 0 (u, drafts and draft unused at 0); vocab at most 393216;
+ * batch 0 is allowed. */
+int mk_verify(int batch, int max_draft, int vocab, const float* target, const float* draft, const int* drafts,
+              const int* n_draft, const float* u, const float* r, int* tokens, int* accepted, mk_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,358 @@
+// Host side of the chunk operators: the checks of a batch, the attention task
+// list and the C ABI of mk_chunk_* (include/mk.h).
+#include <cuda_runtime.h>
+#include <limits.h>
+#include <stdint.h>
+#include <stdio.h>
+#include <string.h>
+
+#include <algorithm>
+#include <new>
+#include <stdexcept>
+#include <vector>
+
+#include "chunk.h"
+#include "mk.h"
+
+namespace mk {
+void set_last_error(const char* msg);
+}
+
+using mk::AttnTask;
+using mk::ChunkReq;
+using mk::JoinTask;
+
+namespace {
+
+int fail(int code, const char* msg) {
+  mk::set_last_error(msg);
+  return code;
+}
+
+int fail_cuda(const char* what, cudaError_t e) {
+  char buf[224];
+  snprintf(buf, sizeof(buf), "%s: %s (%d)", what, cudaGetErrorString(e), (int)e);
+  return fail(MK_ERR_CUDA, buf);
+}
+
+// No C++ exception leaves a C entry: a failed host allocation is reported.
+template <class F>
+int guarded(F&& f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc&) {
+    return fail(MK_ERR_CAPACITY, "out of host memory");
+  } catch (const std::length_error&) {
+    return fail(MK_ERR_CAPACITY, "out of host memory");
+  }
+}
+
+struct Shape {
+  int nq, nkv, d, G;
+  double theta;
+};
+
+int check_shape(const mk_model_dims* m, Shape& s) {
+  if (!m) return fail(MK_ERR_INVALID, "mk_chunk: dims is NULL");
+  s.nq = m->n_q_heads; s.nkv = m->n_kv_heads; s.d = m->head_dim; s.theta = m->rope_theta;
+  if (s.nq < 0 || s.nkv < 1 || s.nq % s.nkv) return fail(MK_ERR_INVALID, "mk_chunk: head counts");
+  if (!(s.theta >= 0.) || s.theta > 3e38) return fail(MK_ERR_INVALID, "mk_chunk: rope_theta must be finite and not negative");
+  s.G = s.nq / s.nkv;
+  if (m->page_size != mk::PAGE) return fail(MK_ERR_UNSUPPORTED, "mk_chunk: page_size must be 16");
+  if (s.d != 64 && s.d != 128) return fail(MK_ERR_UNSUPPORTED, "mk_chunk: head_dim must be 64 or 128");
+  if (s.G > 8 || s.nkv > 65535) return fail(MK_ERR_UNSUPPORTED, "mk_chunk: at most 8 query heads per KV head");
+  return MK_OK;
+}
+
+// What one batch needs on the device, built on the host.
+struct Built {
+  std::vector<ChunkReq> reqs;
+  std::vector<int> pt;
+  std::vector<AttnTask> tasks;
+  std::vector<JoinTask> joins;
+  long long rows = 0, tokens = 0, split_rows = 0, nsplit = 0, joined_rows = 0;
+  int max_pages = 0, max_new_pages = 0;   // of one request: all its pages, those that receive rows
+};
+
+// Row counts and prefix sums; no pages yet.
+int set_lens(const Shape& s, int batch, const int* seq_lens, const int* new_lens, Built& b) {
+  if (batch < 1 || !seq_lens || !new_lens) return fail(MK_ERR_INVALID, "mk_chunk: batch or lengths");
+  if (batch > 65535) return fail(MK_ERR_UNSUPPORTED, "mk_chunk: at most 65535 requests");
+  b.reqs.resize(batch);
+  for (int i = 0; i < batch; ++i) {
+    if (seq_lens[i] < 0 || new_lens[i] < 0) return fail(MK_ERR_INVALID, "mk_chunk: a negative length");
+    const long long total = (long long)seq_lens[i] + new_lens[i];
+    // positions and the ends of the tiles around them stay 32-bit
+    if (total > INT_MAX - 1024) return fail(MK_ERR_UNSUPPORTED, "mk_chunk: a request of over 2^31 - 1025 tokens");
+    ChunkReq& r = b.reqs[i];
+    r = {};
+    r.seq = seq_lens[i]; r.nnew = new_lens[i]; r.row0 = (int)b.rows; r.tok0 = b.tokens;
+    b.rows += new_lens[i];
+    b.tokens += total;
+    if (b.rows > INT_MAX - 1024) return fail(MK_ERR_UNSUPPORTED, "mk_chunk: over 2^31 - 1025 new rows");
+    const int np = (int)((total + mk::PAGE - 1) / mk::PAGE);
+    b.max_pages = std::max(b.max_pages, np);
+    if (new_lens[i]) b.max_new_pages = std::max(b.max_new_pages, np - seq_lens[i] / mk::PAGE);
+  }
+  return MK_OK;
+}
+
+int set_pages(int num_pages, const int* page_table, int max_pages, Built& b) {
+  if (!page_table || max_pages < 1) return fail(MK_ERR_INVALID, "mk_chunk: page table");
+  const int batch = (int)b.reqs.size();
+  std::vector<char> written((size_t)num_pages, 0);
+  for (int i = 0; i < batch; ++i) {
+    ChunkReq& r = b.reqs[i];
+    r.pt = (long long)i * max_pages;
+    const int np = (r.seq + r.nnew + mk::PAGE - 1) / mk::PAGE;
+    if (np > max_pages) return fail(MK_ERR_CAPACITY, "mk_chunk: a request's tokens need more pages than its table row holds");
+    for (int j = 0; j < np; ++j) {
+      const int pg = page_table[r.pt + j];
+      if (pg < 0 || pg >= num_pages) return fail(MK_ERR_INVALID, "mk_chunk: a page outside the pool");
+      if (r.nnew && j >= r.seq / mk::PAGE) {
+        if (written[pg]) return fail(MK_ERR_INVALID, "mk_chunk: two requests' new tokens, or two pages of one, in one page");
+        written[pg] = 1;
+      }
+    }
+  }
+  for (const ChunkReq& r : b.reqs) {
+    const int np = (r.seq + r.nnew + mk::PAGE - 1) / mk::PAGE;
+    const int keep = r.nnew ? r.seq / mk::PAGE : np;   // pages that receive none of its new tokens
+    for (int j = 0; j < keep; ++j)
+      if (written[page_table[r.pt + j]])
+        return fail(MK_ERR_INVALID, "mk_chunk: a page that receives new tokens belongs to another place too");
+  }
+  b.pt.assign(page_table, page_table + (size_t)batch * max_pages);
+  return MK_OK;
+}
+
+// Attention tasks.  A block is the rows of up to two query tiles of one
+// request and KV head (a tile: Q_TILE / G tokens with their G heads).
+void set_tasks(const Shape& s, int ctas, Built& b) {
+  (void)s; (void)ctas; (void)b;
+}
+
+}  // namespace
+
+struct mk_chunk {
+  Shape s;
+  int type = 0, num_pages = 0, device = 0, ctas = 0;
+  Built b;
+  void* blob = nullptr;          // requests, page table, tasks, joins
+  size_t blob_cap = 0;
+  float2* rope = nullptr;
+  size_t rope_cap = 0;
+  float* part = nullptr;         // split rows: sums, then (maximum, sum) pairs
+  size_t part_cap = 0;
+  int* status = nullptr;
+  mk::ChunkView view = {};
+};
+
+namespace {
+
+size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+
+cudaError_t grow(void** p, size_t* cap, size_t need) {
+  if (need <= *cap) return cudaSuccess;
+  cudaFree(*p);                  // waits for the device: no call still reads it
+  *p = nullptr;
+  *cap = 0;
+  const cudaError_t e = cudaMalloc(p, need);
+  if (e == cudaSuccess) *cap = need;
+  return e;
+}
+
+int build(const mk_chunk* c, int batch, const int* seq_lens, const int* new_lens, const int* page_table, int max_pages,
+          Built& b) {
+  int rc = set_lens(c->s, batch, seq_lens, new_lens, b);
+  if (rc == MK_OK) rc = set_pages(c->num_pages, page_table, max_pages, b);
+  return rc;
+}
+
+int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
+  const size_t d = c->s.d;
+  const size_t n_req = up16(nb.reqs.size() * sizeof(ChunkReq)), n_pt = up16(nb.pt.size() * sizeof(int)),
+               n_task = up16(nb.tasks.size() * sizeof(AttnTask)), n_join = up16(nb.joins.size() * sizeof(JoinTask));
+  cudaError_t e = grow(&c->blob, &c->blob_cap, n_req + n_pt + n_task + n_join);
+  if (e == cudaSuccess && c->s.theta > 0.)
+    e = grow((void**)&c->rope, &c->rope_cap, (size_t)nb.rows * (d / 2) * sizeof(float2));
+  if (e == cudaSuccess) e = grow((void**)&c->part, &c->part_cap, (size_t)nb.split_rows * (d + 2) * sizeof(float));
+  if (e != cudaSuccess) return fail_cuda("mk_chunk: device memory", e);
+  std::vector<char> host(n_req + n_pt + n_task + n_join, 0);
+  memcpy(host.data(), nb.reqs.data(), nb.reqs.size() * sizeof(ChunkReq));
+  memcpy(host.data() + n_req, nb.pt.data(), nb.pt.size() * sizeof(int));
+  if (!nb.tasks.empty()) memcpy(host.data() + n_req + n_pt, nb.tasks.data(), nb.tasks.size() * sizeof(AttnTask));
+  if (!nb.joins.empty())
+    memcpy(host.data() + n_req + n_pt + n_task, nb.joins.data(), nb.joins.size() * sizeof(JoinTask));
+  // pageable source: the bytes have left it when the call returns
+  e = cudaMemcpyAsync(c->blob, host.data(), host.size(), cudaMemcpyHostToDevice, st);
+  if (e == cudaSuccess) e = cudaMemsetAsync(c->status, 0, 4 * sizeof(int), st);
+  c->b = std::move(nb);
+  mk::ChunkView& v = c->view;
+  char* base = (char*)c->blob;
+  v.nq = c->s.nq; v.nkv = c->s.nkv; v.d = c->s.d; v.G = c->s.G;
+  v.batch = (int)c->b.reqs.size(); v.rows = (int)c->b.rows; v.num_pages = c->num_pages;
+  v.reqs = (const ChunkReq*)base;
+  v.pt = (const int*)(base + n_req);
+  v.tasks = (const AttnTask*)(base + n_req + n_pt);
+  v.joins = (const JoinTask*)(base + n_req + n_pt + n_task);
+  v.ntasks = (int)c->b.tasks.size(); v.njoins = (int)c->b.joins.size();
+  v.rope = c->s.theta > 0. ? c->rope : nullptr;
+  v.part_o = c->part;
+  v.part_ml = (float2*)(c->part + (size_t)c->b.split_rows * d);
+  v.status = c->status;
+  if (e == cudaSuccess && c->s.theta > 0. && v.rows) e = mk::launch_chunk_rope(v, c->s.theta, c->rope, st);
+  return e == cudaSuccess ? MK_OK : fail_cuda("mk_chunk: upload", e);
+}
+
+// The chunk's memory lives on one device.
+int check_device(const mk_chunk* c) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail_cuda("mk_chunk: current device", e);
+  return dev == c->device ? MK_OK : fail(MK_ERR_INVALID, "mk_chunk: the chunk belongs to another device than the current one");
+}
+
+bool aligned16(const void* p) { return p && (uintptr_t)p % 16 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+void mk_chunk_destroy(mk_chunk* c) {
+  if (!c) return;
+  cudaFree(c->blob);
+  cudaFree(c->rope);
+  cudaFree(c->part);
+  cudaFree(c->status);
+  delete c;
+}
+
+int mk_chunk_create(const mk_model_dims* dims, int kv_type, int num_pages, int batch, const int* seq_lens,
+                    const int* new_lens, const int* page_table, int max_pages_per_seq, mk_chunk** out) {
+  if (!out) return fail(MK_ERR_INVALID, "mk_chunk_create: out is NULL");
+  *out = nullptr;
+  Shape s;
+  const int rs = check_shape(dims, s);
+  if (rs != MK_OK) return rs;
+  if (kv_type != MK_KV_BF16 && kv_type != MK_KV_E4M3) return fail(MK_ERR_INVALID, "mk_chunk_create: kv_type");
+  if (num_pages < 1) return fail(MK_ERR_INVALID, "mk_chunk_create: num_pages");
+  mk_chunk* c = nullptr;
+  const int rc = guarded([&] {
+    c = new mk_chunk();
+    c->s = s; c->type = kv_type; c->num_pages = num_pages;
+    Built b;
+    int r = build(c, batch, seq_lens, new_lens, page_table, max_pages_per_seq, b);
+    if (r != MK_OK) return r;
+    cudaError_t e = cudaGetDevice(&c->device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c->ctas, cudaDevAttrMultiProcessorCount, c->device);
+    if (e == cudaSuccess) e = cudaMalloc((void**)&c->status, 4 * sizeof(int));
+    if (e != cudaSuccess) return fail_cuda("mk_chunk_create", e);
+    set_tasks(s, c->ctas, b);
+    r = commit(c, std::move(b), 0);
+    if (r != MK_OK) return r;
+    e = cudaStreamSynchronize(0);
+    return e == cudaSuccess ? MK_OK : fail_cuda("mk_chunk_create", e);
+  });
+  if (rc != MK_OK) {
+    mk_chunk_destroy(c);
+    return rc;
+  }
+  *out = c;
+  return MK_OK;
+}
+
+int mk_chunk_update(mk_chunk* c, int batch, const int* seq_lens, const int* new_lens, const int* page_table,
+                    int max_pages_per_seq, mk_stream stream) {
+  if (!c) return fail(MK_ERR_INVALID, "mk_chunk_update: chunk is NULL");
+  return guarded([&] {
+    Built b;
+    int rc = build(c, batch, seq_lens, new_lens, page_table, max_pages_per_seq, b);
+    if (rc == MK_OK) rc = check_device(c);
+    if (rc != MK_OK) return rc;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    const cudaError_t e = cudaStreamIsCapturing((cudaStream_t)stream, &cap);
+    if (e != cudaSuccess) return fail_cuda("mk_chunk_update", e);
+    if (cap != cudaStreamCaptureStatusNone) return fail(MK_ERR_INVALID, "mk_chunk_update: the stream is being captured");
+    set_tasks(c->s, c->ctas, b);
+    return commit(c, std::move(b), (cudaStream_t)stream);
+  });
+}
+
+int mk_chunk_append(mk_chunk* c, const void* qkv, int rows_type, long long row_stride, void* kv_pool, void* q,
+                    mk_stream stream) {
+  if (!c) return fail(MK_ERR_INVALID, "mk_chunk_append: chunk is NULL");
+  if (rows_type != MK_ROWS_BF16 && rows_type != MK_ROWS_F32) return fail(MK_ERR_INVALID, "mk_chunk_append: rows_type");
+  const long long el = rows_type == MK_ROWS_F32 ? 4 : 2, width = (long long)c->s.nkv * (c->s.G + 2) * c->s.d;
+  if (row_stride < width || row_stride > (LLONG_MAX >> 36) || row_stride * el % 16)
+    return fail(MK_ERR_INVALID, "mk_chunk_append: row_stride");
+  if (c->b.rows == 0) return check_device(c);
+  if (!aligned16(kv_pool) || !aligned16(qkv) || (c->s.nq ? !aligned16(q) : q != nullptr))
+    return fail(MK_ERR_INVALID, "mk_chunk_append: a buffer is NULL or not 16-byte aligned");
+  const int rc = check_device(c);
+  if (rc != MK_OK) return rc;
+  const cudaError_t e = mk::launch_append(c->view, c->type == MK_KV_E4M3, rows_type == MK_ROWS_F32, qkv, row_stride,
+                                          kv_pool, q, c->b.max_new_pages, (cudaStream_t)stream);
+  return e == cudaSuccess ? MK_OK : fail_cuda("mk_chunk_append", e);
+}
+
+int mk_chunk_attend(mk_chunk* c, const void* q, const void* kv_pool, void* out, mk_stream stream) {
+  if (!c) return fail(MK_ERR_INVALID, "mk_chunk_attend: chunk is NULL");
+  if (!c->s.nq) return fail(MK_ERR_INVALID, "mk_chunk_attend: a chunk without query heads");
+  if (c->b.rows == 0) return check_device(c);
+  if (!aligned16(q) || !aligned16(kv_pool) || !aligned16(out))
+    return fail(MK_ERR_INVALID, "mk_chunk_attend: a buffer is NULL or not 16-byte aligned");
+  const int rc = check_device(c);
+  if (rc != MK_OK) return rc;
+  const cudaError_t e = mk::launch_attend(c->view, c->type == MK_KV_E4M3, q, kv_pool, out, (cudaStream_t)stream);
+  return e == cudaSuccess ? MK_OK : fail_cuda("mk_chunk_attend", e);
+}
+
+int mk_chunk_read(mk_chunk* c, const void* kv_pool, void* out, mk_stream stream) {
+  if (!c) return fail(MK_ERR_INVALID, "mk_chunk_read: chunk is NULL");
+  if (c->b.tokens == 0) return check_device(c);
+  if (!aligned16(kv_pool) || !aligned16(out))
+    return fail(MK_ERR_INVALID, "mk_chunk_read: a buffer is NULL or not 16-byte aligned");
+  const int rc = check_device(c);
+  if (rc != MK_OK) return rc;
+  const cudaError_t e = mk::launch_read(c->view, c->type == MK_KV_E4M3, kv_pool, out, c->b.max_pages, (cudaStream_t)stream);
+  return e == cudaSuccess ? MK_OK : fail_cuda("mk_chunk_read", e);
+}
+
+int mk_chunk_sync(mk_chunk* c, mk_stream stream) {
+  if (!c) return fail(MK_ERR_INVALID, "mk_chunk_sync: chunk is NULL");
+  const int rc = check_device(c);
+  if (rc != MK_OK) return rc;
+  int st = 0;
+  cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&st, c->status, sizeof(int), cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+  return e == cudaSuccess ? st : fail_cuda("mk_chunk_sync", e);
+}
+
+int mk_chunk_info(const mk_chunk* c, int* out, int n) {
+  if (!c || (!out && n > 0)) return fail(MK_ERR_INVALID, "mk_chunk_info");
+  const int v[7] = {(int)c->b.reqs.size(), (int)c->b.rows, (int)std::min<long long>(c->b.tokens, INT_MAX),
+                    (int)c->b.tasks.size(), (int)c->b.nsplit, (int)c->b.joined_rows, c->ctas};
+  for (int i = 0; i < std::min(n, 7); ++i) out[i] = v[i];
+  return MK_OK;
+}
+
+int mk_chunk_inspect(const mk_model_dims* dims, int batch, const int* seq_lens, const int* new_lens, int num_ctas,
+                     int* tasks, int max_tasks) {
+  Shape s;
+  int rc = check_shape(dims, s);
+  if (rc != MK_OK) return rc;
+  if (num_ctas < 1 || max_tasks < 0 || (max_tasks && !tasks)) return fail(MK_ERR_INVALID, "mk_chunk_inspect");
+  return guarded([&] {
+    Built b;
+    int r = set_lens(s, batch, seq_lens, new_lens, b);
+    if (r != MK_OK) return r;
+    set_tasks(s, num_ctas, b);
+    const int n = std::min<int>(max_tasks, (int)b.tasks.size());
+    if (n) memcpy(tasks, b.tasks.data(), (size_t)n * sizeof(AttnTask));
+    return (int)b.tasks.size();
+  });
+}
+
+}  // extern "C"

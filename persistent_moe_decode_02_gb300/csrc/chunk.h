@@ -1,0 +1,60 @@
+// Records shared by the chunk operators' host side (chunk.cu) and their
+// kernels (cache.cu, attend.cu).
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace mk {
+
+constexpr int PAGE = 16;         // tokens of a page
+constexpr int KV_TILE = 128;     // keys of an attention tile (8 pages)
+constexpr int Q_TILE = 128;      // query rows (tokens x the group's heads) of an attention tile
+
+// One request of a chunk.
+struct alignas(16) ChunkReq {
+  int seq, nnew;                 // cached tokens, new tokens
+  int row0;                      // first packed row of its new tokens
+  int pad;
+  long long tok0;                // first packed row of all its tokens (mk_chunk_read)
+  long long pt;                  // first entry of its page-table row
+};
+static_assert(sizeof(ChunkReq) == 32, "request record is 32 bytes");
+
+// One attention task: new rows [tok0, tok0 + ntok) of a request, one KV head,
+// key tiles [tile0, tile0 + ntile).  part >= 0: the task holds a part of the
+// keys and writes its unnormalised rows at split row `part`.
+struct alignas(16) AttnTask {
+  int req, kvh, tok0, ntok, tile0, ntile, part, pad;
+};
+static_assert(sizeof(AttnTask) == 32, "attention task is 32 bytes");
+
+// The join of a block of rows whose keys were split over `nparts` tasks, whose
+// split rows start at part0 + i * (ntok * G).
+struct alignas(16) JoinTask {
+  int req, kvh, tok0, ntok, part0, nparts, pad0, pad1;
+};
+static_assert(sizeof(JoinTask) == 32, "join task is 32 bytes");
+
+// What the kernels of a chunk read.
+struct ChunkView {
+  int nq, nkv, d, G;
+  int batch, rows, num_pages;
+  const ChunkReq* reqs;
+  const int* pt;
+  const float2* rope;            // [rows][d / 2] (cos, sin) of the new rows; NULL: no rotation
+  const AttnTask* tasks;
+  const JoinTask* joins;
+  int ntasks, njoins;
+  float* part_o;                 // [split rows][d] unnormalised sums
+  float2* part_ml;               // [split rows] (maximum, sum) of the softmax
+  int* status;                   // first recorded error, 0 = none
+};
+
+cudaError_t launch_chunk_rope(const ChunkView& c, double theta, float2* tab, cudaStream_t st);
+cudaError_t launch_append(const ChunkView& c, bool e4m3, bool f32, const void* qkv, long long row_stride, void* pool,
+                          void* q, int max_new_pages, cudaStream_t st);
+cudaError_t launch_read(const ChunkView& c, bool e4m3, const void* pool, void* out, int max_pages, cudaStream_t st);
+cudaError_t launch_attend(const ChunkView& c, bool e4m3, const void* q, const void* pool, void* out, cudaStream_t st);
+
+}  // namespace mk

@@ -27,8 +27,11 @@ EXPORTS = [
     "mk_last_error", "mk_decode_step_noalloc", "mk_plan_set_sampling", "mk_plan_set_top_p", "mk_sched_create", "mk_sched_submit", "mk_sched_next",
     "mk_sched_commit", "mk_sched_abandon", "mk_sched_result", "mk_sched_forget", "mk_sched_stats",
     "mk_sched_destroy", "mk_serve_step", "mk_sched_next_rows", "mk_sched_set_prefill", "mk_plan_update_rows",
-    "mk_sched_peek_rows",
+    "mk_sched_peek_rows", "mk_chunk_create", "mk_chunk_update", "mk_chunk_append", "mk_chunk_attend", "mk_chunk_read",
+    "mk_chunk_sync", "mk_chunk_info", "mk_chunk_destroy", "mk_chunk_inspect", "mk_probs", "mk_verify",
 ]
+MK_KV_BF16, MK_KV_E4M3 = 0, 1
+MK_ROWS_BF16, MK_ROWS_F32 = 0, 1
 
 
 class MkModelDims(ctypes.Structure):
@@ -112,11 +115,26 @@ def lib():
         L.mk_sched_destroy.restype = None
         L.mk_serve_step.argtypes = [vp, ctypes.POINTER(vp), ctypes.POINTER(MkModelDims), ctypes.POINTER(MkWeights),
                                     ctypes.POINTER(MkKv), ctypes.POINTER(MkPlanOpts), vp]
+        L.mk_chunk_create.argtypes = [ctypes.POINTER(MkModelDims), i32, i32, i32, p_int, p_int, p_int, i32,
+                                      ctypes.POINTER(vp)]
+        L.mk_chunk_update.argtypes = [vp, i32, p_int, p_int, p_int, i32, vp]
+        L.mk_chunk_append.argtypes = [vp, vp, i32, i64, vp, vp, vp]
+        L.mk_chunk_attend.argtypes = [vp, vp, vp, vp, vp]
+        L.mk_chunk_read.argtypes = [vp, vp, vp, vp]
+        L.mk_chunk_sync.argtypes = [vp, vp]
+        L.mk_chunk_info.argtypes = [vp, p_int, i32]
+        L.mk_chunk_destroy.argtypes = [vp]
+        L.mk_chunk_destroy.restype = None
+        L.mk_chunk_inspect.argtypes = [ctypes.POINTER(MkModelDims), i32, p_int, p_int, i32, p_int, i32]
+        L.mk_probs.argtypes = [vp, i32, i32, i64, ctypes.c_float, vp, vp]
+        L.mk_verify.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
         for f in ("mk_plan_create", "mk_decode_step", "mk_decode_steps", "mk_decode_step_host", "mk_plan_update", "mk_plan_sync",
                   "mk_plan_read_debug", "mk_plan_info", "mk_plan_inspect", "mk_decode_step_noalloc",
                   "mk_plan_set_sampling", "mk_plan_set_top_p", "mk_sched_create", "mk_sched_submit", "mk_sched_next", "mk_sched_commit", "mk_sched_abandon",
                   "mk_sched_result", "mk_sched_forget", "mk_sched_stats", "mk_serve_step", "mk_sched_next_rows",
-                  "mk_sched_set_prefill", "mk_plan_update_rows", "mk_sched_peek_rows"):
+                  "mk_sched_set_prefill", "mk_plan_update_rows", "mk_sched_peek_rows", "mk_chunk_create",
+                  "mk_chunk_update", "mk_chunk_append", "mk_chunk_attend", "mk_chunk_read", "mk_chunk_sync",
+                  "mk_chunk_info", "mk_chunk_inspect", "mk_probs", "mk_verify"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -479,3 +497,181 @@ class Server:
             self.close()
         except Exception:
             pass
+
+
+def _here(name: str, t: torch.Tensor, dtypes, shape=None) -> int:
+    """The address of a contiguous tensor of the current device, checked."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: a tensor of the current CUDA device is wanted, got {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, wanted one of {dtypes}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    return t.data_ptr()
+
+
+def _current() -> int:
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _chunk_dims(D) -> MkModelDims:
+    return MkModelDims(n_q_heads=D.n_q_heads, n_kv_heads=D.n_kv_heads, head_dim=D.head_dim, page_size=D.page_size,
+                       rope_theta=D.rope_theta)
+
+
+_BF16, _U8, _ROWS = (torch.bfloat16,), (torch.uint8,), (torch.bfloat16, torch.float32)
+_F32, _I32 = (torch.float32,), (torch.int32,)
+
+
+class Chunk:
+    """Owns an mk_chunk: the operators over a chunk of new tokens of each
+    request (include/mk.h) - append to the paged cache, causal attention over
+    it, and reading it back.
+
+    D: dims with n_q_heads, n_kv_heads, head_dim, page_size and rope_theta (0:
+    no rotation).  kv_type: "bf16" (pools as Plan's: bf16 [num_pages, nkv, 2,
+    head_dim, page_size]) or "e4m3" (uint8 [num_pages, nkv, 2, head_dim + 1,
+    page_size]: codes, then the slots' scale exponents + 127)."""
+
+    def __init__(self, D, kv_type: str, num_pages: int, seq_lens: Sequence[int], new_lens: Sequence[int], page_table,
+                 max_pages: int):
+        kinds = {"bf16": MK_KV_BF16, "e4m3": MK_KV_E4M3}
+        if kv_type not in kinds:
+            raise ValueError(f"kv_type: {kv_type!r}, wanted one of {tuple(kinds)}")
+        self._dims = _chunk_dims(D)
+        self.kv_type, self.num_pages = kv_type, int(num_pages)
+        self.nq, self.nkv, self.d = D.n_q_heads, D.n_kv_heads, D.head_dim
+        h = ctypes.c_void_p()
+        rc = lib().mk_chunk_create(ctypes.byref(self._dims), kinds[kv_type], num_pages,
+                                   *self._batch(seq_lens, new_lens, page_table, max_pages), ctypes.byref(h))
+        if rc != MK_OK:
+            raise MkError("mk_chunk_create", rc)
+        self.h = h
+        self._lens(seq_lens, new_lens)
+        self._pool = (self.num_pages, self.nkv, 2, self.d + (kv_type == "e4m3"), D.page_size)
+        self._pool_type = _U8 if kv_type == "e4m3" else _BF16
+
+    def _batch(self, seq_lens, new_lens, page_table, max_pages):
+        sl, nl, pt = (np.ascontiguousarray(np.asarray(x), dtype=np.int32) for x in (seq_lens, new_lens, page_table))
+        if len(nl) != len(sl) or pt.size != len(sl) * max_pages:
+            raise ValueError("seq_lens, new_lens and page_table do not describe one batch")
+        p_int = ctypes.POINTER(ctypes.c_int)
+        self._host = (sl, nl, pt)    # outlive the call
+        return (len(sl), sl.ctypes.data_as(p_int), nl.ctypes.data_as(p_int), pt.ctypes.data_as(p_int), int(max_pages))
+
+    def _lens(self, seq_lens, new_lens):
+        self.rows = int(sum(int(x) for x in new_lens))
+        self.tokens = self.rows + int(sum(int(x) for x in seq_lens))
+        self._q = (self.rows, self.nq, self.d)
+
+    def update(self, seq_lens: Sequence[int], new_lens: Sequence[int], page_table, max_pages: int, stream=None) -> None:
+        """Another batch for this chunk (uploaded on the stream)."""
+        rc = lib().mk_chunk_update(self.h, *self._batch(seq_lens, new_lens, page_table, max_pages), _stream(stream))
+        if rc != MK_OK:
+            raise MkError("mk_chunk_update", rc)
+        self._lens(seq_lens, new_lens)
+
+    def append(self, qkv: torch.Tensor, kv_pool: torch.Tensor, q: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Rotate and append the rows qkv [rows, nkv, G + 2, head_dim] (or [rows, nkv * (G + 2) * head_dim]; bf16 or
+        float32, rows may lie apart) to one layer's pool; the rotated queries to q [rows, nq, head_dim] (bf16)."""
+        width = (self.nq + 2 * self.nkv) * self.d
+        if qkv.dim() < 2 or qkv.shape[0] != self.rows or qkv[:1].numel() != width * min(self.rows, 1) or (
+                self.rows and not qkv[0].is_contiguous()):
+            raise ValueError(f"qkv: shape {tuple(qkv.shape)}, wanted {self.rows} contiguous rows of {width}")
+        if not qkv.is_cuda or qkv.device.index != torch.cuda.current_device() or qkv.dtype not in _ROWS:
+            raise ValueError(f"qkv: a bf16 or float32 tensor of the current CUDA device is wanted, got {qkv.dtype} on "
+                             f"{qkv.device}")
+        if (q is None) != (self.nq == 0):
+            raise ValueError("q: wanted exactly when the chunk has query heads")
+        stride = qkv.stride(0) if self.rows > 1 else width
+        rc = lib().mk_chunk_append(self.h, qkv.data_ptr(), int(qkv.dtype == torch.float32), stride,
+                                   _here("kv_pool", kv_pool, self._pool_type, self._pool),
+                                   None if q is None else _here("q", q, _BF16, self._q),
+                                   _current() if stream is None else stream.cuda_stream)
+        if rc != MK_OK:
+            raise MkError("mk_chunk_append", rc)
+
+    def attend(self, q: torch.Tensor, kv_pool: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+        """Causal attention of the rows q [rows, nq, head_dim] over the pages; out like q (bf16)."""
+        rc = lib().mk_chunk_attend(self.h, _here("q", q, _BF16, self._q),
+                                   _here("kv_pool", kv_pool, self._pool_type, self._pool),
+                                   _here("out", out, _BF16, self._q),
+                                   _current() if stream is None else stream.cuda_stream)
+        if rc != MK_OK:
+            raise MkError("mk_chunk_attend", rc)
+
+    def read(self, kv_pool: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+        """Every cached and new position of every request, out [tokens, nkv, 2, head_dim] (bf16)."""
+        rc = lib().mk_chunk_read(self.h, _here("kv_pool", kv_pool, self._pool_type, self._pool),
+                                 _here("out", out, _BF16, (self.tokens, self.nkv, 2, self.d)),
+                                 _current() if stream is None else stream.cuda_stream)
+        if rc != MK_OK:
+            raise MkError("mk_chunk_read", rc)
+
+    def sync(self, stream=None) -> int:
+        """Wait for the stream; the device status."""
+        return lib().mk_chunk_sync(self.h, _stream(stream))
+
+    def info(self) -> dict:
+        buf = (ctypes.c_int * 7)()
+        lib().mk_chunk_info(self.h, buf, 7)
+        return dict(zip(["batch", "rows", "tokens", "tasks", "split_tasks", "joined_rows", "num_ctas"], list(buf)))
+
+    def close(self):
+        if getattr(self, "h", None):
+            lib().mk_chunk_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def inspect_chunk(D, seq_lens: Sequence[int], new_lens: Sequence[int], num_ctas: int) -> torch.Tensor:
+    """Host-only attention task list of a chunk: int tensor [n, 8] (request, KV head, first row, rows, first tile,
+    tiles, first split row or -1, 0)."""
+    dims, n = _chunk_dims(D), len(seq_lens)
+    args = (ctypes.byref(dims), n, _int_array(seq_lens), _int_array(new_lens), num_ctas)
+    count = lib().mk_chunk_inspect(*args, None, 0)
+    if count < 0:
+        raise MkError("mk_chunk_inspect", count)
+    buf = (ctypes.c_int * (8 * count))()
+    lib().mk_chunk_inspect(*args, buf, count)
+    return torch.tensor(list(buf), dtype=torch.int64).view(count, 8)
+
+
+def probs(logits: torch.Tensor, temperature: float, out: torch.Tensor, stream=None) -> None:
+    """softmax(logits / temperature) of float32 rows [rows, vocab] (rows may lie apart) into out [rows, vocab];
+    temperature 0: 1 at the largest logit."""
+    if logits.dim() != 2 or (logits.numel() and logits.stride(1) != 1) or logits.dtype != torch.float32 or (
+            not logits.is_cuda or logits.device.index != torch.cuda.current_device()):
+        raise ValueError("logits: float32 rows [rows, vocab] of the current CUDA device are wanted")
+    rows, vocab = logits.shape
+    rc = lib().mk_probs(logits.data_ptr() if rows else None, rows, vocab, logits.stride(0) if rows > 1 else vocab,
+                        float(temperature), _here("out", out, _F32, (rows, vocab)) if rows else None,
+                        _current() if stream is None else stream.cuda_stream)
+    if rc != MK_OK:
+        raise MkError("mk_probs", rc)
+
+
+def verify(target: torch.Tensor, draft: Optional[torch.Tensor], drafts: torch.Tensor, u: torch.Tensor, r: torch.Tensor,
+           tokens: torch.Tensor, accepted: torch.Tensor, n_draft: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Verify drafted tokens (include/mk.h): target float32 [batch, k + 1, vocab], draft float32 [batch, k, vocab] or
+    None (certain drafts), drafts int32 [batch, k], u float32 [batch, k], r float32 [batch], n_draft int32 [batch] or
+    None (k each); out: tokens int32 [batch, k + 1], accepted int32 [batch]."""
+    if target.dim() != 3:
+        raise ValueError("target: float32 [batch, k + 1, vocab] is wanted")
+    b, k1, v = target.shape
+    rc = lib().mk_verify(b, k1 - 1, v, _here("target", target, _F32),
+                         None if draft is None else _here("draft", draft, _F32, (b, k1 - 1, v)),
+                         _here("drafts", drafts, _I32, (b, k1 - 1)),
+                         None if n_draft is None else _here("n_draft", n_draft, _I32, (b,)),
+                         _here("u", u, _F32, (b, k1 - 1)), _here("r", r, _F32, (b,)),
+                         _here("tokens", tokens, _I32, (b, k1)), _here("accepted", accepted, _I32, (b,)),
+                         _current() if stream is None else stream.cuda_stream)
+    if rc != MK_OK:
+        raise MkError("mk_verify", rc)

@@ -1,0 +1,541 @@
+"""The operators over chunks (mk_chunk_*, mk_probs, mk_verify) on a GPU against
+64-bit CPU forms, at the sizes and masks where they can go wrong, and run
+together as a server uses them."""
+import dataclasses
+import math
+
+import pytest
+import torch
+
+import synth
+from synth.device import DeviceModel, PagedKV, kv_pages_needed
+from tests import chunk_util as cu
+
+pytestmark = pytest.mark.gpu
+
+HEADS = {"g8": (32, 4, 128), "g2d64": (4, 2, 64), "g6": (12, 2, 128), "g1d64": (5, 5, 64), "g3": (3, 1, 128),
+         "g7d64": (14, 2, 64)}
+LENS = {
+    "one_token_alone": ([0], [1]),
+    "one_token": ([333], [1]),
+    "page_ends": ([15, 16, 17, 31], [1, 1, 16, 17]),
+    "tile_ends": ([127, 128, 0], [1, 129, 128]),
+    "drafts": ([700, 0, 41, 1023, 1024, 5], [5, 3, 1, 4, 5, 8]),
+    "prompts": ([0, 0, 0], [300, 77, 129]),
+    "behind_cache": ([500, 1100], [210, 33]),
+    "an_empty_request": ([40, 0, 10], [0, 0, 6]),
+    "long_one_token": ([9001], [1]),
+}
+
+
+@pytest.fixture(scope="module")
+def mk(built):
+    from persistent_moe_decode_02_gb300 import mk
+    return mk
+
+
+def make(mk, heads, kv, lens, seed=1, theta=1e4):
+    nq, nkv, d = HEADS[heads]
+    batch = cu.Batch(*LENS[lens] if isinstance(lens, str) else lens, seed=seed)
+    D = cu.dims(nq, nkv, d, theta)
+    return D, batch, mk.Chunk(D, kv, batch.num_pages, batch.cached, batch.new, batch.flat, batch.width)
+
+
+def behind(batch):
+    """Slots of the requests' last pages behind their last tokens."""
+    s = [batch.slots(b, t, -(-t // cu.PAGE) * cu.PAGE) for b, t in enumerate(batch.total) if t % cu.PAGE]
+    return (torch.cat([x[0] for x in s]), torch.cat([x[1] for x in s])) if s else None
+
+
+def check_attend(mk, heads, kv, lens, seed=1, scale=1.0):
+    D, batch, chunk = make(mk, heads, kv, lens, seed)
+    pool = cu.make_pool(kv, batch.num_pages, D.n_kv_heads, D.head_dim, seed + 2)
+    q = cu.normal((batch.rows, D.n_q_heads, D.head_dim), seed + 3, scale).bfloat16()
+    ref, mag = cu.attend(q, pool, kv, batch, D.n_kv_heads)
+    gone = behind(batch)
+    if gone is not None:   # what lies behind a request's end is no number at all
+        if kv == "bf16":
+            pool[gone[0], :, :, :, gone[1]] = math.nan
+        else:
+            pool[gone[0], :, :, :, gone[1]] = 255   # e4m3 NaN, E8M0 NaN
+    out = torch.full((batch.rows + 1, D.n_q_heads, D.head_dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    chunk.attend(q.cuda(), pool.cuda(), out[:-1])
+    assert chunk.sync() == mk.MK_OK
+    got = out.cpu()
+    assert (got[-1] == 7).all()    # the row behind the last one is left
+    err = (got[:-1].double() - ref).abs()
+    bad = err > cu.attend_bound(ref, mag)
+    assert not bad.any(), (int(bad.sum()), float(err.max()), bad.nonzero()[:5].tolist())
+    chunk.close()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens", list(LENS))
+@pytest.mark.parametrize("heads", ["g8", "g2d64"])
+def test_attend_lengths(mk, heads, kv, lens):
+    check_attend(mk, heads, kv, lens)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads", ["g6", "g1d64", "g3", "g7d64"])
+def test_attend_groups(mk, heads, kv):
+    for lens in ("drafts", "behind_cache"):
+        check_attend(mk, heads, kv, lens, seed=5)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_attend_peaked_scores(mk, kv):
+    # scores of tens of units: the running maximum moves often
+    check_attend(mk, "g8", kv, ([300, 40], [40, 300]), seed=9, scale=6.0)
+
+
+def test_attend_shared_prefix_pages(mk):
+    # two requests read the same cached pages and add rows in pages of their own
+    D = cu.dims(8, 2, 128)
+    batch = cu.Batch([64, 64], [3, 20], seed=3)
+    batch.table[1][:4] = batch.table[0][:4]
+    batch.flat = [p for row in batch.table for p in row]
+    chunk = mk.Chunk(D, "bf16", batch.num_pages, batch.cached, batch.new, batch.flat, batch.width)
+    pool = cu.make_pool("bf16", batch.num_pages, 2, 128, 5)
+    q = cu.normal((23, 8, 128), 6).bfloat16()
+    ref, mag = cu.attend(q, pool, "bf16", batch, 2)
+    out = torch.empty(23, 8, 128, dtype=torch.bfloat16, device="cuda")
+    chunk.attend(q.cuda(), pool.cuda(), out)
+    assert chunk.sync() == mk.MK_OK
+    assert ((out.cpu().double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
+
+
+@pytest.mark.parametrize("rows_type", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,lens", [("g8", "drafts"), ("g8", "behind_cache"), ("g2d64", "page_ends"),
+                                        ("g6", "prompts"), ("g1d64", "an_empty_request"), ("g7d64", "one_token_alone")])
+def test_append(mk, heads, lens, kv, rows_type):
+    D, batch, chunk = make(mk, heads, kv, lens, seed=2)
+    nq, nkv, d = D.n_q_heads, D.n_kv_heads, D.head_dim
+    pool = cu.make_pool(kv, batch.num_pages, nkv, d, 4)
+    wide = cu.normal((batch.rows, nkv * (nq // nkv + 2) * d + 64), 5).to(rows_type)   # rows lie apart
+    wide[0, (nq // nkv) * d:(nq // nkv + 1) * d] = 0                                  # a key of zeros
+    x = wide[:, :-64].view(batch.rows, nkv, nq // nkv + 2, d)
+    pos = batch.positions()
+    turned = cu.rotate(x[:, :, :-1], pos, D.rope_theta)
+    size = (x[:, :, :-1].double()[..., :d // 2].abs() + x[:, :, :-1].double()[..., d // 2:].abs()).repeat(1, 1, 1, 2)
+    ref_q, ref_k, ref_v = turned[:, :, :-1].flatten(1, 2), turned[:, :, -1], x[:, :, -1]
+    # cos and sin rounded to fp32, two products and a sum: under 4 roundings of the pair's size
+    slack = 4 * 2.0 ** -24 * size
+    gpool, gq = pool.cuda(), torch.empty(batch.rows, nq, d, dtype=torch.bfloat16, device="cuda")
+    chunk.append(wide.cuda()[:, :-64], gpool, gq)
+    assert chunk.sync() == mk.MK_OK
+    assert ((gq.cpu().double() - ref_q).abs() <= cu.BF16 * ref_q.abs() + slack[:, :, :-1].flatten(1, 2) * 1.01).all()
+    got, (page, slot) = gpool.cpu(), batch.new_slots()
+    new = got[page, :, :, :, slot]
+    kept, was = got.clone(), pool.clone()
+    kept[page, :, :, :, slot] = 0
+    was[page, :, :, :, slot] = 0
+    assert torch.equal(kept.view(torch.uint8), was.view(torch.uint8))   # nothing but the new slots is written
+    if kv == "bf16":
+        assert torch.equal(new[:, :, 1], ref_v.bfloat16())
+        assert ((new[:, :, 0].double() - ref_k).abs() <= cu.BF16 * ref_k.abs() + slack[:, :, -1] * 1.01).all()
+        return
+    code, k = cu.quantise(ref_v.float())
+    assert torch.equal(new[:, :, 1, :-1], code) and torch.equal(new[:, :, 1, -1].int() - 127, k)
+    k = new[:, :, 0, -1].double() - 127
+    val = torch.ldexp(new[:, :, 0, :-1].contiguous().view(torch.float8_e4m3fn).double(), k.unsqueeze(-1))
+    unit = torch.exp2(k).unsqueeze(-1)
+    assert ((val - ref_k).abs() <= torch.maximum(cu.E4M3_STEP * ref_k.abs(), cu.E4M3_MIN * unit) + 2 * slack[:, :, -1]).all()
+    top = ref_k.abs().amax(-1)
+    # the smallest scale that holds the vector, up to the rotation's own roundings
+    assert (top <= 448 * torch.exp2(k) * (1 + 2.0 ** -20)).all()
+    assert ((top >= 224 * torch.exp2(k) * (1 - 2.0 ** -20)) | (k == -127)).all()
+
+
+def test_append_far_position_and_no_rotation(mk):
+    # a position near 2^18: angles keep their fraction; theta 0 leaves the rows
+    far = 262143
+    for theta in (1e4, 0.0):
+        D = cu.dims(2, 1, 64, theta)
+        width = far // cu.PAGE + 2
+        table = [0] * width
+        table[far // cu.PAGE:] = [1, 2]
+        chunk = mk.Chunk(D, "bf16", 3, [far], [3], table, width)
+        x = cu.normal((3, 1, 4, 64), 8)
+        pool, q = torch.zeros(3, 1, 2, 64, 16, dtype=torch.bfloat16, device="cuda"), torch.empty(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+        chunk.append(x.cuda(), pool, q)
+        assert chunk.sync() == mk.MK_OK
+        ref = cu.rotate(x[:, :, :2], torch.arange(far, far + 3), theta).flatten(1, 2)
+        assert ((q.cpu().double() - ref).abs() <= cu.BF16 * ref.abs() + 2.0 ** -20).all()
+
+
+def test_append_infinities_and_nan_in_8_bits(mk):
+    D = cu.dims(0, 1, 64, 0.0)
+    chunk = mk.Chunk(D, "e4m3", 1, [0], [4], [0], 1)
+    x = cu.normal((4, 1, 2, 64), 3)
+    x[0, 0, 0, 5], x[1, 0, 1, 6], x[2, 0, 0, 7] = math.inf, math.nan, 3e38
+    x[3] = 1e-44
+    pool = torch.zeros(1, 1, 2, 65, 16, dtype=torch.uint8, device="cuda")
+    chunk.append(x.cuda(), pool)
+    out = torch.empty(4, 1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    chunk.read(pool, out)
+    assert chunk.sync() == mk.MK_OK
+    got = out.cpu()
+    assert got[0, 0, 0, 5] == math.inf
+    assert got[1, 0, 1, 6].isnan() and got[1].isnan().sum() == 1      # the vector's others are numbers
+    fine = torch.ones(64, dtype=torch.bool)
+    fine[6] = False
+    assert ((got[1, 0, 1].double() - x[1, 0, 1].double()).abs() <= 2.0 ** -4 * x[1, 0, 1].abs() + 2.0 ** -9)[fine].all()
+    assert abs(float(got[2, 0, 0, 7]) / 3e38 - 1) <= 2.0 ** -4 + cu.BF16
+    assert (got[3].abs() <= 2e-44).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,lens", [("g8", "drafts"), ("g2d64", "an_empty_request"), ("g3", "tile_ends")])
+def test_read(mk, heads, lens, kv):
+    D, batch, chunk = make(mk, heads, kv, lens)
+    pool = cu.make_pool(kv, batch.num_pages, D.n_kv_heads, D.head_dim, 4)
+    ref = torch.cat([cu.rows_of(pool, kv, batch, b) for b in range(len(batch.new)) if batch.total[b]])
+    out = torch.full((ref.shape[0] + 1, *ref.shape[1:]), 7.0, dtype=torch.bfloat16, device="cuda")
+    chunk.read(pool.cuda(), out[:-1])
+    assert chunk.sync() == mk.MK_OK
+    assert torch.equal(out[:-1].cpu(), ref.bfloat16()) and (out[-1] == 7).all()
+
+
+def test_rows_move_between_pools(mk):
+    # out of an 8-bit pool and into a bf16 one at other pages, values unchanged
+    D = cu.dims(0, 2, 128, 0.0)
+    batch, other = cu.Batch([100, 31], [0, 0], seed=1), cu.Batch([0, 0], [100, 31], seed=2)
+    pool = cu.make_pool("e4m3", batch.num_pages, 2, 128, 4)
+    src = mk.Chunk(D, "e4m3", batch.num_pages, batch.cached, batch.new, batch.flat, batch.width)
+    dst = mk.Chunk(D, "bf16", other.num_pages, other.cached, other.new, other.flat, other.width)
+    rows = torch.empty(131, 2, 2, 128, dtype=torch.bfloat16, device="cuda")
+    to = torch.zeros(other.num_pages, 2, 2, 128, 16, dtype=torch.bfloat16, device="cuda")
+    src.read(pool.cuda(), rows)
+    dst.append(rows, to)
+    assert dst.sync() == mk.MK_OK
+    for b in range(2):
+        assert torch.equal(cu.rows_of(to.cpu(), "bf16", other, b), cu.rows_of(pool, "e4m3", batch, b).bfloat16().double())
+
+
+# ---- probabilities and verification ----
+
+def probs_bound(ref):
+    """The exponent's argument is rounded three times (2^-22 of it), the sum about 130 times (2^-17), and the
+    result twice."""
+    x = torch.log2(ref / ref.amax(-1, keepdim=True)).abs().nan_to_num(0, posinf=0)
+    return ref * (2.0 ** -16 + 2.0 ** -22 * x) + 2.0 ** -126
+
+
+@pytest.mark.parametrize("vocab", [1, 3, 4, 127, 2048, 2051, 32000, 151936, 393216])
+@pytest.mark.parametrize("temperature", [0.7, 1.0, 0.05, 40.0])
+def test_probs(mk, vocab, temperature):
+    rows = 3
+    x = cu.normal((rows, vocab + 5), vocab, 3.0)[:, :vocab]
+    ref = torch.softmax(x.double() / torch.tensor(temperature, dtype=torch.float32).double(), -1)
+    gx = torch.empty(rows, vocab + 5, device="cuda")[:, :vocab]
+    gx.copy_(x)
+    out = torch.full((rows + 1, vocab), 7.0, device="cuda")
+    mk.probs(gx, temperature, out[:-1])
+    got = out.cpu()
+    assert ((got[:-1].double() - ref).abs() <= probs_bound(ref)).all()
+    assert (got[-1] == 7).all()
+
+
+@pytest.mark.parametrize("vocab", [5, 3001, 151936])
+def test_probs_masks_and_ends(mk, vocab):
+    low = torch.finfo(torch.float32).min
+    x = cu.normal((8, vocab), 1)
+    x[0, 1:] = -math.inf                  # one left
+    x[1] = -math.inf                      # nothing left
+    x[2] = low                            # every logit the lowest number
+    x[3, ::2] = low                       # some
+    x[4, vocab - 1] = math.nan
+    x[5, 0] = math.inf
+    x[6, vocab // 2:] = -math.inf
+    x[7, 0], x[7, 1] = torch.finfo(torch.float32).max, low
+    for t in (1.0, 0.0):
+        out = torch.empty(8, vocab, device="cuda")
+        mk.probs(x.cuda(), t, out)
+        got = out.cpu()
+        assert got[4].isnan().all() and got[5].isnan().all() and (got[1] == 0).all()
+        fine = [0, 2, 3, 6, 7]
+        if t:
+            ref = torch.softmax(x[fine].double(), -1)
+            assert ((got[fine].double() - ref).abs() <= probs_bound(ref)).all()
+        else:
+            ref = torch.zeros(len(fine), vocab)
+            for i, r in enumerate(fine):   # the lowest index of equal ones
+                ref[i, int((x[r] == x[r].max()).nonzero()[0])] = 1
+            assert torch.equal(got[fine], ref)
+
+
+def test_probs_in_place_and_tiny_temperature(mk):
+    x = cu.normal((4, 4099), 5).cuda()
+    ref = torch.empty_like(x)
+    mk.probs(x, 0.9, ref)
+    mk.probs(x, 0.9, x)
+    assert torch.equal(x, ref)
+    y, out = cu.normal((2, 100), 6).cuda(), torch.empty(2, 100, device="cuda")
+    mk.probs(y, 3e-39, out)               # as good as greedy, and no NaN
+    assert torch.equal(out.argmax(1), y.argmax(1)) and float(out.sum()) == 2
+
+
+def draws(b, k, vocab, seed, near=0.7):
+    g = torch.Generator().manual_seed(seed)
+    t = torch.randn(b, k + 1, vocab, generator=g) * 2
+    d = t[:, :k] + near * torch.randn(b, k, vocab, generator=g)
+    t, d = torch.softmax(t, -1), torch.softmax(d, -1)
+    x = torch.multinomial(d.reshape(-1, vocab), 1, generator=g).view(b, k).int() if k else torch.zeros(b, 0, dtype=torch.int32)
+    return t, d, x, torch.rand(b, k, generator=g), torch.rand(b, generator=g)
+
+
+def check_verify(mk, t, d, x, u, r, count=None):
+    b, k1, _ = t.shape
+    tokens = torch.full((b + 1, k1), 77, dtype=torch.int32, device="cuda")
+    accepted = torch.full((b + 1,), 77, dtype=torch.int32, device="cuda")
+    mk.verify(t.cuda(), None if d is None else d.cuda(), x.cuda(), u.cuda(), r.cuda(), tokens[:-1], accepted[:-1],
+              None if count is None else count.cuda())
+    ref_t, ref_a = cu.verify(t, d, x, u, r, count)
+    assert torch.equal(accepted[:-1].cpu(), torch.from_numpy(ref_a))
+    assert torch.equal(tokens[:-1].cpu(), torch.from_numpy(ref_t))
+    assert (tokens[-1] == 77).all() and int(accepted[-1]) == 77
+
+
+@pytest.mark.parametrize("b,k,vocab", [(1, 0, 11), (1, 1, 1), (3, 4, 5), (7, 3, 2047), (4, 5, 2049), (5, 7, 32000),
+                                       (2, 2, 151936), (1, 1, 393215), (2, 40, 513)])
+@pytest.mark.parametrize("point", [False, True])
+def test_verify(mk, b, k, vocab, point):
+    for seed in range(4):
+        t, d, x, u, r = draws(b, k, vocab, 100 * seed + vocab)
+        count = torch.randint(-1, k + 2, (b,), generator=torch.Generator().manual_seed(seed)).int() if seed % 2 else None
+        check_verify(mk, t, None if point or not k else d, x, u, r, count)
+
+
+def test_verify_ends(mk):
+    vocab = 4097
+    t, d, x, u, r = draws(9, 2, vocab, 5)
+    r[0], r[1], r[2] = 0.0, 1.0, math.nan
+    x[3, 0], x[4, 1] = -1, vocab            # drafts that are no tokens
+    u[5, 0] = math.nan
+    u[0, 0] = u[1, 0] = 2.0                 # refused
+    t[6, 0, 5] = math.nan
+    t[7] = 0                                # nothing to draw
+    d[8] = t[8, :2]                         # no difference, yet refused
+    u[8] = 2.0
+    check_verify(mk, t, d, x, u, r)
+    t[7] = math.nan
+    check_verify(mk, t, None, x, u, r)
+
+
+def test_verify_follows_the_target(mk):
+    # whatever the drafts, the first token's law is the target's: the counts of 60000
+    # draws over 6 tokens, each within 5 standard deviations
+    n, vocab = 60000, 6
+    g = torch.Generator().manual_seed(3)
+    p, q = torch.softmax(torch.randn(vocab, generator=g), 0), torch.softmax(torch.randn(vocab, generator=g), 0)
+    x = torch.multinomial(q, n, replacement=True, generator=g).view(n, 1).int()
+    tokens = torch.empty(n, 2, dtype=torch.int32, device="cuda")
+    accepted = torch.empty(n, dtype=torch.int32, device="cuda")
+    mk.verify(p.expand(n, 2, vocab).contiguous().cuda(), q.expand(n, 1, vocab).contiguous().cuda(), x.cuda(),
+              torch.rand(n, 1, generator=g).cuda(), torch.rand(n, generator=g).cuda(), tokens, accepted)
+    got = torch.bincount(tokens[:, 0].cpu().long(), minlength=vocab).double()
+    assert ((got - n * p.double()).abs() <= 5 * (n * p.double() * (1 - p.double())).sqrt()).all()
+
+
+# ---- how they are called ----
+
+def test_streams_graphs_and_updates(mk):
+    # captured with its inputs, replayed after they changed; a second chunk runs on another stream at the same time
+    D, batch, chunk = make(mk, "g8", "bf16", "drafts", seed=4)
+    D2, batch2, chunk2 = make(mk, "g8", "bf16", "behind_cache", seed=6)
+    work = []
+    for b, c in ((batch, chunk), (batch2, chunk2)):
+        work.append(dict(b=b, c=c, pool=cu.make_pool("bf16", b.num_pages, 4, 128, 9).cuda(),
+                         qkv=torch.empty(b.rows, 4, 10, 128, dtype=torch.bfloat16, device="cuda"),
+                         q=torch.empty(b.rows, 32, 128, dtype=torch.bfloat16, device="cuda"),
+                         out=torch.empty(b.rows, 32, 128, dtype=torch.bfloat16, device="cuda"),
+                         stream=torch.cuda.Stream(), graph=torch.cuda.CUDAGraph()))
+    for w in work:
+        w["qkv"].copy_(cu.normal(w["qkv"].shape, 3).bfloat16())
+    torch.cuda.synchronize()
+    for w in work:
+        with torch.cuda.graph(w["graph"], stream=w["stream"]):
+            w["c"].append(w["qkv"], w["pool"], w["q"])
+            w["c"].attend(w["q"], w["pool"], w["out"])
+            with pytest.raises(mk.MkError):
+                w["c"].update(w["b"].cached, w["b"].new, w["b"].flat, w["b"].width, stream=w["stream"])
+    for turn in range(3):
+        for w in work:
+            w["qkv"].copy_(cu.normal(w["qkv"].shape, 10 + turn).bfloat16())
+        torch.cuda.synchronize()
+        for w in work:
+            with torch.cuda.stream(w["stream"]):
+                w["graph"].replay()
+        torch.cuda.synchronize()
+        for w in work:
+            ref, mag = cu.attend(w["q"].cpu(), w["pool"].cpu(), "bf16", w["b"], 4)
+            assert ((w["out"].cpu().double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
+    # another batch for the same chunk, larger and smaller, on a side stream
+    side = torch.cuda.Stream()
+    for lens in ("prompts", "one_token", "behind_cache"):
+        b = cu.Batch(*LENS[lens], seed=8)
+        pool = cu.make_pool("bf16", max(b.num_pages, batch.num_pages), 4, 128, 2)
+        c = mk.Chunk(D, "bf16", pool.shape[0], batch.cached, batch.new, batch.flat, batch.width)
+        c.update(b.cached, b.new, b.flat, b.width, stream=side)
+        q, out = cu.normal((b.rows, 32, 128), 1).bfloat16(), torch.empty(b.rows, 32, 128, dtype=torch.bfloat16, device="cuda")
+        gq, gp = q.cuda(), pool.cuda()
+        side.wait_stream(torch.cuda.current_stream())
+        c.attend(gq, gp, out, stream=side)
+        assert c.sync(side) == mk.MK_OK
+        ref, mag = cu.attend(q, pool, "bf16", b, 4)
+        assert ((out.cpu().double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
+
+
+def test_same_bits_every_time(mk):
+    D, batch, chunk = make(mk, "g8", "e4m3", ([4000, 9000, 100], [5, 1, 200]))
+    pool = cu.make_pool("e4m3", batch.num_pages, 4, 128, 3).cuda()
+    q = cu.normal((batch.rows, 32, 128), 3).bfloat16().cuda()
+    outs = [torch.empty_like(q) for _ in range(4)]
+    for o in outs:
+        chunk.attend(q, pool, o)
+    assert chunk.sync() == mk.MK_OK
+    assert all(torch.equal(outs[0], o) for o in outs[1:])
+
+
+def test_refused_tensors(mk):
+    D, batch, chunk = make(mk, "g8", "bf16", "one_token")
+    pool = torch.zeros(batch.num_pages, 4, 2, 128, 16, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(1, 32, 128, dtype=torch.bfloat16, device="cuda")
+    for bad in (q.cpu(), q.float(), q[:, :31], q.new_zeros(1, 128, 32).transpose(1, 2)):
+        with pytest.raises(ValueError):
+            chunk.attend(bad, pool, q)
+    with pytest.raises(ValueError):
+        chunk.attend(q, pool[:-1], q)
+    with pytest.raises(ValueError):
+        chunk.append(torch.zeros(1, 4, 10, 128, device="cuda").double(), pool, q)
+    with pytest.raises(ValueError):
+        chunk.append(torch.zeros(1, 4, 10, 128, device="cuda"), pool)
+    with pytest.raises(mk.MkError) as e:   # rows 10 bytes apart from 16-byte steps
+        D1, b1, c1 = make(mk, "g8", "bf16", ([0], [2]))
+        wide = torch.zeros(2, 5125, device="cuda")[:, :5120]
+        c1.append(wide, torch.zeros(b1.num_pages, 4, 2, 128, 16, dtype=torch.bfloat16, device="cuda"), q.new_zeros(2, 32, 128))
+    assert e.value.code == mk.MK_ERR_INVALID
+    x = torch.zeros(4, 100, device="cuda")
+    with pytest.raises(mk.MkError):        # the output starts inside the input
+        mk.probs(x[:2], 1.0, x[1:3])
+
+
+# ---- a run of them, as a server uses them ----
+
+def test_prompt_layer_by_pieces_equals_whole(mk):
+    # one layer's cache filled and attended in one chunk, and in pieces of several sizes: the same values
+    D = cu.dims(32, 4, 128)
+    n = 150
+    x = cu.normal((n, 4, 10, 128), 4).bfloat16().cuda()
+    results = []
+    for cuts in ([n], [1, 15, 17, 64, 53], [128, 22]):
+        batch = cu.Batch([0], [n], seed=1)
+        pool = torch.zeros(batch.num_pages, 4, 2, 128, 16, dtype=torch.bfloat16, device="cuda")
+        out, at = torch.empty(n, 32, 128, dtype=torch.bfloat16, device="cuda"), 0
+        for c in cuts:
+            chunk = mk.Chunk(D, "bf16", batch.num_pages, [at], [c], batch.flat, batch.width)
+            q = torch.empty(c, 32, 128, dtype=torch.bfloat16, device="cuda")
+            chunk.append(x[at:at + c], pool, q)
+            chunk.attend(q, pool, out[at:at + c])
+            assert chunk.sync() == mk.MK_OK
+            at += c
+        results.append((pool.cpu(), out.cpu()))
+    for pool, out in results[1:]:
+        assert torch.equal(pool, results[0][0])
+        # weights rounded against another running maximum: one rounding of the weights and one of the result each
+        assert ((out.double() - results[0][1].double()).abs() <= 4 * cu.BF16 * 1.5).all()
+
+
+def tiny_model():
+    return dataclasses.replace(synth.TINY, n_layers=1), 3
+
+
+def test_appended_prompt_feeds_the_decode_step(mk):
+    # a one-layer model's prompt enters its cache through mk_chunk_append; the
+    # decode step continues from it as from its own prefill rows
+    D, seed = tiny_model()
+    model = DeviceModel(D, seed)
+    w = model.weights()
+    prompt = [(37 * i + 11) % D.vocab for i in range(8)]
+    pages, width = kv_pages_needed(D, [16], 2) + 2, 3
+    table = [2, 0, 1]
+
+    def pools():
+        return [torch.zeros(pages, D.n_kv_heads, 2, D.head_dim, 16, dtype=torch.bfloat16, device="cuda")]
+
+    a, b = pools(), pools()
+    tok = torch.tensor(prompt, dtype=torch.int32, device="cuda")
+    first = mk.Plan(D, w, a, [0], table, width, max_batch=8)
+    first.update_rows(list(range(8)), table * 8, width, [0] * 8)
+    nxt = torch.empty(8, dtype=torch.int32, device="cuda")
+    assert first.step(tok, nxt) == mk.MK_OK and first.sync() == mk.MK_OK
+    # the same rows by hand: embedding, norm and projection in fp32, then the append
+    x = w["embed"][tok.long()].float()
+    x = x * torch.rsqrt((x * x).mean(-1, keepdim=True) + D.rms_eps) * w["attn_norm"][0].float()
+    qkv = (x @ w["wqkv"][0].float().T).view(8, D.n_kv_heads, D.group + 2, D.head_dim)
+    chunk = mk.Chunk(D, "bf16", pages, [0], [8], table, width)
+    q = torch.empty(8, D.n_q_heads, D.head_dim, dtype=torch.bfloat16, device="cuda")
+    chunk.append(qkv, b[0], q)
+    assert chunk.sync() == mk.MK_OK
+    ka, kb = (p[0][table[0], :, :, :, :8].float() for p in (a, b))
+    # both round fp32 sums of other orders to bf16: at most a step apart
+    assert ((ka - kb).abs() <= 2.01 * cu.BF16 * ka.abs() + 1e-4).all()
+    logits = []
+    for pool in (a, b):
+        plan = mk.Plan(D, w, pool, [8], table, width)
+        lg, n1 = torch.empty(1, D.vocab, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+        assert plan.step(nxt[7:8].contiguous(), n1, lg) == mk.MK_OK and plan.sync() == mk.MK_OK
+        logits.append(lg.double())
+        plan.close()
+    first.close()
+    assert float((logits[0] - logits[1]).norm() / logits[0].norm()) <= 1e-2
+
+
+def test_drafted_tokens_through_plan_probs_and_verify(mk):
+    # speculative greedy decoding: the target checks drafts as chunk rows, and what it
+    # accepts is its own greedy continuation, whatever is drafted
+    D, seed = dataclasses.replace(synth.TINY), 3
+    model = DeviceModel(D, seed)
+    w, k, steps = model.weights(), 3, 12
+    width, pages = 4, 8
+    table = [5, 1, 6, 0]
+
+    def pools():
+        return [torch.zeros(pages, D.n_kv_heads, 2, D.head_dim, 16, dtype=torch.bfloat16, device="cuda")
+                for _ in range(D.n_layers)]
+
+    plan = mk.Plan(D, w, pools(), [0], table, width)
+    tok = torch.tensor([7], dtype=torch.int32, device="cuda")
+    plain = [7]
+    for _ in range(steps):
+        nxt = torch.empty(1, dtype=torch.int32, device="cuda")
+        assert plan.step(tok, nxt) == mk.MK_OK and plan.sync() == mk.MK_OK
+        plain.append(int(nxt))
+        tok = nxt
+    plan.close()
+    plan = mk.Plan(D, w, pools(), [0], table, width, max_batch=8)
+    got, turn = [7], 0
+    while len(got) <= steps:
+        right = plain[len(got):len(got) + k]
+        drafts = [x if (turn + i) % 3 else (x + 1) % D.vocab for i, x in enumerate(right)] + [0] * (k - len(right))
+        turn += 1
+        at = len(got) - 1
+        plan.update_rows(list(range(at, at + k + 1)), table * (k + 1), width, [0] * (k + 1))
+        rows = torch.tensor([got[-1]] + drafts, dtype=torch.int32, device="cuda")
+        logits = torch.empty(k + 1, D.vocab, device="cuda")
+        nxt = torch.empty(k + 1, dtype=torch.int32, device="cuda")
+        assert plan.step(rows, nxt, logits) == mk.MK_OK
+        target = torch.empty(k + 1, D.vocab, device="cuda")
+        mk.probs(logits, 0.0, target)
+        tokens, accepted = torch.empty(1, k + 1, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+        mk.verify(target.view(1, k + 1, -1), None, rows[1:].view(1, k), torch.rand(1, k, device="cuda"),
+                  torch.rand(1, device="cuda"), tokens, accepted)
+        assert plan.sync() == mk.MK_OK
+        n = int(accepted)
+        new = tokens[0, :n + 1].tolist()
+        assert (tokens[0, n + 1:] == -1).all() and new[:n] == drafts[:n]
+        got += new
+    plan.close()
+    assert got[:steps + 1] == plain
