@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <functional>
 #include <new>
 #include <stdexcept>
 #include <vector>
@@ -127,9 +128,94 @@ int set_pages(int num_pages, const int* page_table, int max_pages, Built& b) {
 }
 
 // Attention tasks.  A block is the rows of up to two query tiles of one
-// request and KV head (a tile: Q_TILE / G tokens with their G heads).
+// request and KV head (a tile: the G heads of Q_TILE / G tokens); its keys run
+// to its last row's position, in tiles of KV_TILE.  Where the blocks are too
+// few or too uneven to fill the CTAs, their keys are cut into tasks of at most
+// `len` tiles and joined afterwards; `len` is the one of a geometric series
+// whose longest-first schedule ends first.  The unit is the time of a tile
+// (about 0.7 us); a task costs SETUP of them before its first product, and a
+// join after the tasks JOIN.
+struct Block {
+  int req, kvh, tok0, ntok, tiles;
+};
+constexpr double SETUP = 3., JOIN = 4.;
+
+double cost(int tiles) { return SETUP + tiles; }
+
+// When the last CTA is done: `n[t]` tasks of t tiles each, longest first, each
+// to the CTA that is free first.
+double makespan(const std::vector<int>& lens, int ctas) {
+  std::vector<double> heap;      // a binary min-heap of the CTAs' loads
+  double last = 0.;
+  for (int t : lens) {
+    double at = 0.;
+    if ((int)heap.size() >= ctas) {
+      std::pop_heap(heap.begin(), heap.end(), std::greater<double>());
+      at = heap.back();
+      heap.pop_back();
+    }
+    heap.push_back(at + cost(t));
+    last = std::max(last, heap.back());
+    std::push_heap(heap.begin(), heap.end(), std::greater<double>());
+  }
+  return last;
+}
+
+constexpr size_t MAX_PLANNED = 16384;   // tasks: beyond them the blocks fill the CTAs anyway
+
 void set_tasks(const Shape& s, int ctas, Built& b) {
-  (void)s; (void)ctas; (void)b;
+  b.tasks.clear();
+  b.joins.clear();
+  b.split_rows = b.nsplit = b.joined_rows = 0;
+  if (!s.G) return;
+  const int per_tile = mk::Q_TILE / s.G, per_block = 2 * per_tile;
+  std::vector<Block> blocks;
+  int longest = 1;
+  for (int i = 0; i < (int)b.reqs.size(); ++i) {
+    const ChunkReq& r = b.reqs[i];
+    for (int t = 0; t < r.nnew; t += per_block) {
+      const int n = std::min(per_block, r.nnew - t), tiles = (r.seq + t + n + mk::KV_TILE - 1) / mk::KV_TILE;
+      longest = std::max(longest, tiles);
+      for (int g = 0; g < s.nkv; ++g) blocks.push_back({i, g, t, n, tiles});
+    }
+  }
+  int best_len = longest;
+  double best = 1e300;
+  for (int len = longest;; len = std::min(len - 1, (int)(len * 0.85))) {
+    if (len < 1) break;
+    std::vector<int> lens;
+    bool cut = false;
+    for (const Block& k : blocks) {
+      const int parts = (k.tiles + len - 1) / len;
+      cut |= parts > 1;
+      for (int p = 0; p < parts; ++p)
+        lens.push_back((int)((long long)k.tiles * (p + 1) / parts - (long long)k.tiles * p / parts));
+      if (lens.size() > MAX_PLANNED) break;
+    }
+    if (lens.size() > MAX_PLANNED) break;
+    std::sort(lens.begin(), lens.end(), std::greater<int>());
+    const double t = makespan(lens, ctas) + (cut ? JOIN : 0.);
+    if (t < best) {
+      best = t;
+      best_len = len;
+    }
+  }
+  for (const Block& k : blocks) {
+    const int parts = (k.tiles + best_len - 1) / best_len, rows = k.ntok * s.G;
+    if (parts > 1) {
+      b.joins.push_back({k.req, k.kvh, k.tok0, k.ntok, (int)b.split_rows, parts, 0, 0});
+      b.joined_rows += rows;
+    }
+    for (int p = 0; p < parts; ++p) {
+      const int t0 = (int)((long long)k.tiles * p / parts), t1 = (int)((long long)k.tiles * (p + 1) / parts);
+      b.tasks.push_back({k.req, k.kvh, k.tok0, k.ntok, t0, t1 - t0, parts > 1 ? (int)b.split_rows : -1, 0});
+      if (parts > 1) {
+        b.split_rows += rows;
+        ++b.nsplit;
+      }
+    }
+  }
+  std::stable_sort(b.tasks.begin(), b.tasks.end(), [](const AttnTask& x, const AttnTask& y) { return x.ntile > y.ntile; });
 }
 
 }  // namespace
@@ -300,6 +386,9 @@ int mk_chunk_attend(mk_chunk* c, const void* q, const void* kv_pool, void* out, 
   if (!c) return fail(MK_ERR_INVALID, "mk_chunk_attend: chunk is NULL");
   if (!c->s.nq) return fail(MK_ERR_INVALID, "mk_chunk_attend: a chunk without query heads");
   if (c->b.rows == 0) return check_device(c);
+  // the pool's 128-byte rows are counted in 32 bits
+  if ((long long)c->num_pages * c->s.nkv * 2 * (c->s.d / 4) > INT_MAX - 64)
+    return fail(MK_ERR_UNSUPPORTED, "mk_chunk_attend: a pool of 256 GB or more");
   if (!aligned16(q) || !aligned16(kv_pool) || !aligned16(out))
     return fail(MK_ERR_INVALID, "mk_chunk_attend: a buffer is NULL or not 16-byte aligned");
   const int rc = check_device(c);
