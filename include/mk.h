@@ -549,7 +549,7 @@ void mk_chunk_destroy(mk_chunk* c);
 
 /* Host only (no CUDA call): the attention tasks a chunk of these lengths would
  * run on num_ctas CTAs, 8 ints each (request, KV head, first new row, rows,
- * first 128-key tile, tiles, first split row or -1, 0).  Writes up to
+ * first 64-key tile, tiles, first split row or -1, CTA).  Writes up to
  * max_tasks tasks and returns their number, or an error. */
 int mk_chunk_inspect(const mk_model_dims* dims, int batch, const int* seq_lens, const int* new_lens, int num_ctas,
                      int* tasks, int max_tasks);

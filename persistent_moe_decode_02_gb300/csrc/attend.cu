@@ -4,12 +4,13 @@
 // over the positions s up to the row's own, in one pass over the cache with the
 // running maximum m and sum of each row in fp32.
 //
-// One block works on one task: up to two query tiles (128 rows each: 128 / G
+// A block works through its list of tasks; a task is up to two query tiles (128 rows each: 128 / G
 // tokens with the G heads that share a KV head, so a key tile is fetched once
-// for all of them) of one request, against a run of key tiles (128 keys, 8
+// for all of them) of one request, against a run of key tiles (64 keys, 4
 // pages).  Products run on the tensor cores: S = Q K^T into tensor memory,
 // softmax in registers (one thread a row), P back to tensor memory as bf16, O
-// += P V.  With two tiles one's products run while the other's softmax does.
+// += P V.  Each query tile has two S buffers, so the next tile's scores are
+// there when a softmax ends, whatever its latency.
 //
 // How the pages meet the matrix instructions.  A page's K or V block is
 // [d][16 slots] bf16, 32 bytes a dimension: with a 32-byte swizzle that is
@@ -21,7 +22,7 @@
 // Q's columns are stored in the same order, and O's are read in it.
 //
 // 8-bit blocks (codes, then the slots' scales) are copied as they are and
-// turned into that layout by four warps of their own: a code is a bf16 number
+// turned into that layout by warps of their own: a code is a bf16 number
 // after a shift, up to a factor 2^120 that its scale's multiplication takes
 // along, so nothing is rounded.
 #include <cuda.h>
@@ -43,33 +44,39 @@ constexpr int TILE_PAGES = KV_TILE / PAGE;
 constexpr unsigned long long WAIT_NS = 2000000000ull;   // limit of every wait
 constexpr float RESCALE = 8.f;     // a row's sums are rescaled when its maximum grew by a factor of 2^8
 
-// Warps: 0-3 softmax of query tile 0, 4-7 of tile 1, 8 copies, 9 matrix
-// instructions, 10-13 conversion of 8-bit blocks.
-constexpr int W_COPY = 8, W_MMA = 9, W_CONV = 10;
+// Warps: 0-3 softmax of query tile 0, 4-7 of tile 1 (without one: conversion),
+// 8 copies, 9 and 10 matrix instructions of each query tile (two, so that one's
+// products run while the other waits), 11-14 conversion of 8-bit tiles.  A block
+// whose tasks all have one query tile converts K in warps 11-14 and V in 4-7,
+// a page each; another one K in 11 and 12, V in 13 and 14, two pages each.
+constexpr int W_COPY = 8, W_MMA = 9, W_CONV = 11;
 
 template <int D, bool E4M3>
 struct Cfg {
-  static constexpr int THREADS = (E4M3 ? 14 : 10) * 32;
+  static constexpr int THREADS = (E4M3 ? 15 : 11) * 32;
   static constexpr int Q_BYTES = Q_TILE * D * 2;
   static constexpr int PAGE_BYTES = D * PAGE * 2;             // a page's K or V as bf16
   static constexpr int STAGE = TILE_PAGES * PAGE_BYTES;       // a key tile's K or V
   static constexpr int RAW_PAGE = (D + 1) * PAGE;             // a page's 8-bit block
   static constexpr int RAW = TILE_PAGES * RAW_PAGE;
-  // shared memory: two query tiles, the ring of bf16 tiles, the ring of 8-bit
-  // tiles; D = 64 has twice the stages in the same bytes
+  // shared memory: two query tiles, K's and V's rings of bf16 tiles, their
+  // rings of 8-bit tiles; D = 64 has twice the stages in the same bytes
   static constexpr int NST = (E4M3 ? 3 : 5) * (128 / D);
   static constexpr int NRAW = E4M3 ? 4 * (128 / D) : 0;
-  static constexpr int OFF_KV = 2 * Q_BYTES, OFF_RAW = OFF_KV + NST * STAGE, OFF_CTL = OFF_RAW + NRAW * RAW;
+  static constexpr int OFF_KV = 2 * Q_BYTES, OFF_RAW = OFF_KV + 2 * NST * STAGE, OFF_CTL = OFF_RAW + 2 * NRAW * RAW;
+  // V is 0 for K's ring, 1 for V's
+  __device__ static constexpr int kv(int v, int i) { return OFF_KV + (v * NST + i) * STAGE; }
+  __device__ static constexpr int raw(int v, int i) { return OFF_RAW + (v * NRAW + i) * RAW; }
   static constexpr int SMEM = OFF_CTL + 1024 + 1024;          // control words, and room to align the base
-  // tensor memory columns: S (and P over it) of each tile, O of each tile
-  static constexpr int T_S = 0, T_O = 2 * KV_TILE, T_COLS = 512;
+  // tensor memory columns: two S buffers (and P over them) of each query tile, O of each
+  static constexpr int T_S = 0, T_O = 4 * KV_TILE, T_COLS = 512;
   static_assert(T_O + 2 * D <= T_COLS, "tensor memory");
   static_assert(SMEM <= 232448, "shared memory");
 };
 
 struct Ctl {
-  uint64_t full[16], empty[16], raw_full[8], raw_empty[8];
-  uint64_t q_ready, s_full[2], p_ready[2], o_full[2], drain;
+  uint64_t full[2][10], empty[2][10], raw_full[2][8], raw_empty[2][8];
+  uint64_t q_ready[2], s_full[2][2], p_ready[2][2], o_done[2], o_full[2], drain;
   uint32_t tmem;
   int fail;
 };
@@ -96,48 +103,46 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Ctl* ctl,
   }
   return true;
 }
+// The same for one thread, and for a warp, whose lanes agree on the outcome.
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, Ctl* ctl, int* status) {
+  return mbar_try(bar, parity) || wait_slow(bar, parity, ctl, status);
+}
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* ctl, int* status) {
   const bool ok = mbar_try(bar, parity) || wait_slow(bar, parity, ctl, status);
   return __all_sync(FULL, ok);
 }
 
-// Place in a ring of n stages.
-struct Ring {
-  int n, i = 0;
-  uint32_t ph = 0;
-  __device__ explicit Ring(int n_) : n(n_) {}
-  __device__ void next() {
-    if (++i == n) {
-      i = 0;
-      ph ^= 1;
-    }
-  }
+// Softmax of one query tile over a task's key tiles; a thread has a row.  g
+// counts the query tile's key tiles over the tasks before, v_last is the page of
+// V that the request ends within (in the stage that v_full tells of), if any.
+// False when a wait gave up.
+struct RowSums {
+  float m, l;                    // maximum and sum of the softmax
 };
-
-// Softmax of one query tile and its epilogue; a thread has a row.  False when
-// a wait gave up.
 template <int D, bool E4M3>
-__device__ __forceinline__ bool softmax_rows(const Args& a, const AttnTask& t, const ChunkReq& r, int qt, uint32_t tmem,
-                                             Ctl* ctl, int* status) {
+__device__ __forceinline__ bool softmax_rows(const Args& a, const AttnTask& t, int qt, int g, uint32_t tmem, uint8_t* v_last,
+                                             uint64_t* v_full, uint32_t v_phase, RowSums& sums, Ctl* ctl) {
   using C = Cfg<D, E4M3>;
+  int* status = a.c.status;
   const int warp = threadIdx.x / 32 % 4, lane = threadIdx.x % 32, row = warp * 32 + lane;
   const int G = a.c.G, per = Q_TILE / G;
   const int ntok = min(per, t.ntok - qt * per), rows = ntok * G;
   const bool live = warp * 32 < rows;            // a warp without rows only keeps the pace
-  const int tok = t.tok0 + qt * per + min(row / G, ntok - 1), pos = r.seq + tok;
+  const int first_pos = t.pos + qt * per, pos = first_pos + min(row / G, ntok - 1);   // the tile's lowest, the row's own
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-  const uint32_t ts = tmem + lanes + C::T_S + qt * KV_TILE, to = tmem + lanes + C::T_O + qt * D;
+  const uint32_t ts = tmem + lanes + C::T_S + qt * 2 * KV_TILE, to = tmem + lanes + C::T_O + qt * D;
   const float sc = 1.4426950408889634f * rsqrtf((float)D);   // log2(e) / sqrt(d)
-  const int first_pos = r.seq + t.tok0 + qt * per;           // the tile's lowest position
-  float m = -INFINITY, l = 0.f;
+  float m = -INFINITY;
+  f32x2 l2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
   for (int j = 0; j < t.ntile; ++j) {
-    if (!wait(&ctl->s_full[qt], j & 1, ctl, status)) return false;
+    const int at = g + j, buf = at & 1;
+    if (!wait(&ctl->s_full[qt][buf], at >> 1 & 1, ctl, status)) return false;
     tc_after();
     if (live) {
       const int key0 = (t.tile0 + j) * KV_TILE;
       uint32_t s[KV_TILE];
 #pragma unroll
-      for (int c = 0; c < KV_TILE; c += 32) tmem_ld32(ts + c, s + c);
+      for (int c = 0; c < KV_TILE; c += 32) tmem_ld32(ts + buf * KV_TILE + c, s + c);
       tmem_wait_ld();
       if (key0 + KV_TILE - 1 > first_pos) {      // keys behind a row's position
         const int seen = pos - key0 + 1;
@@ -145,18 +150,21 @@ __device__ __forceinline__ bool softmax_rows(const Args& a, const AttnTask& t, c
         for (int c = 0; c < KV_TILE; ++c)
           if (c >= seen) s[c] = 0xff800000u;
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < KV_TILE; ++c) mx[c % 4] = fmaxf(mx[c % 4], __uint_as_float(s[c]));
-      const float top = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+      for (int c = 0; c < KV_TILE; c += 2) mx[c / 2 % 4] = max3(mx[c / 2 % 4], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
       // The old maximum serves while it is not far below: the weights stay
       // within 2^RESCALE, and O keeps its scale.
       if (j == 0) {
         m = top;
       } else if (__any_sync(FULL, (top - m) * sc > RESCALE)) {
         const float f = top > m ? exp2_approx((m - top) * sc) : 1.f;
-        l *= f;
+        l2[0] = mul2(l2[0], pair(f, f));
+        l2[1] = mul2(l2[1], pair(f, f));
         m = top;
+        if (!wait(&ctl->o_done[qt], (at - 1) & 1, ctl, status)) return false;   // the tile before is in O
+        tc_after();
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
@@ -168,29 +176,58 @@ __device__ __forceinline__ bool softmax_rows(const Args& a, const AttnTask& t, c
         }
       }
       const float base = m == -INFINITY ? 0.f : -m * sc;   // a row that sees none of these keys: all weights 0
-      float sum[4] = {};
+      const f32x2 sc2 = pair(sc, sc), base2 = pair(base, base);
 #pragma unroll
       for (int c = 0; c < KV_TILE; c += 2) {
-        const float p0 = exp2_approx(fmaf(__uint_as_float(s[c]), sc, base));
-        const float p1 = exp2_approx(fmaf(__uint_as_float(s[c + 1]), sc, base));
-        sum[c / 2 % 4] += p0 + p1;
+        float p0, p1;
+        split(fma2(pair(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, base2), p0, p1);
+        p0 = exp2_approx(p0);
+        p1 = exp2_approx(p1);
+        l2[c / 2 % 2] = add2(l2[c / 2 % 2], pair(p0, p1));
         s[c / 2] = pack_bf16(p0, p1);            // weights meet V as bf16, their sum stays fp32
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_st32(ts, s);
-      tmem_st32(ts + 32, s + 32);
+      tmem_st32(ts + buf * KV_TILE, s);
       tmem_wait_st();
+    }
+    if (!E4M3 && j == t.ntile - 1 && v_last) {
+      // Slots behind the request's end hold anything, and 0 times a NaN is
+      // one: in V they become 0 (both query tiles' threads write the same).
+      if (!wait(v_full, v_phase, ctl, status)) return false;
+      if (row < D) {
+        const int keep = t.total % PAGE;         // slots of the last page that are the request's
+        uint32_t* chunk = reinterpret_cast<uint32_t*>(v_last + row * 32);
+        const int flip = (row >> 2 & 1) * 4;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+          const uint32_t mask = keep >= 2 * w + 2 ? ~0u : keep == 2 * w + 1 ? 0xffffu : 0u;
+          if (mask != ~0u) chunk[w ^ flip] &= mask;
+        }
+      }
+      fence_async();
     }
     tc_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&ctl->p_ready[qt]);
+    if (lane == 0) mbar_arrive(&ctl->p_ready[qt][buf]);
   }
-  if (!wait(&ctl->o_full[qt], 0, ctl, status)) return false;
-  tc_after();
-  if (!live) return true;
+  float la, lb, lc, ld;
+  split(l2[0], la, lb);
+  split(l2[1], lc, ld);
+  sums = {m, (la + lb) + (lc + ld)};
+  return true;
+}
+
+// O to its place: rows of the output, or split rows with their sums.
+template <int D, bool E4M3>
+__device__ __forceinline__ void store_rows(const Args& a, const AttnTask& t, int qt, uint32_t tmem, RowSums sums) {
+  using C = Cfg<D, E4M3>;
+  const int warp = threadIdx.x / 32 % 4, row = warp * 32 + threadIdx.x % 32;
+  const int G = a.c.G, per = Q_TILE / G, rows = min(per, t.ntok - qt * per) * G;
+  if (warp * 32 >= rows) return;
+  const uint32_t to = tmem + ((uint32_t)(warp * 32) << 16) + C::T_O + qt * D;
   const int in_block = qt * per * G + row;       // row of the task's block
-  const size_t at = ((size_t)(r.row0 + tok) * a.c.nq + (size_t)t.kvh * G + row % G) * D;
-  const float inv = 1.f / l;
+  const size_t at = ((size_t)(t.row + qt * per + row / G) * a.c.nq + (size_t)t.kvh * G + row % G) * D;
+  const float inv = 1.f / sums.l;
+#pragma unroll 1
   for (int c = 0; c < D; c += 32) {
     uint32_t o[32];
     tmem_ld32(to + c, o);
@@ -214,21 +251,29 @@ __device__ __forceinline__ bool softmax_rows(const Args& a, const AttnTask& t, c
       }
     }
   }
-  if (t.part >= 0 && row < rows) a.c.part_ml[(size_t)t.part + in_block] = make_float2(m * sc, l);
-  return true;
+  if (t.part >= 0 && row < rows)
+    a.c.part_ml[(size_t)t.part + in_block] = make_float2(sums.m * (1.4426950408889634f * rsqrtf((float)D)), sums.l);
 }
 
 // A query tile into shared memory: two column halves of 128-byte rows with the
 // 128-byte swizzle, dimensions in the cache's order; rows past the last are 0.
 template <int D>
-__device__ __forceinline__ void load_q(const Args& a, const AttnTask& t, const ChunkReq& r, int qt, uint8_t* dst) {
+__device__ __forceinline__ void load_q(const Args& a, const AttnTask& t, int qt, uint8_t* dst) {
   const int G = a.c.G, per = Q_TILE / G, rows = min(per, t.ntok - qt * per) * G, tid = threadIdx.x % 128;
-  const __nv_bfloat16* src = a.q + ((size_t)(r.row0 + t.tok0 + qt * per) * a.c.nq + (size_t)t.kvh * G) * D;
-#pragma unroll 4
-  for (int x = tid; x < Q_TILE * (D / 8); x += 128) {
-    const int row = x / (D / 8), g = x % (D / 8);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row < rows) v = __ldg(reinterpret_cast<const uint4*>(src + ((size_t)(row / G) * a.c.nq + row % G) * D) + g);
+  const __nv_bfloat16* src = a.q + ((size_t)(t.row + qt * per) * a.c.nq + (size_t)t.kvh * G) * D;
+  constexpr int N = D / 8;                       // 16-byte pieces of a row, and of a thread: all in flight at once
+  const int g = tid % N;
+  uint4 piece[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int row = tid / N + i * (128 / N);
+    piece[i] = make_uint4(0, 0, 0, 0);
+    if (row < rows) piece[i] = __ldg(reinterpret_cast<const uint4*>(src + ((size_t)(row / G) * a.c.nq + row % G) * D) + g);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int row = tid / N + i * (128 / N);
+    uint4 v = piece[i];
     if (g & 1) {                                 // neighbours exchanged
       v.x = v.x << 16 | v.x >> 16; v.y = v.y << 16 | v.y >> 16;
       v.z = v.z << 16 | v.z >> 16; v.w = v.w << 16 | v.w >> 16;
@@ -238,53 +283,82 @@ __device__ __forceinline__ void load_q(const Args& a, const AttnTask& t, const C
   }
 }
 
-// One page's 8-bit block as bf16 in the operands' layout, by 16 threads: rows
-// (dimensions) me, me + 16, ...; `live` slots, the others 0.
+// One page's 8-bit block as bf16 in the operands' layout, by a warp: rows
+// (dimensions) me, me + 32, ...; `live` slots, the others 0.
 template <int D>
 __device__ __forceinline__ void convert_page(const uint8_t* raw, uint8_t* dst, int live, int me) {
-  uint32_t mul[8], far[8];
+  uint32_t mul[8] = {}, far[8] = {};
   bool any_far = false;
   if (live > 0) {
+    // scale 2^(e - 127) times 2^120, as a bf16 number's exponent; above 2^127
+    // (e > 134) the rest comes as a second factor
     const uint4 e4 = *reinterpret_cast<const uint4*>(raw + D * PAGE);
     const uint32_t ew[4] = {e4.x, e4.y, e4.z, e4.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      uint32_t a[2], b[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int slot = 2 * i + h;
-        const int e = ew[slot / 4] >> (slot % 4 * 8) & 0xff;
-        // scale 2^(e - 127) times 2^120, as a bf16 number's exponent; above
-        // 2^127 the rest comes as a second factor
-        const int lo = min(e, 134);
-        a[h] = slot < live ? (uint32_t)(lo + 120) << 7 : 0u;
-        b[h] = (uint32_t)(e - lo + 127) << 7;
-        any_far |= e > 134 && slot < live;
+      const uint32_t e = __byte_perm(ew[i / 2], 0, i % 2 ? 0x4342 : 0x4140);   // two exponents in 16-bit halves
+      const uint32_t lo = __vminu2(e, 134u | 134u << 16);
+      mul[i] = (lo + (120u | 120u << 16)) << 7;
+      far[i] = (e - lo + (127u | 127u << 16)) << 7;
+      any_far |= e != lo;
+      if (live < PAGE) {                         // slots behind the end: code times 0
+        if (2 * i >= live) mul[i] = 0;
+        else if (2 * i + 1 >= live) mul[i] &= 0xffffu;
       }
-      mul[i] = a[0] | a[1] << 16;
-      far[i] = b[0] | b[1] << 16;
     }
   }
-#pragma unroll 2
-  for (int d = me; d < D; d += 16) {
-    uint32_t o[8] = {};
-    if (live > 0) {
-      const uint4 c4 = *reinterpret_cast<const uint4*>(raw + d * PAGE);
-      const uint32_t cw[4] = {c4.x, c4.y, c4.z, c4.w};
+  uint4 code[D / 32];                            // every row's read before the first write: they may not alias
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // two codes into the high bytes of 16-bit halves; sign stays, the
-        // other 7 bits go to bf16's lowest exponent and highest mantissa bits
-        const uint32_t x = __byte_perm(cw[i / 2], 0, i % 2 ? 0x3424 : 0x1404);
-        o[i] = mul_bf16x2((x & 0x80008000u) | (x >> 4 & 0x07f007f0u), mul[i]);
-      }
-      if (any_far)
+  for (int i = 0; i < D / 32; ++i)
+    code[i] = live > 0 ? *reinterpret_cast<const uint4*>(raw + (me + i * 32) * PAGE) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], far[i]);
+  for (int k = 0; k < D / 32; ++k) {
+    const int d = me + k * 32;
+    const uint32_t cw[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // two codes into the high bytes of 16-bit halves; sign stays, the
+      // other 7 bits go to bf16's lowest exponent and highest mantissa bits
+      const uint32_t x = __byte_perm(cw[i / 2], 0, i % 2 ? 0x3424 : 0x1404);
+      o[i] = mul_bf16x2((x & 0x80008000u) | (x >> 4 & 0x07f007f0u), mul[i]);
     }
+    if (any_far)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], far[i]);
     const int row = d ^ (d >> 3 & 3), flip = row >> 2 & 1;
     *reinterpret_cast<uint4*>(dst + row * 32 + flip * 16) = make_uint4(o[0], o[1], o[2], o[3]);
     *reinterpret_cast<uint4*>(dst + row * 32 + (flip ^ 1) * 16) = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// The K (v = 0) or V tiles of a block's tasks to bf16, pages [p0, p1) of each:
+// every converting warp passes every tile in turn, so a barrier is never two
+// phases away from what the warp waits for.
+template <int D>
+__device__ __forceinline__ void convert_tiles(const Args& a, int t0, int t1, uint8_t* smem, int v, int p0, int p1, Ctl* ctl) {
+  using C = Cfg<D, true>;
+  const int lane = threadIdx.x % 32;
+  int ri = 0, si = 0, r_ph = 0, s_ph = 0;
+  bool first = true;                             // the ring's first round: nothing to wait for
+  for (int i = t0; i < t1; ++i) {
+    const int tile0 = __ldg(&a.c.tasks[i].tile0), ntile = __ldg(&a.c.tasks[i].ntile), total = __ldg(&a.c.tasks[i].total);
+    for (int j = 0; j < ntile; ++j) {
+      if (!wait(&ctl->raw_full[v][ri], r_ph, ctl, a.c.status)) return;
+      if (!first && !wait(&ctl->empty[v][si], s_ph ^ 1, ctl, a.c.status)) return;
+      const int left = total - (tile0 + j) * KV_TILE;   // the request's keys from the tile on
+      for (int p = p0; p < p1; ++p)
+        convert_page<D>(smem + C::raw(v, ri) + p * C::RAW_PAGE, smem + C::kv(v, si) + p * C::PAGE_BYTES,
+                        min(PAGE, max(0, left - p * PAGE)), lane);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctl->full[v][si]);
+        mbar_arrive(&ctl->raw_empty[v][ri]);
+      }
+      if (++ri == C::NRAW) { ri = 0; r_ph ^= 1; }
+      if (++si == C::NST) { si = 0; s_ph ^= 1; first = false; }
+    }
   }
 }
 
@@ -293,29 +367,35 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
     k_attend(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map) {
   using C = Cfg<D, E4M3>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::OFF_CTL);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const AttnTask t = a.c.tasks[blockIdx.x];
-  const ChunkReq r = a.c.reqs[t.req];
-  const int nqt = t.ntok > Q_TILE / a.c.G ? 2 : 1;
+  const int per = Q_TILE / a.c.G;
+  const int t0 = __ldg(a.c.cta_start + blockIdx.x), t1 = __ldg(a.c.cta_start + blockIdx.x + 1);
   int* status = a.c.status;
+  const bool two = __ldg(&a.c.tasks[t0].two);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be launched: it waits for the end
   if (tid == 0) {
-    for (int i = 0; i < C::NST; ++i) {
-      mbar_init(&ctl->full[i], E4M3 ? 4 : 1);    // converting warps, or the copy's issue
-      mbar_init(&ctl->empty[i], 1);
+    for (int v = 0; v < 2; ++v) {
+      for (int i = 0; i < C::NST; ++i) {
+        mbar_init(&ctl->full[v][i], !E4M3 ? 1 : two ? 2 : 4);   // the copies' issue, or the converting warps
+        mbar_init(&ctl->empty[v][i], 2);                        // both query tiles' products
+      }
+      for (int i = 0; i < C::NRAW; ++i) {
+        mbar_init(&ctl->raw_full[v][i], 1);
+        mbar_init(&ctl->raw_empty[v][i], two ? 2 : 4);
+      }
     }
-    for (int i = 0; i < C::NRAW; ++i) {
-      mbar_init(&ctl->raw_full[i], 1);
-      mbar_init(&ctl->raw_empty[i], 4);
-    }
-    mbar_init(&ctl->q_ready, 4 * nqt);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->p_ready[i], 4);
+      mbar_init(&ctl->q_ready[i], 4);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&ctl->s_full[i][k], 1);
+        mbar_init(&ctl->p_ready[i][k], 4);
+      }
+      mbar_init(&ctl->o_done[i], 1);
       mbar_init(&ctl->o_full[i], 1);
     }
-    mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->drain, 2);
     ctl->fail = 0;
     fence_barrier_init();
   }
@@ -324,151 +404,155 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
   __syncthreads();
   tc_after();
   const uint32_t tmem = ctl->tmem;
-  const int total = r.seq + r.nnew, npages = (total + PAGE - 1) / PAGE;
-  // K and V tiles pass through the ring in the order of their use: K 0, then
-  // K j + 1 and V j for every j
-  const int uses = 2 * t.ntile;
-  auto tile_of = [&](int u, bool& v) -> int {
-    v = u > 0 && (u % 2 == 0 || u == uses - 1);
-    return u == 0 ? 0 : u == uses - 1 ? t.ntile - 1 : v ? u / 2 - 1 : (u + 1) / 2;
-  };
   bool ok = true;
 
-  if (warp < 4 * nqt) {                          // ---- softmax
-    load_q<D>(a, t, r, warp / 4, smem + (warp / 4) * C::Q_BYTES);
-    fence_async();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ctl->q_ready);
-    ok = softmax_rows<D, E4M3>(a, t, r, warp / 4, tmem, ctl, status);
+  if (warp < 8 && (warp < 4 || two)) {           // ---- softmax of a query tile
+    const int qt = warp / 4;
+    uint8_t* const q_smem = smem + qt * C::Q_BYTES;
+    auto has = [&](const AttnTask& t) { return qt == 0 || t.ntok > per; };
+    auto queries = [&](const AttnTask& t) {      // the tile's queries; the last task's scores are done
+      load_q<D>(a, t, qt, q_smem);
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->q_ready[qt]);
+    };
+    int g = 0, all = 0;                          // key tiles so far: of this query tile, of the block
+    uint32_t tasks = 0;                          // of this query tile
+    AttnTask t = a.c.tasks[t0];
+    if (has(t)) queries(t);
+    for (int i = t0; i < t1; ++i) {
+      const AttnTask next = a.c.tasks[min(i + 1, t1 - 1)];
+      all += t.ntile;
+      if (has(t)) {
+        const int left = t.total - (t.tile0 + t.ntile - 1) * KV_TILE, last = (all - 1) % C::NST;
+        uint8_t* v_last = left < KV_TILE && t.total % PAGE ? smem + C::kv(1, last) + left / PAGE * C::PAGE_BYTES : nullptr;
+        RowSums sums;
+        if (!softmax_rows<D, E4M3>(a, t, qt, g, tmem, v_last, &ctl->full[1][last], (all - 1) / C::NST & 1, sums, ctl)) break;
+        if (i + 1 < t1 && has(next)) queries(next);
+        if (!wait(&ctl->o_full[qt], tasks & 1, ctl, status)) break;
+        tc_after();
+        store_rows<D, E4M3>(a, t, qt, tmem, sums);
+        g += t.ntile;
+        ++tasks;
+      } else if (i + 1 < t1 && has(next)) {
+        queries(next);
+      }
+      t = next;
+    }
   } else if (warp == W_COPY) {                   // ---- copies: a lane has a page
-    const int n = E4M3 ? C::NRAW : C::NST;
-    uint64_t* full = E4M3 ? ctl->raw_full : ctl->full;
-    uint64_t* empty = E4M3 ? ctl->raw_empty : ctl->empty;
-    Ring ring(n);
-    int issued = 0;
-    for (int u = 0; u < uses && ok; ++u, ring.next()) {
-      if (u >= n && !(ok = wait(&empty[ring.i], ring.ph ^ 1, ctl, status))) break;
-      bool v;
-      const int page = (t.tile0 + tile_of(u, v)) * TILE_PAGES + lane;
-      const bool there = lane < TILE_PAGES && page < npages;
-      const int id = there ? __ldg(a.c.pt + r.pt + page) : 0;
+    constexpr int N = E4M3 ? C::NRAW : C::NST;
+    int at[2] = {0, 0};                          // tiles issued of K and V
+    auto full = [&](int v, int i) { return E4M3 ? &ctl->raw_full[v][i] : &ctl->full[v][i]; };
+    auto copy = [&](const AttnTask& t, int v, int j) {
+      const int u = at[v], s = u % N;
+      if (u >= N && !wait(E4M3 ? &ctl->raw_empty[v][s] : &ctl->empty[v][s], (u / N & 1) ^ 1, ctl, status)) return false;
+      const int page = (t.tile0 + j) * TILE_PAGES + lane;
+      const bool there = lane < TILE_PAGES && page < (t.total + PAGE - 1) / PAGE;
+      const int id = there ? __ldg(a.c.pt + t.pt + page) : 0;
       const size_t block = ((size_t)id * a.c.nkv + t.kvh) * 2 + v;
       if (E4M3) {
         const uint32_t bytes = __popc(__ballot_sync(FULL, there)) * C::RAW_PAGE;
-        if (lane == 0) mbar_arrive_tx(&full[ring.i], bytes);
+        if (lane == 0) mbar_arrive_tx(full(v, s), bytes);
         __syncwarp();
-        if (there)
-          bulk_copy(smem + C::OFF_RAW + ring.i * C::RAW + lane * C::RAW_PAGE, a.pool + block * C::RAW_PAGE, C::RAW_PAGE,
-                    &full[ring.i]);
+        if (there) bulk_copy(smem + C::raw(v, s) + lane * C::RAW_PAGE, a.pool + block * C::RAW_PAGE, C::RAW_PAGE, full(v, s));
       } else {
-        if (lane == 0) mbar_arrive_tx(&full[ring.i], C::STAGE);
+        if (lane == 0) mbar_arrive_tx(full(v, s), C::STAGE);
         __syncwarp();
         if (lane < TILE_PAGES)                   // a page past the end: zeros
-          tma_2d(smem + C::OFF_KV + ring.i * C::STAGE + lane * C::PAGE_BYTES, &map, 0,
-                 there ? (int)(block * (D / 4)) : a.oob, &full[ring.i]);
+          tma_2d(smem + C::kv(v, s) + lane * C::PAGE_BYTES, &map, 0, there ? (int)(block * (D / 4)) : a.oob, full(v, s));
       }
-      ++issued;
+      ++at[v];
+      return true;
+    };
+    for (int i = t0; i < t1 && ok; ++i) {        // in the order of use: K goes one tile ahead
+      const AttnTask t = a.c.tasks[i];
+      ok = copy(t, 0, 0);
+      for (int j = 0; j < t.ntile && ok; ++j) ok = (j + 1 == t.ntile || copy(t, 0, j + 1)) && copy(t, 1, j);
     }
     if (!ok)                                     // given up: what is in flight still lands before the block ends
-      for (int u = max(0, issued - n); u < issued; ++u) {
-        const unsigned long long t0 = now_ns();
-        while (!mbar_try(&full[u % n], (u / n) & 1) && now_ns() - t0 < WAIT_NS) {}
-      }
-  } else if (warp == W_MMA) {                    // ---- matrix instructions
-    constexpr uint32_t I_QK = umma_idesc(Q_TILE, KV_TILE, true), I_PV = umma_idesc(Q_TILE, D, false);
-    const uint32_t sq = smem_u32(smem), skv = smem_u32(smem + C::OFF_KV);
-    Ring ring(C::NST);
-    auto scores = [&](int stage, int qt) {       // S = Q K^T, 16 dimensions at a time
+      for (int v = 0; v < 2; ++v)
+        for (int u = max(0, at[v] - N); u < at[v]; ++u) {
+          const unsigned long long since = now_ns();
+          while (!mbar_try(full(v, u % N), u / N & 1) && now_ns() - since < WAIT_NS) {}
+        }
+  } else if (warp == W_MMA || warp == W_MMA + 1) {   // ---- matrix instructions: one thread a query tile
+    const int qt = warp - W_MMA;
+    if (elect_one()) {
+      constexpr uint32_t I_QK = umma_idesc(Q_TILE, KV_TILE, true), I_PV = umma_idesc(Q_TILE, D, false);
+      const uint64_t q_desc = umma_desc(smem_u32(smem + qt * C::Q_BYTES), 16, 1024, 2);
+      const uint64_t k_desc = umma_desc(smem_u32(smem + C::kv(0, 0)), C::PAGE_BYTES, 256, 6);
+      const uint64_t v_desc = umma_desc(smem_u32(smem + C::kv(1, 0)), 16, 256, 6);
+      const uint32_t ts = tmem + C::T_S + qt * 2 * KV_TILE, to = tmem + C::T_O + qt * D;
+      int ki = 0, vi = 0, g = 0;                 // ring places, key tiles of this query tile
+      uint32_t k_ph = 0, v_ph = 0, tasks = 0;
+      auto next_k = [&] { if (++ki == C::NST) { ki = 0; k_ph ^= 1; } };
+      auto next_v = [&] { if (++vi == C::NST) { vi = 0; v_ph ^= 1; } };
+      auto scores = [&](int buf) {               // S = Q K^T, 16 dimensions at a time
+        const uint64_t kd = k_desc + (uint32_t)(ki * C::STAGE >> 4);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        umma_ss(tmem + C::T_S + qt * KV_TILE,
-                umma_desc(sq + qt * C::Q_BYTES + (k / 4) * (Q_TILE * 128) + (k % 4) * 32, 16, 1024, 2),
-                umma_desc(skv + stage * C::STAGE + k * 512, C::PAGE_BYTES, 256, 6), I_QK, k > 0);
-      umma_commit(&ctl->s_full[qt]);
-    };
-    ok = wait(&ctl->q_ready, 0, ctl, status) && wait(&ctl->full[0], 0, ctl, status);
-    if (ok) {
-      tc_after();
-      if (lane == 0) {
-        for (int qt = 0; qt < nqt; ++qt) scores(0, qt);
-        umma_commit(&ctl->empty[0]);
-      }
-      ring.next();
-    }
-    for (int j = 0; j < t.ntile && ok; ++j) {
-      const bool more = j + 1 < t.ntile;
-      int ks = 0;
-      if (more) {
-        ks = ring.i;
-        if (!(ok = wait(&ctl->full[ring.i], ring.ph, ctl, status))) break;
-        ring.next();
-      }
-      const int vs = ring.i;
-      if (!(ok = wait(&ctl->full[ring.i], ring.ph, ctl, status))) break;
-      ring.next();
-      const int key0 = (t.tile0 + j) * KV_TILE;
-      if (!E4M3 && total - key0 < KV_TILE && total % PAGE) {
-        // slots behind the request's end hold anything, and 0 times a NaN is
-        // one: they become 0 (conversion does it for 8-bit blocks)
-        uint8_t* page = smem + C::OFF_KV + vs * C::STAGE + (total - key0) / PAGE * C::PAGE_BYTES;
-        for (int row = lane; row < D; row += 32)
-          for (int s = total % PAGE; s < PAGE; ++s)
-            *reinterpret_cast<uint16_t*>(page + row * 32 + ((s >> 3) ^ (row >> 2 & 1)) * 16 + (s & 7) * 2) = 0;
-        fence_async();
-        __syncwarp();
-      }
-      for (int qt = 0; qt < nqt; ++qt) {
-        if (!(ok = wait(&ctl->p_ready[qt], j & 1, ctl, status))) break;
+        for (int k = 0; k < D / 16; ++k)
+          umma_ss(ts + buf * KV_TILE, q_desc + (((k / 4) * (Q_TILE * 128) + (k % 4) * 32) >> 4), kd + (k * 512 >> 4), I_QK, k > 0);
+        umma_commit(&ctl->s_full[qt][buf]);
+        umma_commit(&ctl->empty[0][ki]);
+        next_k();
+      };
+      for (int i = t0; i < t1 && ok; ++i) {
+        const int ntile = __ldg(&a.c.tasks[i].ntile), ntok = __ldg(&a.c.tasks[i].ntok);
+        if (qt == 1 && ntok <= per) {            // no rows: every tile is done at once
+          for (int j = 0; j < ntile; ++j) {
+            if (!(ok = wait_one(&ctl->full[0][ki], k_ph, ctl, status))) break;
+            mbar_arrive(&ctl->empty[0][ki]);
+            next_k();
+            if (!(ok = wait_one(&ctl->full[1][vi], v_ph, ctl, status))) break;
+            mbar_arrive(&ctl->empty[1][vi]);
+            next_v();
+          }
+          continue;
+        }
+        ok = wait_one(&ctl->q_ready[qt], tasks & 1, ctl, status) && wait_one(&ctl->full[0][ki], k_ph, ctl, status);
+        if (!ok) break;
+        ++tasks;
         tc_after();
-        if (lane == 0) {
+        scores(g & 1);
+        // Scores go one tile ahead, into the buffer that the products of the
+        // tile before have left.
+        for (int j = 0; j < ntile; ++j, ++g) {
+          const bool more = j + 1 < ntile;
+          if (more) {
+            if (!(ok = wait_one(&ctl->full[0][ki], k_ph, ctl, status))) break;
+            scores((g + 1) & 1);
+          }
+          if (!(ok = wait_one(&ctl->full[1][vi], v_ph, ctl, status))) break;
+          if (!(ok = wait_one(&ctl->p_ready[qt][g & 1], g >> 1 & 1, ctl, status))) break;
+          tc_after();
+          const uint64_t vd = v_desc + (uint32_t)(vi * C::STAGE >> 4);
 #pragma unroll
           for (int k = 0; k < TILE_PAGES; ++k)   // O += P V, a page's 16 keys at a time
-            umma_ts(tmem + C::T_O + qt * D, tmem + C::T_S + qt * KV_TILE + k * 8,
-                    umma_desc(skv + vs * C::STAGE + k * C::PAGE_BYTES, 16, 256, 6), I_PV, j > 0 || k > 0);
-          if (more) scores(ks, qt);
-          else umma_commit(&ctl->o_full[qt]);
+            umma_ts(to, ts + (g & 1) * KV_TILE + k * 8, vd + (k * C::PAGE_BYTES >> 4), I_PV, j > 0 || k > 0);
+          umma_commit(&ctl->empty[1][vi]);
+          umma_commit(&ctl->o_done[qt]);
+          if (!more) umma_commit(&ctl->o_full[qt]);
+          next_v();
         }
-        __syncwarp();
       }
-      if (!ok) break;
-      if (lane == 0 && more) {                   // (nobody waits for the last stages)
-        umma_commit(&ctl->empty[vs]);
-        umma_commit(&ctl->empty[ks]);
-      }
-      __syncwarp();
+      // Products and their arrivals are done before the block's memory is
+      // given back, after a wait that gave up too.
+      umma_commit(&ctl->drain);
+      const unsigned long long since = now_ns();
+      while (!mbar_try(&ctl->drain, 0) && now_ns() - since < WAIT_NS) {}
     }
-  } else if (E4M3 && warp >= W_CONV) {           // ---- 8-bit blocks to bf16
-    Ring ring(C::NST), raw(C::NRAW);
-    const int me = tid - W_CONV * 32;
-    for (int u = 0; u < uses; ++u, ring.next(), raw.next()) {
-      if (!(ok = wait(&ctl->raw_full[raw.i], raw.ph, ctl, status))) break;
-      if (u >= C::NST && !(ok = wait(&ctl->empty[ring.i], ring.ph ^ 1, ctl, status))) break;
-      bool v;
-      const int key = (t.tile0 + tile_of(u, v)) * KV_TILE + me / 16 * PAGE;
-      convert_page<D>(smem + C::OFF_RAW + raw.i * C::RAW + me / 16 * C::RAW_PAGE,
-                      smem + C::OFF_KV + ring.i * C::STAGE + me / 16 * C::PAGE_BYTES, min(PAGE, max(0, total - key)), me % 16);
-      fence_async();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&ctl->full[ring.i]);
-        mbar_arrive(&ctl->raw_empty[raw.i]);
-      }
-    }
+    __syncwarp();
+  } else if constexpr (E4M3) {                   // ---- 8-bit tiles to bf16
+    if (!two) convert_tiles<D>(a, t0, t1, smem, warp < 8, warp < 8 ? warp - 4 : warp - W_CONV,
+                               (warp < 8 ? warp - 4 : warp - W_CONV) + 1, ctl);
+    else convert_tiles<D>(a, t0, t1, smem, (warp - W_CONV) / 2, (warp - W_CONV) % 2 * 2, (warp - W_CONV) % 2 * 2 + 2, ctl);
   }
 
   __syncwarp();
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == W_MMA) {
-    if (ctl->fail && lane == 0) {                // products in flight end before their memory is given back
-      umma_commit(&ctl->drain);
-      const unsigned long long t0 = now_ns();
-      while (!mbar_try(&ctl->drain, 0) && now_ns() - t0 < WAIT_NS) {}
-    }
-    __syncwarp();
-    tmem_free<C::T_COLS>(tmem);
-  }
+  if (warp == W_MMA) tmem_free<C::T_COLS>(tmem);
 }
 
 // Joins the parts of rows whose keys were split: a warp has a row.  The order
@@ -476,6 +560,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
 template <int D>
 __global__ void __launch_bounds__(128) k_join(ChunkView c, __nv_bfloat16* out) {
   constexpr int E = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const JoinTask t = c.joins[blockIdx.x];
   const int rows = t.ntok * c.G, row = blockIdx.y * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
   if (row >= rows) return;
@@ -539,9 +624,19 @@ cudaError_t launch(const ChunkView& c, const void* q, const void* pool, void* ou
   cudaError_t e = E4M3 ? cudaSuccess : pool_map(c, pool, &map, &a.oob);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k_attend<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  k_attend<D, E4M3><<<c.ntasks, C::THREADS, C::SMEM, st>>>(a, map);
-  if (c.njoins) k_join<D><<<dim3(c.njoins, (2 * Q_TILE + 3) / 4), 128, 0, st>>>(c, (__nv_bfloat16*)out);
-  return cudaGetLastError();
+  k_attend<D, E4M3><<<c.ctas, C::THREADS, C::SMEM, st>>>(a, map);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !c.njoins) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(c.njoins, (2 * Q_TILE + 3) / 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];                     // launched while the tasks run; it waits for their end itself
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_join<D>, c, (__nv_bfloat16*)out);
 }
 
 }  // namespace

@@ -71,6 +71,7 @@ struct Built {
   std::vector<int> pt;
   std::vector<AttnTask> tasks;
   std::vector<JoinTask> joins;
+  std::vector<int> cta_start;
   long long rows = 0, tokens = 0, split_rows = 0, nsplit = 0, joined_rows = 0;
   int max_pages = 0, max_new_pages = 0;   // of one request: all its pages, those that receive rows
 };
@@ -129,93 +130,121 @@ int set_pages(int num_pages, const int* page_table, int max_pages, Built& b) {
 
 // Attention tasks.  A block is the rows of up to two query tiles of one
 // request and KV head (a tile: the G heads of Q_TILE / G tokens); its keys run
-// to its last row's position, in tiles of KV_TILE.  Where the blocks are too
-// few or too uneven to fill the CTAs, their keys are cut into tasks of at most
-// `len` tiles and joined afterwards; `len` is the one of a geometric series
-// whose longest-first schedule ends first.  The unit is the time of a tile
-// (about 0.7 us); a task costs SETUP of them before its first product, and a
-// join after the tasks JOIN.
+// to its last row's position, in tiles of KV_TILE.  A CTA works through a list
+// of tasks.  Two schedules are weighed against each other, in units of a tile
+// (about 0.75 us): whole blocks, the longest first, each to the CTA with the
+// least work; and the blocks' tiles in one row, cut into runs that are as even
+// as whole tiles allow, where a block that a cut goes through is joined
+// afterwards.  A task costs SETUP beside its tiles (its queries, its first
+// latencies and its epilogue), a join JOIN.
 struct Block {
   int req, kvh, tok0, ntok, tiles;
 };
-constexpr double SETUP = 3., JOIN = 4.;
+constexpr int SETUP = 2, JOIN = 5;
 
-double cost(int tiles) { return SETUP + tiles; }
-
-// When the last CTA is done: `n[t]` tasks of t tiles each, longest first, each
-// to the CTA that is free first.
-double makespan(const std::vector<int>& lens, int ctas) {
-  std::vector<double> heap;      // a binary min-heap of the CTAs' loads
-  double last = 0.;
-  for (int t : lens) {
-    double at = 0.;
-    if ((int)heap.size() >= ctas) {
-      std::pop_heap(heap.begin(), heap.end(), std::greater<double>());
-      at = heap.back();
-      heap.pop_back();
+// Gives every CTA tiles up to `limit` (its tasks' SETUP included) in the row's
+// order; emits (block, first tile, tiles, CTA).  False if the CTAs do not do.
+template <class F>
+bool deal(const std::vector<Block>& blocks, int ctas, long long limit, F&& emit) {
+  int c = 0;
+  long long room = limit;
+  for (size_t i = 0; i < blocks.size(); ++i) {
+    int at = 0;
+    while (at < blocks[i].tiles) {
+      if (room <= SETUP) {
+        if (++c == ctas) return false;
+        room = limit;
+      }
+      const int n = (int)std::min<long long>(blocks[i].tiles - at, room - SETUP);
+      emit(i, at, n, c);
+      room -= SETUP + n;
+      at += n;
     }
-    heap.push_back(at + cost(t));
-    last = std::max(last, heap.back());
-    std::push_heap(heap.begin(), heap.end(), std::greater<double>());
   }
-  return last;
+  return true;
 }
-
-constexpr size_t MAX_PLANNED = 16384;   // tasks: beyond them the blocks fill the CTAs anyway
 
 void set_tasks(const Shape& s, int ctas, Built& b) {
   b.tasks.clear();
   b.joins.clear();
+  b.cta_start.assign(1, 0);
   b.split_rows = b.nsplit = b.joined_rows = 0;
   if (!s.G) return;
   const int per_tile = mk::Q_TILE / s.G, per_block = 2 * per_tile;
   std::vector<Block> blocks;
-  int longest = 1;
+  long long work = 0, longest = 0;
   for (int i = 0; i < (int)b.reqs.size(); ++i) {
     const ChunkReq& r = b.reqs[i];
     for (int t = 0; t < r.nnew; t += per_block) {
       const int n = std::min(per_block, r.nnew - t), tiles = (r.seq + t + n + mk::KV_TILE - 1) / mk::KV_TILE;
-      longest = std::max(longest, tiles);
+      longest = std::max<long long>(longest, tiles);
+      work += (long long)(tiles + SETUP) * s.nkv;
       for (int g = 0; g < s.nkv; ++g) blocks.push_back({i, g, t, n, tiles});
     }
   }
-  int best_len = longest;
-  double best = 1e300;
-  for (int len = longest;; len = std::min(len - 1, (int)(len * 0.85))) {
-    if (len < 1) break;
-    std::vector<int> lens;
-    bool cut = false;
-    for (const Block& k : blocks) {
-      const int parts = (k.tiles + len - 1) / len;
-      cut |= parts > 1;
-      for (int p = 0; p < parts; ++p)
-        lens.push_back((int)((long long)k.tiles * (p + 1) / parts - (long long)k.tiles * p / parts));
-      if (lens.size() > MAX_PLANNED) break;
+  if (blocks.empty()) return;
+  // whole blocks
+  std::vector<int> order(blocks.size()), owner(blocks.size());
+  for (size_t i = 0; i < order.size(); ++i) order[i] = (int)i;
+  std::stable_sort(order.begin(), order.end(), [&](int x, int y) { return blocks[x].tiles > blocks[y].tiles; });
+  std::vector<std::pair<long long, int>> heap;   // (load, CTA), the least first
+  long long whole = 0;
+  for (int i : order) {
+    std::pair<long long, int> at = {0, (int)heap.size()};
+    if ((int)heap.size() >= ctas) {
+      std::pop_heap(heap.begin(), heap.end(), std::greater<>());
+      at = heap.back();
+      heap.pop_back();
     }
-    if (lens.size() > MAX_PLANNED) break;
-    std::sort(lens.begin(), lens.end(), std::greater<int>());
-    const double t = makespan(lens, ctas) + (cut ? JOIN : 0.);
-    if (t < best) {
-      best = t;
-      best_len = len;
-    }
+    at.first += blocks[i].tiles + SETUP;
+    owner[i] = at.second;
+    whole = std::max(whole, at.first);
+    heap.push_back(at);
+    std::push_heap(heap.begin(), heap.end(), std::greater<>());
   }
-  for (const Block& k : blocks) {
-    const int parts = (k.tiles + best_len - 1) / best_len, rows = k.ntok * s.G;
-    if (parts > 1) {
-      b.joins.push_back({k.req, k.kvh, k.tok0, k.ntok, (int)b.split_rows, parts, 0, 0});
-      b.joined_rows += rows;
-    }
-    for (int p = 0; p < parts; ++p) {
-      const int t0 = (int)((long long)k.tiles * p / parts), t1 = (int)((long long)k.tiles * (p + 1) / parts);
-      b.tasks.push_back({k.req, k.kvh, k.tok0, k.ntok, t0, t1 - t0, parts > 1 ? (int)b.split_rows : -1, 0});
-      if (parts > 1) {
-        b.split_rows += rows;
-        ++b.nsplit;
+  // even runs: the smallest limit for which the CTAs do
+  long long lo = std::max<long long>(SETUP + 1, work / ctas), hi = whole;
+  while (lo < hi) {
+    const long long mid = (lo + hi) / 2;
+    if (deal(blocks, ctas, mid, [](size_t, int, int, int) {})) hi = mid;
+    else lo = mid + 1;
+  }
+  const bool runs = hi + JOIN < whole;
+  auto add = [&](size_t i, int tile0, int n, int cta, int part) {
+    const Block& k = blocks[i];
+    const ChunkReq& r = b.reqs[k.req];
+    b.tasks.push_back({k.req, k.kvh, k.tok0, k.ntok, tile0, n, part, cta, r.row0 + k.tok0, r.seq + k.tok0, r.seq + r.nnew,
+                       0, r.pt, 0});
+  };
+  if (runs) {
+    std::vector<int> parts(blocks.size(), 0), first(blocks.size(), -1);
+    deal(blocks, ctas, hi, [&](size_t i, int, int, int) { ++parts[i]; });
+    for (size_t i = 0; i < blocks.size(); ++i)
+      if (parts[i] > 1) {
+        const Block& k = blocks[i];
+        const long long rows = (long long)k.ntok * s.G;
+        first[i] = (int)b.split_rows;
+        b.joins.push_back({k.req, k.kvh, k.tok0, k.ntok, first[i], parts[i], 0, 0});
+        b.joined_rows += rows;
+        b.split_rows += rows * parts[i];
+        b.nsplit += parts[i];
       }
-    }
+    deal(blocks, ctas, hi, [&](size_t i, int at, int n, int c) {
+      add(i, at, n, c, first[i]);
+      if (first[i] >= 0) first[i] += blocks[i].ntok * s.G;
+    });
+  } else {
+    for (int i : order) add(i, 0, blocks[i].tiles, owner[i], -1);
+    std::stable_sort(b.tasks.begin(), b.tasks.end(), [](const AttnTask& x, const AttnTask& y) { return x.cta < y.cta; });
   }
-  std::stable_sort(b.tasks.begin(), b.tasks.end(), [](const AttnTask& x, const AttnTask& y) { return x.ntile > y.ntile; });
+  b.cta_start.assign(b.tasks.back().cta + 2, 0);
+  for (const AttnTask& t : b.tasks) ++b.cta_start[t.cta + 1];
+  for (size_t i = 1; i < b.cta_start.size(); ++i) b.cta_start[i] += b.cta_start[i - 1];
+  for (size_t c = 0; c + 1 < b.cta_start.size(); ++c) {
+    int two = 0;
+    for (int i = b.cta_start[c]; i < b.cta_start[c + 1]; ++i) two |= b.tasks[i].ntok > per_tile;
+    for (int i = b.cta_start[c]; i < b.cta_start[c + 1]; ++i) b.tasks[i].two = two;
+  }
 }
 
 }  // namespace
@@ -258,18 +287,20 @@ int build(const mk_chunk* c, int batch, const int* seq_lens, const int* new_lens
 int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
   const size_t d = c->s.d;
   const size_t n_req = up16(nb.reqs.size() * sizeof(ChunkReq)), n_pt = up16(nb.pt.size() * sizeof(int)),
-               n_task = up16(nb.tasks.size() * sizeof(AttnTask)), n_join = up16(nb.joins.size() * sizeof(JoinTask));
-  cudaError_t e = grow(&c->blob, &c->blob_cap, n_req + n_pt + n_task + n_join);
+               n_task = up16(nb.tasks.size() * sizeof(AttnTask)), n_join = up16(nb.joins.size() * sizeof(JoinTask)),
+               n_cta = up16(nb.cta_start.size() * sizeof(int)), n_all = n_req + n_pt + n_task + n_join + n_cta;
+  cudaError_t e = grow(&c->blob, &c->blob_cap, n_all);
   if (e == cudaSuccess && c->s.theta > 0.)
     e = grow((void**)&c->rope, &c->rope_cap, (size_t)nb.rows * (d / 2) * sizeof(float2));
   if (e == cudaSuccess) e = grow((void**)&c->part, &c->part_cap, (size_t)nb.split_rows * (d + 2) * sizeof(float));
   if (e != cudaSuccess) return fail_cuda("mk_chunk: device memory", e);
-  std::vector<char> host(n_req + n_pt + n_task + n_join, 0);
+  std::vector<char> host(n_all, 0);
   memcpy(host.data(), nb.reqs.data(), nb.reqs.size() * sizeof(ChunkReq));
   memcpy(host.data() + n_req, nb.pt.data(), nb.pt.size() * sizeof(int));
   if (!nb.tasks.empty()) memcpy(host.data() + n_req + n_pt, nb.tasks.data(), nb.tasks.size() * sizeof(AttnTask));
   if (!nb.joins.empty())
     memcpy(host.data() + n_req + n_pt + n_task, nb.joins.data(), nb.joins.size() * sizeof(JoinTask));
+  memcpy(host.data() + n_all - n_cta, nb.cta_start.data(), nb.cta_start.size() * sizeof(int));
   // pageable source: the bytes have left it when the call returns
   e = cudaMemcpyAsync(c->blob, host.data(), host.size(), cudaMemcpyHostToDevice, st);
   if (e == cudaSuccess) e = cudaMemsetAsync(c->status, 0, 4 * sizeof(int), st);
@@ -282,7 +313,8 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
   v.pt = (const int*)(base + n_req);
   v.tasks = (const AttnTask*)(base + n_req + n_pt);
   v.joins = (const JoinTask*)(base + n_req + n_pt + n_task);
-  v.ntasks = (int)c->b.tasks.size(); v.njoins = (int)c->b.joins.size();
+  v.cta_start = (const int*)(base + n_all - n_cta);
+  v.ctas = (int)c->b.cta_start.size() - 1; v.njoins = (int)c->b.joins.size();
   v.rope = c->s.theta > 0. ? c->rope : nullptr;
   v.part_o = c->part;
   v.part_ml = (float2*)(c->part + (size_t)c->b.split_rows * d);
@@ -439,7 +471,7 @@ int mk_chunk_inspect(const mk_model_dims* dims, int batch, const int* seq_lens, 
     if (r != MK_OK) return r;
     set_tasks(s, num_ctas, b);
     const int n = std::min<int>(max_tasks, (int)b.tasks.size());
-    if (n) memcpy(tasks, b.tasks.data(), (size_t)n * sizeof(AttnTask));
+    for (int i = 0; i < n; ++i) memcpy(tasks + 8 * i, &b.tasks[i], 8 * sizeof(int));   // the record's first words
     return (int)b.tasks.size();
   });
 }

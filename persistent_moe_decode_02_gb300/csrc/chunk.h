@@ -8,7 +8,7 @@
 namespace mk {
 
 constexpr int PAGE = 16;         // tokens of a page
-constexpr int KV_TILE = 128;     // keys of an attention tile (8 pages)
+constexpr int KV_TILE = 64;      // keys of an attention tile (4 pages)
 constexpr int Q_TILE = 128;      // query rows (tokens x the group's heads) of an attention tile
 
 // One request of a chunk.
@@ -23,11 +23,17 @@ static_assert(sizeof(ChunkReq) == 32, "request record is 32 bytes");
 
 // One attention task: new rows [tok0, tok0 + ntok) of a request, one KV head,
 // key tiles [tile0, tile0 + ntile).  part >= 0: the task holds a part of the
-// keys and writes its unnormalised rows at split row `part`.
+// keys and writes its unnormalised rows at split row `part`.  The rest says
+// again what the kernel would have to look up for it.
 struct alignas(16) AttnTask {
-  int req, kvh, tok0, ntok, tile0, ntile, part, pad;
+  int req, kvh, tok0, ntok, tile0, ntile, part, cta;
+  int row, pos;                  // packed row and position of the first row
+  int total;                     // cached and new tokens of the request
+  int two;                       // 1: some task of this CTA has two query tiles
+  long long pt;                  // its page-table row
+  long long pad2;
 };
-static_assert(sizeof(AttnTask) == 32, "attention task is 32 bytes");
+static_assert(sizeof(AttnTask) == 64, "attention task is 64 bytes");
 
 // The join of a block of rows whose keys were split over `nparts` tasks, whose
 // split rows start at part0 + i * (ntok * G).
@@ -43,9 +49,10 @@ struct ChunkView {
   const ChunkReq* reqs;
   const int* pt;
   const float2* rope;            // [rows][d / 2] (cos, sin) of the new rows; NULL: no rotation
-  const AttnTask* tasks;
+  const AttnTask* tasks;         // in the order of the CTAs
+  const int* cta_start;          // [ctas + 1]
   const JoinTask* joins;
-  int ntasks, njoins;
+  int ctas, njoins;
   float* part_o;                 // [split rows][d] unnormalised sums
   float2* part_ml;               // [split rows] (maximum, sum) of the softmax
   int* status;                   // first recorded error, 0 = none

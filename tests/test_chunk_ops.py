@@ -89,6 +89,17 @@ def test_attend_peaked_scores(mk, kv):
     check_attend(mk, "g8", kv, ([300, 40], [40, 300]), seed=9, scale=6.0)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("heads,most", [("g8", 16), ("g2d64", 70), ("g8", 300)])
+def test_attend_many_requests(mk, heads, kv, most):
+    # more blocks of rows than CTAs: each works through several tasks, of one query tile and of two
+    g = torch.Generator().manual_seed(most)
+    cached = torch.randint(0, 700, (70,), generator=g).tolist()
+    new = torch.randint(0, most + 1, (70,), generator=g).tolist()
+    check_attend(mk, heads, kv, (cached, new), seed=most)
+    check_attend(mk, heads, kv, (cached + [30000], new + [1]), seed=most + 1)   # and one that is split
+
+
 def test_attend_shared_prefix_pages(mk):
     # two requests read the same cached pages and add rows in pages of their own
     D = cu.dims(8, 2, 128)
