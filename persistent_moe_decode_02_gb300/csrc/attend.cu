@@ -87,6 +87,7 @@ struct Args {
   const __nv_bfloat16* q;
   const uint8_t* pool;       // 8-bit pool
   __nv_bfloat16* out;
+  bool wide_out;             // out is 32-byte aligned
   int oob;                   // a row of the tensor map past its end: reads zeros
 };
 
@@ -216,6 +217,19 @@ __device__ __forceinline__ bool softmax_rows(const Args& a, const AttnTask& t, i
   return true;
 }
 
+// 32 bytes of a thread: a whole sector in one store where the address allows
+// it (16-byte stores of 32 rows took 3.1 us a tile, these 1.9).
+__device__ __forceinline__ void store32(void* p, const uint32_t* v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // O to its place: rows of the output, or split rows with their sums.
 template <int D, bool E4M3>
 __device__ __forceinline__ void store_rows(const Args& a, const AttnTask& t, int qt, uint32_t tmem, RowSums sums) {
@@ -233,21 +247,19 @@ __device__ __forceinline__ void store_rows(const Args& a, const AttnTask& t, int
     tmem_ld32(to + c, o);
     tmem_wait_ld();
     if (row < rows) {
+      uint32_t v[32];                            // 8 columns at a time: dimensions exchanged by (column >> 3) & 3
 #pragma unroll
-      for (int g = 0; g < 32; g += 8) {          // 8 columns: dimensions exchanged by (column >> 3) & 3
-        const int x = g >> 3 & 3;
-        float v[8];
+      for (int i = 0; i < 32; ++i) v[i] = o[(i & ~7) + ((i & 7) ^ (i >> 3))];
+      if (t.part < 0) {
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o[g + (i ^ x)]);
-        if (t.part < 0) {
-          *reinterpret_cast<uint4*>(a.out + at + c + g) =
-              make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
-                         pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
-        } else {
-          float4* po = reinterpret_cast<float4*>(a.c.part_o + ((size_t)t.part + in_block) * D + c + g);
-          po[0] = make_float4(v[0], v[1], v[2], v[3]);
-          po[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
+        for (int i = 0; i < 16; ++i) w[i] = pack_bf16(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv);
+        store32(a.out + at + c, w, a.wide_out);
+        store32(a.out + at + c + 16, w + 8, a.wide_out);
+      } else {
+        float* po = a.c.part_o + ((size_t)t.part + in_block) * D + c;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) store32(po + i, v + i, true);
       }
     }
   }
@@ -262,13 +274,14 @@ __device__ __forceinline__ void load_q(const Args& a, const AttnTask& t, int qt,
   const int G = a.c.G, per = Q_TILE / G, rows = min(per, t.ntok - qt * per) * G, tid = threadIdx.x % 128;
   const __nv_bfloat16* src = a.q + ((size_t)(t.row + qt * per) * a.c.nq + (size_t)t.kvh * G) * D;
   constexpr int N = D / 8;                       // 16-byte pieces of a row, and of a thread: all in flight at once
-  const int g = tid % N;
+  const int g = tid % N, by_g = (65536 + G - 1) / G;   // row / G = row * by_g >> 16 for rows of a tile
   uint4 piece[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int row = tid / N + i * (128 / N);
     piece[i] = make_uint4(0, 0, 0, 0);
-    if (row < rows) piece[i] = __ldg(reinterpret_cast<const uint4*>(src + ((size_t)(row / G) * a.c.nq + row % G) * D) + g);
+    const int token = row * by_g >> 16;
+    if (row < rows) piece[i] = __ldg(reinterpret_cast<const uint4*>(src + ((size_t)token * a.c.nq + (row - token * G)) * D) + g);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -281,6 +294,16 @@ __device__ __forceinline__ void load_q(const Args& a, const AttnTask& t, int qt,
     if (g & 2) v = make_uint4(v.y, v.x, v.w, v.z);   // pairs exchanged
     *reinterpret_cast<uint4*>(dst + (g / 8) * (Q_TILE * 128) + row * 128 + ((g % 8) ^ (row & 7)) * 16) = v;
   }
+}
+
+// The same queries on their way to L2 while the task before is worked on.
+template <int D>
+__device__ __forceinline__ void prefetch_q(const Args& a, const AttnTask& t, int qt) {
+  const int G = a.c.G, per = Q_TILE / G, rows = min(per, t.ntok - qt * per) * G, row = threadIdx.x % 128;
+  if (row >= rows) return;
+  const __nv_bfloat16* src = a.q + ((size_t)(t.row + qt * per + row / G) * a.c.nq + (size_t)t.kvh * G + row % G) * D;
+#pragma unroll
+  for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i));
 }
 
 // One page's 8-bit block as bf16 in the operands' layout, by a warp: rows
@@ -423,6 +446,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
     for (int i = t0; i < t1; ++i) {
       const AttnTask next = a.c.tasks[min(i + 1, t1 - 1)];
       all += t.ntile;
+      if (i + 1 < t1 && has(next)) prefetch_q<D>(a, next, qt);
       if (has(t)) {
         const int left = t.total - (t.tile0 + t.ntile - 1) * KV_TILE, last = (all - 1) % C::NST;
         uint8_t* v_last = left < KV_TILE && t.total % PAGE ? smem + C::kv(1, last) + left / PAGE * C::PAGE_BYTES : nullptr;
@@ -555,36 +579,46 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
   if (warp == W_MMA) tmem_free<C::T_COLS>(tmem);
 }
 
-// Joins the parts of rows whose keys were split: a warp has a row.  The order
-// of the sum is the parts', so the same call gives the same bits.
-template <int D>
+// Joins the parts of rows whose keys were split; W warps share a row (4 where
+// a row has many parts: 38 of them took 4.9 us with one).  The order of the
+// sums is fixed, so the same call gives the same bits.
+template <int D, int W>
 __global__ void __launch_bounds__(128) k_join(ChunkView c, __nv_bfloat16* out) {
   constexpr int E = D / 32;
+  __shared__ float part[W][D + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const JoinTask t = c.joins[blockIdx.x];
-  const int rows = t.ntok * c.G, row = blockIdx.y * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (row >= rows) return;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rows = t.ntok * c.G, row = W == 4 ? blockIdx.y : blockIdx.y * 4 + warp, w = W == 4 ? warp : 0;
+  if (row >= rows) return;                       // the whole block where warps share a row
+  const float2* ml = c.part_ml + (size_t)t.part0 + row;
+  const float* po = c.part_o + ((size_t)t.part0 + row) * D + lane * E;
   float m = -INFINITY;
-  for (int p = lane; p < t.nparts; p += 32) m = fmaxf(m, c.part_ml[(size_t)t.part0 + (size_t)p * rows + row].x);
+  for (int p = lane; p < t.nparts; p += 32) m = fmaxf(m, ml[(size_t)p * rows].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
   float acc[E] = {}, l = 0.f;
-#pragma unroll 4
-  for (int p = 0; p < t.nparts; ++p) {
-    const size_t at = (size_t)t.part0 + (size_t)p * rows + row;
-    const float2 ml = c.part_ml[at];
-    const float w = exp2f(ml.x - m);             // 0 for a part whose keys this row does not see
-    l += ml.y * w;
+#pragma unroll 8
+  for (int p = w; p < t.nparts; p += W) {
+    const float2 s = ml[(size_t)p * rows];
+    const float f = exp2f(s.x - m);              // 0 for a part whose keys this row does not see
+    l += s.y * f;
     float v[E];
-    if (E == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(c.part_o + at * D + lane * 4);
-      v[0] = x.x; v[1] = x.y; v[E - 2] = x.z; v[E - 1] = x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(c.part_o + at * D + lane * 2);
-      v[0] = x.x; v[1] = x.y;
-    }
+    if constexpr (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(po + (size_t)p * rows * D);
+    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(po + (size_t)p * rows * D);
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += w * v[e];
+    for (int e = 0; e < E; ++e) acc[e] += f * v[e];
+  }
+  if constexpr (W == 4) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) part[w][lane * E + e] = acc[e];
+    if (lane == 0) part[w][D] = l;
+    __syncthreads();
+    if (w) return;
+    l = (part[0][D] + part[1][D]) + (part[2][D] + part[3][D]);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      acc[e] = (part[0][lane * E + e] + part[1][lane * E + e]) + (part[2][lane * E + e] + part[3][lane * E + e]);
   }
   const float inv = 1.f / l;
   const ChunkReq r = c.reqs[t.req];
@@ -619,7 +653,7 @@ cudaError_t pool_map(const ChunkView& c, const void* pool, CUtensorMap* map, int
 template <int D, bool E4M3>
 cudaError_t launch(const ChunkView& c, const void* q, const void* pool, void* out, cudaStream_t st) {
   using C = Cfg<D, E4M3>;
-  Args a = {c, (const __nv_bfloat16*)q, (const uint8_t*)pool, (__nv_bfloat16*)out, 0};
+  Args a = {c, (const __nv_bfloat16*)q, (const uint8_t*)pool, (__nv_bfloat16*)out, (uintptr_t)out % 32 == 0, 0};
   CUtensorMap map = {};
   cudaError_t e = E4M3 ? cudaSuccess : pool_map(c, pool, &map, &a.oob);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k_attend<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -628,7 +662,8 @@ cudaError_t launch(const ChunkView& c, const void* q, const void* pool, void* ou
   e = cudaGetLastError();
   if (e != cudaSuccess || !c.njoins) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(c.njoins, (2 * Q_TILE + 3) / 4);
+  const bool many = c.max_parts > 8;
+  cfg.gridDim = dim3(c.njoins, many ? c.max_join_rows : (c.max_join_rows + 3) / 4);
   cfg.blockDim = dim3(128);
   cfg.stream = st;
   cudaLaunchAttribute at[1];                     // launched while the tasks run; it waits for their end itself
@@ -636,7 +671,7 @@ cudaError_t launch(const ChunkView& c, const void* q, const void* pool, void* ou
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_join<D>, c, (__nv_bfloat16*)out);
+  return cudaLaunchKernelEx(&cfg, many ? k_join<D, 4> : k_join<D, 1>, c, (__nv_bfloat16*)out);
 }
 
 }  // namespace

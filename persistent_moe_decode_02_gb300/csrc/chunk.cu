@@ -315,6 +315,11 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
   v.joins = (const JoinTask*)(base + n_req + n_pt + n_task);
   v.cta_start = (const int*)(base + n_all - n_cta);
   v.ctas = (int)c->b.cta_start.size() - 1; v.njoins = (int)c->b.joins.size();
+  v.max_parts = v.max_join_rows = 0;
+  for (const JoinTask& j : c->b.joins) {
+    v.max_parts = std::max(v.max_parts, j.nparts);
+    v.max_join_rows = std::max(v.max_join_rows, j.ntok * v.G);
+  }
   v.rope = c->s.theta > 0. ? c->rope : nullptr;
   v.part_o = c->part;
   v.part_ml = (float2*)(c->part + (size_t)c->b.split_rows * d);

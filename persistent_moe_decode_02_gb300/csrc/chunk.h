@@ -53,6 +53,7 @@ struct ChunkView {
   const int* cta_start;          // [ctas + 1]
   const JoinTask* joins;
   int ctas, njoins;
+  int max_parts, max_join_rows;  // of one join
   float* part_o;                 // [split rows][d] unnormalised sums
   float2* part_ml;               // [split rows] (maximum, sum) of the softmax
   int* status;                   // first recorded error, 0 = none

@@ -2,13 +2,15 @@
 // them (mk_probs, mk_verify in include/mk.h).
 //
 // A row of the vocabulary is one cluster's work: each block holds its segment
-// of the row in shared memory, so the row is read once whatever is done with
+// of the row in registers, so the row is read once whatever is done with
 // it, and the blocks exchange their totals through distributed shared memory.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 #include <stdio.h>
+
+#include <type_traits>
 
 #include "mk.h"
 
@@ -20,30 +22,20 @@ namespace {
 
 constexpr int NT = 512, NW = NT / 32;
 constexpr int MAX_CLUSTER = 8;
-constexpr int MAX_VOCAB = 393216;            // a block's segment of it: 192 KB of shared memory
 constexpr int STEP = NT * 4;                  // elements of one pass of a block: 4 consecutive ones a thread
-constexpr int MAX_PASSES = MAX_VOCAB / MAX_CLUSTER / STEP;
+constexpr int MAX_PASSES = 24;                // kept in registers: 96 of a thread
+constexpr int MAX_VOCAB = MAX_CLUSTER * MAX_PASSES * STEP;   // 393216
 constexpr unsigned FULL = 0xffffffffu;
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-// 4 elements of a row into shared memory without a stay in registers; those
-// past the end are not read.  `wide`: both addresses are 16-byte aligned.
-__device__ __forceinline__ void fetch4(float* dst, const float* src, int left, bool wide) {
-  if (wide && left >= 4) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < left) asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst + e)), "l"(src + e) : "memory");
-  }
-}
-__device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-// 4 elements of a row, 0 past its end.
-__device__ __forceinline__ float4 load4(const float* p, int left, bool wide) {
+// 4 elements of a row, `none` past its end.  `wide`: the address is 16-byte aligned.
+__device__ __forceinline__ float4 load4(const float* p, int left, bool wide, float none) {
   if (wide && left >= 4) return __ldg(reinterpret_cast<const float4*>(p));
-  return make_float4(__ldg(p), left > 1 ? __ldg(p + 1) : 0.f, left > 2 ? __ldg(p + 2) : 0.f, left > 3 ? __ldg(p + 3) : 0.f);
+  float4 v = make_float4(none, none, none, none);
+  if (left > 0) v.x = __ldg(p);
+  if (left > 1) v.y = __ldg(p + 1);
+  if (left > 2) v.z = __ldg(p + 2);
+  if (left > 3) v.w = __ldg(p + 3);
+  return v;
 }
 
 // One block's segment of a row.
@@ -56,97 +48,135 @@ __device__ __forceinline__ Segment segment(int vocab, int blocks, int rank) {
   return {b, min(per, vocab - b)};
 }
 
-// (maximum, its lowest index, unusable) of a set of logits.
-struct Top {
-  float m;
-  int at;
-  int bad;
-};
-__device__ __forceinline__ Top join(Top a, Top b) {
-  const bool second = b.m > a.m || (b.m == a.m && b.at < a.at);
-  return {second ? b.m : a.m, second ? b.at : a.at, a.bad | b.bad};
+// The larger of two, a NaN if there is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
 }
 
+// softmax(logits * scale / log2(e)), scale 0: greedy.  A block holds PASSES x
+// STEP elements of its row in registers: the row is read once, the exponential
+// taken once (against the block's own maximum), and written once.
+template <int PASSES>
 __global__ void __launch_bounds__(NT) k_probs(const float* logits, int vocab, long long row_stride, float scale,
                                               float* probs, int wide_in, int wide_out) {
-  extern __shared__ float4 seg4[];
-  float* x = reinterpret_cast<float*>(seg4);
-  __shared__ Top wtop[NW];
-  __shared__ float wsum[NW];
-  __shared__ struct { Top top; float sum; } parts[MAX_CLUSTER];
+  __shared__ float wmax[NW], wsum[NW];
+  __shared__ int wat[NW];
+  __shared__ struct { float m, sum; int at; } parts[MAX_CLUSTER];
   cg::cluster_group cl = cg::this_cluster();
   cl.barrier_arrive();                        // every block of the cluster runs before one writes into another
   const int blocks = (int)cl.num_blocks(), rank = (int)cl.block_rank(), tid = threadIdx.x;
   const size_t row = blockIdx.x / blocks;
   const Segment s = segment(vocab, blocks, rank);
   const float* src = logits + row * row_stride + s.begin;
-  for (int i = tid * 4; i < s.n; i += STEP) fetch4(x + i, src + i, s.n - i, wide_in);
-  fetch_wait();                               // a thread reads only what it fetched
-  Top t = {-INFINITY, 0x7fffffff, 0};
-  for (int i = tid * 4; i < s.n; i += STEP)
+  float4 x[PASSES];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (i + e < s.n) {
-        const float v = x[i + e];
-        if (!(v < INFINITY)) t.bad = 1;       // NaN or +infinity
-        if (v > t.m) { t.m = v; t.at = s.begin + i + e; }   // strictly: the lowest index stays
-      }
+  for (int p = 0; p < PASSES; ++p) {
+    const int i = p * STEP + tid * 4;
+    x[p] = load4(src + i, s.n - i, wide_in, -INFINITY);
+  }
+  float m = -INFINITY;                        // a NaN or +infinity in the row makes this one
 #pragma unroll
-  for (int o = 16; o; o >>= 1)
-    t = join(t, {__shfl_xor_sync(FULL, t.m, o), __shfl_xor_sync(FULL, t.at, o), __shfl_xor_sync(FULL, t.bad, o)});
-  if (tid % 32 == 0) wtop[tid / 32] = t;
+  for (int p = 0; p < PASSES; ++p) m = max_nan(m, max_nan(max_nan(x[p].x, x[p].y), max_nan(x[p].z, x[p].w)));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(FULL, m, o));
+  if (tid % 32 == 0) wmax[tid / 32] = m;
   __syncthreads();
-  t = wtop[0];
+  m = wmax[0];
 #pragma unroll
-  for (int w = 1; w < NW; ++w) t = join(t, wtop[w]);
+  for (int w = 1; w < NW; ++w) m = max_nan(m, wmax[w]);
   float sum = 0.f;
-  if (scale > 0.f && t.m > -INFINITY)
-    for (int i = tid * 4; i < s.n; i += STEP)
+  int at = 0x7fffffff;                        // greedy: the maximum's lowest index
+  if (scale > 0.f) {
+    const float base = m == -INFINITY ? 0.f : m;   // a segment of nothing but -infinity: zeros
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i + e < s.n) sum += exp2f((x[i + e] - t.m) * scale);
+    for (int p = 0; p < PASSES; ++p) {
+      x[p].x = exp2f((x[p].x - base) * scale);
+      x[p].y = exp2f((x[p].y - base) * scale);
+      x[p].z = exp2f((x[p].z - base) * scale);
+      x[p].w = exp2f((x[p].w - base) * scale);
+      sum += (x[p].x + x[p].y) + (x[p].z + x[p].w);
+    }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-  if (tid % 32 == 0) wsum[tid / 32] = sum;
-  __syncthreads();
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+    if (tid % 32 == 0) wsum[tid / 32] = sum;
+  } else {
+#pragma unroll
+    for (int p = PASSES - 1; p >= 0; --p) {
+      const int i = s.begin + p * STEP + tid * 4;
+      at = x[p].x == m ? i : x[p].y == m ? i + 1 : x[p].z == m ? i + 2 : x[p].w == m ? i + 3 : at;
+    }
+    at = __reduce_min_sync(FULL, at);
+    if (tid % 32 == 0) wat[tid / 32] = at;
+  }
   cl.barrier_wait();
+  __syncthreads();
   if (tid < blocks) {                         // this block's totals into every block's table
-    float b = 0.f;
-    for (int w = 0; w < NW; ++w) b += wsum[w];
+    sum = 0.f;
+    at = 0x7fffffff;
+    for (int w = 0; w < NW; ++w)
+      if (scale > 0.f) sum += wsum[w];
+      else at = min(at, wat[w]);
     auto* p = cl.map_shared_rank(&parts[rank], tid);
-    p->top = t;
-    p->sum = b;
+    p->m = m;
+    p->sum = sum;
+    p->at = at;
   }
   cl.sync();
-  t = parts[0].top;
-  for (int r = 1; r < blocks; ++r) t = join(t, parts[r].top);
-  float total = 0.f;
-  for (int r = 0; r < blocks; ++r)
-    if (parts[r].sum > 0.f) total += parts[r].sum * exp2f((parts[r].top.m - t.m) * scale);
-  const float inv = 1.f / total;
+  float top = parts[0].m;
+  for (int r = 1; r < blocks; ++r) top = max_nan(top, parts[r].m);
   float* dst = probs + row * vocab + s.begin;
-  for (int i = tid * 4; i < s.n; i += STEP) {
-    float v[4];
+  float f = 0.f;                              // from the block's own maximum and sum to the row's
+  if (!(top < INFINITY)) {
+    f = NAN;
+  } else if (scale > 0.f && top > -INFINITY) {
+    float total = 0.f;
+    for (int r = 0; r < blocks; ++r) total += parts[r].sum * exp2f((parts[r].m - top) * scale);
+    f = exp2f((m - top) * scale) / total;
+  }
+  int pick = 0x7fffffff;
+  if (scale == 0.f && top > -INFINITY)
+    for (int r = 0; r < blocks; ++r)
+      if (parts[r].m == top) pick = min(pick, parts[r].at);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (scale > 0.f) v[e] = i + e < s.n && t.m > -INFINITY ? exp2f((x[i + e] - t.m) * scale) * inv : 0.f;
-      else v[e] = s.begin + i + e == t.at && t.m > -INFINITY ? 1.f : 0.f;
-      if (t.bad) v[e] = __int_as_float(0x7fffffff);
+  for (int p = 0; p < PASSES; ++p) {
+    const int i = p * STEP + tid * 4;
+    float4 v;
+    if (scale > 0.f && f == f) v = make_float4(x[p].x * f, x[p].y * f, x[p].z * f, x[p].w * f);
+    else v = make_float4(f, f, f, f);
+    if (f == f && pick >= s.begin + i && pick < s.begin + i + 4) {
+      v.x = pick == s.begin + i;
+      v.y = pick == s.begin + i + 1;
+      v.z = pick == s.begin + i + 2;
+      v.w = pick == s.begin + i + 3;
     }
     if (wide_out && i + 4 <= s.n) {
-      *reinterpret_cast<float4*>(dst + i) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(dst + i) = v;
     } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i + e < s.n) dst[i + e] = v[e];
+      if (i < s.n) dst[i] = v.x;
+      if (i + 1 < s.n) dst[i + 1] = v.y;
+      if (i + 2 < s.n) dst[i + 2] = v.z;
+      if (i + 3 < s.n) dst[i + 3] = v.w;
     }
   }
 }
 
 // A weight as a whole number of 2^-40: sums of those do not depend on their
-// order, so any split of the row draws the same token.
-__device__ __forceinline__ unsigned long long mass(float w) {
-  return w > 0.f ? __float2ull_rn(fminf(w, 1.f) * 1099511627776.f) : 0ull;
+// order, so any split of the row draws the same token.  In two 20-bit parts
+// (scaling by 2^20 and the remainder are exact), so that a group's sums fit 32
+// bits and a warp adds them in one instruction.
+struct Mass {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Mass mass(float w) {
+  const float x = (w > 0.f ? fminf(w, 1.f) : 0.f) * 1048576.f, h = truncf(x);
+  return {(uint32_t)h, __float2uint_rn((x - h) * 1048576.f)};
+}
+__device__ __forceinline__ unsigned long long whole_mass(Mass m) { return ((unsigned long long)m.hi << 20) + m.lo; }
+__device__ __forceinline__ Mass mass4(float4 w) {
+  const Mass a = mass(w.x), b = mass(w.y), c = mass(w.z), d = mass(w.w);
+  return {a.hi + b.hi + c.hi + d.hi, a.lo + b.lo + c.lo + d.lo};
 }
 
 struct VerifyArgs {
@@ -157,9 +187,9 @@ struct VerifyArgs {
   int *out, *accepted;
 };
 
+template <int PASSES>
 __global__ void __launch_bounds__(NT) k_verify(VerifyArgs a) {
-  extern __shared__ float4 seg4[];
-  __shared__ unsigned long long sums[MAX_PASSES * NW], totals[MAX_CLUSTER];
+  __shared__ unsigned long long sums[PASSES * NW], totals[MAX_CLUSTER];
   __shared__ int n_acc;
   cg::cluster_group cl = cg::this_cluster();
   cl.barrier_arrive();
@@ -191,39 +221,44 @@ __global__ void __launch_bounds__(NT) k_verify(VerifyArgs a) {
   const int acc = n_acc;
   const bool refused = acc < n;
   const Segment s = segment(V, blocks, rank);
-  float* w = reinterpret_cast<float*>(seg4);
   const float* trow = target + (size_t)acc * V + s.begin;
   const float* drow = refused && draft ? draft + (size_t)acc * V + s.begin : nullptr;
   const int gone = refused && !draft ? tok[acc] - s.begin : -1;   // a certain draft's place in this segment
-  const int passes = (s.n + STEP - 1) / STEP;
   cl.barrier_wait();
   unsigned long long total = 0, before = 0;
   for (int whole = refused ? 0 : 1; whole < 2; ++whole) {
     const float* less = whole ? nullptr : drow;
-#pragma unroll 4
-    for (int i = tid * 4; i < s.n; i += STEP) {
-      float4 t = load4(trow + i, s.n - i, a.wide);
-      if (less) {
-        const float4 d = load4(less + i, s.n - i, a.wide);
-        t.x -= d.x; t.y -= d.y; t.z -= d.z; t.w -= d.w;
-      }
-      *reinterpret_cast<float4*>(w + i) = t;
-    }
-    if (!whole && gone >= 0 && gone < s.n && gone % STEP / 4 == tid) w[gone] -= 1.f;
-    for (int p = 0; p < passes; ++p) {
+    auto spared = [&](float4 w, float4 d, int i) {   // weights at element i of the segment
+      const int at = whole ? -1 : gone - i;
+      return make_float4(w.x - d.x - (at == 0), w.y - d.y - (at == 1), w.z - d.z - (at == 2), w.w - d.w - (at == 3));
+    };
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 w[PASSES];
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
       const int i = p * STEP + tid * 4;
-      unsigned long long m = 0;
+      w[p] = load4(trow + i, s.n - i, a.wide, 0.f);
+    }
+    if (less) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (i + e < s.n) m += mass(w[i + e]);
+      for (int p = 0; p < PASSES; ++p) {
+        const int i = p * STEP + tid * 4;
+        w[p] = spared(w[p], load4(less + i, s.n - i, a.wide, 0.f), i);
+      }
+    } else {
 #pragma unroll
-      for (int o = 16; o; o >>= 1) m += __shfl_xor_sync(FULL, m, o);
-      if (lane == 0) sums[p * NW + warp] = m;
+      for (int p = 0; p < PASSES; ++p) w[p] = spared(w[p], none, p * STEP + tid * 4);
+    }
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      const Mass m = mass4(w[p]);
+      const Mass g = {__reduce_add_sync(FULL, m.hi), __reduce_add_sync(FULL, m.lo)};
+      if (lane == 0) sums[p * NW + warp] = whole_mass(g);
     }
     __syncthreads();
     if (warp == 0) {
       unsigned long long m = 0;
-      for (int k = lane; k < passes * NW; k += 32) m += sums[k];
+      for (int k = lane; k < PASSES * NW; k += 32) m += sums[k];
 #pragma unroll
       for (int o = 16; o; o >>= 1) m += __shfl_xor_sync(FULL, m, o);
       if (lane < blocks) *cl.map_shared_rank(&totals[rank], lane) = m;
@@ -235,39 +270,37 @@ __global__ void __launch_bounds__(NT) k_verify(VerifyArgs a) {
       total += totals[r];
     }
     if (total > 0) {
-      if (warp == 0) {
-        const float rv = a.r[b];
-        // floor(r 2^24), 0 for a NaN
-        const unsigned long long U = rv > 0.f ? (unsigned long long)fminf(floorf(rv * 16777216.f), 16777215.f) : 0ull;
-        unsigned long long at = __umul64hi(total, U << 40);       // floor(total U / 2^24)
-        const unsigned long long mine = totals[rank];
-        if (at >= before && at - before < mine) {                  // the token lies in this segment
-          at -= before;
-          int k = 0;
-          for (;; k += 32) {                                       // its group of 128
-            const unsigned long long v = k + lane < passes * NW ? sums[k + lane] : 0ull;
-            unsigned long long up = v;
+      const float rv = a.r[b];
+      // floor(r 2^24), 0 for a NaN
+      const unsigned long long U = rv > 0.f ? (unsigned long long)fminf(floorf(rv * 16777216.f), 16777215.f) : 0ull;
+      unsigned long long at = __umul64hi(total, U << 40);         // floor(total U / 2^24)
+      const unsigned long long mine = totals[rank];
+      if (at >= before && at - before < mine) {                    // the token lies in this segment
+        at -= before;
+        int k = 0;
+        for (;; k += 32) {                                         // its group of 128: every warp finds it
+          const unsigned long long v = k + lane < PASSES * NW ? sums[k + lane] : 0ull;
+          unsigned long long up = v;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const unsigned long long o2 = __shfl_up_sync(FULL, up, o);
-              if (lane >= o) up += o2;
-            }
-            const unsigned hit = __ballot_sync(FULL, up > at);
-            if (hit) {
-              const int l = __ffs(hit) - 1;
-              at -= __shfl_sync(FULL, up - v, l);
-              k += l;
-              break;
-            }
-            at -= __shfl_sync(FULL, up, 31);
+          for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long o2 = __shfl_up_sync(FULL, up, o);
+            if (lane >= o) up += o2;
           }
-          const int i = k / NW * STEP + k % NW * 128 + lane * 4;
-          unsigned long long m[4], v = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            m[e] = i + e < s.n ? mass(w[i + e]) : 0ull;
-            v += m[e];
+          const unsigned hit = __ballot_sync(FULL, up > at);
+          if (hit) {
+            const int l = __ffs(hit) - 1;
+            at -= __shfl_sync(FULL, up - v, l);
+            k += l;
+            break;
           }
+          at -= __shfl_sync(FULL, up, 31);
+        }
+        if (warp == k % NW) {                                      // and the one that holds it the token
+          const int i = k / NW * STEP + tid * 4;
+          const float4 g = spared(load4(trow + i, s.n - i, a.wide, 0.f), less ? load4(less + i, s.n - i, a.wide, 0.f) : none, i);
+          const unsigned long long m[4] = {whole_mass(mass(g.x)), whole_mass(mass(g.y)), whole_mass(mass(g.z)),
+                                           whole_mass(mass(g.w))};
+          const unsigned long long v = m[0] + m[1] + m[2] + m[3];
           unsigned long long up = v;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -313,14 +346,22 @@ int cluster_of(int vocab) {
   return c;
 }
 
+// The instance whose registers hold a segment: f(passes) with one of a few.
+template <class F>
+cudaError_t with_passes(int vocab, int cluster, F&& f) {
+  const int per = ((vocab + cluster - 1) / cluster + 3) / 4 * 4, n = (per + STEP - 1) / STEP;
+  if (n <= 2) return f(std::integral_constant<int, 2>());
+  if (n <= 5) return f(std::integral_constant<int, 5>());
+  if (n <= 10) return f(std::integral_constant<int, 10>());
+  if (n <= 16) return f(std::integral_constant<int, 16>());
+  return f(std::integral_constant<int, MAX_PASSES>());
+}
+
 template <class... A>
-cudaError_t launch_rows(void (*k)(A...), long long rows, int cluster, size_t smem, cudaStream_t st, A... args) {
-  cudaError_t e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_rows(void (*k)(A...), long long rows, int cluster, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * cluster));
   cfg.blockDim = dim3(NT);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -329,10 +370,6 @@ cudaError_t launch_rows(void (*k)(A...), long long rows, int cluster, size_t sme
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k, args...);
-}
-
-size_t segment_bytes(int vocab, int cluster) {
-  return (size_t)((vocab + cluster - 1) / cluster + 3) / 4 * 16;
 }
 
 bool aligned(const void* p, size_t n) { return p && (uintptr_t)p % n == 0; }
@@ -363,8 +400,9 @@ int mk_probs(const float* logits, int rows, int vocab, long long row_stride, flo
   const int c = cluster_of(vocab);
   const float scale = temperature > 0.f ? fminf(1.4426950408889634f / temperature, 3.4e38f) : 0.f;   // log2(e) / T
   const int win = aligned(logits, 16) && row_stride % 4 == 0, wout = aligned(probs, 16) && vocab % 4 == 0;
-  const cudaError_t e = launch_rows(k_probs, rows, c, segment_bytes(vocab, c), (cudaStream_t)stream, logits, vocab,
-                                    row_stride, scale, probs, win, wout);
+  const cudaError_t e = with_passes(vocab, c, [&](auto n) {
+    return launch_rows(k_probs<n.value>, rows, c, (cudaStream_t)stream, logits, vocab, row_stride, scale, probs, win, wout);
+  });
   return e == cudaSuccess ? MK_OK : fail_cuda("mk_probs", e);
 }
 
@@ -382,8 +420,7 @@ int mk_verify(int batch, int max_draft, int vocab, const float* target, const fl
   const int c = cluster_of(vocab);
   VerifyArgs a = {max_draft, vocab, 0, target, draft, drafts, n_draft, u, r, tokens, accepted};
   a.wide = aligned(target, 16) && (!draft || aligned(draft, 16)) && vocab % 4 == 0;
-  const size_t smem = segment_bytes(vocab, c);
-  const cudaError_t e = launch_rows(k_verify, batch, c, smem, (cudaStream_t)stream, a);
+  const cudaError_t e = with_passes(vocab, c, [&](auto n) { return launch_rows(k_verify<n.value>, batch, c, (cudaStream_t)stream, a); });
   return e == cudaSuccess ? MK_OK : fail_cuda("mk_verify", e);
 }
 

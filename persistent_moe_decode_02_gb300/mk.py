@@ -501,7 +501,7 @@ class Server:
 
 def _here(name: str, t: torch.Tensor, dtypes, shape=None) -> int:
     """The address of a contiguous tensor of the current device, checked."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != _device():
         raise ValueError(f"{name}: a tensor of the current CUDA device is wanted, got {t.device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, wanted one of {dtypes}")
@@ -512,8 +512,14 @@ def _here(name: str, t: torch.Tensor, dtypes, shape=None) -> int:
     return t.data_ptr()
 
 
-def _current() -> int:
-    return torch.cuda.current_stream().cuda_stream
+# These calls take microseconds, so the current device and stream are asked for without the objects around them.
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _on(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(_device())
 
 
 def _chunk_dims(D) -> MkModelDims:
@@ -580,7 +586,7 @@ class Chunk:
         if qkv.dim() < 2 or qkv.shape[0] != self.rows or qkv[:1].numel() != width * min(self.rows, 1) or (
                 self.rows and not qkv[0].is_contiguous()):
             raise ValueError(f"qkv: shape {tuple(qkv.shape)}, wanted {self.rows} contiguous rows of {width}")
-        if not qkv.is_cuda or qkv.device.index != torch.cuda.current_device() or qkv.dtype not in _ROWS:
+        if qkv.get_device() != _device() or qkv.dtype not in _ROWS:
             raise ValueError(f"qkv: a bf16 or float32 tensor of the current CUDA device is wanted, got {qkv.dtype} on "
                              f"{qkv.device}")
         if (q is None) != (self.nq == 0):
@@ -589,7 +595,7 @@ class Chunk:
         rc = lib().mk_chunk_append(self.h, qkv.data_ptr(), int(qkv.dtype == torch.float32), stride,
                                    _here("kv_pool", kv_pool, self._pool_type, self._pool),
                                    None if q is None else _here("q", q, _BF16, self._q),
-                                   _current() if stream is None else stream.cuda_stream)
+                                   _on(stream))
         if rc != MK_OK:
             raise MkError("mk_chunk_append", rc)
 
@@ -598,7 +604,7 @@ class Chunk:
         rc = lib().mk_chunk_attend(self.h, _here("q", q, _BF16, self._q),
                                    _here("kv_pool", kv_pool, self._pool_type, self._pool),
                                    _here("out", out, _BF16, self._q),
-                                   _current() if stream is None else stream.cuda_stream)
+                                   _on(stream))
         if rc != MK_OK:
             raise MkError("mk_chunk_attend", rc)
 
@@ -606,7 +612,7 @@ class Chunk:
         """Every cached and new position of every request, out [tokens, nkv, 2, head_dim] (bf16)."""
         rc = lib().mk_chunk_read(self.h, _here("kv_pool", kv_pool, self._pool_type, self._pool),
                                  _here("out", out, _BF16, (self.tokens, self.nkv, 2, self.d)),
-                                 _current() if stream is None else stream.cuda_stream)
+                                 _on(stream))
         if rc != MK_OK:
             raise MkError("mk_chunk_read", rc)
 
@@ -648,12 +654,12 @@ def probs(logits: torch.Tensor, temperature: float, out: torch.Tensor, stream=No
     """softmax(logits / temperature) of float32 rows [rows, vocab] (rows may lie apart) into out [rows, vocab];
     temperature 0: 1 at the largest logit."""
     if logits.dim() != 2 or (logits.numel() and logits.stride(1) != 1) or logits.dtype != torch.float32 or (
-            not logits.is_cuda or logits.device.index != torch.cuda.current_device()):
+            logits.get_device() != _device()):
         raise ValueError("logits: float32 rows [rows, vocab] of the current CUDA device are wanted")
     rows, vocab = logits.shape
     rc = lib().mk_probs(logits.data_ptr() if rows else None, rows, vocab, logits.stride(0) if rows > 1 else vocab,
                         float(temperature), _here("out", out, _F32, (rows, vocab)) if rows else None,
-                        _current() if stream is None else stream.cuda_stream)
+                        _on(stream))
     if rc != MK_OK:
         raise MkError("mk_probs", rc)
 
@@ -672,6 +678,6 @@ def verify(target: torch.Tensor, draft: Optional[torch.Tensor], drafts: torch.Te
                          None if n_draft is None else _here("n_draft", n_draft, _I32, (b,)),
                          _here("u", u, _F32, (b, k1 - 1)), _here("r", r, _F32, (b,)),
                          _here("tokens", tokens, _I32, (b, k1)), _here("accepted", accepted, _I32, (b,)),
-                         _current() if stream is None else stream.cuda_stream)
+                         _on(stream))
     if rc != MK_OK:
         raise MkError("mk_verify", rc)
