@@ -41,19 +41,20 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
 
-// Two 8-element pieces of one head, half a head apart, rotated at row `row`.
-template <int D>
-__device__ __forceinline__ void rotate8(const float2* rope, int row, int i, float (&a)[8], float (&b)[8]) {
-  if (!rope) return;
-  const float4* cs = reinterpret_cast<const float4*>(rope + (size_t)row * (D / 2) + i);
+// (cos, sin) of 8 dimensions of a row.
+struct Turn {
+  float4 cs[4];
+};
+// Two 8-element pieces of one head, half a head apart, rotated.
+__device__ __forceinline__ void rotate8(const Turn& t, float (&a)[8], float (&b)[8]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float4 t = __ldg(cs + j);   // (cos, sin) of two dimensions
+    const float4 c = t.cs[j];
     const float a0 = a[2 * j], a1 = a[2 * j + 1], b0 = b[2 * j], b1 = b[2 * j + 1];
-    a[2 * j] = a0 * t.x - b0 * t.y;
-    b[2 * j] = b0 * t.x + a0 * t.y;
-    a[2 * j + 1] = a1 * t.z - b1 * t.w;
-    b[2 * j + 1] = b1 * t.z + a1 * t.w;
+    a[2 * j] = a0 * c.x - b0 * c.y;
+    b[2 * j] = b0 * c.x + a0 * c.y;
+    a[2 * j + 1] = a1 * c.z - b1 * c.w;
+    b[2 * j + 1] = b1 * c.z + a1 * c.w;
   }
 }
 
@@ -82,15 +83,17 @@ __device__ __forceinline__ int scale_exp(float amax) {
   return k < -127 ? -127 : k;
 }
 
-// A value by 2^-k, exactly or correctly rounded (two factors: 2^127 alone is
-// beyond a float's exponent when k is -127 and -k + 127 overflows).
-__device__ __forceinline__ float times_pow2(float x, int k) { return ldexpf(x, k); }
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }   // k in [-126, 127]
 
-// Append: grid (pages that receive rows, KV heads, requests).
+// Append: grid (pages that receive rows, KV heads, requests).  A thread has one
+// token and the same 8 dimensions of either half of a head: its angles are read
+// once for all heads, whose loads do not wait for one another.
 template <int D, bool E4M3, class T>
 __global__ void __launch_bounds__(NT) k_append(ChunkView c, const T* qkv, long long row_stride, void* pool,
                                                __nv_bfloat16* q) {
   constexpr int LD = D + 1;                      // odd pitch: columns of the transpose fall into different banks
+  constexpr int C = D / 16;                      // threads of a token and head
+  constexpr int HS = NT / (PAGE * C);            // heads at a time
   __shared__ float kv[2][PAGE][LD];
   __shared__ int exps[2][PAGE];
   const ChunkReq r = c.reqs[blockIdx.z];
@@ -99,126 +102,151 @@ __global__ void __launch_bounds__(NT) k_append(ChunkView c, const T* qkv, long l
   const int p0 = max(j * PAGE, r.seq), p1 = min(j * PAGE + PAGE, r.seq + r.nnew);
   if (p0 >= p1) return;
   const int n = p1 - p0, slot0 = p0 - j * PAGE, row = r.row0 + p0 - r.seq;
-  constexpr int C = D / 16;                      // 8-element pieces of half a head
-  const T* src = qkv + (size_t)row * row_stride + (size_t)g * (G + 2) * D;
-  // queries and keys: a thread takes the pieces at i and i + D / 2 of a head
-  for (int x = tid; x < n * (G + 1) * C; x += NT) {
-    const int i = x % C * 8, h = x / C % (G + 1), t = x / (C * (G + 1));
-    const T* p = src + (size_t)t * row_stride + (size_t)h * D + i;
-    float a[8], b[8];
-    load8(p, a);
-    load8(p + D / 2, b);
-    rotate8<D>(c.rope, row + t, i, a, b);
-    if (h < G) {
-      __nv_bfloat16* o = q + ((size_t)(row + t) * c.nq + (size_t)g * G + h) * D + i;
-      *reinterpret_cast<uint4*>(o) = pack8(a);
-      *reinterpret_cast<uint4*>(o + D / 2) = pack8(b);
-    } else {
+  const int i = tid % C * 8, t = tid / C % PAGE, hs = tid / (C * PAGE);
+  const size_t block = ((size_t)__ldg(c.pt + r.pt + j) * c.nkv + g) * 2;   // the page's K block, in blocks
+  if (t < n) {
+    const T* src = qkv + (size_t)(row + t) * row_stride + (size_t)g * (G + 2) * D + i;
+    Turn turn;
+    if (c.rope) {
+      const float4* cs = reinterpret_cast<const float4*>(c.rope + (size_t)(row + t) * (D / 2) + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) turn.cs[e] = __ldg(cs + e);
+    }
+    __nv_bfloat16* dst = q + ((size_t)(row + t) * c.nq + (size_t)g * G) * D + i;
+#pragma unroll 4
+    for (int h = hs; h < G; h += HS) {
+      float a[8], b[8];
+      load8(src + (size_t)h * D, a);
+      load8(src + (size_t)h * D + D / 2, b);
+      if (c.rope) rotate8(turn, a, b);
+      *reinterpret_cast<uint4*>(dst + (size_t)h * D) = pack8(a);
+      *reinterpret_cast<uint4*>(dst + (size_t)h * D + D / 2) = pack8(b);
+    }
+    if (hs == 0) {
+      float a[8], b[8], v[8], w[8];
+      load8(src + (size_t)G * D, a);
+      load8(src + (size_t)G * D + D / 2, b);
+      load8(src + (size_t)(G + 1) * D, v);
+      load8(src + (size_t)(G + 1) * D + D / 2, w);
+      if (c.rope) rotate8(turn, a, b);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         kv[0][t][i + e] = a[e];
         kv[0][t][i + D / 2 + e] = b[e];
+        kv[1][t][i + e] = v[e];
+        kv[1][t][i + D / 2 + e] = w[e];
       }
     }
   }
-  for (int x = tid; x < n * (D / 8); x += NT) {
-    const int i = x % (D / 8) * 8, t = x / (D / 8);
-    float a[8];
-    load8(src + (size_t)t * row_stride + (size_t)(G + 1) * D + i, a);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) kv[1][t][i + e] = a[e];
-  }
   __syncthreads();
-  const size_t block = ((size_t)c.pt[r.pt + j] * c.nkv + g) * 2;   // the page's K block, in blocks
-  if (E4M3) {
+  if constexpr (E4M3) {
     // 4 threads take one vector's largest magnitude
-    const int w = tid / 4, t = w % PAGE, which = w / PAGE;
+    const int w = tid / 4, tw = w % PAGE, which = w / PAGE;
     float m = 0.f;
-    if (t < n)
-      for (int i = tid % 4; i < D; i += 4) {
-        const float v = fabsf(kv[which][t][i]);
-        m = fmaxf(m, v);                         // a NaN leaves the others' maximum
-      }
+    if (tw < n)
+      for (int x = tid % 4; x < D; x += 4) m = fmaxf(m, fabsf(kv[which][tw][x]));   // a NaN leaves the others' maximum
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    if (tid % 4 == 0) exps[which][t] = scale_exp(m);
+    if (tid % 4 == 0) exps[which][tw] = scale_exp(m);
     __syncthreads();
     uint8_t* out = reinterpret_cast<uint8_t*>(pool) + block * (D + 1) * PAGE;
     for (int x = tid; x < 2 * (D + 1); x += NT) {
-      const int which2 = x / (D + 1), i = x % (D + 1);
+      const int which2 = x / (D + 1), d = x % (D + 1);
       uint8_t* o = out + (size_t)x * PAGE + slot0;
-      alignas(16) uint8_t b[PAGE];
+      uint32_t b[4];
 #pragma unroll
-      for (int t2 = 0; t2 < PAGE; ++t2) {
-        if (t2 >= n) break;
-        const int k = exps[which2][t2];
-        b[t2] = i == D ? (uint8_t)(k + 127)
-                       : (uint8_t)__nv_cvt_float_to_fp8(times_pow2(kv[which2][t2][i], -k), __NV_SATFINITE, __NV_E4M3);
+      for (int w4 = 0; w4 < 4; ++w4) {
+        b[w4] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const int t2 = w4 * 4 + e;
+          const int k0 = exps[which2][t2], k1 = exps[which2][t2 + 1];
+          uint32_t two;
+          if (d == D) {
+            two = (uint32_t)(k0 + 127) | (uint32_t)(k1 + 127) << 8;
+          } else {
+            // by 2^-k in two factors: 2^127 and beyond is no factor of its own
+            const float v0 = kv[which2][t2][d] * pow2(-(k0 >> 1)) * pow2(-(k0 - (k0 >> 1)));
+            const float v1 = kv[which2][t2 + 1][d] * pow2(-(k1 >> 1)) * pow2(-(k1 - (k1 >> 1)));
+            two = __nv_cvt_float2_to_fp8x2(make_float2(v0, v1), __NV_SATFINITE, __NV_E4M3);
+          }
+          b[w4] |= two << (8 * e);
+        }
       }
       if (n == PAGE) {
-        *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(b);
+        *reinterpret_cast<uint4*>(o) = make_uint4(b[0], b[1], b[2], b[3]);
       } else {
 #pragma unroll
         for (int t2 = 0; t2 < PAGE; ++t2)
-          if (t2 < n) o[t2] = b[t2];             // only the new tokens' slots
+          if (t2 < n) o[t2] = (uint8_t)(b[t2 / 4] >> (t2 % 4 * 8));   // only the new tokens' slots
       }
     }
   } else {
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(pool) + block * D * PAGE;
     for (int x = tid; x < 2 * D; x += NT) {
-      const int which = x / D, i = x % D;
+      const int which = x / D, d = x % D;
       __nv_bfloat16* o = out + (size_t)x * PAGE + slot0;
       if (n == PAGE) {
         uint32_t w[8];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) w[t] = pack2(kv[which][2 * t][i], kv[which][2 * t + 1][i]);
+        for (int t2 = 0; t2 < 8; ++t2) w[t2] = pack2(kv[which][2 * t2][d], kv[which][2 * t2 + 1][d]);
         reinterpret_cast<uint4*>(o)[0] = make_uint4(w[0], w[1], w[2], w[3]);
         reinterpret_cast<uint4*>(o)[1] = make_uint4(w[4], w[5], w[6], w[7]);
       } else {
-        for (int t = 0; t < n; ++t) o[t] = __float2bfloat16_rn(kv[which][t][i]);
+        for (int t2 = 0; t2 < n; ++t2) o[t2] = __float2bfloat16_rn(kv[which][t2][d]);
       }
     }
   }
 }
 
-// Read: grid (pages, KV heads, requests).  Codes and scales give the value
-// exactly in fp32; the rounding to bf16 changes it only outside bf16's normal
-// range.
+// Read: grid (pages, KV heads, requests).  A thread has two dimensions of the
+// page's 16 tokens.  Codes and scales give the value exactly in fp32; the
+// rounding to bf16 changes it only outside bf16's normal range.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(NT) k_read(ChunkView c, const void* pool, __nv_bfloat16* out) {
-  constexpr int LD = 2 * D + 8;                  // 16-byte rows for the way out
-  __shared__ alignas(16) __nv_bfloat16 buf[PAGE][LD];
+  constexpr int LD = D + 4;                      // words of a token's row: 16-byte rows for the way out
+  __shared__ alignas(16) uint32_t buf[PAGE][LD];
   const ChunkReq r = c.reqs[blockIdx.z];
   const int g = blockIdx.y, j = blockIdx.x, tid = threadIdx.x;
   const int n = min(PAGE, r.seq + r.nnew - j * PAGE);
   if (n <= 0) return;
-  const size_t block = ((size_t)c.pt[r.pt + j] * c.nkv + g) * 2;
-  for (int x = tid; x < 2 * D; x += NT) {
-    if (E4M3) {
-      const uint8_t* b = reinterpret_cast<const uint8_t*>(pool) + (block + x / D) * (D + 1) * PAGE;
-      alignas(16) uint8_t code[PAGE], ex[PAGE];
-      *reinterpret_cast<uint4*>(code) = __ldg(reinterpret_cast<const uint4*>(b + (size_t)(x % D) * PAGE));
-      *reinterpret_cast<uint4*>(ex) = __ldg(reinterpret_cast<const uint4*>(b + (size_t)D * PAGE));
+  const size_t block = ((size_t)__ldg(c.pt + r.pt + j) * c.nkv + g) * 2;
+  for (int x = tid; x < D; x += NT) {            // dimensions 2x and 2x + 1 of K, then V
+    if constexpr (E4M3) {
+      const uint8_t* b = reinterpret_cast<const uint8_t*>(pool) + (block + x / (D / 2)) * (D + 1) * PAGE;
+      const uint4* rows = reinterpret_cast<const uint4*>(b) + x % (D / 2) * 2;
+      const uint4 lo4 = __ldg(rows), hi4 = __ldg(rows + 1), ex4 = __ldg(reinterpret_cast<const uint4*>(b) + D);
+      const uint32_t lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w},
+                     ex[4] = {ex4.x, ex4.y, ex4.z, ex4.w};
 #pragma unroll
-      for (int t = 0; t < PAGE; ++t) {
-        const __half_raw h = __nv_cvt_fp8_to_halfraw(code[t], __NV_E4M3);
-        buf[t][x] = __float2bfloat16_rn(times_pow2(__half2float(__half(h)), (int)ex[t] - 127));
+      for (int t = 0; t < PAGE; t += 2) {
+        const int at = t % 4 * 8;
+        const __half2 l = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(lo[t / 4] >> at), __NV_E4M3));
+        const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(hi[t / 4] >> at), __NV_E4M3));
+        const uint32_t e0 = ex[t / 4] >> at & 0xff, e1 = ex[t / 4] >> (at + 8) & 0xff;
+        const float s0 = e0 ? __uint_as_float(e0 << 23) : __uint_as_float(0x400000u);   // 2^(e - 127)
+        const float s1 = e1 ? __uint_as_float(e1 << 23) : __uint_as_float(0x400000u);
+        buf[t][x] = pack2(__low2float(l) * s0, __low2float(h) * s0);
+        buf[t + 1][x] = pack2(__high2float(l) * s1, __high2float(h) * s1);
       }
     } else {
-      const uint4* b = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(pool) + block * D * PAGE +
-                                                      (size_t)x * PAGE);
-      alignas(16) __nv_bfloat16 v[PAGE];
-      reinterpret_cast<uint4*>(v)[0] = __ldg(b);
-      reinterpret_cast<uint4*>(v)[1] = __ldg(b + 1);
+      const uint4* rows = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(pool) + block * D * PAGE) +
+                          (size_t)x * 4;
+      const uint4 v[4] = {__ldg(rows), __ldg(rows + 1), __ldg(rows + 2), __ldg(rows + 3)};
+      const uint32_t lo[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+      const uint32_t hi[8] = {v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
 #pragma unroll
-      for (int t = 0; t < PAGE; ++t) buf[t][x] = v[t];
+      for (int t = 0; t < 8; ++t) {
+        buf[2 * t][x] = __byte_perm(lo[t], hi[t], 0x5410);
+        buf[2 * t + 1][x] = __byte_perm(lo[t], hi[t], 0x7632);
+      }
     }
   }
   __syncthreads();
   const size_t row0 = (size_t)r.tok0 + (size_t)j * PAGE;
   for (int x = tid; x < n * (D / 4); x += NT) {
-    const int i = x % (D / 4) * 8, t = x / (D / 4);
-    *reinterpret_cast<uint4*>(out + ((row0 + t) * c.nkv + g) * 2 * D + i) = *reinterpret_cast<const uint4*>(&buf[t][i]);
+    const int i = x % (D / 4), t = x / (D / 4);
+    *reinterpret_cast<uint4*>(out + ((row0 + t) * c.nkv + g) * 2 * D + i * 8) = *reinterpret_cast<const uint4*>(&buf[t][i * 4]);
   }
 }
 

@@ -188,37 +188,39 @@ struct VerifyArgs {
 };
 
 template <int PASSES>
-__global__ void __launch_bounds__(NT) k_verify(VerifyArgs a) {
+__global__ void __launch_bounds__(NT, PASSES <= 10 ? 2 : 1) k_verify(VerifyArgs a) {
   __shared__ unsigned long long sums[PASSES * NW], totals[MAX_CLUSTER];
-  __shared__ int n_acc;
+  __shared__ int n_acc, n_all;
   cg::cluster_group cl = cg::this_cluster();
   cl.barrier_arrive();
   const int blocks = (int)cl.num_blocks(), rank = (int)cl.block_rank(), tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int b = blockIdx.x / blocks, V = a.vocab;
-  const int n = a.count ? min(max(a.count[b], 0), a.drafts) : a.drafts;
   const float* target = a.target + (size_t)b * (a.drafts + 1) * V;
   const float* draft = a.draft ? a.draft + (size_t)b * a.drafts * V : nullptr;
   const int* tok = a.tok + (size_t)b * a.drafts;
   if (warp == 0) {                            // every block of the cluster decides alike
+    const int given = a.count ? a.count[b] : a.drafts, n = min(max(given, 0), a.drafts);
     int first = n;
-    for (int i0 = 0; i0 < n && first == n; i0 += 32) {
-      const int i = i0 + lane;
-      bool ok = true;
-      if (i < n) {
-        const int x = tok[i];
-        ok = x >= 0 && x < V;
-        if (ok) {
-          const double q = draft ? draft[(size_t)i * V + x] : 1.0;   // products of 24-bit factors are exact in 53
-          ok = (double)a.u[(size_t)b * a.drafts + i] * q < (double)target[(size_t)i * V + x];
-        }
+    for (int i0 = 0; i0 < a.drafts; i0 += 32) {
+      const int i = i0 + lane;                // (tokens and numbers of places past n are read, in their rows)
+      const int x = i < a.drafts ? tok[i] : -1;
+      const float u = i < a.drafts ? a.u[(size_t)b * a.drafts + i] : 0.f;
+      bool ok = x >= 0 && x < V;
+      if (ok) {
+        const double q = draft ? draft[(size_t)i * V + x] : 1.0;   // products of 24-bit factors are exact in 53
+        ok = (double)u * q < (double)target[(size_t)i * V + x];
       }
-      const unsigned no = __ballot_sync(FULL, !ok);
+      const unsigned no = __ballot_sync(FULL, i < n && !ok);
       if (no) first = i0 + __ffs(no) - 1;
+      if (no || i0 + 32 >= n) break;
     }
-    if (lane == 0) n_acc = first;
+    if (lane == 0) {
+      n_acc = first;
+      n_all = n;
+    }
   }
   __syncthreads();
-  const int acc = n_acc;
+  const int acc = n_acc, n = n_all;
   const bool refused = acc < n;
   const Segment s = segment(V, blocks, rank);
   const float* trow = target + (size_t)acc * V + s.begin;
