@@ -22,9 +22,8 @@
 // Q's columns are stored in the same order, and O's are read in it.
 //
 // 8-bit blocks (codes, then the slots' scales) are copied as they are and
-// turned into that layout by warps of their own: a code is a bf16 number
-// after a shift, up to a factor 2^120 that its scale's multiplication takes
-// along, so nothing is rounded.
+// turned into that layout by warps of their own: a code times a power of two is
+// a bf16 number, so nothing is rounded (outside bf16's normal range).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -310,45 +309,27 @@ __device__ __forceinline__ void prefetch_q(const Args& a, const AttnTask& t, int
 // (dimensions) me, me + 32, ...; `live` slots, the others 0.
 template <int D>
 __device__ __forceinline__ void convert_page(const uint8_t* raw, uint8_t* dst, int live, int me) {
-  uint32_t mul[8] = {}, far[8] = {};
-  bool any_far = false;
-  if (live > 0) {
-    // scale 2^(e - 127) times 2^120, as a bf16 number's exponent; above 2^127
-    // (e > 134) the rest comes as a second factor
+  uint32_t scale[8];                             // 2^(e - 127): e is a bf16 number's exponent too (0: a vector of zeros)
+  uint4 code[D / 32];                            // every row's read before the first write: they may not alias
+  {
     const uint4 e4 = *reinterpret_cast<const uint4*>(raw + D * PAGE);
     const uint32_t ew[4] = {e4.x, e4.y, e4.z, e4.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t e = __byte_perm(ew[i / 2], 0, i % 2 ? 0x4342 : 0x4140);   // two exponents in 16-bit halves
-      const uint32_t lo = __vminu2(e, 134u | 134u << 16);
-      mul[i] = (lo + (120u | 120u << 16)) << 7;
-      far[i] = (e - lo + (127u | 127u << 16)) << 7;
-      any_far |= e != lo;
-      if (live < PAGE) {                         // slots behind the end: code times 0
-        if (2 * i >= live) mul[i] = 0;
-        else if (2 * i + 1 >= live) mul[i] &= 0xffffu;
-      }
-    }
-  }
-  uint4 code[D / 32];                            // every row's read before the first write: they may not alias
+    for (int i = 0; i < 8; ++i) scale[i] = __byte_perm(ew[i / 2], 0, i % 2 ? 0x4342 : 0x4140) << 7;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i)
-    code[i] = live > 0 ? *reinterpret_cast<const uint4*>(raw + (me + i * 32) * PAGE) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < D / 32; ++i) code[i] = *reinterpret_cast<const uint4*>(raw + (me + i * 32) * PAGE);
+  }
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) {
     const int d = me + k * 32;
     const uint32_t cw[4] = {code[k].x, code[k].y, code[k].z, code[k].w};
     uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // two codes into the high bytes of 16-bit halves; sign stays, the
-      // other 7 bits go to bf16's lowest exponent and highest mantissa bits
-      const uint32_t x = __byte_perm(cw[i / 2], 0, i % 2 ? 0x3424 : 0x1404);
-      o[i] = mul_bf16x2((x & 0x80008000u) | (x >> 4 & 0x07f007f0u), mul[i]);
-    }
-    if (any_far)
+    for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(e4m3x2_to_bf16x2(cw[i / 2] >> (i % 2 * 16)), scale[i]);
+    if (live < PAGE) {                           // the request's last page
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], far[i]);
+      for (int i = 0; i < 8; ++i) o[i] = live >= 2 * i + 2 ? o[i] : live == 2 * i + 1 ? o[i] & 0xffffu : 0u;
+    }
     const int row = d ^ (d >> 3 & 3), flip = row >> 2 & 1;
     *reinterpret_cast<uint4*>(dst + row * 32 + flip * 16) = make_uint4(o[0], o[1], o[2], o[3]);
     *reinterpret_cast<uint4*>(dst + row * 32 + (flip ^ 1) * 16) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -467,12 +448,11 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
     constexpr int N = E4M3 ? C::NRAW : C::NST;
     int at[2] = {0, 0};                          // tiles issued of K and V
     auto full = [&](int v, int i) { return E4M3 ? &ctl->raw_full[v][i] : &ctl->full[v][i]; };
-    auto copy = [&](const AttnTask& t, int v, int j) {
+    auto copy = [&](const AttnTask& t, int v, int j, int ids) {
       const int u = at[v], s = u % N;
       if (u >= N && !wait(E4M3 ? &ctl->raw_empty[v][s] : &ctl->empty[v][s], (u / N & 1) ^ 1, ctl, status)) return false;
-      const int page = (t.tile0 + j) * TILE_PAGES + lane;
-      const bool there = lane < TILE_PAGES && page < (t.total + PAGE - 1) / PAGE;
-      const int id = there ? __ldg(a.c.pt + t.pt + page) : 0;
+      const int id = __shfl_sync(FULL, ids, (j * TILE_PAGES + lane) % 32);
+      const bool there = lane < TILE_PAGES && id >= 0;
       const size_t block = ((size_t)id * a.c.nkv + t.kvh) * 2 + v;
       if (E4M3) {
         const uint32_t bytes = __popc(__ballot_sync(FULL, there)) * C::RAW_PAGE;
@@ -490,8 +470,22 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
     };
     for (int i = t0; i < t1 && ok; ++i) {        // in the order of use: K goes one tile ahead
       const AttnTask t = a.c.tasks[i];
-      ok = copy(t, 0, 0);
-      for (int j = 0; j < t.ntile && ok; ++j) ok = (j + 1 == t.ntile || copy(t, 0, j + 1)) && copy(t, 1, j);
+      // page numbers of 8 tiles, a lane each, and of the next 8
+      constexpr int GROUP = 32 / TILE_PAGES;
+      const int npages = (t.total + PAGE - 1) / PAGE;
+      auto pages = [&](int j) {
+        const int page = (t.tile0 + j) * TILE_PAGES + lane;
+        return page < npages ? __ldg(a.c.pt + t.pt + page) : -1;
+      };
+      int ids = pages(0), more = pages(GROUP);
+      ok = copy(t, 0, 0, ids);
+      for (int j = 0; j < t.ntile && ok; ++j) {
+        if (j > 0 && j % GROUP == 0) {
+          ids = more;
+          more = pages(j + GROUP);
+        }
+        ok = (j + 1 == t.ntile || copy(t, 0, j + 1, (j + 1) % GROUP ? ids : more)) && copy(t, 1, j, ids);
+      }
     }
     if (!ok)                                     // given up: what is in flight still lands before the block ends
       for (int v = 0; v < 2; ++v)

@@ -169,6 +169,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Two e4m3 codes as bf16, exactly: by way of fp16 and fp32, whose upper half a
+// bf16 number is.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes) {
+  uint32_t h, lo, hi;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+  asm("{\n .reg .b16 a, b;\n .reg .f32 x, y;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 x, a;\n cvt.f32.f16 y, b;\n mov.b32 %0, x;\n"
+      " mov.b32 %1, y;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(h));
+  return __byte_perm(lo, hi, 0x7632);
+}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
