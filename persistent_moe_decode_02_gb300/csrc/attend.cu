@@ -57,15 +57,15 @@ struct Cfg {
   static constexpr int PAGE_BYTES = D * PAGE * 2;             // a page's K or V as bf16
   static constexpr int STAGE = TILE_PAGES * PAGE_BYTES;       // a key tile's K or V
   static constexpr int RAW_PAGE = (D + 1) * PAGE;             // a page's 8-bit block
-  static constexpr int RAW = TILE_PAGES * RAW_PAGE;
-  // shared memory: two query tiles, K's and V's rings of bf16 tiles, their
-  // rings of 8-bit tiles; D = 64 has twice the stages in the same bytes
+  static constexpr int RAW = TILE_PAGES * 2 * RAW_PAGE;       // a tile's K and V, page by page as in the pool
+  // shared memory: two query tiles, K's and V's rings of bf16 tiles, a ring
+  // of 8-bit tiles; D = 64 has twice the stages in the same bytes
   static constexpr int NST = (E4M3 ? 3 : 5) * (128 / D);
   static constexpr int NRAW = E4M3 ? 4 * (128 / D) : 0;
-  static constexpr int OFF_KV = 2 * Q_BYTES, OFF_RAW = OFF_KV + 2 * NST * STAGE, OFF_CTL = OFF_RAW + 2 * NRAW * RAW;
+  static constexpr int OFF_KV = 2 * Q_BYTES, OFF_RAW = OFF_KV + 2 * NST * STAGE, OFF_CTL = OFF_RAW + NRAW * RAW;
   // V is 0 for K's ring, 1 for V's
   __device__ static constexpr int kv(int v, int i) { return OFF_KV + (v * NST + i) * STAGE; }
-  __device__ static constexpr int raw(int v, int i) { return OFF_RAW + (v * NRAW + i) * RAW; }
+  __device__ static constexpr int raw(int i, int page, int v) { return OFF_RAW + i * RAW + (page * 2 + v) * RAW_PAGE; }
   static constexpr int SMEM = OFF_CTL + 1024 + 1024;          // control words, and room to align the base
   // tensor memory columns: two S buffers (and P over them) of each query tile, O of each
   static constexpr int T_S = 0, T_O = 4 * KV_TILE, T_COLS = 512;
@@ -74,7 +74,7 @@ struct Cfg {
 };
 
 struct Ctl {
-  uint64_t full[2][10], empty[2][10], raw_full[2][8], raw_empty[2][8];
+  uint64_t full[2][10], empty[2][10], raw_full[8], raw_empty[8];
   uint64_t q_ready[2], s_full[2][2], p_ready[2][2], o_done[2], o_full[2], drain;
   uint32_t tmem;
   int fail;
@@ -348,17 +348,17 @@ __device__ __forceinline__ void convert_tiles(const Args& a, int t0, int t1, uin
   for (int i = t0; i < t1; ++i) {
     const int tile0 = __ldg(&a.c.tasks[i].tile0), ntile = __ldg(&a.c.tasks[i].ntile), total = __ldg(&a.c.tasks[i].total);
     for (int j = 0; j < ntile; ++j) {
-      if (!wait(&ctl->raw_full[v][ri], r_ph, ctl, a.c.status)) return;
+      if (!wait(&ctl->raw_full[ri], r_ph, ctl, a.c.status)) return;
       if (!first && !wait(&ctl->empty[v][si], s_ph ^ 1, ctl, a.c.status)) return;
       const int left = total - (tile0 + j) * KV_TILE;   // the request's keys from the tile on
       for (int p = p0; p < p1; ++p)
-        convert_page<D>(smem + C::raw(v, ri) + p * C::RAW_PAGE, smem + C::kv(v, si) + p * C::PAGE_BYTES,
+        convert_page<D>(smem + C::raw(ri, p, v), smem + C::kv(v, si) + p * C::PAGE_BYTES,
                         min(PAGE, max(0, left - p * PAGE)), lane);
       fence_async();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&ctl->full[v][si]);
-        mbar_arrive(&ctl->raw_empty[v][ri]);
+        mbar_arrive(&ctl->raw_empty[ri]);
       }
       if (++ri == C::NRAW) { ri = 0; r_ph ^= 1; }
       if (++si == C::NST) { si = 0; s_ph ^= 1; first = false; }
@@ -385,10 +385,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
         mbar_init(&ctl->full[v][i], !E4M3 ? 1 : two ? 2 : 4);   // the copies' issue, or the converting warps
         mbar_init(&ctl->empty[v][i], 2);                        // both query tiles' products
       }
-      for (int i = 0; i < C::NRAW; ++i) {
-        mbar_init(&ctl->raw_full[v][i], 1);
-        mbar_init(&ctl->raw_empty[v][i], two ? 2 : 4);
-      }
+    }
+    for (int i = 0; i < C::NRAW; ++i) {
+      mbar_init(&ctl->raw_full[i], 1);
+      mbar_init(&ctl->raw_empty[i], two ? 4 : 8);   // the converting warps
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->q_ready[i], 4);
@@ -444,31 +444,41 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
       }
       t = next;
     }
-  } else if (warp == W_COPY) {                   // ---- copies: a lane has a page
+  } else if (warp == W_COPY) {                   // ---- copies
+    // issued by one lane: by four, a page each, they took twice the time
     constexpr int N = E4M3 ? C::NRAW : C::NST;
-    int at[2] = {0, 0};                          // tiles issued of K and V
-    auto full = [&](int v, int i) { return E4M3 ? &ctl->raw_full[v][i] : &ctl->full[v][i]; };
+    int at[2] = {0, 0};                          // tiles issued of K and V (8 bits: of both)
+    auto full = [&](int v, int i) { return E4M3 ? &ctl->raw_full[i] : &ctl->full[v][i]; };
     auto copy = [&](const AttnTask& t, int v, int j, int ids) {
       const int u = at[v], s = u % N;
-      if (u >= N && !wait(E4M3 ? &ctl->raw_empty[v][s] : &ctl->empty[v][s], (u / N & 1) ^ 1, ctl, status)) return false;
-      const int id = __shfl_sync(FULL, ids, (j * TILE_PAGES + lane) % 32);
-      const bool there = lane < TILE_PAGES && id >= 0;
-      const size_t block = ((size_t)id * a.c.nkv + t.kvh) * 2 + v;
-      if (E4M3) {
-        const uint32_t bytes = __popc(__ballot_sync(FULL, there)) * C::RAW_PAGE;
-        if (lane == 0) mbar_arrive_tx(full(v, s), bytes);
-        __syncwarp();
-        if (there) bulk_copy(smem + C::raw(v, s) + lane * C::RAW_PAGE, a.pool + block * C::RAW_PAGE, C::RAW_PAGE, full(v, s));
-      } else {
-        if (lane == 0) mbar_arrive_tx(full(v, s), C::STAGE);
-        __syncwarp();
-        if (lane < TILE_PAGES)                   // a page past the end: zeros
-          tma_2d(smem + C::kv(v, s) + lane * C::PAGE_BYTES, &map, 0, there ? (int)(block * (D / 4)) : a.oob, full(v, s));
+      if (u >= N && !wait(E4M3 ? &ctl->raw_empty[s] : &ctl->empty[v][s], (u / N & 1) ^ 1, ctl, status)) return false;
+      int id[TILE_PAGES];
+#pragma unroll
+      for (int p = 0; p < TILE_PAGES; ++p) id[p] = __shfl_sync(FULL, ids, (j * TILE_PAGES + p) % 32);
+      if (elect_one()) {
+        if constexpr (E4M3) {                    // a page's K and V blocks lie side by side
+          uint32_t pages = 0;
+#pragma unroll
+          for (int p = 0; p < TILE_PAGES; ++p) pages += id[p] >= 0;
+          mbar_arrive_tx(full(v, s), pages * 2 * C::RAW_PAGE);
+#pragma unroll
+          for (int p = 0; p < TILE_PAGES; ++p)
+            if (id[p] >= 0)
+              bulk_copy(smem + C::raw(s, p, 0), a.pool + ((size_t)id[p] * a.c.nkv + t.kvh) * 2 * C::RAW_PAGE, 2 * C::RAW_PAGE,
+                        full(v, s));
+        } else {                                 // a page past the end: zeros
+          mbar_arrive_tx(full(v, s), C::STAGE);
+#pragma unroll
+          for (int p = 0; p < TILE_PAGES; ++p)
+            tma_2d(smem + C::kv(v, s) + p * C::PAGE_BYTES, &map, 0,
+                   id[p] >= 0 ? (int)(((size_t)id[p] * a.c.nkv + t.kvh) * 2 + v) * (D / 4) : a.oob, full(v, s));
+        }
       }
+      __syncwarp();
       ++at[v];
       return true;
     };
-    for (int i = t0; i < t1 && ok; ++i) {        // in the order of use: K goes one tile ahead
+    for (int i = t0; i < t1 && ok; ++i) {
       const AttnTask t = a.c.tasks[i];
       // page numbers of 8 tiles, a lane each, and of the next 8
       constexpr int GROUP = 32 / TILE_PAGES;
@@ -478,13 +488,14 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
         return page < npages ? __ldg(a.c.pt + t.pt + page) : -1;
       };
       int ids = pages(0), more = pages(GROUP);
-      ok = copy(t, 0, 0, ids);
+      if (!E4M3) ok = copy(t, 0, 0, ids);        // in the order of use: K goes one tile ahead
       for (int j = 0; j < t.ntile && ok; ++j) {
         if (j > 0 && j % GROUP == 0) {
           ids = more;
           more = pages(j + GROUP);
         }
-        ok = (j + 1 == t.ntile || copy(t, 0, j + 1, (j + 1) % GROUP ? ids : more)) && copy(t, 1, j, ids);
+        if (E4M3) ok = copy(t, 0, j, ids);
+        else ok = (j + 1 == t.ntile || copy(t, 0, j + 1, (j + 1) % GROUP ? ids : more)) && copy(t, 1, j, ids);
       }
     }
     if (!ok)                                     // given up: what is in flight still lands before the block ends
