@@ -496,14 +496,18 @@ typedef struct mk_chunk mk_chunk;
  * (MK_ERR_CAPACITY beyond max_pages_per_seq); a page that receives new tokens
  * belongs to one request, others may be shared.  Device memory (tables, the
  * rotation's angles and the space for split rows) is allocated on the current
- * device, where all later calls must run (MK_ERR_INVALID elsewhere). */
+ * device, where all later calls must run (MK_ERR_INVALID elsewhere); like
+ * mk_plan_create, not while a stream is captured. */
 int mk_chunk_create(const mk_model_dims* dims, int kv_type, int num_pages, int batch, const int* seq_lens,
                     const int* new_lens, const int* page_table, int max_pages_per_seq, mk_chunk** out);
 
 /* Another batch for the same chunk object, checked like mk_chunk_create's;
  * uploaded on `stream`.  Work already enqueued on other streams must be
- * ordered before it.  On an error the chunk keeps its batch, except after
- * MK_ERR_CUDA.  Not during a stream capture (MK_ERR_INVALID). */
+ * ordered before it.  On an error the chunk keeps its batch; after an
+ * MK_ERR_CUDA of the upload itself it has none until an update succeeds.  Not
+ * during a stream capture (MK_ERR_INVALID).  Graphs that captured calls for an
+ * earlier batch have to be captured again: replayed all the same, those calls
+ * write nothing and mk_chunk_sync returns MK_ERR_INVALID. */
 int mk_chunk_update(mk_chunk* c, int batch, const int* seq_lens, const int* new_lens, const int* page_table,
                     int max_pages_per_seq, mk_stream stream);
 
@@ -525,7 +529,7 @@ int mk_chunk_append(mk_chunk* c, const void* qkv, int rows_type, long long row_s
  * head_dim], 16-byte aligned; scores are scaled by 1 / sqrt(head_dim), softmax
  * statistics and sums are fp32.  The cached values of the positions below
  * seq_lens[b] + new_lens[b] must be finite; slots behind them may hold
- * anything.  Calls on one chunk share its space for split rows: enqueue them
+ * anything.  out may be q itself.  Calls on one chunk share its space for split rows: enqueue them
  * on one stream, or one after another, replays of graphs that captured them
  * among them (chunks of their own run at the same time). */
 int mk_chunk_attend(mk_chunk* c, const void* q, const void* kv_pool, void* out, mk_stream stream);
@@ -538,7 +542,8 @@ int mk_chunk_read(mk_chunk* c, const void* kv_pool, void* out, mk_stream stream)
 
 /* Wait for `stream`, then return the device status: MK_OK, or
  * MK_ERR_DEP_TIMEOUT when a bounded wait inside mk_chunk_attend ran out (its
- * output is then void).  mk_chunk_update clears it. */
+ * output is then void), or MK_ERR_INVALID when a graph replayed calls of an
+ * earlier batch.  mk_chunk_update clears it. */
 int mk_chunk_sync(mk_chunk* c, mk_stream stream);
 
 /* [batch, rows, cached + new tokens, attention tasks, tasks that write split

@@ -377,6 +377,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
   const int per = Q_TILE / a.c.G;
   const int t0 = __ldg(a.c.cta_start + blockIdx.x), t1 = __ldg(a.c.cta_start + blockIdx.x + 1);
   int* status = a.c.status;
+  if (stale(a.c)) return;
   const bool two = __ldg(&a.c.tasks[t0].two);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be launched: it waits for the end
   if (tid == 0) {
@@ -593,6 +594,7 @@ __global__ void __launch_bounds__(128) k_join(ChunkView c, __nv_bfloat16* out) {
   __shared__ float part[W][D + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const JoinTask t = c.joins[blockIdx.x];
+  if (stale(c)) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rows = t.ntok * c.G, row = W == 4 ? blockIdx.y : blockIdx.y * 4 + warp, w = W == 4 ? warp : 0;
   if (row >= rows) return;                       // the whole block where warps share a row
@@ -663,20 +665,14 @@ cudaError_t launch(const ChunkView& c, const void* q, const void* pool, void* ou
   cudaError_t e = E4M3 ? cudaSuccess : pool_map(c, pool, &map, &a.oob);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k_attend<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  k_attend<D, E4M3><<<c.ctas, C::THREADS, C::SMEM, st>>>(a, map);
-  e = cudaGetLastError();
+  e = launch_kernel(k_attend<D, E4M3>, c.ctas, C::THREADS, C::SMEM, st, nullptr, a, map);
   if (e != cudaSuccess || !c.njoins) return e;
-  cudaLaunchConfig_t cfg = {};
   const bool many = c.max_parts > 8;
-  cfg.gridDim = dim3(c.njoins, many ? c.max_join_rows : (c.max_join_rows + 3) / 4);
-  cfg.blockDim = dim3(128);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];                     // launched while the tasks run; it waits for their end itself
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, many ? k_join<D, 4> : k_join<D, 1>, c, (__nv_bfloat16*)out);
+  cudaLaunchAttribute at;                        // launched while the tasks run; it waits for their end itself
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  return launch_kernel(many ? k_join<D, 4> : k_join<D, 1>, dim3(c.njoins, many ? c.max_join_rows : (c.max_join_rows + 3) / 4),
+                       128, 0, st, &at, c, (__nv_bfloat16*)out);
 }
 
 }  // namespace

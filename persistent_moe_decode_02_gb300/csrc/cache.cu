@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(NT) k_append(ChunkView c, const T* qkv, long l
   __shared__ float kv[2][PAGE][LD];
   __shared__ int exps[2][PAGE];
   const ChunkReq r = c.reqs[blockIdx.z];
+  if (stale(c)) return;
   const int g = blockIdx.y, G = c.G, tid = threadIdx.x;
   const int j = r.seq / PAGE + blockIdx.x;       // page of the request
   const int p0 = max(j * PAGE, r.seq), p1 = min(j * PAGE + PAGE, r.seq + r.nnew);
@@ -207,6 +208,7 @@ __global__ void __launch_bounds__(NT) k_read(ChunkView c, const void* pool, __nv
   constexpr int LD = D + 4;                      // words of a token's row: 16-byte rows for the way out
   __shared__ alignas(16) uint32_t buf[PAGE][LD];
   const ChunkReq r = c.reqs[blockIdx.z];
+  if (stale(c)) return;
   const int g = blockIdx.y, j = blockIdx.x, tid = threadIdx.x;
   const int n = min(PAGE, r.seq + r.nnew - j * PAGE);
   if (n <= 0) return;
@@ -256,41 +258,36 @@ cudaError_t launch_chunk_rope(const ChunkView& c, double theta, float2* tab, cud
   const int half = c.d / 2;
   const long long most = (long long)c.rows * half;
   const int blocks = (int)(most < 256 * 1024 ? (most + 255) / 256 : 1024);
-  k_chunk_rope<<<dim3(blocks, c.batch), 256, 0, st>>>(c.reqs, half, c.d, theta, tab);
-  return cudaGetLastError();
+  return launch_kernel(k_chunk_rope, dim3(blocks, c.batch), 256, 0, st, nullptr, c.reqs, half, c.d, theta, tab);
 }
+
+namespace {
+
+template <int D, bool E4M3>
+cudaError_t append(const ChunkView& c, bool f32, const void* qkv, long long row_stride, void* pool, void* q, dim3 grid,
+                   cudaStream_t st) {
+  const auto o = (__nv_bfloat16*)q;
+  if (f32) return launch_kernel(k_append<D, E4M3, float>, grid, NT, 0, st, nullptr, c, (const float*)qkv, row_stride, pool, o);
+  return launch_kernel(k_append<D, E4M3, __nv_bfloat16>, grid, NT, 0, st, nullptr, c, (const __nv_bfloat16*)qkv, row_stride,
+                       pool, o);
+}
+
+}  // namespace
 
 cudaError_t launch_append(const ChunkView& c, bool e4m3, bool f32, const void* qkv, long long row_stride, void* pool,
                           void* q, int max_new_pages, cudaStream_t st) {
   const dim3 grid(max_new_pages, c.nkv, c.batch);
-  const auto bf = (const __nv_bfloat16*)qkv;
-  const auto fl = (const float*)qkv;
-  const auto o = (__nv_bfloat16*)q;
-  if (c.d == 64) {
-    if (e4m3) f32 ? k_append<64, true><<<grid, NT, 0, st>>>(c, fl, row_stride, pool, o)
-                  : k_append<64, true><<<grid, NT, 0, st>>>(c, bf, row_stride, pool, o);
-    else f32 ? k_append<64, false><<<grid, NT, 0, st>>>(c, fl, row_stride, pool, o)
-             : k_append<64, false><<<grid, NT, 0, st>>>(c, bf, row_stride, pool, o);
-  } else {
-    if (e4m3) f32 ? k_append<128, true><<<grid, NT, 0, st>>>(c, fl, row_stride, pool, o)
-                  : k_append<128, true><<<grid, NT, 0, st>>>(c, bf, row_stride, pool, o);
-    else f32 ? k_append<128, false><<<grid, NT, 0, st>>>(c, fl, row_stride, pool, o)
-             : k_append<128, false><<<grid, NT, 0, st>>>(c, bf, row_stride, pool, o);
-  }
-  return cudaGetLastError();
+  if (c.d == 64)
+    return e4m3 ? append<64, true>(c, f32, qkv, row_stride, pool, q, grid, st)
+                : append<64, false>(c, f32, qkv, row_stride, pool, q, grid, st);
+  return e4m3 ? append<128, true>(c, f32, qkv, row_stride, pool, q, grid, st)
+              : append<128, false>(c, f32, qkv, row_stride, pool, q, grid, st);
 }
 
 cudaError_t launch_read(const ChunkView& c, bool e4m3, const void* pool, void* out, int max_pages, cudaStream_t st) {
   const dim3 grid(max_pages, c.nkv, c.batch);
-  const auto o = (__nv_bfloat16*)out;
-  if (c.d == 64) {
-    if (e4m3) k_read<64, true><<<grid, NT, 0, st>>>(c, pool, o);
-    else k_read<64, false><<<grid, NT, 0, st>>>(c, pool, o);
-  } else {
-    if (e4m3) k_read<128, true><<<grid, NT, 0, st>>>(c, pool, o);
-    else k_read<128, false><<<grid, NT, 0, st>>>(c, pool, o);
-  }
-  return cudaGetLastError();
+  const auto k = c.d == 64 ? (e4m3 ? k_read<64, true> : k_read<64, false>) : (e4m3 ? k_read<128, true> : k_read<128, false>);
+  return launch_kernel(k, grid, NT, 0, st, nullptr, c, pool, (__nv_bfloat16*)out);
 }
 
 }  // namespace mk

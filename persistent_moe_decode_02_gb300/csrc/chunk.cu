@@ -31,6 +31,7 @@ int fail(int code, const char* msg) {
 }
 
 int fail_cuda(const char* what, cudaError_t e) {
+  cudaGetLastError();   // reported here: not to the caller's next question
   char buf[224];
   snprintf(buf, sizeof(buf), "%s: %s (%d)", what, cudaGetErrorString(e), (int)e);
   return fail(MK_ERR_CUDA, buf);
@@ -259,7 +260,10 @@ struct mk_chunk {
   size_t rope_cap = 0;
   float* part = nullptr;         // split rows: sums, then (maximum, sum) pairs
   size_t part_cap = 0;
-  int* status = nullptr;
+  int* status = nullptr;         // [0] first recorded error, [1] generation of the tables
+  int gen = 0;
+  bool lost = false;             // an upload failed: the tables hold no batch
+  std::vector<void*> retired;    // outgrown memory: graphs of earlier batches may name it, so it stays
   mk::ChunkView view = {};
 };
 
@@ -267,14 +271,17 @@ namespace {
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
-cudaError_t grow(void** p, size_t* cap, size_t need) {
+cudaError_t grow(mk_chunk* c, void** p, size_t* cap, size_t need) {
   if (need <= *cap) return cudaSuccess;
-  cudaFree(*p);                  // waits for the device: no call still reads it
-  *p = nullptr;
-  *cap = 0;
-  const cudaError_t e = cudaMalloc(p, need);
-  if (e == cudaSuccess) *cap = need;
-  return e;
+  void* q = nullptr;
+  c->retired.reserve(c->retired.size() + 1);
+  if (*cap) need = std::max(need, *cap + *cap / 2);
+  const cudaError_t e = cudaMalloc(&q, need);
+  if (e != cudaSuccess) return e;
+  if (*p) c->retired.push_back(*p);
+  *p = q;
+  *cap = need;
+  return cudaSuccess;
 }
 
 int build(const mk_chunk* c, int batch, const int* seq_lens, const int* new_lens, const int* page_table, int max_pages,
@@ -289,10 +296,10 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
   const size_t n_req = up16(nb.reqs.size() * sizeof(ChunkReq)), n_pt = up16(nb.pt.size() * sizeof(int)),
                n_task = up16(nb.tasks.size() * sizeof(AttnTask)), n_join = up16(nb.joins.size() * sizeof(JoinTask)),
                n_cta = up16(nb.cta_start.size() * sizeof(int)), n_all = n_req + n_pt + n_task + n_join + n_cta;
-  cudaError_t e = grow(&c->blob, &c->blob_cap, n_all);
+  cudaError_t e = grow(c, &c->blob, &c->blob_cap, n_all);
   if (e == cudaSuccess && c->s.theta > 0.)
-    e = grow((void**)&c->rope, &c->rope_cap, (size_t)nb.rows * (d / 2) * sizeof(float2));
-  if (e == cudaSuccess) e = grow((void**)&c->part, &c->part_cap, (size_t)nb.split_rows * (d + 2) * sizeof(float));
+    e = grow(c, (void**)&c->rope, &c->rope_cap, (size_t)nb.rows * (d / 2) * sizeof(float2));
+  if (e == cudaSuccess) e = grow(c, (void**)&c->part, &c->part_cap, (size_t)nb.split_rows * (d + 2) * sizeof(float));
   if (e != cudaSuccess) return fail_cuda("mk_chunk: device memory", e);
   std::vector<char> host(n_all, 0);
   memcpy(host.data(), nb.reqs.data(), nb.reqs.size() * sizeof(ChunkReq));
@@ -301,9 +308,10 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
   if (!nb.joins.empty())
     memcpy(host.data() + n_req + n_pt + n_task, nb.joins.data(), nb.joins.size() * sizeof(JoinTask));
   memcpy(host.data() + n_all - n_cta, nb.cta_start.data(), nb.cta_start.size() * sizeof(int));
-  // pageable source: the bytes have left it when the call returns
+  // pageable sources: the bytes have left them when the calls return
   e = cudaMemcpyAsync(c->blob, host.data(), host.size(), cudaMemcpyHostToDevice, st);
-  if (e == cudaSuccess) e = cudaMemsetAsync(c->status, 0, 4 * sizeof(int), st);
+  const int head[2] = {0, ++c->gen};
+  if (e == cudaSuccess) e = cudaMemcpyAsync(c->status, head, sizeof(head), cudaMemcpyHostToDevice, st);
   c->b = std::move(nb);
   mk::ChunkView& v = c->view;
   char* base = (char*)c->blob;
@@ -324,7 +332,9 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
   v.part_o = c->part;
   v.part_ml = (float2*)(c->part + (size_t)c->b.split_rows * d);
   v.status = c->status;
+  v.gen = c->gen;
   if (e == cudaSuccess && c->s.theta > 0. && v.rows) e = mk::launch_chunk_rope(v, c->s.theta, c->rope, st);
+  c->lost = e != cudaSuccess;
   return e == cudaSuccess ? MK_OK : fail_cuda("mk_chunk: upload", e);
 }
 
@@ -333,6 +343,7 @@ int check_device(const mk_chunk* c) {
   int dev = -1;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail_cuda("mk_chunk: current device", e);
+  if (c->lost) return fail(MK_ERR_INVALID, "mk_chunk: the last update failed; update again");
   return dev == c->device ? MK_OK : fail(MK_ERR_INVALID, "mk_chunk: the chunk belongs to another device than the current one");
 }
 
@@ -348,6 +359,7 @@ void mk_chunk_destroy(mk_chunk* c) {
   cudaFree(c->rope);
   cudaFree(c->part);
   cudaFree(c->status);
+  for (void* p : c->retired) cudaFree(p);
   delete c;
 }
 
@@ -391,10 +403,17 @@ int mk_chunk_update(mk_chunk* c, int batch, const int* seq_lens, const int* new_
   return guarded([&] {
     Built b;
     int rc = build(c, batch, seq_lens, new_lens, page_table, max_pages_per_seq, b);
-    if (rc == MK_OK) rc = check_device(c);
     if (rc != MK_OK) return rc;
+    const bool lost = c->lost;
+    c->lost = false;
+    rc = check_device(c);
+    if (rc != MK_OK) {
+      c->lost = lost;
+      return rc;
+    }
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     const cudaError_t e = cudaStreamIsCapturing((cudaStream_t)stream, &cap);
+    c->lost = lost;
     if (e != cudaSuccess) return fail_cuda("mk_chunk_update", e);
     if (cap != cudaStreamCaptureStatusNone) return fail(MK_ERR_INVALID, "mk_chunk_update: the stream is being captured");
     set_tasks(c->s, c->ctas, b);

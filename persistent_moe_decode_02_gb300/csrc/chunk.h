@@ -56,8 +56,33 @@ struct ChunkView {
   int max_parts, max_join_rows;  // of one join
   float* part_o;                 // [split rows][d] unnormalised sums
   float2* part_ml;               // [split rows] (maximum, sum) of the softmax
-  int* status;                   // first recorded error, 0 = none
+  int* status;                   // [0] first recorded error, 0 = none; [1] generation of the tables
+  int gen;                       // the generation that this view was made for
 };
+
+#if defined(__CUDACC__)
+// A graph may replay a call whose chunk was updated since: the view's counts
+// then no longer fit the tables, and the kernel leaves everything as it is.
+__device__ __forceinline__ bool stale(const ChunkView& c) {
+  if (__ldg(c.status + 1) == c.gen) return false;   // (nothing writes it while a kernel runs)
+  if (blockIdx.x + blockIdx.y + blockIdx.z + threadIdx.x == 0) atomicCAS(c.status, 0, -1);   // MK_ERR_INVALID
+  return true;
+}
+
+// Launch, with the call's own error and none that was left before.
+template <class... A, class... B>
+cudaError_t launch_kernel(void (*k)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, cudaLaunchAttribute* at,
+                          B&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = at ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k, static_cast<A>(args)...);
+}
+#endif
 
 cudaError_t launch_chunk_rope(const ChunkView& c, double theta, float2* tab, cudaStream_t st);
 cudaError_t launch_append(const ChunkView& c, bool e4m3, bool f32, const void* qkv, long long row_stride, void* pool,

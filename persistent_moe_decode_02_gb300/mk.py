@@ -582,16 +582,20 @@ class Chunk:
     def append(self, qkv: torch.Tensor, kv_pool: torch.Tensor, q: Optional[torch.Tensor] = None, stream=None) -> None:
         """Rotate and append the rows qkv [rows, nkv, G + 2, head_dim] (or [rows, nkv * (G + 2) * head_dim]; bf16 or
         float32, rows may lie apart) to one layer's pool; the rotated queries to q [rows, nq, head_dim] (bf16)."""
-        width = (self.nq + 2 * self.nkv) * self.d
-        if qkv.dim() < 2 or qkv.shape[0] != self.rows or qkv[:1].numel() != width * min(self.rows, 1) or (
-                self.rows and not qkv[0].is_contiguous()):
-            raise ValueError(f"qkv: shape {tuple(qkv.shape)}, wanted {self.rows} contiguous rows of {width}")
+        width, n = (self.nq + 2 * self.nkv) * self.d, 1
+        shape, steps = qkv.shape, qkv.stride()
+        fits = len(shape) > 1 and shape[0] == self.rows
+        for i in range(len(shape) - 1, 0, -1):     # what follows the first dimension is one contiguous row
+            fits = fits and (steps[i] == n or shape[i] == 1)
+            n *= shape[i]
+        if not fits or n != width:
+            raise ValueError(f"qkv: shape {tuple(shape)}, wanted {self.rows} contiguous rows of {width}")
         if qkv.get_device() != _device() or qkv.dtype not in _ROWS:
             raise ValueError(f"qkv: a bf16 or float32 tensor of the current CUDA device is wanted, got {qkv.dtype} on "
                              f"{qkv.device}")
         if (q is None) != (self.nq == 0):
             raise ValueError("q: wanted exactly when the chunk has query heads")
-        stride = qkv.stride(0) if self.rows > 1 else width
+        stride = steps[0] if self.rows > 1 else width
         rc = lib().mk_chunk_append(self.h, qkv.data_ptr(), int(qkv.dtype == torch.float32), stride,
                                    _here("kv_pool", kv_pool, self._pool_type, self._pool),
                                    None if q is None else _here("q", q, _BF16, self._q),

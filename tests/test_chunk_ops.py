@@ -399,6 +399,79 @@ def test_streams_graphs_and_updates(mk):
         assert ((out.cpu().double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
 
 
+def test_graph_of_an_earlier_batch_does_nothing(mk):
+    # a captured call whose chunk was updated since: reported, and nothing is written
+    D, batch, chunk = make(mk, "g8", "bf16", "behind_cache", seed=4)
+    pool = cu.make_pool("bf16", batch.num_pages, 4, 128, 9).cuda()
+    was = pool.clone()
+    qkv = cu.normal((batch.rows, 4, 10, 128), 3).bfloat16().cuda()
+    q = torch.full((batch.rows, 32, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    out, back = q.clone(), torch.full((sum(batch.total), 4, 2, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chunk.append(qkv, pool, q)
+        chunk.attend(q, pool, out)
+        chunk.read(pool, back)
+    for cached, new in (([3], [1]), ([0] * 40, [70] * 40)):
+        b = cu.Batch(cached, new, spare=0)
+        table = [p % batch.num_pages if p >= 0 else -1 for p in b.flat] if len(cached) == 1 else None
+        if table is None:   # far more pages than the pool has: only the tables grow
+            big = mk.Chunk(D, "bf16", b.num_pages, [1], [1], [0], 1)
+            big.update(b.cached, b.new, b.flat, b.width)
+            big.close()
+            continue
+        chunk.update(cached, new, table, b.width)
+        graph.replay()
+        assert chunk.sync() == mk.MK_ERR_INVALID
+        assert torch.equal(pool, was) and (q == 5).all() and (out == 5).all() and (back == 5).all()
+    chunk.update(batch.cached, batch.new, batch.flat, batch.width)
+    assert chunk.sync() == mk.MK_OK
+    chunk.append(qkv, pool, q)
+    chunk.attend(q, pool, out)
+    assert chunk.sync() == mk.MK_OK
+    ref, mag = cu.attend(q.cpu(), pool.cpu(), "bf16", batch, 4)
+    assert ((out.cpu().double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
+
+
+def test_attend_onto_its_queries(mk):
+    for lens in ("prompts", "long_one_token"):
+        D, batch, chunk = make(mk, "g8", "bf16", lens)
+        pool = cu.make_pool("bf16", batch.num_pages, 4, 128, 3).cuda()
+        q = cu.normal((batch.rows, 32, 128), 3).bfloat16().cuda()
+        out = torch.empty_like(q)
+        chunk.attend(q, pool, out)
+        chunk.attend(q, pool, q)
+        assert chunk.sync() == mk.MK_OK and torch.equal(q, out)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_pages_beyond_4_gb(mk, kv):
+    # pages at both ends of a pool of more than 2^32 bytes
+    D = cu.dims(8, 8, 128)
+    d = 128 + (kv == "e4m3")
+    pages = (1 << 32) // (8 * 2 * d * 16 * (1 if kv == "e4m3" else 2)) + 50
+    pool = torch.zeros(pages, 8, 2, d, 16, dtype=torch.uint8 if kv == "e4m3" else torch.bfloat16, device="cuda")
+    batch = cu.Batch([70], [5], seed=1, spare=0)
+    far = [pages - 1 - 2 * p if p % 2 else p for p in batch.flat]
+    chunk = mk.Chunk(D, kv, pages, [0], [75], far, batch.width)
+    x = cu.normal((75, 8, 3, 128), 4).bfloat16().cuda()
+    q = torch.empty(75, 8, 128, dtype=torch.bfloat16, device="cuda")
+    chunk.append(x, pool, q)
+    out, back = torch.empty_like(q), torch.empty(75, 8, 2, 128, dtype=torch.bfloat16, device="cuda")
+    chunk.attend(q, pool, out)
+    chunk.read(pool, back)
+    assert chunk.sync() == mk.MK_OK
+    near = torch.zeros(batch.num_pages, 8, 2, d, 16, dtype=pool.dtype)
+    for mine, there in zip(batch.flat, far):
+        near[mine] = pool[there].cpu()
+    whole = cu.Batch([0], [75], spare=0)
+    whole.table, whole.num_pages = batch.table, batch.num_pages
+    ref, mag = cu.attend(q.cpu(), near, kv, whole, 8)
+    assert ((out.cpu().double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
+    assert torch.equal(back.cpu(), cu.rows_of(near, kv, whole, 0).bfloat16())
+    assert (back.cpu()[:, :, 1].double() - x.cpu()[:, :, 2].double()).abs().max() <= 2.0 ** -4 * 6
+
+
 def test_same_bits_every_time(mk):
     D, batch, chunk = make(mk, "g8", "e4m3", ([4000, 9000, 100], [5, 1, 200]))
     pool = cu.make_pool("e4m3", batch.num_pages, 4, 128, 3).cuda()
