@@ -60,15 +60,27 @@ __device__ __forceinline__ void rotate8(const Turn& t, float (&a)[8], float (&b)
 
 // cos and sin of position * theta^(-2i/d), the angle and its functions in 64
 // bits: in 32 an angle near 2^18 would be off by 2^-7.  Once for a chunk, read
-// by every layer's append.
-__global__ void k_chunk_rope(const ChunkReq* reqs, int half, int d, double theta, float2* tab) {
+// by every layer's append.  A thread turns one dimension pair through
+// ROPE_RUN positions by the angle between neighbours, which costs 4 operations
+// a position instead of about 100 (errors add up to less than 2^-48).
+constexpr int ROPE_RUN = 16;
+struct Freq {
+  double of[64];                                 // theta^(-2i/d)
+};
+__global__ void k_chunk_rope(const ChunkReq* reqs, int half, const __grid_constant__ Freq freq, float2* tab) {
   const ChunkReq r = reqs[blockIdx.y];
-  const long long n = (long long)r.nnew * half;
+  const long long n = (long long)((r.nnew + ROPE_RUN - 1) / ROPE_RUN) * half;
   for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < n; x += (long long)gridDim.x * blockDim.x) {
-    const int t = (int)(x / half), i = (int)(x % half);
-    double s, c;
-    sincos((double)(r.seq + t) * pow(theta, -2.0 * i / d), &s, &c);
-    tab[(size_t)(r.row0 + t) * half + i] = make_float2((float)c, (float)s);
+    const int t0 = (int)(x / half) * ROPE_RUN, i = (int)(x % half);
+    double s, c, ds, dc;
+    sincos((double)(r.seq + t0) * freq.of[i], &s, &c);
+    sincos(freq.of[i], &ds, &dc);
+    for (int t = t0; t < min(t0 + ROPE_RUN, r.nnew); ++t) {
+      tab[(size_t)(r.row0 + t) * half + i] = make_float2((float)c, (float)s);
+      const double c1 = c * dc - s * ds;
+      s = s * dc + c * ds;
+      c = c1;
+    }
   }
 }
 
@@ -254,11 +266,13 @@ __global__ void __launch_bounds__(NT) k_read(ChunkView c, const void* pool, __nv
 
 }  // namespace
 
-cudaError_t launch_chunk_rope(const ChunkView& c, double theta, float2* tab, cudaStream_t st) {
+cudaError_t launch_chunk_rope(const ChunkView& c, double theta, float2* tab, int max_new, cudaStream_t st) {
   const int half = c.d / 2;
-  const long long most = (long long)c.rows * half;
+  const long long most = ((long long)max_new + ROPE_RUN - 1) / ROPE_RUN * half;
   const int blocks = (int)(most < 256 * 1024 ? (most + 255) / 256 : 1024);
-  return launch_kernel(k_chunk_rope, dim3(blocks, c.batch), 256, 0, st, nullptr, c.reqs, half, c.d, theta, tab);
+  Freq freq = {};
+  for (int i = 0; i < half; ++i) freq.of[i] = pow(theta, -2.0 * i / c.d);
+  return launch_kernel(k_chunk_rope, dim3(blocks, c.batch), 256, 0, st, nullptr, c.reqs, half, freq, tab);
 }
 
 namespace {

@@ -74,7 +74,7 @@ struct Built {
   std::vector<JoinTask> joins;
   std::vector<int> cta_start;
   long long rows = 0, tokens = 0, split_rows = 0, nsplit = 0, joined_rows = 0;
-  int max_pages = 0, max_new_pages = 0;   // of one request: all its pages, those that receive rows
+  int max_pages = 0, max_new_pages = 0, max_new = 0;   // of one request: all its pages, those that receive rows, rows
 };
 
 // Row counts and prefix sums; no pages yet.
@@ -95,6 +95,7 @@ int set_lens(const Shape& s, int batch, const int* seq_lens, const int* new_lens
     if (b.rows > INT_MAX - 1024) return fail(MK_ERR_UNSUPPORTED, "mk_chunk: over 2^31 - 1025 new rows");
     const int np = (int)((total + mk::PAGE - 1) / mk::PAGE);
     b.max_pages = std::max(b.max_pages, np);
+    b.max_new = std::max(b.max_new, new_lens[i]);
     if (new_lens[i]) b.max_new_pages = std::max(b.max_new_pages, np - seq_lens[i] / mk::PAGE);
   }
   return MK_OK;
@@ -254,12 +255,10 @@ struct mk_chunk {
   Shape s;
   int type = 0, num_pages = 0, device = 0, ctas = 0;
   Built b;
-  void* blob = nullptr;          // requests, page table, tasks, joins
-  size_t blob_cap = 0;
-  float2* rope = nullptr;
-  size_t rope_cap = 0;
-  float* part = nullptr;         // split rows: sums, then (maximum, sum) pairs
-  size_t part_cap = 0;
+  // requests, page table, tasks, joins, CTAs' first tasks; the rotation's
+  // angles; split rows: sums, then (maximum, sum) pairs
+  char* mem = nullptr;
+  size_t mem_cap = 0;
   int* status = nullptr;         // [0] first recorded error, [1] generation of the tables
   int gen = 0;
   bool lost = false;             // an upload failed: the tables hold no batch
@@ -271,16 +270,16 @@ namespace {
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
-cudaError_t grow(mk_chunk* c, void** p, size_t* cap, size_t need) {
-  if (need <= *cap) return cudaSuccess;
+cudaError_t grow(mk_chunk* c, size_t need) {
+  if (need <= c->mem_cap) return cudaSuccess;
   void* q = nullptr;
   c->retired.reserve(c->retired.size() + 1);
-  if (*cap) need = std::max(need, *cap + *cap / 2);
+  need = std::max(need, c->mem_cap + c->mem_cap / 2);
   const cudaError_t e = cudaMalloc(&q, need);
   if (e != cudaSuccess) return e;
-  if (*p) c->retired.push_back(*p);
-  *p = q;
-  *cap = need;
+  if (c->mem) c->retired.push_back(c->mem);
+  c->mem = (char*)q;
+  c->mem_cap = need;
   return cudaSuccess;
 }
 
@@ -296,10 +295,9 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
   const size_t n_req = up16(nb.reqs.size() * sizeof(ChunkReq)), n_pt = up16(nb.pt.size() * sizeof(int)),
                n_task = up16(nb.tasks.size() * sizeof(AttnTask)), n_join = up16(nb.joins.size() * sizeof(JoinTask)),
                n_cta = up16(nb.cta_start.size() * sizeof(int)), n_all = n_req + n_pt + n_task + n_join + n_cta;
-  cudaError_t e = grow(c, &c->blob, &c->blob_cap, n_all);
-  if (e == cudaSuccess && c->s.theta > 0.)
-    e = grow(c, (void**)&c->rope, &c->rope_cap, (size_t)nb.rows * (d / 2) * sizeof(float2));
-  if (e == cudaSuccess) e = grow(c, (void**)&c->part, &c->part_cap, (size_t)nb.split_rows * (d + 2) * sizeof(float));
+  const size_t n_rope = c->s.theta > 0. ? up16((size_t)nb.rows * (d / 2) * sizeof(float2)) : 0;
+  const size_t off_rope = (n_all + 255) / 256 * 256, off_part = (off_rope + n_rope + 255) / 256 * 256;
+  cudaError_t e = grow(c, off_part + (size_t)nb.split_rows * (d + 2) * sizeof(float));
   if (e != cudaSuccess) return fail_cuda("mk_chunk: device memory", e);
   std::vector<char> host(n_all, 0);
   memcpy(host.data(), nb.reqs.data(), nb.reqs.size() * sizeof(ChunkReq));
@@ -309,12 +307,12 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
     memcpy(host.data() + n_req + n_pt + n_task, nb.joins.data(), nb.joins.size() * sizeof(JoinTask));
   memcpy(host.data() + n_all - n_cta, nb.cta_start.data(), nb.cta_start.size() * sizeof(int));
   // pageable sources: the bytes have left them when the calls return
-  e = cudaMemcpyAsync(c->blob, host.data(), host.size(), cudaMemcpyHostToDevice, st);
+  e = cudaMemcpyAsync(c->mem, host.data(), host.size(), cudaMemcpyHostToDevice, st);
   const int head[2] = {0, ++c->gen};
   if (e == cudaSuccess) e = cudaMemcpyAsync(c->status, head, sizeof(head), cudaMemcpyHostToDevice, st);
   c->b = std::move(nb);
   mk::ChunkView& v = c->view;
-  char* base = (char*)c->blob;
+  char* base = c->mem;
   v.nq = c->s.nq; v.nkv = c->s.nkv; v.d = c->s.d; v.G = c->s.G;
   v.batch = (int)c->b.reqs.size(); v.rows = (int)c->b.rows; v.num_pages = c->num_pages;
   v.reqs = (const ChunkReq*)base;
@@ -328,12 +326,13 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
     v.max_parts = std::max(v.max_parts, j.nparts);
     v.max_join_rows = std::max(v.max_join_rows, j.ntok * v.G);
   }
-  v.rope = c->s.theta > 0. ? c->rope : nullptr;
-  v.part_o = c->part;
-  v.part_ml = (float2*)(c->part + (size_t)c->b.split_rows * d);
+  v.rope = c->s.theta > 0. ? (const float2*)(base + off_rope) : nullptr;
+  v.part_o = (float*)(base + off_part);
+  v.part_ml = (float2*)(v.part_o + (size_t)c->b.split_rows * d);
   v.status = c->status;
   v.gen = c->gen;
-  if (e == cudaSuccess && c->s.theta > 0. && v.rows) e = mk::launch_chunk_rope(v, c->s.theta, c->rope, st);
+  if (e == cudaSuccess && v.rope && v.rows)
+    e = mk::launch_chunk_rope(v, c->s.theta, (float2*)(base + off_rope), c->b.max_new, st);
   c->lost = e != cudaSuccess;
   return e == cudaSuccess ? MK_OK : fail_cuda("mk_chunk: upload", e);
 }
@@ -355,9 +354,7 @@ extern "C" {
 
 void mk_chunk_destroy(mk_chunk* c) {
   if (!c) return;
-  cudaFree(c->blob);
-  cudaFree(c->rope);
-  cudaFree(c->part);
+  cudaFree(c->mem);
   cudaFree(c->status);
   for (void* p : c->retired) cudaFree(p);
   delete c;

@@ -84,7 +84,7 @@ cudaError_t launch_kernel(void (*k)(A...), dim3 grid, dim3 block, size_t smem, c
 }
 #endif
 
-cudaError_t launch_chunk_rope(const ChunkView& c, double theta, float2* tab, cudaStream_t st);
+cudaError_t launch_chunk_rope(const ChunkView& c, double theta, float2* tab, int max_new, cudaStream_t st);
 cudaError_t launch_append(const ChunkView& c, bool e4m3, bool f32, const void* qkv, long long row_stride, void* pool,
                           void* q, int max_new_pages, cudaStream_t st);
 cudaError_t launch_read(const ChunkView& c, bool e4m3, const void* pool, void* out, int max_pages, cudaStream_t st);
