@@ -3,9 +3,10 @@
 //
 // A row of the vocabulary is one cluster's work: each block holds its segment
 // of the row in registers, so the row is read once whatever is done with
-// it, and the blocks exchange their totals through distributed shared memory.  160 rows of 151936 take 42.6 us (4.6 TB/s, 0.67 of a copy's rate:
-// the 1280 blocks are 4.2 rounds of what fits the SMs at once, two on each); one
-// row 4.5 us.  A verification reads the row or two that its draw needs, not the
+// it, and the blocks exchange their totals through distributed shared memory.
+// 160 rows of 151936 take 42.6 us (4.6 TB/s, 0.67 of a copy's rate: the 1280
+// blocks are 4.2 rounds of what fits the SMs at once, two on each); one row 4.5
+// us.  A verification reads the row or two that its draw needs, not the
 // others: 32 of them with five drafts take 12.4 us, one 6.7 us, a chain of five
 // dependent reads and two exchanges.
 #include <cooperative_groups.h>
