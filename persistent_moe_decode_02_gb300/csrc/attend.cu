@@ -47,6 +47,7 @@
 #include <math.h>
 
 #include "chunk.h"
+#include "launch.cuh"
 #include "mk.h"
 #include "ptx.cuh"
 
@@ -396,7 +397,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
   int* status = a.c.status;
   if (stale(a.c)) return;
   const bool two = __ldg(&a.c.tasks[t0].two);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the join may be launched: it waits for the end
   if (tid == 0) {
     for (int v = 0; v < 2; ++v) {
       for (int i = 0; i < C::NST; ++i) {
@@ -427,6 +427,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
   tc_after();
   const uint32_t tmem = ctl->tmem;
   bool ok = true;
+  // So far only the chunk's own tables were read, which no kernel writes.
+  await_stream();
+  allow_next();
 
   if (warp < 8 && (warp < 4 || two)) {           // ---- softmax of a query tile
     const int qt = warp / 4;
@@ -609,7 +612,8 @@ template <int D, int W>
 __global__ void __launch_bounds__(128) k_join(ChunkView c, __nv_bfloat16* out) {
   constexpr int E = D / 32;
   __shared__ float part[W][D + 1];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  await_stream();
+  allow_next();
   const JoinTask t = c.joins[blockIdx.x];
   if (stale(c)) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -682,14 +686,11 @@ cudaError_t launch(const ChunkView& c, const void* q, const void* pool, void* ou
   cudaError_t e = E4M3 ? cudaSuccess : pool_map(c, pool, &map, &a.oob);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(k_attend<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(k_attend<D, E4M3>, c.ctas, C::THREADS, C::SMEM, st, nullptr, a, map);
+  e = launch_kernel(k_attend<D, E4M3>, c.ctas, C::THREADS, C::SMEM, 1, st, a, map);
   if (e != cudaSuccess || !c.njoins) return e;
   const bool many = c.max_parts > 8;
-  cudaLaunchAttribute at;                        // launched while the tasks run; it waits for their end itself
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
   return launch_kernel(many ? k_join<D, 4> : k_join<D, 1>, dim3(c.njoins, many ? c.max_join_rows : (c.max_join_rows + 3) / 4),
-                       128, 0, st, &at, c, (__nv_bfloat16*)out);
+                       128, 0, 1, st, c, (__nv_bfloat16*)out);
 }
 
 }  // namespace

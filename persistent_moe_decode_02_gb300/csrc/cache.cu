@@ -15,6 +15,7 @@
 #include <math.h>
 
 #include "chunk.h"
+#include "launch.cuh"
 
 namespace mk {
 namespace {
@@ -72,6 +73,8 @@ struct Freq {
   double of[64];                                 // theta^(-2i/d)
 };
 __global__ void k_chunk_rope(const ChunkReq* reqs, int half, const __grid_constant__ Freq freq, float2* tab) {
+  await_stream();
+  allow_next();
   const ChunkReq r = reqs[blockIdx.y];
   const long long n = (long long)((r.nnew + ROPE_RUN - 1) / ROPE_RUN) * half;
   for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < n; x += (long long)gridDim.x * blockDim.x) {
@@ -112,6 +115,8 @@ __global__ void __launch_bounds__(NT) k_append(ChunkView c, const T* qkv, long l
   constexpr int HS = NT / (PAGE * C);            // heads at a time
   __shared__ float kv[2][PAGE][LD];
   __shared__ int exps[2][PAGE];
+  await_stream();
+  allow_next();
   const ChunkReq r = c.reqs[blockIdx.z];
   if (stale(c)) return;
   const int g = blockIdx.y, G = c.G, tid = threadIdx.x;
@@ -223,6 +228,8 @@ template <int D, bool E4M3>
 __global__ void __launch_bounds__(NT) k_read(ChunkView c, const void* pool, __nv_bfloat16* out) {
   constexpr int LD = D + 4;                      // words of a token's row: 16-byte rows for the way out
   __shared__ alignas(16) uint32_t buf[PAGE][LD];
+  await_stream();
+  allow_next();
   const ChunkReq r = c.reqs[blockIdx.z];
   if (stale(c)) return;
   const int g = blockIdx.y, j = blockIdx.x, tid = threadIdx.x;
@@ -276,7 +283,7 @@ cudaError_t launch_chunk_rope(const ChunkView& c, double theta, float2* tab, int
   const int blocks = (int)(most < 256 * 1024 ? (most + 255) / 256 : 1024);
   Freq freq = {};
   for (int i = 0; i < half; ++i) freq.of[i] = pow(theta, -2.0 * i / c.d);
-  return launch_kernel(k_chunk_rope, dim3(blocks, c.batch), 256, 0, st, nullptr, c.reqs, half, freq, tab);
+  return launch_kernel(k_chunk_rope, dim3(blocks, c.batch), 256, 0, 1, st, c.reqs, half, freq, tab);
 }
 
 namespace {
@@ -285,8 +292,8 @@ template <int D, bool E4M3>
 cudaError_t append(const ChunkView& c, bool f32, const void* qkv, long long row_stride, void* pool, void* q, dim3 grid,
                    cudaStream_t st) {
   const auto o = (__nv_bfloat16*)q;
-  if (f32) return launch_kernel(k_append<D, E4M3, float>, grid, NT, 0, st, nullptr, c, (const float*)qkv, row_stride, pool, o);
-  return launch_kernel(k_append<D, E4M3, __nv_bfloat16>, grid, NT, 0, st, nullptr, c, (const __nv_bfloat16*)qkv, row_stride,
+  if (f32) return launch_kernel(k_append<D, E4M3, float>, grid, NT, 0, 1, st, c, (const float*)qkv, row_stride, pool, o);
+  return launch_kernel(k_append<D, E4M3, __nv_bfloat16>, grid, NT, 0, 1, st, c, (const __nv_bfloat16*)qkv, row_stride,
                        pool, o);
 }
 
@@ -305,7 +312,7 @@ cudaError_t launch_append(const ChunkView& c, bool e4m3, bool f32, const void* q
 cudaError_t launch_read(const ChunkView& c, bool e4m3, const void* pool, void* out, int max_pages, cudaStream_t st) {
   const dim3 grid(max_pages, c.nkv, c.batch);
   const auto k = c.d == 64 ? (e4m3 ? k_read<64, true> : k_read<64, false>) : (e4m3 ? k_read<128, true> : k_read<128, false>);
-  return launch_kernel(k, grid, NT, 0, st, nullptr, c, pool, (__nv_bfloat16*)out);
+  return launch_kernel(k, grid, NT, 0, 1, st, c, pool, (__nv_bfloat16*)out);
 }
 
 }  // namespace mk

@@ -68,20 +68,6 @@ __device__ __forceinline__ bool stale(const ChunkView& c) {
   if (blockIdx.x + blockIdx.y + blockIdx.z + threadIdx.x == 0) atomicCAS(c.status, 0, -1);   // MK_ERR_INVALID
   return true;
 }
-
-// Launch, with the call's own error and none that was left before.
-template <class... A, class... B>
-cudaError_t launch_kernel(void (*k)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, cudaLaunchAttribute* at,
-                          B&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = at;
-  cfg.numAttrs = at ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k, static_cast<A>(args)...);
-}
 #endif
 
 cudaError_t launch_chunk_rope(const ChunkView& c, double theta, float2* tab, int max_new, cudaStream_t st);

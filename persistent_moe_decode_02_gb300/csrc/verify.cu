@@ -17,6 +17,7 @@
 
 #include <type_traits>
 
+#include "launch.cuh"
 #include "mk.h"
 
 namespace cg = cooperative_groups;
@@ -69,6 +70,8 @@ __global__ void __launch_bounds__(NT) k_probs(const float* logits, int vocab, lo
   __shared__ float wmax[NW], wsum[NW];
   __shared__ int wat[NW];
   __shared__ struct { float m, sum; int at; } parts[FEW];
+  await_stream();
+  allow_next();
   cg::cluster_group cl = cg::this_cluster();
   cl.barrier_arrive();                        // every block of the cluster runs before one writes into another
   const int blocks = (int)cl.num_blocks(), rank = (int)cl.block_rank(), tid = threadIdx.x;
@@ -196,6 +199,8 @@ template <int PASSES>
 __global__ void __launch_bounds__(NT, PASSES <= 10 ? 2 : 1) k_verify(VerifyArgs a) {
   __shared__ unsigned long long sums[PASSES * NW], totals[FEW];
   __shared__ int n_acc, n_all;
+  await_stream();
+  allow_next();
   cg::cluster_group cl = cg::this_cluster();
   cl.barrier_arrive();
   const int blocks = (int)cl.num_blocks(), rank = (int)cl.block_rank(), tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -374,21 +379,11 @@ cudaError_t with_passes(int vocab, int cluster, F&& f) {
 
 template <class... A>
 cudaError_t launch_rows(void (*k)(A...), long long rows, int cluster, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * cluster));
-  cfg.blockDim = dim3(NT);
-  cfg.stream = st;
   if (cluster > MANY) {
     const cudaError_t e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = cluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, args...);
+  return launch_kernel(k, dim3((unsigned)(rows * cluster)), NT, 0, cluster, st, args...);
 }
 
 bool aligned(const void* p, size_t n) { return p && (uintptr_t)p % n == 0; }

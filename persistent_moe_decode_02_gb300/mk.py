@@ -499,27 +499,23 @@ class Server:
             pass
 
 
-def _here(name: str, t: torch.Tensor, dtypes, shape=None) -> int:
+def _here(name: str, t: torch.Tensor, dtype, shape, dev: int) -> int:
     """The address of a contiguous tensor of the current device, checked."""
-    if t.get_device() != _device():
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    if t.get_device() != dev:
         raise ValueError(f"{name}: a tensor of the current CUDA device is wanted, got {t.device}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: dtype {t.dtype}, wanted one of {dtypes}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name}: {t.dtype} of {tuple(t.shape)}{'' if t.is_contiguous() else ', not contiguous'}; wanted "
+                     f"contiguous {dtype} of {tuple(shape)}")
 
 
 # These calls take microseconds, so the current device and stream are asked for without the objects around them.
-_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+def _device() -> int:
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else torch.cuda.current_device()
 
 
-def _on(stream) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(_device())
+def _on(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _chunk_dims(D) -> MkModelDims:
@@ -527,8 +523,7 @@ def _chunk_dims(D) -> MkModelDims:
                        rope_theta=D.rope_theta)
 
 
-_BF16, _U8, _ROWS = (torch.bfloat16,), (torch.uint8,), (torch.bfloat16, torch.float32)
-_F32, _I32 = (torch.float32,), (torch.int32,)
+_BF16, _U8, _F32, _I32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
 
 
 class Chunk:
@@ -556,7 +551,7 @@ class Chunk:
             raise MkError("mk_chunk_create", rc)
         self.h = h
         self._lens(seq_lens, new_lens)
-        self._pool = (self.num_pages, self.nkv, 2, self.d + (kv_type == "e4m3"), D.page_size)
+        self._pool = torch.Size((self.num_pages, self.nkv, 2, self.d + (kv_type == "e4m3"), D.page_size))
         self._pool_type = _U8 if kv_type == "e4m3" else _BF16
 
     def _batch(self, seq_lens, new_lens, page_table, max_pages):
@@ -570,7 +565,8 @@ class Chunk:
     def _lens(self, seq_lens, new_lens):
         self.rows = int(sum(int(x) for x in new_lens))
         self.tokens = self.rows + int(sum(int(x) for x in seq_lens))
-        self._q = (self.rows, self.nq, self.d)
+        self._q = torch.Size((self.rows, self.nq, self.d))
+        self._kv = torch.Size((self.tokens, self.nkv, 2, self.d))
 
     def update(self, seq_lens: Sequence[int], new_lens: Sequence[int], page_table, max_pages: int, stream=None) -> None:
         """Another batch for this chunk (uploaded on the stream)."""
@@ -590,33 +586,33 @@ class Chunk:
             n *= shape[i]
         if not fits or n != width:
             raise ValueError(f"qkv: shape {tuple(shape)}, wanted {self.rows} contiguous rows of {width}")
-        if qkv.get_device() != _device() or qkv.dtype not in _ROWS:
+        dev = _device()
+        if qkv.get_device() != dev or qkv.dtype not in (_BF16, _F32):
             raise ValueError(f"qkv: a bf16 or float32 tensor of the current CUDA device is wanted, got {qkv.dtype} on "
                              f"{qkv.device}")
         if (q is None) != (self.nq == 0):
             raise ValueError("q: wanted exactly when the chunk has query heads")
         stride = steps[0] if self.rows > 1 else width
-        rc = lib().mk_chunk_append(self.h, qkv.data_ptr(), int(qkv.dtype == torch.float32), stride,
-                                   _here("kv_pool", kv_pool, self._pool_type, self._pool),
-                                   None if q is None else _here("q", q, _BF16, self._q),
-                                   _on(stream))
+        rc = lib().mk_chunk_append(self.h, qkv.data_ptr(), int(qkv.dtype is _F32), stride,
+                                   _here("kv_pool", kv_pool, self._pool_type, self._pool, dev),
+                                   None if q is None else _here("q", q, _BF16, self._q, dev), _on(stream, dev))
         if rc != MK_OK:
             raise MkError("mk_chunk_append", rc)
 
     def attend(self, q: torch.Tensor, kv_pool: torch.Tensor, out: torch.Tensor, stream=None) -> None:
         """Causal attention of the rows q [rows, nq, head_dim] over the pages; out like q (bf16)."""
-        rc = lib().mk_chunk_attend(self.h, _here("q", q, _BF16, self._q),
-                                   _here("kv_pool", kv_pool, self._pool_type, self._pool),
-                                   _here("out", out, _BF16, self._q),
-                                   _on(stream))
+        dev = _device()
+        rc = lib().mk_chunk_attend(self.h, _here("q", q, _BF16, self._q, dev),
+                                   _here("kv_pool", kv_pool, self._pool_type, self._pool, dev),
+                                   _here("out", out, _BF16, self._q, dev), _on(stream, dev))
         if rc != MK_OK:
             raise MkError("mk_chunk_attend", rc)
 
     def read(self, kv_pool: torch.Tensor, out: torch.Tensor, stream=None) -> None:
         """Every cached and new position of every request, out [tokens, nkv, 2, head_dim] (bf16)."""
-        rc = lib().mk_chunk_read(self.h, _here("kv_pool", kv_pool, self._pool_type, self._pool),
-                                 _here("out", out, _BF16, (self.tokens, self.nkv, 2, self.d)),
-                                 _on(stream))
+        dev = _device()
+        rc = lib().mk_chunk_read(self.h, _here("kv_pool", kv_pool, self._pool_type, self._pool, dev),
+                                 _here("out", out, _BF16, self._kv, dev), _on(stream, dev))
         if rc != MK_OK:
             raise MkError("mk_chunk_read", rc)
 
@@ -657,13 +653,13 @@ def inspect_chunk(D, seq_lens: Sequence[int], new_lens: Sequence[int], num_ctas:
 def probs(logits: torch.Tensor, temperature: float, out: torch.Tensor, stream=None) -> None:
     """softmax(logits / temperature) of float32 rows [rows, vocab] (rows may lie apart) into out [rows, vocab];
     temperature 0: 1 at the largest logit."""
-    if logits.dim() != 2 or (logits.numel() and logits.stride(1) != 1) or logits.dtype != torch.float32 or (
-            logits.get_device() != _device()):
+    dev = _device()
+    if logits.dim() != 2 or logits.dtype is not _F32 or logits.get_device() != dev or (
+            logits.numel() and logits.stride(1) != 1 and logits.shape[1] != 1):
         raise ValueError("logits: float32 rows [rows, vocab] of the current CUDA device are wanted")
     rows, vocab = logits.shape
     rc = lib().mk_probs(logits.data_ptr() if rows else None, rows, vocab, logits.stride(0) if rows > 1 else vocab,
-                        float(temperature), _here("out", out, _F32, (rows, vocab)) if rows else None,
-                        _on(stream))
+                        float(temperature), _here("out", out, _F32, logits.shape, dev) if rows else None, _on(stream, dev))
     if rc != MK_OK:
         raise MkError("mk_probs", rc)
 
@@ -676,12 +672,13 @@ def verify(target: torch.Tensor, draft: Optional[torch.Tensor], drafts: torch.Te
     if target.dim() != 3:
         raise ValueError("target: float32 [batch, k + 1, vocab] is wanted")
     b, k1, v = target.shape
-    rc = lib().mk_verify(b, k1 - 1, v, _here("target", target, _F32),
-                         None if draft is None else _here("draft", draft, _F32, (b, k1 - 1, v)),
-                         _here("drafts", drafts, _I32, (b, k1 - 1)),
-                         None if n_draft is None else _here("n_draft", n_draft, _I32, (b,)),
-                         _here("u", u, _F32, (b, k1 - 1)), _here("r", r, _F32, (b,)),
-                         _here("tokens", tokens, _I32, (b, k1)), _here("accepted", accepted, _I32, (b,)),
-                         _on(stream))
+    dev, each, row = _device(), (b, k1 - 1), (b,)
+    rc = lib().mk_verify(b, k1 - 1, v, _here("target", target, _F32, target.shape, dev),
+                         None if draft is None else _here("draft", draft, _F32, (b, k1 - 1, v), dev),
+                         _here("drafts", drafts, _I32, each, dev),
+                         None if n_draft is None else _here("n_draft", n_draft, _I32, row, dev),
+                         _here("u", u, _F32, each, dev), _here("r", r, _F32, row, dev),
+                         _here("tokens", tokens, _I32, (b, k1), dev), _here("accepted", accepted, _I32, row, dev),
+                         _on(stream, dev))
     if rc != MK_OK:
         raise MkError("mk_verify", rc)
