@@ -15,7 +15,7 @@ __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.laun
 // Launches a kernel that begins with await_stream() while the kernel before it
 // still runs, so that a chain of short ones does not pay each one's launch
 // (one token's attention over 8K cached tokens and its join, call after call:
-// 12.3 us, 10.0 so).  Returns the call's own error, none that was left before.
+// 12.3 us, 9.3 so).  Returns the call's own error, none that was left before.
 template <class... A, class... B>
 cudaError_t launch_kernel(void (*k)(A...), dim3 grid, dim3 block, size_t smem, int cluster, cudaStream_t st, B&&... args) {
   cudaLaunchConfig_t cfg = {};

@@ -4,7 +4,7 @@
 // A row of the vocabulary is one cluster's work: each block holds its segment
 // of the row in registers, so the row is read once whatever is done with
 // it, and the blocks exchange their totals through distributed shared memory.
-// 160 rows of 151936 take 42.6 us (4.6 TB/s, 0.67 of a copy's rate: the 1280
+// 160 rows of 151936 take 39.9 us (4.9 TB/s, 0.72 of a copy's rate: the 1280
 // blocks are 4.2 rounds of what fits the SMs at once, two on each); one row 4.5
 // us.  A verification reads the row or two that its draw needs, not the
 // others: 32 of them with five drafts take 12.4 us, one 6.7 us, a chain of five
@@ -31,6 +31,7 @@ constexpr int MANY = 8, FEW = 16;             // blocks of a row's cluster at mo
 constexpr int STEP = NT * 4;                  // elements of one pass of a block: 4 consecutive ones a thread
 constexpr int MAX_PASSES = 24;                // kept in registers: 96 of a thread
 constexpr int MAX_VOCAB = MANY * MAX_PASSES * STEP;   // 393216
+constexpr int AHEAD = 2 * 152;                // blocks that run at once (a multiple of every cluster's size)
 constexpr unsigned FULL = 0xffffffffu;
 
 // 4 elements of a row, `none` past its end.  `wide`: the address is 16-byte aligned.
@@ -84,6 +85,11 @@ __global__ void __launch_bounds__(NT) k_probs(const float* logits, int vocab, lo
     const int i = p * STEP + tid * 4;
     x[p] = load4(src + i, s.n - i, wide_in, -INFINITY);
   }
+  // The segment that a block of the next round will read is on its way to L2
+  // while this one computes and writes.
+  const unsigned ahead = blockIdx.x + AHEAD;
+  if (wide_in && ahead < gridDim.x && tid == 0 && s.n >= 4)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(logits + (ahead / blocks) * row_stride + s.begin), "r"(s.n / 4 * 16));
   float m = -INFINITY;                        // a NaN or +infinity in the row makes this one
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) m = max_nan(m, max_nan(max_nan(x[p].x, x[p].y), max_nan(x[p].z, x[p].w)));
@@ -358,7 +364,7 @@ int fail_cuda(const char* what, cudaError_t e) {
 // of probabilities and 6.7 of verification then instead of 5.4 and 9.1, 9 rows
 // 5.7 and 8.0 instead of 5.6 and 9.6.  With more rows the blocks' number costs
 // more than their shorter chains give (16 verifications: 12.2 us instead of
-// 10.9; 160 rows of probabilities: 54.6 us instead of 42.6).
+// 10.9; 160 rows of probabilities: 54.6 us instead of 42.6 at the time).
 int cluster_of(int vocab, long long rows) {
   const int most = rows * FEW <= 152 ? FEW : MANY;
   int c = 1;
