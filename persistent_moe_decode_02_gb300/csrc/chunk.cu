@@ -138,11 +138,13 @@ int set_pages(int num_pages, const int* page_table, int max_pages, Built& b) {
 // least work; and the blocks' tiles in one row, cut into runs that are as even
 // as whole tiles allow, where a block that a cut goes through is joined
 // afterwards.  A task costs SETUP beside its tiles (its queries, its first
-// latencies and its epilogue), a join JOIN.
+// latencies and its epilogue), a join JOIN.  (SETUP 2, 4, 6, 8, 10: 161, 129,
+// 120, 117 and 122 us for requests of 1500, 900 and 333 new rows behind 0, 5000
+// and 8192 cached ones; batches of one kind hardly move.)
 struct Block {
   int req, kvh, tok0, ntok, tiles;
 };
-constexpr int SETUP = 2, JOIN = 5;
+constexpr int SETUP = 8, JOIN = 5;
 
 // Gives every CTA tiles up to `limit` (its tasks' SETUP included) in the row's
 // order; emits (block, first tile, tiles, CTA).  False if the CTAs do not do.
