@@ -47,7 +47,6 @@
 #include <math.h>
 
 #include "chunk.h"
-#include "launch.cuh"
 #include "mk.h"
 #include "ptx.cuh"
 
@@ -396,7 +395,19 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
   const int t0 = __ldg(a.c.cta_start + blockIdx.x), t1 = __ldg(a.c.cta_start + blockIdx.x + 1);
   int* status = a.c.status;
   if (stale(a.c)) return;
-  const bool two = __ldg(&a.c.tasks[t0].two);
+  // the first task, and the copying warp's first pages, arrive during the setup
+  AttnTask t = a.c.tasks[t0];
+  const bool two = t.two;
+  constexpr int GROUP = 32 / TILE_PAGES;         // tiles whose page numbers a warp's lanes hold
+  auto pages = [&](const AttnTask& t, int j) {
+    const int page = (t.tile0 + j) * TILE_PAGES + lane;
+    return page < (t.total + PAGE - 1) / PAGE ? __ldg(a.c.pt + t.pt + page) : -1;
+  };
+  int ids = -1, more = -1;
+  if (warp == W_COPY) {
+    ids = pages(t, 0);
+    more = pages(t, GROUP);
+  }
   if (tid == 0) {
     for (int v = 0; v < 2; ++v) {
       for (int i = 0; i < C::NST; ++i) {
@@ -443,7 +454,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
     };
     int g = 0, all = 0;                          // key tiles so far: of this query tile, of the block
     uint32_t tasks = 0;                          // of this query tile
-    AttnTask t = a.c.tasks[t0];
     if (has(t)) queries(t);
     for (int i = t0; i < t1; ++i) {
       const AttnTask next = a.c.tasks[min(i + 1, t1 - 1)];
@@ -499,21 +509,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::THREADS, 1)
       ++at[v];
       return true;
     };
-    for (int i = t0; i < t1 && ok; ++i) {
-      const AttnTask t = a.c.tasks[i];
-      // page numbers of 8 tiles, a lane each, and of the next 8
-      constexpr int GROUP = 32 / TILE_PAGES;
-      const int npages = (t.total + PAGE - 1) / PAGE;
-      auto pages = [&](int j) {
-        const int page = (t.tile0 + j) * TILE_PAGES + lane;
-        return page < npages ? __ldg(a.c.pt + t.pt + page) : -1;
-      };
-      int ids = pages(0), more = pages(GROUP);
+    for (int i = t0; i < t1 && ok; ++i) {        // page numbers: those of 8 tiles, and of the next 8
+      if (i > t0) {
+        t = a.c.tasks[i];
+        ids = pages(t, 0);
+        more = pages(t, GROUP);
+      }
       if (!E4M3) ok = copy(t, 0, 0, ids);        // in the order of use: K goes one tile ahead
       for (int j = 0; j < t.ntile && ok; ++j) {
         if (j > 0 && j % GROUP == 0) {
           ids = more;
-          more = pages(j + GROUP);
+          more = pages(t, j + GROUP);
         }
         if (E4M3) ok = copy(t, 0, j, ids);
         else ok = (j + 1 == t.ntile || copy(t, 0, j + 1, (j + 1) % GROUP ? ids : more)) && copy(t, 1, j, ids);
@@ -612,13 +618,14 @@ template <int D, int W>
 __global__ void __launch_bounds__(128) k_join(ChunkView c, __nv_bfloat16* out) {
   constexpr int E = D / 32;
   __shared__ float part[W][D + 1];
-  await_stream();
-  allow_next();
   const JoinTask t = c.joins[blockIdx.x];
+  const ChunkReq r = c.reqs[t.req];
   if (stale(c)) return;
+  allow_next();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rows = t.ntok * c.G, row = W == 4 ? blockIdx.y : blockIdx.y * 4 + warp, w = W == 4 ? warp : 0;
   if (row >= rows) return;                       // the whole block where warps share a row
+  await_stream();
   const float2* ml = c.part_ml + (size_t)t.part0 + row;
   const float* po = c.part_o + ((size_t)t.part0 + row) * D + lane * E;
   float m = -INFINITY;
@@ -649,7 +656,6 @@ __global__ void __launch_bounds__(128) k_join(ChunkView c, __nv_bfloat16* out) {
       acc[e] = (part[0][lane * E + e] + part[1][lane * E + e]) + (part[2][lane * E + e] + part[3][lane * E + e]);
   }
   const float inv = 1.f / l;
-  const ChunkReq r = c.reqs[t.req];
   uint32_t* o = reinterpret_cast<uint32_t*>(
       out + ((size_t)(r.row0 + t.tok0 + row / c.G) * c.nq + (size_t)t.kvh * c.G + row % c.G) * D + lane * E);
 #pragma unroll

@@ -15,7 +15,6 @@
 #include <math.h>
 
 #include "chunk.h"
-#include "launch.cuh"
 
 namespace mk {
 namespace {
@@ -115,17 +114,17 @@ __global__ void __launch_bounds__(NT) k_append(ChunkView c, const T* qkv, long l
   constexpr int HS = NT / (PAGE * C);            // heads at a time
   __shared__ float kv[2][PAGE][LD];
   __shared__ int exps[2][PAGE];
-  await_stream();
-  allow_next();
-  const ChunkReq r = c.reqs[blockIdx.z];
+  const ChunkReq r = c.reqs[blockIdx.z];         // the chunk's tables: no kernel writes them
   if (stale(c)) return;
   const int g = blockIdx.y, G = c.G, tid = threadIdx.x;
   const int j = r.seq / PAGE + blockIdx.x;       // page of the request
   const int p0 = max(j * PAGE, r.seq), p1 = min(j * PAGE + PAGE, r.seq + r.nnew);
+  allow_next();
   if (p0 >= p1) return;
   const int n = p1 - p0, slot0 = p0 - j * PAGE, row = r.row0 + p0 - r.seq;
   const int i = tid % C * 8, t = tid / C % PAGE, hs = tid / (C * PAGE);
   const size_t block = ((size_t)__ldg(c.pt + r.pt + j) * c.nkv + g) * 2;   // the page's K block, in blocks
+  await_stream();
   if (t < n) {
     const T* src = qkv + (size_t)(row + t) * row_stride + (size_t)g * (G + 2) * D + i;
     Turn turn;
@@ -228,14 +227,14 @@ template <int D, bool E4M3>
 __global__ void __launch_bounds__(NT) k_read(ChunkView c, const void* pool, __nv_bfloat16* out) {
   constexpr int LD = D + 4;                      // words of a token's row: 16-byte rows for the way out
   __shared__ alignas(16) uint32_t buf[PAGE][LD];
-  await_stream();
-  allow_next();
-  const ChunkReq r = c.reqs[blockIdx.z];
+  const ChunkReq r = c.reqs[blockIdx.z];         // the chunk's tables: no kernel writes them
   if (stale(c)) return;
   const int g = blockIdx.y, j = blockIdx.x, tid = threadIdx.x;
   const int n = min(PAGE, r.seq + r.nnew - j * PAGE);
+  allow_next();
   if (n <= 0) return;
   const size_t block = ((size_t)__ldg(c.pt + r.pt + j) * c.nkv + g) * 2;
+  await_stream();
   for (int x = tid; x < D; x += NT) {            // dimensions 2x and 2x + 1 of K, then V
     if constexpr (E4M3) {
       const uint8_t* b = reinterpret_cast<const uint8_t*>(pool) + (block + x / (D / 2)) * (D + 1) * PAGE;

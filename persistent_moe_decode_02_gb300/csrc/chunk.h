@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "launch.cuh"
+
 namespace mk {
 
 constexpr int PAGE = 16;         // tokens of a page
@@ -60,20 +62,19 @@ struct ChunkView {
   int gen;                       // the generation that this view was made for
 };
 
-#if defined(__CUDACC__)
-// A graph may replay a call whose chunk was updated since: the view's counts
-// then no longer fit the tables, and the kernel leaves everything as it is.
-__device__ __forceinline__ bool stale(const ChunkView& c) {
-  if (__ldg(c.status + 1) == c.gen) return false;   // (nothing writes it while a kernel runs)
-  if (blockIdx.x + blockIdx.y + blockIdx.z + threadIdx.x == 0) atomicCAS(c.status, 0, -1);   // MK_ERR_INVALID
-  return true;
-}
-#endif
-
 cudaError_t launch_chunk_rope(const ChunkView& c, double theta, float2* tab, int max_new, cudaStream_t st);
 cudaError_t launch_append(const ChunkView& c, bool e4m3, bool f32, const void* qkv, long long row_stride, void* pool,
                           void* q, int max_new_pages, cudaStream_t st);
 cudaError_t launch_read(const ChunkView& c, bool e4m3, const void* pool, void* out, int max_pages, cudaStream_t st);
 cudaError_t launch_attend(const ChunkView& c, bool e4m3, const void* q, const void* pool, void* out, cudaStream_t st);
+
+// A graph may replay a call whose chunk was updated since: the view's counts
+// then no longer fit the tables, and the kernel leaves everything as it is.
+__device__ __forceinline__ bool stale(const ChunkView& c) {
+  if (__ldg(c.status + 1) == c.gen) return false;   // (nothing writes it while a kernel runs)
+  await_stream();                // a kernel does not end before the one before it
+  if (blockIdx.x + blockIdx.y + blockIdx.z + threadIdx.x == 0) atomicCAS(c.status, 0, -1);   // MK_ERR_INVALID
+  return true;
+}
 
 }  // namespace mk
