@@ -18,11 +18,11 @@
 // What bounds it.  Two query tiles take about 1440 cycles a key tile, of which
 // the products need 1280 (Q K^T with 64 keys reads Q from shared memory for
 // half the work, 48 cycles an instruction instead of 32): 2048 rows of 32 heads
-// over 30000 cached tokens take 627 us, 1.66 PFLOP/s, 0.88 of a large library
+// over 30000 cached tokens take 630 us, 1.65 PFLOP/s, 0.87 of a large library
 // product.  One query tile (single tokens, drafts) is bound by device memory:
-// one token over 262144 takes 88 us, 6.1 TB/s, 0.90 of a copy's rate.  What a
+// one token over 262144 takes 83 us, 6.4 TB/s, 0.95 of a copy's rate.  What a
 // task adds (its queries, its epilogue: 4 to 5 us) weighs on short prompts:
-// 4095 rows from nothing take 100 us.
+// 4095 rows from nothing take 100 us, 0.73 of the products' floor.
 //
 // How the pages meet the matrix instructions.  A page's K or V block is
 // [d][16 slots] bf16, 32 bytes a dimension: with a 32-byte swizzle that is
@@ -36,8 +36,8 @@
 // 8-bit blocks (codes, then the slots' scales) are copied as they are and
 // turned into that layout by warps of their own: a code times a power of two is
 // a bf16 number, so nothing is rounded (outside bf16's normal range).  The
-// conversion bounds them: 37 rows over 109594 tokens take 46 us (the same over
-// bf16 pages, twice the bytes, 44), 1024 rows over 30000 cached ones 413 us.
+// conversion bounds them: 37 rows over 109594 tokens take 43 us (the same over
+// bf16 pages, twice the bytes, 42), 1024 rows over 30000 cached ones 434 us.
 // (K's codes fed to 8-bit products as they lie, with Q in two parts and the
 // scales on the scores, left V alone to convert, and took 75 and 546 us with
 // 57 and 580 at the time: the softmax then had the scales' work.)
