@@ -128,6 +128,12 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* ctl, i
   const bool ok = mbar_try(bar, parity) || wait_slow(bar, parity, ctl, status);
   return __all_sync(FULL, ok);
 }
+// Two of them at once.
+__device__ __forceinline__ bool wait_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, Ctl* ctl, int* status) {
+  const bool ra = mbar_try(a, pa), rb = mbar_try(b, pb);
+  const bool ok = (ra || wait_slow(a, pa, ctl, status)) && (rb || wait_slow(b, pb, ctl, status));
+  return __all_sync(FULL, ok);
+}
 
 // Softmax of one query tile over a task's key tiles; a thread has a row.  g
 // counts the query tile's key tiles over the tasks before, v_last is the page of
@@ -361,24 +367,20 @@ __device__ __forceinline__ void convert_tiles(const Args& a, int t0, int t1, uin
   using C = Cfg<D, true>;
   const int lane = threadIdx.x % 32;
   int ri = 0, si = 0, r_ph = 0, s_ph = 0;
-  bool first = true;                             // the ring's first round: nothing to wait for
   for (int i = t0; i < t1; ++i) {
     const int tile0 = __ldg(&a.c.tasks[i].tile0), ntile = __ldg(&a.c.tasks[i].ntile), total = __ldg(&a.c.tasks[i].total);
     for (int j = 0; j < ntile; ++j) {
-      if (!wait(&ctl->raw_full[ri], r_ph, ctl, a.c.status)) return;
-      if (!first && !wait(&ctl->empty[v][si], s_ph ^ 1, ctl, a.c.status)) return;
+      // (a fresh barrier has no phase behind it, and says that one of parity 1 is over)
+      if (!wait_both(&ctl->raw_full[ri], r_ph, &ctl->empty[v][si], s_ph ^ 1, ctl, a.c.status)) return;
       const int left = total - (tile0 + j) * KV_TILE;   // the request's keys from the tile on
       for (int p = p0; p < p1; ++p)
         convert_page<D>(smem + C::raw(ri, p, v), smem + C::kv(v, si) + p * C::PAGE_BYTES,
                         min(PAGE, max(0, left - p * PAGE)), lane);
       fence_async();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&ctl->full[v][si]);
-        mbar_arrive(&ctl->raw_empty[ri]);
-      }
+      if (lane < 2) mbar_arrive(lane ? &ctl->raw_empty[ri] : &ctl->full[v][si]);
       if (++ri == C::NRAW) { ri = 0; r_ph ^= 1; }
-      if (++si == C::NST) { si = 0; s_ph ^= 1; first = false; }
+      if (++si == C::NST) { si = 0; s_ph ^= 1; }
     }
   }
 }
