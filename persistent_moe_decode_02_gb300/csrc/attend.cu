@@ -692,7 +692,7 @@ cudaError_t launch(const ChunkView& c, const void* q, const void* pool, void* ou
   Args a = {c, (const __nv_bfloat16*)q, (const uint8_t*)pool, (__nv_bfloat16*)out, (uintptr_t)out % 32 == 0, 0};
   CUtensorMap map = {};
   cudaError_t e = E4M3 ? cudaSuccess : pool_map(c, pool, &map, &a.oob);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_attend<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e == cudaSuccess) e = allow((const void*)k_attend<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   e = launch_kernel(k_attend<D, E4M3>, c.ctas, C::THREADS, C::SMEM, 1, st, a, map);
   if (e != cudaSuccess || !c.njoins) return e;

@@ -32,6 +32,7 @@ int fail(int code, const char* msg) {
 
 int fail_cuda(const char* what, cudaError_t e) {
   cudaGetLastError();   // reported here: not to the caller's next question
+  mk::allowed = {};
   char buf[224];
   snprintf(buf, sizeof(buf), "%s: %s (%d)", what, cudaGetErrorString(e), (int)e);
   return fail(MK_ERR_CUDA, buf);

@@ -34,4 +34,27 @@ cudaError_t launch_kernel(void (*k)(A...), dim3 grid, dim3 block, size_t smem, i
   return cudaLaunchKernelEx(&cfg, k, static_cast<A>(args)...);
 }
 
+// Kernels' attributes that this thread of the host has asked for already (asking
+// takes as long as a fifth of a launch).  Forgotten after any error, so that a
+// device whose context was made anew is asked again.
+struct Allowed {
+  struct Asked {
+    const void* kernel;
+    int dev, what;
+  } asked[16];
+  int n;
+};
+inline thread_local Allowed allowed = {};
+
+inline cudaError_t allow(const void* kernel, cudaFuncAttribute what, int value) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  for (const Allowed::Asked& a : allowed.asked)
+    if (a.kernel == kernel && a.dev == dev && a.what == (int)what) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, what, value);
+  if (e == cudaSuccess) allowed.asked[allowed.n++ % 16] = {kernel, dev, (int)what};
+  return e;
+}
+
 }  // namespace mk

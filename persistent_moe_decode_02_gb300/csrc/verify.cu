@@ -360,6 +360,7 @@ int fail(int code, const char* msg) {
 
 int fail_cuda(const char* what, cudaError_t e) {
   cudaGetLastError();   // reported here: not to the caller's next question
+  allowed = {};
   char buf[224];
   snprintf(buf, sizeof(buf), "%s: %s (%d)", what, cudaGetErrorString(e), (int)e);
   return fail(MK_ERR_CUDA, buf);
@@ -393,7 +394,7 @@ cudaError_t with_passes(int vocab, int cluster, F&& f) {
 template <class... A>
 cudaError_t launch_rows(void (*k)(A...), long long rows, int cluster, cudaStream_t st, A... args) {
   if (cluster > MANY) {
-    const cudaError_t e = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e = allow((const void*)k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
   }
   return launch_kernel(k, dim3((unsigned)(rows * cluster)), NT, 0, cluster, st, args...);
