@@ -416,15 +416,15 @@ int mk_probs(const float* logits, int rows, int vocab, long long row_stride, flo
   if (row_stride < vocab || row_stride > (1ll << 34)) return fail(MK_ERR_INVALID, "mk_probs: row_stride");
   if (!(temperature >= 0.f) || !isfinite(temperature) || (temperature > 0.f && !isfinite(1.f / temperature)))
     return fail(MK_ERR_INVALID, "mk_probs: temperature must be 0 (greedy) or a finite value whose inverse is finite");
+  if (rows == 0) return MK_OK;
   if (!aligned(logits, 4) || !aligned(probs, 4)) return fail(MK_ERR_INVALID, "mk_probs: a buffer is NULL or not aligned to its type");
   {
     const char *l0 = (const char*)logits, *p0 = (const char*)probs;
-    const char* l1 = l0 + 4 * ((size_t)(rows ? rows - 1 : 0) * row_stride + vocab);
+    const char* l1 = l0 + 4 * ((size_t)(rows - 1) * row_stride + vocab);
     const char* p1 = p0 + 4 * (size_t)rows * vocab;
-    if (rows && l0 < p1 && p0 < l1 && !(l0 == p0 && row_stride == vocab))
+    if (l0 < p1 && p0 < l1 && !(l0 == p0 && row_stride == vocab))
       return fail(MK_ERR_INVALID, "mk_probs: probs overlaps the logits in other places than their own");
   }
-  if (rows == 0) return MK_OK;
   const int c = cluster_of(vocab, rows);
   const float scale = temperature > 0.f ? fminf(1.4426950408889634f / temperature, 3.4e38f) : 0.f;   // log2(e) / T
   const int win = aligned(logits, 16) && row_stride % 4 == 0, wout = aligned(probs, 16) && vocab % 4 == 0;
@@ -440,11 +440,11 @@ int mk_verify(int batch, int max_draft, int vocab, const float* target, const fl
   if (batch < 0 || max_draft < 0 || vocab < 1) return fail(MK_ERR_INVALID, "mk_verify: batch, max_draft or vocab");
   if (vocab > MAX_VOCAB) return fail(MK_ERR_UNSUPPORTED, "mk_verify: vocab above 393216");
   if (batch > (1 << 20) || max_draft > (1 << 20)) return fail(MK_ERR_UNSUPPORTED, "mk_verify: batch or max_draft above 2^20");
+  if (batch == 0) return MK_OK;
   if (!aligned(target, 4) || !aligned(r, 4) || !aligned(tokens, 4) || !aligned(accepted, 4) ||
       (max_draft && (!aligned(drafts, 4) || !aligned(u, 4))) || (draft && !aligned(draft, 4)) ||
       (n_draft && !aligned(n_draft, 4)))
     return fail(MK_ERR_INVALID, "mk_verify: a buffer is NULL or not aligned to its type");
-  if (batch == 0) return MK_OK;
   const int c = cluster_of(vocab, batch);
   VerifyArgs a = {max_draft, vocab, 0, target, draft, drafts, n_draft, u, r, tokens, accepted};
   a.wide = aligned(target, 16) && (!draft || aligned(draft, 16)) && vocab % 4 == 0;

@@ -623,3 +623,48 @@ def test_drafted_tokens_through_plan_probs_and_verify(mk):
         got += new
     plan.close()
     assert got[:steps + 1] == plain
+
+
+def test_beside_decode_steps_on_another_stream(mk):
+    # a chunk's calls on one stream while decode steps run on another: the results of either alone
+    D, seed = synth.TINY, 3
+    w, width, pages, steps = DeviceModel(D, seed).weights(), 3, 6, 12
+    tokens = []
+    C, batch, chunk = make(mk, "g8", "e4m3", ([4000, 9000, 100], [5, 1, 200]))
+    pool = cu.make_pool("e4m3", batch.num_pages, 4, 128, 3).cuda()
+    q = cu.normal((batch.rows, 32, 128), 3).bfloat16().cuda()
+    alone = torch.empty_like(q)
+    chunk.attend(q, pool, alone)
+    assert chunk.sync() == mk.MK_OK
+    for beside in (False, True):
+        pools = [torch.zeros(pages, D.n_kv_heads, 2, D.head_dim, 16, dtype=torch.bfloat16, device="cuda")
+                 for _ in range(D.n_layers)]
+        plan = mk.Plan(D, w, pools, [0], [4, 1, 2], width)
+        out = torch.zeros(steps + 1, 1, dtype=torch.int32, device="cuda")
+        out[0] = 7
+        outs = [torch.empty_like(q) for _ in range(steps)]
+        torch.cuda.synchronize()
+        one, two = torch.cuda.Stream(), torch.cuda.Stream()
+        for i in range(steps):
+            assert plan.step(out[i], out[i + 1], stream=one) == mk.MK_OK
+            if beside:
+                chunk.attend(q, pool, outs[i], stream=two)
+        assert plan.sync(one) == mk.MK_OK and chunk.sync(two) == mk.MK_OK
+        tokens.append(out.tolist())
+        assert not beside or all(torch.equal(alone, o) for o in outs)
+        plan.close()
+    assert tokens[0] == tokens[1]
+
+
+def test_nothing_new(mk):
+    # no rows: the calls do nothing, and what is cached can be read
+    D, batch, chunk = make(mk, "g8", "bf16", ([20, 0], [0, 0]))
+    pool = cu.make_pool("bf16", batch.num_pages, 4, 128, 3)
+    none = torch.empty(0, 32, 128, dtype=torch.bfloat16, device="cuda")
+    chunk.append(torch.empty(0, 4, 10, 128, device="cuda"), pool.cuda(), none)
+    chunk.attend(none, pool.cuda(), none)
+    out = torch.empty(20, 4, 2, 128, dtype=torch.bfloat16, device="cuda")
+    chunk.read(pool.cuda(), out)
+    assert chunk.sync() == mk.MK_OK
+    assert torch.equal(out.cpu(), cu.rows_of(pool, "bf16", batch, 0).bfloat16())
+    mk.probs(torch.empty(0, 50, device="cuda"), 1.0, torch.empty(0, 50, device="cuda"))
