@@ -555,8 +555,14 @@ class Chunk:
         self._pool_type = _U8 if kv_type == "e4m3" else _BF16
 
     def _batch(self, seq_lens, new_lens, page_table, max_pages):
-        sl, nl, pt = (np.ascontiguousarray(np.asarray(x), dtype=np.int32) for x in (seq_lens, new_lens, page_table))
-        if len(nl) != len(sl) or pt.size != len(sl) * max_pages:
+        def ints(x):
+            x = np.asarray(x)
+            if x.size and (x.dtype.kind not in "iu" or x.min() < -2 ** 31 or x.max() >= 2 ** 31):
+                raise ValueError("seq_lens, new_lens and page_table hold 32-bit integers")
+            return np.ascontiguousarray(x, dtype=np.int32)
+
+        sl, nl, pt = ints(seq_lens), ints(new_lens), ints(page_table)
+        if sl.ndim != 1 or nl.shape != sl.shape or pt.size != len(sl) * max_pages:
             raise ValueError("seq_lens, new_lens and page_table do not describe one batch")
         p_int = ctypes.POINTER(ctypes.c_int)
         self._host = (sl, nl, pt)    # outlive the call

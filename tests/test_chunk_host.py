@@ -47,6 +47,9 @@ def test_refused_batches(mk):
         mk.Chunk(cu.dims(8, 2, 64), "fp8", 8, [0], [1], [0], 1)
     with pytest.raises(ValueError):
         mk.Chunk(cu.dims(8, 2, 64), "bf16", 8, [0, 1], [1], [0], 1)
+    for cached, new, table in (([2 ** 32 + 5], [1], [0]), ([0], [1.5], [0]), ([0], [1], [2 ** 31]), ([[0]], [[1]], [0])):
+        with pytest.raises(ValueError):
+            mk.Chunk(cu.dims(8, 2, 64), "bf16", 8, cached, new, table, 1)
 
 
 def test_refused_null_and_numbers(mk):
