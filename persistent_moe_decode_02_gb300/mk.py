@@ -647,6 +647,8 @@ def inspect_chunk(D, seq_lens: Sequence[int], new_lens: Sequence[int], num_ctas:
     """Host-only attention task list of a chunk: int tensor [n, 8] (request, KV head, first row, rows, first
     64-key tile, tiles, first split row or -1, CTA)."""
     dims, n = _chunk_dims(D), len(seq_lens)
+    if len(new_lens) != n:
+        raise ValueError("seq_lens and new_lens do not describe one batch")
     args = (ctypes.byref(dims), n, _int_array(seq_lens), _int_array(new_lens), num_ctas)
     count = lib().mk_chunk_inspect(*args, None, 0)
     if count < 0:

@@ -137,6 +137,8 @@ def test_inspect_refuses(mk):
         assert e.value.code == code
     with pytest.raises(mk.MkError):
         mk.inspect_chunk(cu.dims(8, 2, 64), [1], [1], 0)
+    with pytest.raises(ValueError):
+        mk.inspect_chunk(cu.dims(8, 2, 64), [1, 2], [1], 4)
 
 
 def test_the_64_bit_forms_themselves():
