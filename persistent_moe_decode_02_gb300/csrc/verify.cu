@@ -34,13 +34,14 @@ constexpr int MAX_VOCAB = MANY * MAX_PASSES * STEP;   // 393216
 constexpr int AHEAD = 2 * 152;                // blocks that run at once (a multiple of every cluster's size)
 constexpr unsigned FULL = 0xffffffffu;
 
-// 4 elements of a row, `none` past its end.  `wide`: the address is 16-byte aligned.
-__device__ __forceinline__ float4 load4(const float* p, int left, bool wide, float none) {
-  if (wide && left >= 4) return __ldg(reinterpret_cast<const float4*>(p));
+// 4 elements of a row, `none` past its end and in the `skip` places before its
+// start.  `wide`: the address is 16-byte aligned.
+__device__ __forceinline__ float4 load4(const float* p, int left, bool wide, float none, int skip = 0) {
+  if (wide && left >= 4 && skip <= 0) return __ldg(reinterpret_cast<const float4*>(p));
   float4 v = make_float4(none, none, none, none);
-  if (left > 0) v.x = __ldg(p);
-  if (left > 1) v.y = __ldg(p + 1);
-  if (left > 2) v.z = __ldg(p + 2);
+  if (left > 0 && skip <= 0) v.x = __ldg(p);
+  if (left > 1 && skip <= 1) v.y = __ldg(p + 1);
+  if (left > 2 && skip <= 2) v.z = __ldg(p + 2);
   if (left > 3) v.w = __ldg(p + 3);
   return v;
 }
@@ -67,7 +68,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // taken once (against the block's own maximum), and written once.
 template <int PASSES>
 __global__ void __launch_bounds__(NT) k_probs(const float* logits, int vocab, long long row_stride, float scale,
-                                              float* probs, int wide_in, int wide_out) {
+                                              float* probs, int shiftable) {
   __shared__ float wmax[NW], wsum[NW];
   __shared__ int wat[NW];
   __shared__ struct { float m, sum; int at; } parts[FEW];
@@ -77,19 +78,27 @@ __global__ void __launch_bounds__(NT) k_probs(const float* logits, int vocab, lo
   cl.barrier_arrive();                        // every block of the cluster runs before one writes into another
   const int blocks = (int)cl.num_blocks(), rank = (int)cl.block_rank(), tid = threadIdx.x;
   const size_t row = blockIdx.x / blocks;
-  const Segment s = segment(vocab, blocks, rank);
-  const float* src = logits + row * row_stride + s.begin;
+  // A row may start anywhere, and its 16-byte pieces where its address says: it
+  // is taken to begin `shift` elements earlier, whose places stay empty.
+  const float* first = logits + row * row_stride;
+  const int shift = shiftable ? (int)((uintptr_t)first / 4 % 4) : 0;
+  const Segment s = segment(vocab + shift, blocks, rank);
+  const float* src = first - shift + s.begin;
+  const bool wide_in = (uintptr_t)src % 16 == 0;
+  const int skip = shift - s.begin;           // (positive in the first block of the row only)
   float4 x[PASSES];
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     const int i = p * STEP + tid * 4;
-    x[p] = load4(src + i, s.n - i, wide_in, -INFINITY);
+    x[p] = load4(src + i, s.n - i, wide_in, -INFINITY, skip - i);
   }
   // The segment that a block of the next round will read is on its way to L2
   // while this one computes and writes.
   const unsigned ahead = blockIdx.x + AHEAD;
-  if (wide_in && ahead < gridDim.x && tid == 0 && s.n >= 4)
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(logits + (ahead / blocks) * row_stride + s.begin), "r"(s.n / 4 * 16));
+  if (ahead < gridDim.x && tid == 0 && s.n > 8) {
+    const uintptr_t at = ((uintptr_t)(logits + (ahead / blocks) * row_stride + s.begin) + 15) & ~(uintptr_t)15;
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"((s.n - 8) / 4 * 16));
+  }
   float m = -INFINITY;                        // a NaN or +infinity in the row makes this one
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) m = max_nan(m, max_nan(max_nan(x[p].x, x[p].y), max_nan(x[p].z, x[p].w)));
@@ -118,7 +127,7 @@ __global__ void __launch_bounds__(NT) k_probs(const float* logits, int vocab, lo
   } else {
 #pragma unroll
     for (int p = PASSES - 1; p >= 0; --p) {
-      const int i = s.begin + p * STEP + tid * 4;
+      const int i = s.begin - shift + p * STEP + tid * 4;
       at = x[p].x == m ? i : x[p].y == m ? i + 1 : x[p].z == m ? i + 2 : x[p].w == m ? i + 3 : at;
     }
     at = __reduce_min_sync(FULL, at);
@@ -140,7 +149,9 @@ __global__ void __launch_bounds__(NT) k_probs(const float* logits, int vocab, lo
   cl.sync();
   float top = parts[0].m;
   for (int r = 1; r < blocks; ++r) top = max_nan(top, parts[r].m);
-  float* dst = probs + row * vocab + s.begin;
+  float* dst = probs + row * vocab - shift + s.begin;
+  const bool wide_out = (uintptr_t)dst % 16 == 0;
+  const int base_at = s.begin - shift;
   float f = 0.f;                              // from the block's own maximum and sum to the row's
   if (!(top < INFINITY)) {
     f = NAN;
@@ -159,19 +170,19 @@ __global__ void __launch_bounds__(NT) k_probs(const float* logits, int vocab, lo
     float4 v;
     if (scale > 0.f && f == f) v = make_float4(x[p].x * f, x[p].y * f, x[p].z * f, x[p].w * f);
     else v = make_float4(f, f, f, f);
-    if (f == f && pick >= s.begin + i && pick < s.begin + i + 4) {
-      v.x = pick == s.begin + i;
-      v.y = pick == s.begin + i + 1;
-      v.z = pick == s.begin + i + 2;
-      v.w = pick == s.begin + i + 3;
+    if (f == f && pick >= base_at + i && pick < base_at + i + 4) {
+      v.x = pick == base_at + i;
+      v.y = pick == base_at + i + 1;
+      v.z = pick == base_at + i + 2;
+      v.w = pick == base_at + i + 3;
     }
-    if (wide_out && i + 4 <= s.n) {
+    if (wide_out && i + 4 <= s.n && i >= skip) {
       *reinterpret_cast<float4*>(dst + i) = v;
     } else {
-      if (i < s.n) dst[i] = v.x;
-      if (i + 1 < s.n) dst[i + 1] = v.y;
-      if (i + 2 < s.n) dst[i + 2] = v.z;
-      if (i + 3 < s.n) dst[i + 3] = v.w;
+      if (i < s.n && i >= skip) dst[i] = v.x;
+      if (i + 1 < s.n && i + 1 >= skip) dst[i + 1] = v.y;
+      if (i + 2 < s.n && i + 2 >= skip) dst[i + 2] = v.z;
+      if (i + 3 < s.n && i + 3 >= skip) dst[i + 3] = v.w;
     }
   }
 }
@@ -427,9 +438,9 @@ int mk_probs(const float* logits, int rows, int vocab, long long row_stride, flo
   }
   const int c = cluster_of(vocab, rows);
   const float scale = temperature > 0.f ? fminf(1.4426950408889634f / temperature, 3.4e38f) : 0.f;   // log2(e) / T
-  const int win = aligned(logits, 16) && row_stride % 4 == 0, wout = aligned(probs, 16) && vocab % 4 == 0;
-  const cudaError_t e = with_passes(vocab, c, [&](auto n) {
-    return launch_rows(k_probs<n.value>, rows, c, (cudaStream_t)stream, logits, vocab, row_stride, scale, probs, win, wout);
+  const int shiftable = vocab + 3 <= MAX_VOCAB;   // (at the limit itself there is no room for a shift)
+  const cudaError_t e = with_passes(vocab + 3 * shiftable, c, [&](auto n) {
+    return launch_rows(k_probs<n.value>, rows, c, (cudaStream_t)stream, logits, vocab, row_stride, scale, probs, shiftable);
   });
   return e == cudaSuccess ? MK_OK : fail_cuda("mk_probs", e);
 }
