@@ -377,17 +377,18 @@ int fail_cuda(const char* what, cudaError_t e) {
   return fail(MK_ERR_CUDA, buf);
 }
 
-// Blocks of a row's cluster: enough that a segment has a pass or more for each,
-// at most 8.  16 (beyond what every device has to offer, so asked for) where
-// all of the rows' blocks have an SM of their own: of 151936, 1 row takes 4.5 us
-// of probabilities and 6.7 of verification then instead of 5.4 and 9.1, 9 rows
-// 5.7 and 8.0 instead of 5.6 and 9.6.  With more rows the blocks' number costs
-// more than their shorter chains give (16 verifications: 12.2 us instead of
-// 10.9; 160 rows of probabilities: 54.6 us instead of 42.6 at the time).
+// Blocks of a row's cluster.  Few rows, whose blocks all have an SM of their
+// own, are split as far as a pass for each block, into 16 at most (beyond what
+// every device has to offer, so asked for): of 151936, 1 row takes 4.5 us of
+// probabilities and 6.7 of verification then instead of 5.4 and 9.1 with 8, 9
+// rows 5.7 and 8.0 instead of 5.6 and 9.6.  Of many rows a block takes four
+// passes before the row is split further, into 8 at most (160 rows of 32000:
+// 10.4 us, 14.4 when split down to a pass; 120 of 9000: 4.0 and 11.1; 16
+// verifications of 151936: 10.9 us, 12.2 with 16 blocks a row).
 int cluster_of(int vocab, long long rows) {
-  const int most = rows * FEW <= 152 ? FEW : MANY;
+  const bool few = rows * FEW <= 152;
   int c = 1;
-  while (c < most && vocab > c * STEP) c *= 2;
+  while (c < (few ? FEW : MANY) && vocab > c * STEP * (few ? 1 : 4)) c *= 2;
   return c;
 }
 
@@ -396,7 +397,10 @@ template <class F>
 cudaError_t with_passes(int vocab, int cluster, F&& f) {
   const int per = ((vocab + cluster - 1) / cluster + 3) / 4 * 4, n = (per + STEP - 1) / STEP;
   if (n <= 2) return f(std::integral_constant<int, 2>());
-  if (n <= 5) return f(std::integral_constant<int, 5>());
+  if (n <= 3) return f(std::integral_constant<int, 3>());
+  if (n <= 4) return f(std::integral_constant<int, 4>());
+  if (n <= 6) return f(std::integral_constant<int, 6>());
+  if (n <= 8) return f(std::integral_constant<int, 8>());
   if (n <= 10) return f(std::integral_constant<int, 10>());
   if (n <= 16) return f(std::integral_constant<int, 16>());
   return f(std::integral_constant<int, MAX_PASSES>());
