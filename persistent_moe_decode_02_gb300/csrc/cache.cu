@@ -6,10 +6,12 @@
 // one KV head: its 16 tokens x 2 vectors are transposed through shared memory,
 // so global memory sees whole rows of a token on one side and the page's
 // contiguous block on the other.  8000 rows of 32 + 8 heads of 128 enter bf16
-// pages in 31 us (5.3 TB/s, 0.78 of a copy's rate), 8144 fp32 rows 8-bit pages
-// in 45 us (5.4 TB/s); 65000 tokens come back from bf16 pages in 43.5 us (6.1
-// TB/s), 55395 from 8 bits in 29 us (5.9 TB/s).  A few rows take 2 to 5 us, a
-// launch and its chain of loads.
+// pages in 30 us (5.5 TB/s, 0.81 of a copy's rate), 8144 fp32 rows 8-bit pages
+// in 44 us (5.4 TB/s); 65000 tokens come back from bf16 pages in 41.8 us (6.4
+// TB/s), 55395 from 8 bits in 27.6 us (6.2 TB/s).  A few rows take 2 to 4 us, a
+// launch and its chain of loads.  Grids hold the pages that are there: with the
+// longest request's for each, a ragged batch (14700 tokens and three short
+// ones) took 16.4 us to read, 10.6 so.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math.h>
@@ -103,7 +105,7 @@ __device__ __forceinline__ int scale_exp(float amax) {
 
 __device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }   // k in [-126, 127]
 
-// Append: grid (pages that receive rows, KV heads, requests).  A thread has one
+// Append: grid (pages that receive rows, KV heads).  A thread has one
 // token and the same 8 dimensions of either half of a head: its angles are read
 // once for all heads, whose loads do not wait for one another.
 template <int D, bool E4M3, class T>
@@ -114,16 +116,12 @@ __global__ void __launch_bounds__(NT) k_append(ChunkView c, const T* qkv, long l
   constexpr int HS = NT / (PAGE * C);            // heads at a time
   __shared__ float kv[2][PAGE][LD];
   __shared__ int exps[2][PAGE];
-  const ChunkReq r = c.reqs[blockIdx.z];         // the chunk's tables: no kernel writes them
+  const AppendPage at = c.appends[blockIdx.x];   // the chunk's tables: no kernel writes them
   if (stale(c)) return;
-  const int g = blockIdx.y, G = c.G, tid = threadIdx.x;
-  const int j = r.seq / PAGE + blockIdx.x;       // page of the request
-  const int p0 = max(j * PAGE, r.seq), p1 = min(j * PAGE + PAGE, r.seq + r.nnew);
   allow_next();
-  if (p0 >= p1) return;
-  const int n = p1 - p0, slot0 = p0 - j * PAGE, row = r.row0 + p0 - r.seq;
+  const int g = blockIdx.y, G = c.G, tid = threadIdx.x, n = at.n, slot0 = at.slot, row = at.row;
   const int i = tid % C * 8, t = tid / C % PAGE, hs = tid / (C * PAGE);
-  const size_t block = ((size_t)__ldg(c.pt + r.pt + j) * c.nkv + g) * 2;   // the page's K block, in blocks
+  const size_t block = ((size_t)at.page * c.nkv + g) * 2;   // the page's K block, in blocks
   await_stream();
   if (t < n) {
     const T* src = qkv + (size_t)(row + t) * row_stride + (size_t)g * (G + 2) * D + i;
@@ -220,19 +218,23 @@ __global__ void __launch_bounds__(NT) k_append(ChunkView c, const T* qkv, long l
   }
 }
 
-// Read: grid (pages, KV heads, requests).  A thread has two dimensions of the
+// Read: grid (all requests' pages, KV heads).  A thread has two dimensions of the
 // page's 16 tokens.  Codes and scales give the value exactly in fp32; the
 // rounding to bf16 changes it only outside bf16's normal range.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(NT) k_read(ChunkView c, const void* pool, __nv_bfloat16* out) {
   constexpr int LD = D + 4;                      // words of a token's row: 16-byte rows for the way out
   __shared__ alignas(16) uint32_t buf[PAGE][LD];
-  const ChunkReq r = c.reqs[blockIdx.z];         // the chunk's tables: no kernel writes them
   if (stale(c)) return;
-  const int g = blockIdx.y, j = blockIdx.x, tid = threadIdx.x;
-  const int n = min(PAGE, r.seq + r.nnew - j * PAGE);
   allow_next();
-  if (n <= 0) return;
+  int lo = 0, hi = c.batch - 1;                  // the request of this page: the last one that starts at or before it
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (__ldg(&c.reqs[mid].page0) <= (int)blockIdx.x) lo = mid;
+    else hi = mid - 1;
+  }
+  const ChunkReq r = c.reqs[lo];
+  const int g = blockIdx.y, j = blockIdx.x - r.page0, tid = threadIdx.x, n = min(PAGE, r.seq + r.nnew - j * PAGE);
   const size_t block = ((size_t)__ldg(c.pt + r.pt + j) * c.nkv + g) * 2;
   await_stream();
   for (int x = tid; x < D; x += NT) {            // dimensions 2x and 2x + 1 of K, then V
@@ -299,8 +301,8 @@ cudaError_t append(const ChunkView& c, bool f32, const void* qkv, long long row_
 }  // namespace
 
 cudaError_t launch_append(const ChunkView& c, bool e4m3, bool f32, const void* qkv, long long row_stride, void* pool,
-                          void* q, int max_new_pages, cudaStream_t st) {
-  const dim3 grid(max_new_pages, c.nkv, c.batch);
+                          void* q, cudaStream_t st) {
+  const dim3 grid(c.nappends, c.nkv);
   if (c.d == 64)
     return e4m3 ? append<64, true>(c, f32, qkv, row_stride, pool, q, grid, st)
                 : append<64, false>(c, f32, qkv, row_stride, pool, q, grid, st);
@@ -308,8 +310,8 @@ cudaError_t launch_append(const ChunkView& c, bool e4m3, bool f32, const void* q
               : append<128, false>(c, f32, qkv, row_stride, pool, q, grid, st);
 }
 
-cudaError_t launch_read(const ChunkView& c, bool e4m3, const void* pool, void* out, int max_pages, cudaStream_t st) {
-  const dim3 grid(max_pages, c.nkv, c.batch);
+cudaError_t launch_read(const ChunkView& c, bool e4m3, const void* pool, void* out, cudaStream_t st) {
+  const dim3 grid(c.npages, c.nkv);
   const auto k = c.d == 64 ? (e4m3 ? k_read<64, true> : k_read<64, false>) : (e4m3 ? k_read<128, true> : k_read<128, false>);
   return launch_kernel(k, grid, NT, 0, 1, st, c, pool, (__nv_bfloat16*)out);
 }

@@ -19,6 +19,7 @@ namespace mk {
 void set_last_error(const char* msg);
 }
 
+using mk::AppendPage;
 using mk::AttnTask;
 using mk::ChunkReq;
 using mk::JoinTask;
@@ -71,11 +72,12 @@ int check_shape(const mk_model_dims* m, Shape& s) {
 struct Built {
   std::vector<ChunkReq> reqs;
   std::vector<int> pt;
+  std::vector<AppendPage> appends;
   std::vector<AttnTask> tasks;
   std::vector<JoinTask> joins;
   std::vector<int> cta_start;
-  long long rows = 0, tokens = 0, split_rows = 0, nsplit = 0, joined_rows = 0;
-  int max_pages = 0, max_new_pages = 0, max_new = 0;   // of one request: all its pages, those that receive rows, rows
+  long long rows = 0, tokens = 0, pages = 0, split_rows = 0, nsplit = 0, joined_rows = 0;
+  int max_new = 0;               // rows of one request
 };
 
 // Row counts and prefix sums; no pages yet.
@@ -94,10 +96,10 @@ int set_lens(const Shape& s, int batch, const int* seq_lens, const int* new_lens
     b.rows += new_lens[i];
     b.tokens += total;
     if (b.rows > INT_MAX - 1024) return fail(MK_ERR_UNSUPPORTED, "mk_chunk: over 2^31 - 1025 new rows");
-    const int np = (int)((total + mk::PAGE - 1) / mk::PAGE);
-    b.max_pages = std::max(b.max_pages, np);
+    r.page0 = (int)b.pages;
+    b.pages += (total + mk::PAGE - 1) / mk::PAGE;
+    if (b.pages > INT_MAX - 1024) return fail(MK_ERR_UNSUPPORTED, "mk_chunk: over 2^31 - 1025 pages");
     b.max_new = std::max(b.max_new, new_lens[i]);
-    if (new_lens[i]) b.max_new_pages = std::max(b.max_new_pages, np - seq_lens[i] / mk::PAGE);
   }
   return MK_OK;
 }
@@ -117,6 +119,8 @@ int set_pages(int num_pages, const int* page_table, int max_pages, Built& b) {
       if (r.nnew && j >= r.seq / mk::PAGE) {
         if (written[pg]) return fail(MK_ERR_INVALID, "mk_chunk: two requests' new tokens, or two pages of one, in one page");
         written[pg] = 1;
+        const int p0 = std::max(j * mk::PAGE, r.seq), p1 = std::min(j * mk::PAGE + mk::PAGE, r.seq + r.nnew);
+        b.appends.push_back({pg, r.row0 + p0 - r.seq, p1 - p0, p0 - j * mk::PAGE});
       }
     }
   }
@@ -297,7 +301,8 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
   const size_t d = c->s.d;
   const size_t n_req = up16(nb.reqs.size() * sizeof(ChunkReq)), n_pt = up16(nb.pt.size() * sizeof(int)),
                n_task = up16(nb.tasks.size() * sizeof(AttnTask)), n_join = up16(nb.joins.size() * sizeof(JoinTask)),
-               n_cta = up16(nb.cta_start.size() * sizeof(int)), n_all = n_req + n_pt + n_task + n_join + n_cta;
+               n_cta = up16(nb.cta_start.size() * sizeof(int)), n_app = nb.appends.size() * sizeof(AppendPage),
+               n_all = n_req + n_pt + n_task + n_join + n_app + n_cta;
   const size_t n_rope = c->s.theta > 0. ? up16((size_t)nb.rows * (d / 2) * sizeof(float2)) : 0;
   const size_t off_rope = (n_all + 255) / 256 * 256, off_part = (off_rope + n_rope + 255) / 256 * 256;
   cudaError_t e = grow(c, off_part + (size_t)nb.split_rows * (d + 2) * sizeof(float));
@@ -308,6 +313,7 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
   if (!nb.tasks.empty()) memcpy(host.data() + n_req + n_pt, nb.tasks.data(), nb.tasks.size() * sizeof(AttnTask));
   if (!nb.joins.empty())
     memcpy(host.data() + n_req + n_pt + n_task, nb.joins.data(), nb.joins.size() * sizeof(JoinTask));
+  if (n_app) memcpy(host.data() + n_all - n_cta - n_app, nb.appends.data(), n_app);
   memcpy(host.data() + n_all - n_cta, nb.cta_start.data(), nb.cta_start.size() * sizeof(int));
   // pageable sources: the bytes have left them when the calls return
   e = cudaMemcpyAsync(c->mem, host.data(), host.size(), cudaMemcpyHostToDevice, st);
@@ -323,6 +329,8 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
   v.tasks = (const AttnTask*)(base + n_req + n_pt);
   v.joins = (const JoinTask*)(base + n_req + n_pt + n_task);
   v.cta_start = (const int*)(base + n_all - n_cta);
+  v.appends = (const AppendPage*)(base + n_all - n_cta - n_app);
+  v.nappends = (int)c->b.appends.size(); v.npages = (int)c->b.pages;
   v.ctas = (int)c->b.cta_start.size() - 1; v.njoins = (int)c->b.joins.size();
   v.max_parts = v.max_join_rows = 0;
   for (const JoinTask& j : c->b.joins) {
@@ -434,7 +442,7 @@ int mk_chunk_append(mk_chunk* c, const void* qkv, int rows_type, long long row_s
   const int rc = check_device(c);
   if (rc != MK_OK) return rc;
   const cudaError_t e = mk::launch_append(c->view, c->type == MK_KV_E4M3, rows_type == MK_ROWS_F32, qkv, row_stride,
-                                          kv_pool, q, c->b.max_new_pages, (cudaStream_t)stream);
+                                          kv_pool, q, (cudaStream_t)stream);
   return e == cudaSuccess ? MK_OK : fail_cuda("mk_chunk_append", e);
 }
 
@@ -460,7 +468,7 @@ int mk_chunk_read(mk_chunk* c, const void* kv_pool, void* out, mk_stream stream)
     return fail(MK_ERR_INVALID, "mk_chunk_read: a buffer is NULL or not 16-byte aligned");
   const int rc = check_device(c);
   if (rc != MK_OK) return rc;
-  const cudaError_t e = mk::launch_read(c->view, c->type == MK_KV_E4M3, kv_pool, out, c->b.max_pages, (cudaStream_t)stream);
+  const cudaError_t e = mk::launch_read(c->view, c->type == MK_KV_E4M3, kv_pool, out, (cudaStream_t)stream);
   return e == cudaSuccess ? MK_OK : fail_cuda("mk_chunk_read", e);
 }
 

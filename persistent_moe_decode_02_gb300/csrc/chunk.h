@@ -17,11 +17,19 @@ constexpr int Q_TILE = 128;      // query rows (tokens x the group's heads) of a
 struct alignas(16) ChunkReq {
   int seq, nnew;                 // cached tokens, new tokens
   int row0;                      // first packed row of its new tokens
-  int pad;
+  int page0;                     // first page of it, counted over all requests' pages
   long long tok0;                // first packed row of all its tokens (mk_chunk_read)
   long long pt;                  // first entry of its page-table row
 };
 static_assert(sizeof(ChunkReq) == 32, "request record is 32 bytes");
+
+// One page that receives new rows (mk_chunk_append).
+struct alignas(16) AppendPage {
+  int page;                      // in the pool
+  int row, n;                    // first packed row, rows
+  int slot;                      // of the first row
+};
+static_assert(sizeof(AppendPage) == 16, "append record is 16 bytes");
 
 // One attention task: new rows [tok0, tok0 + ntok) of a request, one KV head,
 // key tiles [tile0, tile0 + ntile).  part >= 0: the task holds a part of the
@@ -49,6 +57,8 @@ struct ChunkView {
   int nq, nkv, d, G;
   int batch, rows, num_pages;
   const ChunkReq* reqs;
+  const AppendPage* appends;     // every page that receives rows
+  int nappends, npages;          // and their number; all requests' pages
   const int* pt;
   const float2* rope;            // [rows][d / 2] (cos, sin) of the new rows; NULL: no rotation
   const AttnTask* tasks;         // in the order of the CTAs
@@ -64,8 +74,8 @@ struct ChunkView {
 
 cudaError_t launch_chunk_rope(const ChunkView& c, double theta, float2* tab, int max_new, cudaStream_t st);
 cudaError_t launch_append(const ChunkView& c, bool e4m3, bool f32, const void* qkv, long long row_stride, void* pool,
-                          void* q, int max_new_pages, cudaStream_t st);
-cudaError_t launch_read(const ChunkView& c, bool e4m3, const void* pool, void* out, int max_pages, cudaStream_t st);
+                          void* q, cudaStream_t st);
+cudaError_t launch_read(const ChunkView& c, bool e4m3, const void* pool, void* out, cudaStream_t st);
 cudaError_t launch_attend(const ChunkView& c, bool e4m3, const void* q, const void* pool, void* out, cudaStream_t st);
 
 // A graph may replay a call whose chunk was updated since: the view's counts
