@@ -620,8 +620,7 @@ template <int D, int W>
 __global__ void __launch_bounds__(128) k_join(ChunkView c, __nv_bfloat16* out) {
   constexpr int E = D / 32;
   __shared__ float part[W][D + 1];
-  const JoinTask t = c.joins[blockIdx.x];
-  const ChunkReq r = c.reqs[t.req];
+  const JoinTask t = c.joins[blockIdx.x];        // within the chunk's memory; nothing of it is used before the next line
   if (stale(c)) return;
   allow_next();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -659,7 +658,7 @@ __global__ void __launch_bounds__(128) k_join(ChunkView c, __nv_bfloat16* out) {
   }
   const float inv = 1.f / l;
   uint32_t* o = reinterpret_cast<uint32_t*>(
-      out + ((size_t)(r.row0 + t.tok0 + row / c.G) * c.nq + (size_t)t.kvh * c.G + row % c.G) * D + lane * E);
+      out + ((size_t)(t.row + row / c.G) * c.nq + (size_t)t.kvh * c.G + row % c.G) * D + lane * E);
 #pragma unroll
   for (int e = 0; e < E; e += 2) o[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
 }

@@ -233,7 +233,7 @@ void set_tasks(const Shape& s, int ctas, Built& b) {
         const Block& k = blocks[i];
         const long long rows = (long long)k.ntok * s.G;
         first[i] = (int)b.split_rows;
-        b.joins.push_back({k.req, k.kvh, k.tok0, k.ntok, first[i], parts[i], 0, 0});
+        b.joins.push_back({k.req, k.kvh, k.tok0, k.ntok, first[i], parts[i], b.reqs[k.req].row0 + k.tok0, 0});
         b.joined_rows += rows;
         b.split_rows += rows * parts[i];
         b.nsplit += parts[i];

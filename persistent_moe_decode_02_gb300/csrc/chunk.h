@@ -48,7 +48,9 @@ static_assert(sizeof(AttnTask) == 64, "attention task is 64 bytes");
 // The join of a block of rows whose keys were split over `nparts` tasks, whose
 // split rows start at part0 + i * (ntok * G).
 struct alignas(16) JoinTask {
-  int req, kvh, tok0, ntok, part0, nparts, pad0, pad1;
+  int req, kvh, tok0, ntok, part0, nparts;
+  int row;                       // packed row of the first row
+  int pad;
 };
 static_assert(sizeof(JoinTask) == 32, "join task is 32 bytes");
 
@@ -80,6 +82,8 @@ cudaError_t launch_attend(const ChunkView& c, bool e4m3, const void* q, const vo
 
 // A graph may replay a call whose chunk was updated since: the view's counts
 // then no longer fit the tables, and the kernel leaves everything as it is.
+// Asked before anything that a table holds is used as an index: the bytes
+// there may be another table's, or angles.
 __device__ __forceinline__ bool stale(const ChunkView& c) {
   if (__ldg(c.status + 1) == c.gen) return false;   // (nothing writes it while a kernel runs)
   await_stream();                // a kernel does not end before the one before it

@@ -668,3 +668,45 @@ def test_nothing_new(mk):
     assert chunk.sync() == mk.MK_OK
     assert torch.equal(out.cpu(), cu.rows_of(pool, "bf16", batch, 0).bfloat16())
     mk.probs(torch.empty(0, 50, device="cuda"), 1.0, torch.empty(0, 50, device="cuda"))
+
+
+# ---- graphs of an earlier batch, once more ----
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_graph_of_an_earlier_batch_over_other_tables(mk, kv):
+    # the captured chunk itself gets batches whose tables, angles and split rows lie where the captured calls' join
+    # records were (a page table of 512 entries puts those at byte 10272 of the chunk's memory)
+    D, width, pages = cu.dims(32, 4, 128), 512, 600
+    order = torch.randperm(pages, generator=torch.Generator().manual_seed(1)).tolist()
+    table = lambda n, first=0: order[first:first + n] + [-1] * (width - n)
+    chunk = mk.Chunk(D, kv, pages, [8191], [1], table(512), width)
+    assert chunk.info()["joined_rows"] == 32
+    pool = cu.make_pool(kv, pages, 4, 128, 3)
+    gpool = pool.cuda()
+    full = lambda *shape: torch.full(shape, 5.0, dtype=torch.bfloat16, device="cuda")
+    qkv, q, out, back = cu.normal((1, 4, 10, 128), 4).bfloat16().cuda(), full(1, 32, 128), full(1, 32, 128), full(8192, 4, 2, 128)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chunk.append(qkv, gpool, q)
+        chunk.attend(q, gpool, out)
+        chunk.read(gpool, back)
+    for cached, new in (([0], [300]), ([7], [1]), ([100, 3000], [2, 40]), ([0, 0, 0], [1100, 1, 90])):
+        tables, at = [], 0
+        for c, n in zip(cached, new):
+            tables += table(-(-(c + n) // cu.PAGE), at)
+            at += -(-(c + n) // cu.PAGE)
+        chunk.update(cached, new, tables, width)
+        graph.replay()
+        assert chunk.sync() == mk.MK_ERR_INVALID
+        assert torch.equal(gpool.cpu().view(torch.uint8), pool.view(torch.uint8))
+        assert (q == 5).all() and (out == 5).all() and (back == 5).all()
+        # and the new batch is served
+        chunk.update(cached, new, tables, width)
+        b = cu.Batch(cached, new)
+        b.table = [tables[i * width:(i + 1) * width] for i in range(len(new))]
+        q2 = cu.normal((b.rows, 32, 128), 6).bfloat16()
+        out2 = torch.empty(b.rows, 32, 128, dtype=torch.bfloat16, device="cuda")
+        chunk.attend(q2.cuda(), gpool, out2)
+        assert chunk.sync() == mk.MK_OK
+        ref, mag = cu.attend(q2, pool, kv, b, 4)
+        assert ((out2.cpu().double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
