@@ -303,7 +303,7 @@ __device__ __forceinline__ void load_q(const Args& a, const AttnTask& t, int qt,
     const int row = tid / N + i * (128 / N);
     piece[i] = make_uint4(0, 0, 0, 0);
     const int token = row * by_g >> 16;
-    if (row < rows) piece[i] = __ldg(reinterpret_cast<const uint4*>(src + ((size_t)token * a.c.nq + (row - token * G)) * D) + g);
+    if (row < rows) piece[i] = reinterpret_cast<const uint4*>(src + ((size_t)token * a.c.nq + (row - token * G)) * D)[g];
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {

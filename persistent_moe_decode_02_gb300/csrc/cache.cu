@@ -5,11 +5,11 @@
 // large calls and launch latency the small ones.  A block takes one page of
 // one KV head: its 16 tokens x 2 vectors are transposed through shared memory,
 // so global memory sees whole rows of a token on one side and the page's
-// contiguous block on the other.  8000 rows of 32 + 8 heads of 128 enter bf16
-// pages in 30 us (5.5 TB/s, 0.81 of a copy's rate), 8144 fp32 rows 8-bit pages
-// in 44 us (5.4 TB/s); 65000 tokens come back from bf16 pages in 41.8 us (6.4
-// TB/s), 55395 from 8 bits in 27.6 us (6.2 TB/s).  A few rows take 2 to 4 us, a
-// launch and its chain of loads.  Grids hold the pages that are there: with the
+// contiguous block on the other.  8000 rows of 32 query and 4 KV heads of 128
+// enter bf16 pages in 27.5 us (5.9 TB/s, 0.88 of a copy's rate), 8144 fp32 rows
+// 8-bit pages in 43.6 us (5.5 TB/s); 65000 tokens come back from bf16 pages in
+// 41.8 us (6.4 TB/s), 55395 from 8 bits in 27.8 us (6.1 TB/s).  A few rows take
+// 2 to 4 us, a launch and its chain of loads.  Grids hold the pages that are there: with the
 // longest request's for each, a ragged batch (14700 tokens and three short
 // ones) took 16.4 us to read, 10.6 so.
 #include <cuda_bf16.h>
@@ -23,20 +23,31 @@ namespace {
 
 constexpr int NT = 128;          // threads of a block
 
-// 8 consecutive elements as fp32.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// 8 consecutive elements as they lie, and as fp32.
+template <class T>
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+};
+template <class T>
+__device__ __forceinline__ Raw8<T> load8(const T* p) {
+  return *reinterpret_cast<const Raw8<T>*>(p);
+}
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = __uint_as_float(w[i] << 16);
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[4 * i] = __uint_as_float(r.w[i].x);
+    v[4 * i + 1] = __uint_as_float(r.w[i].y);
+    v[4 * i + 2] = __uint_as_float(r.w[i].z);
+    v[4 * i + 3] = __uint_as_float(r.w[i].w);
+  }
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -114,6 +125,7 @@ __global__ void __launch_bounds__(NT) k_append(ChunkView c, const T* qkv, long l
   constexpr int LD = D + 1;                      // odd pitch: columns of the transpose fall into different banks
   constexpr int C = D / 16;                      // threads of a token and head
   constexpr int HS = NT / (PAGE * C);            // heads at a time
+  constexpr int AHEAD = 8 / sizeof(T);           // and in flight for each thread: 128 bytes
   __shared__ float kv[2][PAGE][LD];
   __shared__ int exps[2][PAGE];
   const AppendPage at = c.appends[blockIdx.x];   // the chunk's tables: no kernel writes them
@@ -129,24 +141,36 @@ __global__ void __launch_bounds__(NT) k_append(ChunkView c, const T* qkv, long l
     if (c.rope) {
       const float4* cs = reinterpret_cast<const float4*>(c.rope + (size_t)(row + t) * (D / 2) + i);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) turn.cs[e] = __ldg(cs + e);
+      for (int e = 0; e < 4; ++e) turn.cs[e] = cs[e];
     }
     __nv_bfloat16* dst = q + ((size_t)(row + t) * c.nq + (size_t)g * G) * D + i;
-#pragma unroll 4
-    for (int h = hs; h < G; h += HS) {
-      float a[8], b[8];
-      load8(src + (size_t)h * D, a);
-      load8(src + (size_t)h * D + D / 2, b);
-      if (c.rope) rotate8(turn, a, b);
-      *reinterpret_cast<uint4*>(dst + (size_t)h * D) = pack8(a);
-      *reinterpret_cast<uint4*>(dst + (size_t)h * D + D / 2) = pack8(b);
+    // A load does not pass a store that might meet it, so AHEAD heads' loads
+    // come before their stores.
+    for (int h0 = hs; h0 < G; h0 += AHEAD * HS) {
+      Raw8<T> lo[AHEAD], hi[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (h0 + k * HS < G) {
+          lo[k] = load8(src + (size_t)(h0 + k * HS) * D);
+          hi[k] = load8(src + (size_t)(h0 + k * HS) * D + D / 2);
+        }
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k)
+        if (h0 + k * HS < G) {
+          float a[8], b[8];
+          unpack8(lo[k], a);
+          unpack8(hi[k], b);
+          if (c.rope) rotate8(turn, a, b);
+          *reinterpret_cast<uint4*>(dst + (size_t)(h0 + k * HS) * D) = pack8(a);
+          *reinterpret_cast<uint4*>(dst + (size_t)(h0 + k * HS) * D + D / 2) = pack8(b);
+        }
     }
     if (hs == 0) {
       float a[8], b[8], v[8], w[8];
-      load8(src + (size_t)G * D, a);
-      load8(src + (size_t)G * D + D / 2, b);
-      load8(src + (size_t)(G + 1) * D, v);
-      load8(src + (size_t)(G + 1) * D + D / 2, w);
+      unpack8(load8(src + (size_t)G * D), a);
+      unpack8(load8(src + (size_t)G * D + D / 2), b);
+      unpack8(load8(src + (size_t)(G + 1) * D), v);
+      unpack8(load8(src + (size_t)(G + 1) * D + D / 2), w);
       if (c.rope) rotate8(turn, a, b);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -241,7 +265,7 @@ __global__ void __launch_bounds__(NT) k_read(ChunkView c, const void* pool, __nv
     if constexpr (E4M3) {
       const uint8_t* b = reinterpret_cast<const uint8_t*>(pool) + (block + x / (D / 2)) * (D + 1) * PAGE;
       const uint4* rows = reinterpret_cast<const uint4*>(b) + x % (D / 2) * 2;
-      const uint4 lo4 = __ldg(rows), hi4 = __ldg(rows + 1), ex4 = __ldg(reinterpret_cast<const uint4*>(b) + D);
+      const uint4 lo4 = rows[0], hi4 = rows[1], ex4 = reinterpret_cast<const uint4*>(b)[D];
       const uint32_t lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w},
                      ex[4] = {ex4.x, ex4.y, ex4.z, ex4.w};
 #pragma unroll
@@ -258,7 +282,7 @@ __global__ void __launch_bounds__(NT) k_read(ChunkView c, const void* pool, __nv
     } else {
       const uint4* rows = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(pool) + block * D * PAGE) +
                           (size_t)x * 4;
-      const uint4 v[4] = {__ldg(rows), __ldg(rows + 1), __ldg(rows + 2), __ldg(rows + 3)};
+      const uint4 v[4] = {rows[0], rows[1], rows[2], rows[3]};
       const uint32_t lo[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
       const uint32_t hi[8] = {v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
 #pragma unroll

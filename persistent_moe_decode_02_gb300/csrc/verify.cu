@@ -37,12 +37,12 @@ constexpr unsigned FULL = 0xffffffffu;
 // 4 elements of a row, `none` past its end and in the `skip` places before its
 // start.  `wide`: the address is 16-byte aligned.
 __device__ __forceinline__ float4 load4(const float* p, int left, bool wide, float none, int skip = 0) {
-  if (wide && left >= 4 && skip <= 0) return __ldg(reinterpret_cast<const float4*>(p));
+  if (wide && left >= 4 && skip <= 0) return *reinterpret_cast<const float4*>(p);
   float4 v = make_float4(none, none, none, none);
-  if (left > 0 && skip <= 0) v.x = __ldg(p);
-  if (left > 1 && skip <= 1) v.y = __ldg(p + 1);
-  if (left > 2 && skip <= 2) v.z = __ldg(p + 2);
-  if (left > 3) v.w = __ldg(p + 3);
+  if (left > 0 && skip <= 0) v.x = p[0];
+  if (left > 1 && skip <= 1) v.y = p[1];
+  if (left > 2 && skip <= 2) v.z = p[2];
+  if (left > 3) v.w = p[3];
   return v;
 }
 

@@ -710,3 +710,100 @@ def test_graph_of_an_earlier_batch_over_other_tables(mk, kv):
         assert chunk.sync() == mk.MK_OK
         ref, mag = cu.attend(q2, pool, kv, b, 4)
         assert ((out2.cpu().double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
+
+
+# ---- calls that follow one another without a wait ----
+
+def stored(kv, x):
+    """What a pool gives back for rows x, as bf16."""
+    if kv == "bf16":
+        return x.bfloat16()
+    code, k = cu.quantise(x.float())
+    return torch.ldexp(code.view(torch.float8_e4m3fn).double(), k.double().unsqueeze(-1)).bfloat16()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens", ["drafts", "behind_cache"])
+def test_chain_on_one_stream_reads_what_was_just_written(mk, kv, lens, captured):
+    # read, append and attend over the same slots and buffers turn after turn, nothing waited for; no rotation, so
+    # that queries and cached rows are known to the last bit
+    D, batch, chunk = make(mk, "g8", kv, lens, seed=4, theta=0.0)
+    turns, stream = 6, torch.cuda.Stream()
+    pool = cu.make_pool(kv, batch.num_pages, 4, 128, 9)
+    x = [cu.normal((batch.rows, 4, 10, 128), 50 + i).bfloat16() for i in range(turns)]
+    gpool, gx = pool.cuda(), [t.cuda() for t in x]
+    page, slot = (t.cuda() for t in batch.new_slots())
+    qkv, q = torch.empty_like(gx[0]), torch.empty(batch.rows, 32, 128, dtype=torch.bfloat16, device="cuda")
+    out, back = torch.empty_like(q), torch.empty(sum(batch.total), 4, 2, 128, dtype=torch.bfloat16, device="cuda")
+    again = torch.empty_like(back)
+
+    def calls():
+        chunk.read(gpool, back)
+        chunk.append(qkv, gpool, q)
+        chunk.attend(q, gpool, out)
+        chunk.read(gpool, again)
+
+    torch.cuda.synchronize()
+    got = []
+    with torch.cuda.stream(stream):
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                calls()
+        for i in range(turns):
+            qkv.copy_(gx[i])
+            if i % 2:      # what a call that wrote nothing would leave
+                q.fill_(math.nan)
+                gpool[page, :, :, :, slot] = 3
+            graph.replay() if captured else calls()
+            got.append([t.clone() for t in (q, out, back, again)])
+    assert chunk.sync(stream) == mk.MK_OK
+    page, slot = page.cpu(), slot.cpu()
+    rows = torch.cat([torch.arange(sum(batch.total[:b]) + c, sum(batch.total[:b]) + t)
+                      for b, (c, t) in enumerate(zip(batch.cached, batch.total))])
+    for i in range(turns):
+        gq, gout, gback, gagain = (t.cpu() for t in got[i])
+        assert torch.equal(gq, x[i][:, :, :8].flatten(1, 2))
+        assert torch.equal(gagain[rows], stored(kv, x[i][:, :, 8:]))
+        if i and not i % 2:
+            assert torch.equal(gback, got[i - 1][3].cpu())
+        code = x[i][:, :, 8:]
+        if kv == "bf16":
+            pool[page, :, :, :, slot] = code
+        else:
+            c, k = cu.quantise(code.float())
+            pool[page, :, :, :, slot] = torch.cat([c, (k + 127).to(torch.uint8).unsqueeze(-1)], -1)
+        ref, mag = cu.attend(gq, pool, kv, batch, 4)
+        assert ((gout.double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
+        assert torch.equal(gagain, torch.cat([cu.rows_of(pool, kv, batch, b) for b in range(len(batch.new))]).bfloat16())
+
+
+@pytest.mark.parametrize("rows,vocab", [(4, 32000), (48, 2051)])
+def test_probabilities_in_place_then_verified_without_a_wait(mk, rows, vocab):
+    # logits become probabilities in their own buffer, which the verification reads; the next logits come into the same
+    k, turns = 3, 5
+    b = rows // (k + 1)
+    logits = [cu.normal((rows, vocab), 7 + i, 2.0).cuda() for i in range(turns)]
+    near = [cu.normal((b * k, vocab), 70 + i, 2.0).cuda() for i in range(turns)]
+    g = torch.Generator().manual_seed(1)
+    x = torch.randint(0, vocab, (b, k), generator=g).int().cuda()
+    u, r = torch.rand(b, k, generator=g).cuda() * 2, torch.rand(b, generator=g).cuda()
+    t, d = torch.empty(rows, vocab, device="cuda"), torch.empty(b * k, vocab, device="cuda")
+    tokens, accepted = torch.empty(b, k + 1, dtype=torch.int32, device="cuda"), torch.empty(b, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    got = []
+    for i in range(turns):
+        t.copy_(logits[i])
+        d.copy_(near[i])
+        mk.probs(t, 0.8, t)
+        mk.probs(d, 0.8, d)
+        mk.verify(t.view(b, k + 1, vocab), d.view(b, k, vocab), x, u, r, tokens, accepted)
+        got.append([y.clone() for y in (t, d, tokens, accepted)])
+    for i in range(turns):
+        gt, gd, gtok, gacc = (y.cpu() for y in got[i])
+        for y, l in ((gt, logits[i]), (gd, near[i])):
+            ref = torch.softmax(l.cpu().double() / torch.tensor(0.8, dtype=torch.float32).double(), -1)
+            assert ((y.double() - ref).abs() <= probs_bound(ref)).all()
+        ref_t, ref_a = cu.verify(gt.view(b, k + 1, vocab), gd.view(b, k, vocab), x.cpu(), u.cpu(), r.cpu())
+        assert torch.equal(gacc, torch.from_numpy(ref_a)) and torch.equal(gtok, torch.from_numpy(ref_t))
