@@ -474,9 +474,9 @@ int mk_serve_step(mk_sched* s, mk_plan** plan, const mk_model_dims* dims, const 
  *               row each slot's scale as E8M0, the biased exponent k + 127 of
  *               a power of two: a value is code * 2^k.  A token's scale in a
  *               head's K or V is the smallest power of two with
- *               |value| <= 448 * 2^k for the whole vector (k = -127 for a
- *               vector of zeros), so reading back is exact in bf16 unless the
- *               value underflows or overflows there */
+ *               |value| <= 448 * 2^k for the whole vector, -127 at least
+ *               (which a vector of zeros has), so reading back is exact in
+ *               bf16 unless the value underflows or overflows there */
 enum { MK_KV_BF16 = 0, MK_KV_E4M3 = 1 };
 enum { MK_ROWS_BF16 = 0, MK_ROWS_F32 = 1 };
 

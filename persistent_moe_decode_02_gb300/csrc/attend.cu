@@ -36,7 +36,7 @@
 // 8-bit blocks (codes, then the slots' scales) are copied as they are and
 // turned into that layout by warps of their own: a code times a power of two is
 // a bf16 number, so nothing is rounded (outside bf16's normal range).  The
-// conversion bounds them: 37 rows over 109594 tokens take 43 us (the same over
+// conversion bounds them: 37 rows over 109594 tokens take 43.8 us (the same over
 // bf16 pages, twice the bytes, 42), 1024 rows over 30000 cached ones 434 us.
 // (K's codes fed to 8-bit products as they lie, with Q in two parts and the
 // scales on the scores, left V alone to convert, and took 75 and 546 us with
@@ -332,13 +332,16 @@ __device__ __forceinline__ void prefetch_q(const Args& a, const AttnTask& t, int
 // (dimensions) me, me + 32, ...; `live` slots, the others 0.
 template <int D>
 __device__ __forceinline__ void convert_page(const uint8_t* raw, uint8_t* dst, int live, int me) {
-  uint32_t scale[8];                             // 2^(e - 127): e is a bf16 number's exponent too (0: a vector of zeros)
+  // 2^(e - 127): e is a bf16 number's exponent too, and 2^-127 the subnormal
+  // 0x40 (its maximum is a fiftieth of the time of few rows; asking first
+  // whether a page has such a slot was no less)
+  uint32_t scale[8];
   uint4 code[D / 32];                            // every row's read before the first write: they may not alias
   {
     const uint4 e4 = *reinterpret_cast<const uint4*>(raw + D * PAGE);
     const uint32_t ew[4] = {e4.x, e4.y, e4.z, e4.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) scale[i] = __byte_perm(ew[i / 2], 0, i % 2 ? 0x4342 : 0x4140) << 7;
+    for (int i = 0; i < 8; ++i) scale[i] = __vmaxu2(__byte_perm(ew[i / 2], 0, i % 2 ? 0x4342 : 0x4140) << 7, 0x00400040u);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) code[i] = *reinterpret_cast<const uint4*>(raw + (me + i * 32) * PAGE);
   }

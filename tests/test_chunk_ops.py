@@ -807,3 +807,33 @@ def test_probabilities_in_place_then_verified_without_a_wait(mk, rows, vocab):
             assert ((y.double() - ref).abs() <= probs_bound(ref)).all()
         ref_t, ref_a = cu.verify(gt.view(b, k + 1, vocab), gd.view(b, k, vocab), x.cpu(), u.cpu(), r.cpu())
         assert torch.equal(gacc, torch.from_numpy(ref_a)) and torch.equal(gtok, torch.from_numpy(ref_t))
+
+
+# ---- values at the ends of the 8-bit pool's range ----
+
+def test_attend_reads_8_bit_vectors_of_the_smallest_scale(mk):
+    # keys and values of 2^-121: their scale is 2^-127, which no normal bf16 number holds; queries of 2^121 bring
+    # the scores back to a few units
+    n, D = 5, cu.dims(8, 2, 128, 0.0)
+    batch = cu.Batch([0], [n], seed=2)
+    chunk = mk.Chunk(D, "e4m3", batch.num_pages, batch.cached, batch.new, batch.flat, batch.width)
+    x = cu.normal((n, 2, 6, 128), 1)
+    x[:, :, :4] *= 2.0 ** 121
+    x[:, :, 4:] *= 2.0 ** -121
+    pool = torch.zeros(batch.num_pages, 2, 2, 129, 16, dtype=torch.uint8, device="cuda")
+    q = torch.empty(n, 8, 128, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty_like(q)
+    chunk.append(x.cuda(), pool, q)
+    chunk.attend(q, pool, out)
+    assert chunk.sync() == mk.MK_OK
+    page, slot = batch.new_slots()
+    assert (pool.cpu()[page, :, :, -1, slot] == 0).all()
+    ref, mag = cu.attend(q.cpu(), pool.cpu(), "e4m3", batch, 2)
+    # attend_bound without its absolute part, and what a product or a sum may lose below fp32's normal numbers: one
+    # 2^-126 for each of the row's keys (which is why there are few)
+    bound = cu.BF16 * ref.abs() + (cu.BF16 + 2.0 ** -13) * mag + n * 2.0 ** -126
+    assert ((out.cpu().double() - ref).abs() <= bound).all()
+    assert (ref.abs() > bound).double().mean() > 0.8   # zeros would not do
+    back = torch.empty(n, 2, 2, 128, dtype=torch.bfloat16, device="cuda")
+    chunk.read(pool, back)
+    assert torch.equal(back.cpu(), cu.rows_of(pool.cpu(), "e4m3", batch, 0).bfloat16())
