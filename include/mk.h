@@ -503,7 +503,9 @@ int mk_chunk_create(const mk_model_dims* dims, int kv_type, int num_pages, int b
 
 /* Another batch for the same chunk object, checked like mk_chunk_create's;
  * uploaded on `stream`.  Work already enqueued on other streams must be
- * ordered before it.  On an error the chunk keeps its batch; after an
+ * ordered before it.  The host arrays are free when it returns, and it does
+ * not wait for the work in front of it, except for the upload of the update
+ * before last and where memory has to grow.  On an error the chunk keeps its batch; after an
  * MK_ERR_CUDA of the upload itself it has none until an update succeeds.  Not
  * during a stream capture (MK_ERR_INVALID).  Graphs that captured calls for an
  * earlier batch have to be captured again: replayed all the same, those calls

@@ -258,6 +258,15 @@ void set_tasks(const Shape& s, int ctas, Built& b) {
 
 }  // namespace
 
+// Page-locked memory that an upload leaves from.  Two take turns: an update
+// waits for the upload two before it, never for the work in front of its own
+// (from pageable memory a copy of more than 64 KB waited for all of it).
+struct Stage {
+  char* mem = nullptr;
+  size_t cap = 0;
+  cudaEvent_t sent = nullptr;    // behind the last upload
+};
+
 struct mk_chunk {
   Shape s;
   int type = 0, num_pages = 0, device = 0, ctas = 0;
@@ -268,6 +277,8 @@ struct mk_chunk {
   size_t mem_cap = 0;
   int* status = nullptr;         // [0] first recorded error, [1] generation of the tables
   int gen = 0;
+  Stage stage[2];
+  int turn = 0;                  // the one used last
   bool lost = false;             // an upload failed: the tables hold no batch
   std::vector<void*> retired;    // outgrown memory: graphs of earlier batches may name it, so it stays
   mk::ChunkView view = {};
@@ -290,6 +301,21 @@ cudaError_t grow(mk_chunk* c, size_t need) {
   return cudaSuccess;
 }
 
+// The next stage with room for `need` bytes.
+cudaError_t next_stage(mk_chunk* c, size_t need, Stage** out) {
+  Stage& s = *(*out = &c->stage[c->turn ^ 1]);
+  cudaError_t e = s.sent ? cudaEventSynchronize(s.sent) : cudaEventCreateWithFlags(&s.sent, cudaEventDisableTiming);
+  if (e == cudaSuccess && need > s.cap) {
+    if (s.mem) cudaFreeHost(s.mem);
+    s.mem = nullptr;
+    s.cap = 0;
+    e = cudaMallocHost((void**)&s.mem, need + need / 2);
+    if (e == cudaSuccess) s.cap = need + need / 2;
+  }
+  if (e == cudaSuccess) c->turn ^= 1;
+  return e;
+}
+
 int build(const mk_chunk* c, int batch, const int* seq_lens, const int* new_lens, const int* page_table, int max_pages,
           Built& b) {
   int rc = set_lens(c->s, batch, seq_lens, new_lens, b);
@@ -307,18 +333,23 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
   const size_t off_rope = (n_all + 255) / 256 * 256, off_part = (off_rope + n_rope + 255) / 256 * 256;
   cudaError_t e = grow(c, off_part + (size_t)nb.split_rows * (d + 2) * sizeof(float));
   if (e != cudaSuccess) return fail_cuda("mk_chunk: device memory", e);
-  std::vector<char> host(n_all, 0);
-  memcpy(host.data(), nb.reqs.data(), nb.reqs.size() * sizeof(ChunkReq));
-  memcpy(host.data() + n_req, nb.pt.data(), nb.pt.size() * sizeof(int));
-  if (!nb.tasks.empty()) memcpy(host.data() + n_req + n_pt, nb.tasks.data(), nb.tasks.size() * sizeof(AttnTask));
+  Stage* stage = nullptr;
+  e = next_stage(c, n_all + 2 * sizeof(int), &stage);
+  if (e != cudaSuccess) return fail_cuda("mk_chunk: page-locked memory", e);
+  char* host = stage->mem;
+  memcpy(host, nb.reqs.data(), nb.reqs.size() * sizeof(ChunkReq));
+  memcpy(host + n_req, nb.pt.data(), nb.pt.size() * sizeof(int));
+  if (!nb.tasks.empty()) memcpy(host + n_req + n_pt, nb.tasks.data(), nb.tasks.size() * sizeof(AttnTask));
   if (!nb.joins.empty())
-    memcpy(host.data() + n_req + n_pt + n_task, nb.joins.data(), nb.joins.size() * sizeof(JoinTask));
-  if (n_app) memcpy(host.data() + n_all - n_cta - n_app, nb.appends.data(), n_app);
-  memcpy(host.data() + n_all - n_cta, nb.cta_start.data(), nb.cta_start.size() * sizeof(int));
-  // pageable sources: the bytes have left them when the calls return
-  e = cudaMemcpyAsync(c->mem, host.data(), host.size(), cudaMemcpyHostToDevice, st);
+    memcpy(host + n_req + n_pt + n_task, nb.joins.data(), nb.joins.size() * sizeof(JoinTask));
+  if (n_app) memcpy(host + n_all - n_cta - n_app, nb.appends.data(), n_app);
+  memcpy(host + n_all - n_cta, nb.cta_start.data(), nb.cta_start.size() * sizeof(int));
   const int head[2] = {0, ++c->gen};
-  if (e == cudaSuccess) e = cudaMemcpyAsync(c->status, head, sizeof(head), cudaMemcpyHostToDevice, st);
+  memcpy(host + n_all, head, sizeof(head));
+  e = cudaMemcpyAsync(c->mem, host, n_all, cudaMemcpyHostToDevice, st);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(c->status, host + n_all, sizeof(head), cudaMemcpyHostToDevice, st);
+  const cudaError_t sent = cudaEventRecord(stage->sent, st);   // after a failed copy too: the other may be on its way
+  if (e == cudaSuccess) e = sent;
   c->b = std::move(nb);
   mk::ChunkView& v = c->view;
   char* base = c->mem;
@@ -365,6 +396,13 @@ extern "C" {
 
 void mk_chunk_destroy(mk_chunk* c) {
   if (!c) return;
+  for (Stage& s : c->stage) {
+    if (s.sent) {
+      cudaEventSynchronize(s.sent);
+      cudaEventDestroy(s.sent);
+    }
+    if (s.mem) cudaFreeHost(s.mem);
+  }
   cudaFree(c->mem);
   cudaFree(c->status);
   for (void* p : c->retired) cudaFree(p);

@@ -837,3 +837,34 @@ def test_attend_reads_8_bit_vectors_of_the_smallest_scale(mk):
     back = torch.empty(n, 2, 2, 128, dtype=torch.bfloat16, device="cuda")
     chunk.read(pool, back)
     assert torch.equal(back.cpu(), cu.rows_of(pool.cpu(), "e4m3", batch, 0).bfloat16())
+
+
+# ---- updates ----
+
+def test_updates_do_not_wait_for_the_stream(mk):
+    # batches of 1000 requests (tables of more than 64 KB) behind work of a tenth of a second: the first two updates
+    # return before it ends, the third takes the first one's memory, and every call sees its own batch
+    D, n = cu.dims(8, 1, 64, 0.0), 1000
+    batches = [cu.Batch([40 + 16 * i] * n, [1 + i] * n, seed=i) for i in range(3)]
+    pages = max(b.num_pages for b in batches)
+    pool = cu.make_pool("bf16", pages, 1, 64, 3)
+    gpool, width = pool.cuda(), max(b.width for b in batches)
+    flat = [[p for row in b.table for p in row + [-1] * (width - b.width)] for b in batches]
+    first = max(batches, key=lambda b: b.rows)
+    chunk = mk.Chunk(D, "bf16", pages, first.cached, first.new, flat[2], width)
+    for _ in range(2):      # both buffers and the device's memory have their size
+        chunk.update(first.cached, first.new, flat[2], width)
+    q = [cu.normal((b.rows, 8, 64), 5 + i).bfloat16() for i, b in enumerate(batches)]
+    gq, out = [t.cuda() for t in q], [torch.empty(t.shape, dtype=torch.bfloat16, device="cuda") for t in q]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    asleep = torch.cuda.Event()
+    asleep.record()
+    for i, b in enumerate(batches):
+        chunk.update(b.cached, b.new, flat[i], width)
+        assert i == 2 or not asleep.query()
+        chunk.attend(gq[i], gpool, out[i])
+    assert chunk.sync() == mk.MK_OK
+    for i, b in enumerate(batches):
+        ref, mag = cu.attend(q[i], pool, "bf16", b, 1)
+        assert ((out[i].cpu().double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
