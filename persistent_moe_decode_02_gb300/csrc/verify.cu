@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(NT) k_probs(const float* logits, int vocab, lo
   // The segment that a block of the next round will read is on its way to L2
   // while this one computes and writes.
   const unsigned ahead = blockIdx.x + AHEAD;
-  if (ahead < gridDim.x && tid == 0 && s.n > 8) {
+  if (ahead < gridDim.x && tid == 0 && s.n >= 12) {   // (s.n - 8: whatever the rows' shifts, within the row)
     const uintptr_t at = ((uintptr_t)(logits + (ahead / blocks) * row_stride + s.begin) + 15) & ~(uintptr_t)15;
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"((s.n - 8) / 4 * 16));
   }

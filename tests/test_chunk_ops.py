@@ -868,3 +868,18 @@ def test_updates_do_not_wait_for_the_stream(mk):
     for i, b in enumerate(batches):
         ref, mag = cu.attend(q[i], pool, "bf16", b, 1)
         assert ((out[i].cpu().double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
+
+
+# ---- many rows: clusters of 1 to 8 blocks, every number of passes, the rows fetched ahead ----
+
+@pytest.mark.parametrize("vocab", [8, 9, 10, 11, 12, 13, 16, 17])
+def test_probs_many_rows_of_a_few(mk, vocab):
+    # more rows than run at once: each block fetches a later row's segment ahead, or nothing of one too short
+    rows = 700
+    for stride in (vocab, vocab + 3):
+        x = cu.normal((rows, stride), vocab, 3.0)
+        ref = torch.softmax(x[:, :vocab].double(), -1)
+        out = torch.full((rows + 1, vocab), 7.0, device="cuda")
+        mk.probs(x.cuda()[:, :vocab], 1.0, out[:-1])
+        got = out.cpu()
+        assert ((got[:-1].double() - ref).abs() <= probs_bound(ref)).all() and (got[-1] == 7).all()
