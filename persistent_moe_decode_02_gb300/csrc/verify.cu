@@ -19,6 +19,7 @@
 
 #include "launch.cuh"
 #include "mk.h"
+#include "rows.h"
 
 namespace cg = cooperative_groups;
 
@@ -26,12 +27,7 @@ namespace mk {
 void set_last_error(const char* msg);
 namespace {
 
-constexpr int NT = 512, NW = NT / 32;
-constexpr int MANY = 8, FEW = 16;             // blocks of a row's cluster at most: of many rows, of few
-constexpr int STEP = NT * 4;                  // elements of one pass of a block: 4 consecutive ones a thread
-constexpr int MAX_PASSES = 24;                // kept in registers: 96 of a thread
-constexpr int MAX_VOCAB = MANY * MAX_PASSES * STEP;   // 393216
-constexpr int AHEAD = 2 * 152;                // blocks that run at once (a multiple of every cluster's size)
+constexpr int NT = ROW_THREADS, NW = NT / 32;
 constexpr unsigned FULL = 0xffffffffu;
 
 // 4 elements of a row, `none` past its end and in the `skip` places before its
@@ -68,7 +64,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // taken once (against the block's own maximum), and written once.
 template <int PASSES>
 __global__ void __launch_bounds__(NT) k_probs(const float* logits, int vocab, long long row_stride, float scale,
-                                              float* probs, int shiftable) {
+                                              float* probs, int shiftable, int at_once) {
   __shared__ float wmax[NW], wsum[NW];
   __shared__ int wat[NW];
   __shared__ struct { float m, sum; int at; } parts[FEW];
@@ -94,7 +90,7 @@ __global__ void __launch_bounds__(NT) k_probs(const float* logits, int vocab, lo
   }
   // The segment that a block of the next round will read is on its way to L2
   // while this one computes and writes.
-  const unsigned ahead = blockIdx.x + AHEAD;
+  const unsigned ahead = blockIdx.x + at_once;
   if (ahead < gridDim.x && tid == 0 && s.n >= 12) {   // (s.n - 8: whatever the rows' shifts, within the row)
     const uintptr_t at = ((uintptr_t)(logits + (ahead / blocks) * row_stride + s.begin) + 15) & ~(uintptr_t)15;
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"((s.n - 8) / 4 * 16));
@@ -364,6 +360,17 @@ __global__ void __launch_bounds__(NT, PASSES <= 10 ? 2 : 1) k_verify(VerifyArgs 
   }
 }
 
+// What a thread of the host knows of the device that it launches on.
+struct Known {
+  int dev = -1, sms = 0;
+  struct {
+    const void* kernel;
+    bool ok;
+  } wide[16] = {};                            // whether 16 blocks of a kernel can run as one cluster
+  int n = 0;
+};
+thread_local Known known;
+
 int fail(int code, const char* msg) {
   set_last_error(msg);
   return code;
@@ -372,30 +379,16 @@ int fail(int code, const char* msg) {
 int fail_cuda(const char* what, cudaError_t e) {
   cudaGetLastError();   // reported here: not to the caller's next question
   allowed = {};
+  known = {};
   char buf[224];
   snprintf(buf, sizeof(buf), "%s: %s (%d)", what, cudaGetErrorString(e), (int)e);
   return fail(MK_ERR_CUDA, buf);
 }
 
-// Blocks of a row's cluster.  Few rows, whose blocks all have an SM of their
-// own, are split as far as a pass for each block, into 16 at most (beyond what
-// every device has to offer, so asked for): of 151936, 1 row takes 4.5 us of
-// probabilities and 6.7 of verification then instead of 5.4 and 9.1 with 8, 9
-// rows 5.7 and 8.0 instead of 5.6 and 9.6.  Of many rows a block takes four
-// passes before the row is split further, into 8 at most (160 rows of 32000:
-// 10.4 us, 14.4 when split down to a pass; 120 of 9000: 4.0 and 11.1; 16
-// verifications of 151936: 10.9 us, 12.2 with 16 blocks a row).
-int cluster_of(int vocab, long long rows) {
-  const bool few = rows * FEW <= 152;
-  int c = 1;
-  while (c < (few ? FEW : MANY) && vocab > c * STEP * (few ? 1 : 4)) c *= 2;
-  return c;
-}
-
 // The instance whose registers hold a segment: f(passes) with one of a few.
 template <class F>
 cudaError_t with_passes(int vocab, int cluster, F&& f) {
-  const int per = ((vocab + cluster - 1) / cluster + 3) / 4 * 4, n = (per + STEP - 1) / STEP;
+  const int n = passes_of(vocab, cluster);
   if (n <= 2) return f(std::integral_constant<int, 2>());
   if (n <= 3) return f(std::integral_constant<int, 3>());
   if (n <= 4) return f(std::integral_constant<int, 4>());
@@ -406,13 +399,61 @@ cudaError_t with_passes(int vocab, int cluster, F&& f) {
   return f(std::integral_constant<int, MAX_PASSES>());
 }
 
-template <class... A>
-cudaError_t launch_rows(void (*k)(A...), long long rows, int cluster, cudaStream_t st, A... args) {
-  if (cluster > MANY) {
-    const cudaError_t e = allow((const void*)k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
+cudaError_t know_device() {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev == known.dev) return e;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  known = {};
+  known.dev = dev;
+  known.sms = sms;
+  return cudaSuccess;
+}
+
+// Allows a kernel clusters of 16 and asks whether the device has room for one.
+cudaError_t wide_cluster(const void* kernel, bool* ok) {
+  cudaError_t e = allow(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  for (const auto& w : known.wide)
+    if (w.kernel == kernel) {
+      *ok = w.ok;
+      return cudaSuccess;
+    }
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = FEW;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = FEW;
+  cfg.blockDim = NT;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+  if (e != cudaSuccess) {                     // no room is an answer too
+    cudaGetLastError();
+    n = 0;
   }
-  return launch_kernel(k, dim3((unsigned)(rows * cluster)), NT, 0, cluster, st, args...);
+  *ok = n > 0;
+  known.wide[known.n++ % 16] = {kernel, *ok};
+  return cudaSuccess;
+}
+
+// Launches rows of (at most) `vocab` elements: kernel(passes) is the instance,
+// launch(instance, cluster) its call.
+template <class K, class L>
+cudaError_t launch_rows(int vocab, int limit, long long rows, K&& kernel, L&& launch) {
+  cudaError_t e = know_device();
+  if (e != cudaSuccess) return e;
+  int c = cluster_of(limit, rows, known.sms, FEW);
+  if (c > MANY) {
+    bool ok = false;
+    e = with_passes(vocab, c, [&](auto n) { return wide_cluster((const void*)kernel(n), &ok); });
+    if (e != cudaSuccess) return e;
+    if (!ok) c = cluster_of(limit, rows, known.sms, MANY);
+  }
+  return with_passes(vocab, c, [&](auto n) { return launch(kernel(n), c); });
 }
 
 bool aligned(const void* p, size_t n) { return p && (uintptr_t)p % n == 0; }
@@ -440,12 +481,14 @@ int mk_probs(const float* logits, int rows, int vocab, long long row_stride, flo
     if (l0 < p1 && p0 < l1 && !(l0 == p0 && row_stride == vocab))
       return fail(MK_ERR_INVALID, "mk_probs: probs overlaps the logits in other places than their own");
   }
-  const int c = cluster_of(vocab, rows);
   const float scale = temperature > 0.f ? fminf(1.4426950408889634f / temperature, 3.4e38f) : 0.f;   // log2(e) / T
   const int shiftable = vocab + 3 <= MAX_VOCAB;   // (at the limit itself there is no room for a shift)
-  const cudaError_t e = with_passes(vocab + 3 * shiftable, c, [&](auto n) {
-    return launch_rows(k_probs<n.value>, rows, c, (cudaStream_t)stream, logits, vocab, row_stride, scale, probs, shiftable);
-  });
+  const cudaError_t e = launch_rows(
+      vocab + 3 * shiftable, vocab, rows, [](auto n) { return k_probs<n.value>; },
+      [&](auto k, int c) {
+        return launch_kernel(k, dim3((unsigned)(rows * c)), NT, 0, c, (cudaStream_t)stream, logits, vocab, row_stride, scale,
+                             probs, shiftable, blocks_at_once(known.sms));
+      });
   return e == cudaSuccess ? MK_OK : fail_cuda("mk_probs", e);
 }
 
@@ -460,10 +503,11 @@ int mk_verify(int batch, int max_draft, int vocab, const float* target, const fl
       (max_draft && (!aligned(drafts, 4) || !aligned(u, 4))) || (draft && !aligned(draft, 4)) ||
       (n_draft && !aligned(n_draft, 4)))
     return fail(MK_ERR_INVALID, "mk_verify: a buffer is NULL or not aligned to its type");
-  const int c = cluster_of(vocab, batch);
   VerifyArgs a = {max_draft, vocab, 0, target, draft, drafts, n_draft, u, r, tokens, accepted};
   a.wide = aligned(target, 16) && (!draft || aligned(draft, 16)) && vocab % 4 == 0;
-  const cudaError_t e = with_passes(vocab, c, [&](auto n) { return launch_rows(k_verify<n.value>, batch, c, (cudaStream_t)stream, a); });
+  const cudaError_t e = launch_rows(
+      vocab, vocab, batch, [](auto n) { return k_verify<n.value>; },
+      [&](auto k, int c) { return launch_kernel(k, dim3((unsigned)(batch * c)), NT, 0, c, (cudaStream_t)stream, a); });
   return e == cudaSuccess ? MK_OK : fail_cuda("mk_verify", e);
 }
 

@@ -156,3 +156,39 @@ def test_the_64_bit_forms_themselves():
     err = torch.maximum(cu.E4M3_STEP * x.double().abs(), cu.E4M3_MIN * torch.exp2(k.double()).unsqueeze(-1))
     assert ((back - x.double()).abs() <= err).all()
     assert (x.abs().amax(-1) <= 448 * torch.exp2(k.float())).all() and (x.abs().amax(-1) > 224 * torch.exp2(k.float())).all()
+
+
+def test_rows_are_split_by_what_the_device_has(tmp_path):
+    # the host rule of mk_probs and mk_verify by itself: 16 blocks a row only where few rows leave each block an SM and
+    # the device offers clusters of 16, and every row fits the largest instance
+    import os
+    import subprocess
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "persistent_moe_decode_02_gb300", "csrc")
+    src = tmp_path / "rows.cpp"
+    src.write_text('''#include <cstdio>
+#include <initializer_list>
+#include "rows.h"
+int main() {
+  for (int sms : {152, 80, 16, 8})
+    for (int most : {16, 8})
+      for (long long rows : {1, 5, 9, 10, 160})
+        for (int vocab : {1, 2048, 2049, 16385, 151936, 393213, 393216})
+          std::printf("%d %d %lld %d %d %d %d\\n", sms, most, rows, vocab, mk::cluster_of(vocab, rows, sms, most),
+                      mk::passes_of(vocab, mk::cluster_of(vocab, rows, sms, most)), mk::blocks_at_once(sms));
+}
+''')
+    exe = tmp_path / "rows"
+    subprocess.run(["g++", "-std=c++17", "-I", csrc, str(src), "-o", str(exe)], check=True)
+    table = {}
+    for line in subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.splitlines():
+        sms, most, rows, vocab, c, passes, ahead = map(int, line.split())
+        table[sms, most, rows, vocab] = c
+        assert c in (1, 2, 4, 8, 16) and passes <= 24
+        assert c <= (most if rows * 16 <= sms else 8)
+        assert ahead % 16 == 0 and 0 < ahead <= 2 * sms
+    assert len(table) == 4 * 2 * 5 * 7
+    assert [table[152, 16, r, 151936] for r in (1, 9, 10, 160)] == [16, 16, 8, 8]
+    assert table[152, 8, 1, 151936] == 8 and table[152, 8, 1, 393216] == 8
+    assert table[80, 16, 5, 151936] == 16 and table[80, 16, 9, 151936] == 8   # 144 blocks on 80 SMs are not few
+    assert table[8, 16, 1, 151936] == 8
+    assert table[152, 16, 1, 2048] == 1 and table[152, 16, 1, 2049] == 2 and table[152, 16, 160, 16385] == 4
