@@ -883,3 +883,70 @@ def test_probs_many_rows_of_a_few(mk, vocab):
         mk.probs(x.cuda()[:, :vocab], 1.0, out[:-1])
         got = out.cpu()
         assert ((got[:-1].double() - ref).abs() <= probs_bound(ref)).all() and (got[-1] == 7).all()
+
+
+@pytest.mark.parametrize("rows,vocab,stride", [
+    (9, 16385, 16385), (10, 2049, 2050), (10, 8193, 8193), (10, 16385, 16390), (40, 32769, 32769), (320, 9001, 9003),
+    (160, 32000, 32000), (40, 151935, 151935), (40, 151936, 151936), (10, 151936, 151939), (10, 230000, 230001),
+    (9, 393216, 393216), (10, 393213, 393213), (10, 393214, 393217), (10, 393216, 393216), (12, 393212, 393215)])
+def test_probs_many_rows(mk, rows, vocab, stride):
+    for temperature in (0.7, 0.0):
+        x = cu.normal((rows, stride), vocab % 1000 + rows, 3.0)
+        x[rows // 2, vocab - 1] = 50.0     # (its last element leads one row)
+        out = torch.full((rows + 1, vocab), 7.0, device="cuda")
+        mk.probs(x.cuda()[:, :vocab], temperature, out[:-1])
+        got = out.cpu()
+        assert (got[-1] == 7).all()
+        if temperature:
+            ref = torch.softmax(x[:, :vocab].double() / torch.tensor(temperature, dtype=torch.float32).double(), -1)
+            assert ((got[:-1].double() - ref).abs() <= probs_bound(ref)).all()
+        else:
+            ref = torch.zeros(rows, vocab).scatter_(1, x[:, :vocab].argmax(1, keepdim=True), 1.0)
+            assert torch.equal(got[:-1], ref)
+
+
+@pytest.mark.parametrize("b,k,vocab", [(9, 2, 151936), (10, 1, 151935), (33, 2, 50257), (40, 3, 9001), (12, 2, 32000),
+                                       (10, 1, 230001), (10, 0, 393216), (11, 1, 393215), (160, 1, 2052)])
+def test_verify_many_requests(mk, b, k, vocab):
+    t, d, x, u, r = draws(b, k, vocab, vocab + b)
+    check_verify(mk, t, d if k else None, x, u, r)
+    if k:
+        u[::2] = 2.0                       # every other request's first draft is refused: a row of differences
+        check_verify(mk, t, d, x, u, r)
+        check_verify(mk, t, None, x, u, r)
+
+
+@pytest.mark.parametrize("b", [3, 12])
+def test_verify_rows_that_are_not_16_byte_aligned(mk, b):
+    # a vocabulary of whole 16-byte pieces in buffers that start 4 bytes into one
+    t, d, x, u, r = draws(b, 2, 4096, 31)
+    u[0, 0] = 2.0
+
+    def shifted(y):
+        flat = torch.empty(y.numel() + 1, device="cuda")[1:]
+        flat.copy_(y.flatten())
+        return flat.view(y.shape)
+
+    tokens, accepted = torch.empty(b, 3, dtype=torch.int32, device="cuda"), torch.empty(b, dtype=torch.int32, device="cuda")
+    ref_t, ref_a = cu.verify(t, d, x, u, r)
+    for gt, gd in ((shifted(t), d.cuda()), (t.cuda(), shifted(d)), (shifted(t), shifted(d))):
+        assert (gt.data_ptr() | gd.data_ptr()) % 16 == 4
+        mk.verify(gt, gd, x.cuda(), u.cuda(), r.cuda(), tokens, accepted)
+        assert torch.equal(tokens.cpu(), torch.from_numpy(ref_t)) and torch.equal(accepted.cpu(), torch.from_numpy(ref_a))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_attend_into_rows_between_sectors(mk, kv):
+    # an output that is 16- but not 32-byte aligned, whole and split rows
+    for lens in ("prompts", "long_one_token"):
+        D, batch, chunk = make(mk, "g2d64", kv, lens, seed=7)
+        pool = cu.make_pool(kv, batch.num_pages, 2, 64, 3).cuda()
+        q = cu.normal((batch.rows, 4, 64), 3).bfloat16().cuda()
+        out = torch.empty_like(q)
+        flat = torch.full((q.numel() + 16,), 7.0, dtype=torch.bfloat16, device="cuda")
+        odd = flat[8:-8].view(q.shape)
+        assert odd.data_ptr() % 32 == 16
+        chunk.attend(q, pool, out)
+        chunk.attend(q, pool, odd)
+        assert chunk.sync() == mk.MK_OK
+        assert torch.equal(odd, out) and (flat[:8] == 7).all() and (flat[-8:] == 7).all()
