@@ -531,9 +531,10 @@ int mk_chunk_append(mk_chunk* c, const void* qkv, int rows_type, long long row_s
  * head_dim], 16-byte aligned; scores are scaled by 1 / sqrt(head_dim), softmax
  * statistics and sums are fp32.  The cached values of the positions below
  * seq_lens[b] + new_lens[b] must be finite; slots behind them may hold
- * anything.  out may be q itself.  Calls on one chunk share its space for split rows: enqueue them
- * on one stream, or one after another, replays of graphs that captured them
- * among them (chunks of their own run at the same time). */
+ * anything.  out may be q itself.  Calls on one chunk share its space for
+ * split rows: enqueue them on one stream, or one after another, replays of
+ * graphs that captured them among them (chunks of their own run at the same
+ * time).  MK_ERR_UNSUPPORTED for a bf16 pool of 256 GB or more. */
 int mk_chunk_attend(mk_chunk* c, const void* q, const void* kv_pool, void* out, mk_stream stream);
 
 /* Read the cache back: every position below seq_lens[b] + new_lens[b] of every

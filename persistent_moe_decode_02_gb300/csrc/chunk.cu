@@ -488,9 +488,9 @@ int mk_chunk_attend(mk_chunk* c, const void* q, const void* kv_pool, void* out, 
   if (!c) return fail(MK_ERR_INVALID, "mk_chunk_attend: chunk is NULL");
   if (!c->s.nq) return fail(MK_ERR_INVALID, "mk_chunk_attend: a chunk without query heads");
   if (c->b.rows == 0) return check_device(c);
-  // the pool's 128-byte rows are counted in 32 bits
-  if ((long long)c->num_pages * c->s.nkv * 2 * (c->s.d / 4) > INT_MAX - 64)
-    return fail(MK_ERR_UNSUPPORTED, "mk_chunk_attend: a pool of 256 GB or more");
+  // a bf16 pool's 128-byte rows are counted in 32 bits
+  if (c->type == MK_KV_BF16 && (long long)c->num_pages * c->s.nkv * 2 * (c->s.d / 4) > INT_MAX - 64)
+    return fail(MK_ERR_UNSUPPORTED, "mk_chunk_attend: a bf16 pool of 256 GB or more");
   if (!aligned16(q) || !aligned16(kv_pool) || !aligned16(out))
     return fail(MK_ERR_INVALID, "mk_chunk_attend: a buffer is NULL or not 16-byte aligned");
   const int rc = check_device(c);

@@ -1,6 +1,7 @@
 """The operators over chunks (mk_chunk_*, mk_probs, mk_verify) on a GPU against
 64-bit CPU forms, at the sizes and masks where they can go wrong, and run
 together as a server uses them."""
+import ctypes
 import dataclasses
 import math
 
@@ -950,3 +951,35 @@ def test_attend_into_rows_between_sectors(mk, kv):
         chunk.attend(q, pool, odd)
         assert chunk.sync() == mk.MK_OK
         assert torch.equal(odd, out) and (flat[:8] == 7).all() and (flat[-8:] == 7).all()
+
+
+def test_attend_over_a_large_8_bit_pool(mk):
+    # 139 GB of pages (as many as a bf16 pool of 256 GB has), the batch's at its end: the same bits as in a small pool
+    D = cu.dims(16, 8, 128)
+    pages = (1 << 31) // (8 * 2 * 32) + 96
+    if torch.cuda.mem_get_info()[0] < 170 << 30:
+        pytest.skip("needs 170 GB of free memory")
+    batch = cu.Batch([0], [75], seed=1, spare=0)
+    x = cu.normal((75, 8, 4, 128), 4).bfloat16().cuda()
+    results = []
+    for size, table in ((batch.num_pages, batch.flat), (pages, [pages - 1 - p for p in batch.flat])):
+        pool = torch.empty(size, 8, 2, 129, 16, dtype=torch.uint8, device="cuda")
+        for p in table:
+            pool[p].zero_()
+        chunk = mk.Chunk(D, "e4m3", size, [0], [75], table, batch.width)
+        q = torch.empty(75, 16, 128, dtype=torch.bfloat16, device="cuda")
+        out, back = torch.empty_like(q), torch.empty(75, 8, 2, 128, dtype=torch.bfloat16, device="cuda")
+        chunk.append(x, pool, q)
+        chunk.attend(q, pool, out)
+        chunk.read(pool, back)
+        assert chunk.sync() == mk.MK_OK
+        results.append((out, back))
+        del pool
+        torch.cuda.empty_cache()
+    assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
+    assert results[0][0].float().abs().max() > 0.1
+    # a bf16 pool of as many pages is refused before anything is launched
+    chunk = mk.Chunk(D, "bf16", pages, [0], [75], batch.flat, batch.width)
+    q = results[0][0]
+    at = [ctypes.c_void_p(t.data_ptr()) for t in (q, x, torch.empty_like(q))]
+    assert mk.lib().mk_chunk_attend(chunk.h, *at, None) == mk.MK_ERR_UNSUPPORTED
