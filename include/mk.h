@@ -483,7 +483,8 @@ enum { MK_ROWS_BF16 = 0, MK_ROWS_F32 = 1 };
 /* A chunk: `batch` requests, request b with seq_lens[b] >= 0 cached tokens and
  * new_lens[b] >= 0 new ones at positions seq_lens[b] .. seq_lens[b] +
  * new_lens[b] - 1.  Rows of new tokens are packed: request 0's, then request
- * 1's, and so on.  One chunk serves every layer of a model. */
+ * 1's, and so on.  One chunk serves every layer of a model; one host thread at
+ * a time calls on it. */
 typedef struct mk_chunk mk_chunk;
 
 /* Builds a chunk for `batch` requests (at most 65535).  Of dims only
@@ -520,8 +521,9 @@ int mk_chunk_update(mk_chunk* c, int batch, const int* seq_lens, const int* new_
  * their positions (angles and sums in fp32 or better); queries are written to
  * q (device bf16 [rows, n_q_heads, head_dim]; NULL when n_q_heads is 0), keys
  * and values into kv_pool at their tokens' slots, rounded to the pool's type.
- * Nothing else of the pool is written.  qkv, q and kv_pool 16-byte aligned,
- * row_stride * element size a multiple of 16. */
+ * Nothing else of the pool is written.  qkv, q and kv_pool 16-byte aligned and
+ * apart (MK_ERR_INVALID where they overlap), row_stride * element size a
+ * multiple of 16. */
 int mk_chunk_append(mk_chunk* c, const void* qkv, int rows_type, long long row_stride, void* kv_pool, void* q,
                     mk_stream stream);
 
@@ -531,7 +533,8 @@ int mk_chunk_append(mk_chunk* c, const void* qkv, int rows_type, long long row_s
  * head_dim], 16-byte aligned; scores are scaled by 1 / sqrt(head_dim), softmax
  * statistics and sums are fp32.  The cached values of the positions below
  * seq_lens[b] + new_lens[b] must be finite; slots behind them may hold
- * anything.  out may be q itself.  Calls on one chunk share its space for
+ * anything.  out may be q itself, but may not overlap it otherwise, nor the
+ * pool.  Calls on one chunk share its space for
  * split rows: enqueue them on one stream, or one after another, replays of
  * graphs that captured them among them (chunks of their own run at the same
  * time).  MK_ERR_UNSUPPORTED for a bf16 pool of 256 GB or more. */
@@ -539,7 +542,7 @@ int mk_chunk_attend(mk_chunk* c, const void* q, const void* kv_pool, void* out, 
 
 /* Read the cache back: every position below seq_lens[b] + new_lens[b] of every
  * request, packed (request 0's first), as bf16 [tokens, n_kv_heads, 2,
- * head_dim] (K, then V; 16-byte aligned).  A chunk with n_q_heads 0 and
+ * head_dim] (K, then V; 16-byte aligned, not in the pool).  A chunk with n_q_heads 0 and
  * rope_theta 0 appends such rows to another pool. */
 int mk_chunk_read(mk_chunk* c, const void* kv_pool, void* out, mk_stream stream);
 
@@ -594,7 +597,9 @@ int mk_probs(const float* logits, int rows, int vocab, long long row_stride, flo
  * tokens[b, :] (device int32 [batch, max_draft + 1]) = the accepted drafts,
  * the drawn token, then -1; accepted[b] (device int32) their number.
  * max_draft >= 0 (u, drafts and draft unused at 0); vocab at most 393216;
- * batch 0 is allowed. */
+ * batch 0 is allowed.  tokens and accepted overlap no other buffer
+ * (MK_ERR_INVALID), except that tokens may begin where drafts does at
+ * batch 1. */
 int mk_verify(int batch, int max_draft, int vocab, const float* target, const float* draft, const int* drafts,
               const int* n_draft, const float* u, const float* r, int* tokens, int* accepted, mk_stream stream);
 

@@ -388,6 +388,11 @@ int check_device(const mk_chunk* c) {
   return dev == c->device ? MK_OK : fail(MK_ERR_INVALID, "mk_chunk: the chunk belongs to another device than the current one");
 }
 
+size_t pool_bytes(const mk_chunk* c) {
+  return (size_t)c->num_pages * c->s.nkv * 2 * mk::PAGE * (c->type == MK_KV_E4M3 ? c->s.d + 1 : c->s.d * 2);
+}
+size_t query_bytes(const mk_chunk* c) { return (size_t)c->b.rows * c->s.nq * c->s.d * 2; }
+
 bool aligned16(const void* p) { return p && (uintptr_t)p % 16 == 0; }
 
 }  // namespace
@@ -477,6 +482,9 @@ int mk_chunk_append(mk_chunk* c, const void* qkv, int rows_type, long long row_s
   if (c->b.rows == 0) return check_device(c);
   if (!aligned16(kv_pool) || !aligned16(qkv) || (c->s.nq ? !aligned16(q) : q != nullptr))
     return fail(MK_ERR_INVALID, "mk_chunk_append: a buffer is NULL or not 16-byte aligned");
+  const size_t nx = (size_t)((c->b.rows - 1) * row_stride + width) * el, nq = q ? query_bytes(c) : 0;
+  if (mk::meet(qkv, nx, kv_pool, pool_bytes(c)) || mk::meet(q, nq, qkv, nx) || mk::meet(q, nq, kv_pool, pool_bytes(c)))
+    return fail(MK_ERR_INVALID, "mk_chunk_append: two of the buffers overlap");
   const int rc = check_device(c);
   if (rc != MK_OK) return rc;
   const cudaError_t e = mk::launch_append(c->view, c->type == MK_KV_E4M3, rows_type == MK_ROWS_F32, qkv, row_stride,
@@ -493,6 +501,8 @@ int mk_chunk_attend(mk_chunk* c, const void* q, const void* kv_pool, void* out, 
     return fail(MK_ERR_UNSUPPORTED, "mk_chunk_attend: a bf16 pool of 256 GB or more");
   if (!aligned16(q) || !aligned16(kv_pool) || !aligned16(out))
     return fail(MK_ERR_INVALID, "mk_chunk_attend: a buffer is NULL or not 16-byte aligned");
+  if ((out != q && mk::meet(out, query_bytes(c), q, query_bytes(c))) || mk::meet(out, query_bytes(c), kv_pool, pool_bytes(c)))
+    return fail(MK_ERR_INVALID, "mk_chunk_attend: out overlaps the pool, or q in another place than its own");
   const int rc = check_device(c);
   if (rc != MK_OK) return rc;
   const cudaError_t e = mk::launch_attend(c->view, c->type == MK_KV_E4M3, q, kv_pool, out, (cudaStream_t)stream);
@@ -504,6 +514,8 @@ int mk_chunk_read(mk_chunk* c, const void* kv_pool, void* out, mk_stream stream)
   if (c->b.tokens == 0) return check_device(c);
   if (!aligned16(kv_pool) || !aligned16(out))
     return fail(MK_ERR_INVALID, "mk_chunk_read: a buffer is NULL or not 16-byte aligned");
+  if (mk::meet(out, (size_t)c->b.tokens * c->s.nkv * 2 * c->s.d * 2, kv_pool, pool_bytes(c)))
+    return fail(MK_ERR_INVALID, "mk_chunk_read: out overlaps the pool");
   const int rc = check_device(c);
   if (rc != MK_OK) return rc;
   const cudaError_t e = mk::launch_read(c->view, c->type == MK_KV_E4M3, kv_pool, out, (cudaStream_t)stream);

@@ -1,6 +1,8 @@
 // Launches of the operators' kernels.
 #pragma once
 #include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
 
 namespace mk {
 
@@ -14,6 +16,12 @@ __device__ __forceinline__ void await_stream() { asm volatile("griddepcontrol.wa
 // The next kernel may be launched; its own await_stream() still waits for this
 // one's end.
 __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Whether two ranges of memory meet.
+inline bool meet(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + nb && y < x + na;
+}
 
 // Launches a kernel that begins with await_stream() while the kernel before it
 // still runs, so that a chain of short ones does not pay each one's launch

@@ -503,6 +503,19 @@ int mk_verify(int batch, int max_draft, int vocab, const float* target, const fl
       (max_draft && (!aligned(drafts, 4) || !aligned(u, 4))) || (draft && !aligned(draft, 4)) ||
       (n_draft && !aligned(n_draft, 4)))
     return fail(MK_ERR_INVALID, "mk_verify: a buffer is NULL or not aligned to its type");
+  {
+    const size_t b = 4 * (size_t)batch, k = max_draft, v = vocab;
+    const struct {
+      const void* at;
+      size_t n;
+    } in[] = {{target, b * (k + 1) * v}, {draft, draft ? b * k * v : 0}, {drafts, b * k}, {n_draft, n_draft ? b : 0},
+              {u, b * k}, {r, b}};
+    bool bad = meet(tokens, b * (k + 1), accepted, b);
+    for (const auto& i : in)      // (one request's tokens may take its drafts' place: each draft stays where it is)
+      bad |= i.n && (meet(accepted, b, i.at, i.n) ||
+                     (meet(tokens, b * (k + 1), i.at, i.n) && !(i.at == drafts && tokens == drafts && batch == 1)));
+    if (bad) return fail(MK_ERR_INVALID, "mk_verify: tokens or accepted overlap another buffer");
+  }
   VerifyArgs a = {max_draft, vocab, 0, target, draft, drafts, n_draft, u, r, tokens, accepted};
   a.wide = aligned(target, 16) && (!draft || aligned(draft, 16)) && vocab % 4 == 0;
   const cudaError_t e = launch_rows(

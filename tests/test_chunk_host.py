@@ -192,3 +192,22 @@ int main() {
     assert table[80, 16, 5, 151936] == 16 and table[80, 16, 9, 151936] == 8   # 144 blocks on 80 SMs are not few
     assert table[8, 16, 1, 151936] == 8
     assert table[152, 16, 1, 2048] == 1 and table[152, 16, 1, 2049] == 2 and table[152, 16, 160, 16385] == 4
+
+
+def test_verify_refuses_outputs_over_other_buffers(mk):
+    # addresses that nothing reads: every call is refused before a CUDA call
+    L, vp = mk.lib(), ctypes.c_void_p
+    at = {n: (i + 1) << 20 for i, n in enumerate(("t", "d", "x", "n", "u", "r", "o", "c"))}
+
+    def verify(b=2, k=2, v=8, **over):
+        a = {**at, **over}
+        return L.mk_verify(b, k, v, *(vp(a[n]) for n in ("t", "d", "x", "n", "u", "r", "o", "c")), None)
+
+    b, k, v = 2, 2, 8
+    size = {"t": b * (k + 1) * v * 4, "d": b * k * v * 4, "x": b * k * 4, "n": b * 4, "u": b * k * 4, "r": b * 4}
+    for name, n in size.items():
+        for out, m in (("o", b * (k + 1) * 4), ("c", b * 4)):
+            for place in (at[name], at[name] + n - 4, at[name] - m + 4):     # whole, its last word, its first
+                assert verify(**{out: place}) == mk.MK_ERR_INVALID, (name, out)
+    assert verify(c=at["o"]) == verify(c=at["o"] + b * (k + 1) * 4 - 4) == mk.MK_ERR_INVALID
+    assert verify(b=1, o=at["x"] + 4) == mk.MK_ERR_INVALID

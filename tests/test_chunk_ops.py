@@ -983,3 +983,41 @@ def test_attend_over_a_large_8_bit_pool(mk):
     q = results[0][0]
     at = [ctypes.c_void_p(t.data_ptr()) for t in (q, x, torch.empty_like(q))]
     assert mk.lib().mk_chunk_attend(chunk.h, *at, None) == mk.MK_ERR_UNSUPPORTED
+
+
+# ---- buffers that overlap ----
+
+def test_refused_overlaps(mk):
+    D, batch, chunk = make(mk, "g2d64", "bf16", ([30], [4]))
+    pages, n = batch.num_pages, 4
+    whole = torch.zeros(pages * 2 * 2 * 64 * 16 + 8192, dtype=torch.bfloat16, device="cuda")
+    was = whole.clone()
+    pool = whole[:-8192].view(pages, 2, 2, 64, 16)
+    edge = lambda size, shape: whole[-8192 - 8:][:size].view(shape)        # its first 16 bytes are the pool's last
+    rows, q = torch.zeros(n, 2, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, 4, 64, dtype=torch.bfloat16, device="cuda")
+    both = torch.zeros(n * 512 + n * 256, dtype=torch.bfloat16, device="cuda")
+    bad = [lambda: chunk.append(edge(n * 512, (n, 2, 4, 64)), pool, q), lambda: chunk.append(rows, pool, edge(n * 256, (n, 4, 64))),
+           lambda: chunk.append(both[:n * 512].view(n, 2, 4, 64), pool, both[n * 512 - 8:][:n * 256].view(n, 4, 64)),
+           lambda: chunk.attend(q, pool, edge(n * 256, (n, 4, 64))),
+           lambda: chunk.attend(both[:n * 256].view(n, 4, 64), pool, both[8:][:n * 256].view(n, 4, 64)),
+           lambda: chunk.read(pool, whole[8:][:34 * 256].view(34, 2, 2, 64))]
+    for call in bad:
+        with pytest.raises(mk.MkError) as e:
+            call()
+        assert e.value.code == mk.MK_ERR_INVALID
+    assert torch.equal(whole, was)
+    # side by side is apart
+    chunk.append(both[:n * 512].view(n, 2, 4, 64), pool, both[n * 512:].view(n, 4, 64))
+    chunk.attend(whole[-8192:][:n * 256].view(n, 4, 64), pool, whole[-8192 + n * 256:][:n * 256].view(n, 4, 64))
+    assert chunk.sync() == mk.MK_OK
+
+
+def test_verify_one_request_in_its_drafts_place(mk):
+    t, d, x, u, r = draws(1, 4, 5000, 3)
+    for u0 in (0.0, 2.0):
+        u[0, 2] = u0
+        ref_t, ref_a = cu.verify(t, d, x, u, r)
+        tokens, accepted = torch.full((1, 5), 9, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+        tokens[0, :4] = x[0].cuda()
+        mk.verify(t.cuda(), d.cuda(), tokens[:, :4], u.cuda(), r.cuda(), tokens, accepted)
+        assert torch.equal(tokens.cpu(), torch.from_numpy(ref_t)) and torch.equal(accepted.cpu(), torch.from_numpy(ref_a))
