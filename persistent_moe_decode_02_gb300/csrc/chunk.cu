@@ -323,7 +323,9 @@ int build(const mk_chunk* c, int batch, const int* seq_lens, const int* new_lens
   return rc;
 }
 
-int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
+// `once`: the caller waits for the stream, so any memory will do (a stage costs
+// 0.1 ms to make and 0.2 to give back, more than a chunk of one batch).
+int commit(mk_chunk* c, Built&& nb, cudaStream_t st, bool once) {
   const size_t d = c->s.d;
   const size_t n_req = up16(nb.reqs.size() * sizeof(ChunkReq)), n_pt = up16(nb.pt.size() * sizeof(int)),
                n_task = up16(nb.tasks.size() * sizeof(AttnTask)), n_join = up16(nb.joins.size() * sizeof(JoinTask)),
@@ -333,10 +335,13 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
   const size_t off_rope = (n_all + 255) / 256 * 256, off_part = (off_rope + n_rope + 255) / 256 * 256;
   cudaError_t e = grow(c, off_part + (size_t)nb.split_rows * (d + 2) * sizeof(float));
   if (e != cudaSuccess) return fail_cuda("mk_chunk: device memory", e);
+  std::vector<char> plain(once ? n_all + 2 * sizeof(int) : 0);
   Stage* stage = nullptr;
-  e = next_stage(c, n_all + 2 * sizeof(int), &stage);
-  if (e != cudaSuccess) return fail_cuda("mk_chunk: page-locked memory", e);
-  char* host = stage->mem;
+  if (!once) {
+    e = next_stage(c, n_all + 2 * sizeof(int), &stage);
+    if (e != cudaSuccess) return fail_cuda("mk_chunk: page-locked memory", e);
+  }
+  char* host = once ? plain.data() : stage->mem;
   memcpy(host, nb.reqs.data(), nb.reqs.size() * sizeof(ChunkReq));
   memcpy(host + n_req, nb.pt.data(), nb.pt.size() * sizeof(int));
   if (!nb.tasks.empty()) memcpy(host + n_req + n_pt, nb.tasks.data(), nb.tasks.size() * sizeof(AttnTask));
@@ -348,7 +353,7 @@ int commit(mk_chunk* c, Built&& nb, cudaStream_t st) {
   memcpy(host + n_all, head, sizeof(head));
   e = cudaMemcpyAsync(c->mem, host, n_all, cudaMemcpyHostToDevice, st);
   if (e == cudaSuccess) e = cudaMemcpyAsync(c->status, host + n_all, sizeof(head), cudaMemcpyHostToDevice, st);
-  const cudaError_t sent = cudaEventRecord(stage->sent, st);   // after a failed copy too: the other may be on its way
+  const cudaError_t sent = once ? cudaStreamSynchronize(st) : cudaEventRecord(stage->sent, st);   // after a failed copy too
   if (e == cudaSuccess) e = sent;
   c->b = std::move(nb);
   mk::ChunkView& v = c->view;
@@ -435,7 +440,7 @@ int mk_chunk_create(const mk_model_dims* dims, int kv_type, int num_pages, int b
     if (e == cudaSuccess) e = cudaMalloc((void**)&c->status, 4 * sizeof(int));
     if (e != cudaSuccess) return fail_cuda("mk_chunk_create", e);
     set_tasks(s, c->ctas, b);
-    r = commit(c, std::move(b), 0);
+    r = commit(c, std::move(b), 0, true);
     if (r != MK_OK) return r;
     e = cudaStreamSynchronize(0);
     return e == cudaSuccess ? MK_OK : fail_cuda("mk_chunk_create", e);
@@ -468,7 +473,7 @@ int mk_chunk_update(mk_chunk* c, int batch, const int* seq_lens, const int* new_
     if (e != cudaSuccess) return fail_cuda("mk_chunk_update", e);
     if (cap != cudaStreamCaptureStatusNone) return fail(MK_ERR_INVALID, "mk_chunk_update: the stream is being captured");
     set_tasks(c->s, c->ctas, b);
-    return commit(c, std::move(b), (cudaStream_t)stream);
+    return commit(c, std::move(b), (cudaStream_t)stream, false);
   });
 }
 
