@@ -531,7 +531,9 @@ int mk_chunk_append(mk_chunk* c, const void* qkv, int rows_type, long long row_s
  * their own keys and values already (mk_chunk_append): row i of request b sees
  * positions 0 .. seq_lens[b] + i.  q, out: device bf16 [rows, n_q_heads,
  * head_dim], 16-byte aligned; scores are scaled by 1 / sqrt(head_dim), softmax
- * statistics and sums are fp32.  The cached values of the positions below
+ * statistics and sums are fp32.  A weight meets its value rounded to bf16, and
+ * the queries are bf16 as given; the decode step's attention keeps both close
+ * to fp32, so the two differ by about a rounding to bf16.  The cached values of the positions below
  * seq_lens[b] + new_lens[b] must be finite; slots behind them may hold
  * anything.  out may be q itself, but may not overlap it otherwise, nor the
  * pool.  Calls on one chunk share its space for

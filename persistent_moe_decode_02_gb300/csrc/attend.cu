@@ -9,7 +9,9 @@
 // head, so a key tile is fetched once for all of them) against a run of key
 // tiles (64 keys, 4 pages).  Products run on the tensor cores: S = Q K^T into
 // tensor memory, softmax in registers (one thread a row), P back to tensor
-// memory as bf16, O += P V.  Each query tile has two S buffers, so the next
+// memory as bf16 (half a step of bf16 off; the decode step, which waits for
+// memory anyway, multiplies queries and weights as pairs of bf16 instead: here
+// a pair would double the products of P V), O += P V.  Each query tile has two S buffers, so the next
 // tile's scores are there when a softmax ends, whatever its latency.  (Tiles of
 // 128 keys with one S buffer, whose products take a fifth less of the pipe's
 // time, took 997 us for the chunk below: a softmax then waits for the scores
@@ -18,11 +20,15 @@
 // What bounds it.  Two query tiles take about 1440 cycles a key tile, of which
 // the products need 1280 (Q K^T with 64 keys reads Q from shared memory for
 // half the work, 48 cycles an instruction instead of 32): 2048 rows of 32 heads
-// over 30000 cached tokens take 630 us, 1.65 PFLOP/s, 0.87 of a large library
-// product.  One query tile (single tokens, drafts) is bound by device memory:
-// one token over 262144 takes 83 us, 6.4 TB/s, 0.95 of a copy's rate.  What a
-// task adds (its queries, its epilogue: 4 to 5 us) weighs on short prompts:
-// 4095 rows from nothing take 100 us, 0.73 of the products' floor.
+// over 30000 cached tokens take 627 us in short bursts, 1.66 PFLOP/s, 0.88 of a
+// large library product, and 675 to 680 call after call, when the clock falls
+// (1.53 PFLOP/s).  At head_dim 64 the products are half and the time is not:
+// the softmax's own chain takes 1450 cycles for the same scores (1024 rows over
+// 30000: 293 us, 318 at 128).  One query tile (single tokens, drafts) is bound
+// by device memory: one token over 262144 takes 85 us, 6.3 TB/s, 0.94 of a
+// copy's rate.  What a task adds (its queries, its epilogue: 4 to 5 us) weighs
+// on short prompts: 4095 rows from nothing take 99 us, 0.73 of the products'
+// floor.
 //
 // How the pages meet the matrix instructions.  A page's K or V block is
 // [d][16 slots] bf16, 32 bytes a dimension: with a 32-byte swizzle that is
@@ -35,9 +41,14 @@
 //
 // 8-bit blocks (codes, then the slots' scales) are copied as they are and
 // turned into that layout by warps of their own: a code times a power of two is
-// a bf16 number, so nothing is rounded (outside bf16's normal range).  The
-// conversion bounds them: 37 rows over 109594 tokens take 43.8 us (the same over
-// bf16 pages, twice the bytes, 42), 1024 rows over 30000 cached ones 434 us.
+// a bf16 number, so nothing is rounded (outside bf16's normal range).  A tile
+// then passes one step more before its products, and no pipe is full: of few
+// rows the issue slots are half taken, shared memory's two ports together 0.6,
+// the ALUs 0.36, the conversions' own unit 0.08.  37 rows over 109594 tokens
+// take 43.3 us (the same over bf16 pages, twice the bytes, 42.6), 1024 rows over
+// 30000 cached ones 428 us.  The 15 warps' 128 registers a thread spill 60 bytes
+// at head_dim 128 and 52 at 64; 11 warps of bf16 have 168 and spill none at 128,
+// 4 at 64.
 // (K's codes fed to 8-bit products as they lie, with Q in two parts and the
 // scales on the scores, left V alone to convert, and took 75 and 546 us with
 // 57 and 580 at the time: the softmax then had the scales' work.)

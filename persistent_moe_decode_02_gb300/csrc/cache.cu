@@ -6,12 +6,12 @@
 // one KV head: its 16 tokens x 2 vectors are transposed through shared memory,
 // so global memory sees whole rows of a token on one side and the page's
 // contiguous block on the other.  8000 rows of 32 query and 4 KV heads of 128
-// enter bf16 pages in 27.5 us (5.9 TB/s, 0.88 of a copy's rate), 8144 fp32 rows
+// enter bf16 pages in 27.5 us (6.0 TB/s, 0.89 of a copy's rate), 8144 fp32 rows
 // 8-bit pages in 43.6 us (5.5 TB/s); 65000 tokens come back from bf16 pages in
-// 41.8 us (6.4 TB/s), 55395 from 8 bits in 27.8 us (6.1 TB/s).  A few rows take
-// 2 to 4 us, a launch and its chain of loads.  Grids hold the pages that are there: with the
+// 42.0 us (6.3 TB/s), 55395 from 8 bits in 27.4 us (6.2 TB/s).  A few rows take
+// 1.5 to 3.5 us, a launch and its chain of loads.  Grids hold the pages that are there: with the
 // longest request's for each, a ragged batch (14700 tokens and three short
-// ones) took 16.4 us to read, 10.6 so.
+// ones) took 16.4 us to read, 11 so.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math.h>

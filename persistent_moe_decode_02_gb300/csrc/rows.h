@@ -14,11 +14,12 @@ constexpr int MAX_VOCAB = MANY * MAX_PASSES * STEP;   // 393216
 // most.  Few rows, whose blocks all have an SM of their own, are split as far
 // as a pass for each block, into 16 at most (beyond what every device has to
 // offer, so asked for; where it is not, `most` is 8): of 151936, 1 row takes
-// 4.5 us of probabilities and 5.8 of verification then instead of 5.4 and 9.1
-// with 8, 9 rows 5.7 and 8.0 instead of 5.6 and 9.6.  Of many rows a block
+// 4.2 us of probabilities and 5.5 of verification then instead of 4.9 and 7.4
+// with 8, 9 rows 5.6 and 7.1 instead of 5.2 and 7.7.  Of many rows a block
 // takes four passes before the row is split further, into 8 at most (160 rows
-// of 32000: 10.4 us, 14.4 when split down to a pass; 120 of 9000: 4.0 and
-// 11.1; 16 verifications of 151936: 10.9 us, 12.2 with 16 blocks a row).
+// of 32000: 9.8 us, 14.4 when split down to a pass; 120 of 9000: 3.8 and 11.1;
+// 16 verifications of 151936: 9.2 us, 12.2 with 16 blocks a row when one of 8
+// took 10.9).
 inline int cluster_of(int vocab, long long rows, int sms, int most) {
   const bool few = rows * FEW <= sms;
   if (!few && most > MANY) most = MANY;

@@ -4,11 +4,13 @@
 // A row of the vocabulary is one cluster's work: each block holds its segment
 // of the row in registers, so the row is read once whatever is done with
 // it, and the blocks exchange their totals through distributed shared memory.
-// 160 rows of 151936 take 39.9 us (4.9 TB/s, 0.72 of a copy's rate: the 1280
-// blocks are 4.2 rounds of what fits the SMs at once, two on each); one row 4.5
-// us.  A verification reads the row or two that its draw needs, not the
-// others: 32 of them with five drafts take 11.6 us, one 5.8 us, a chain of five
-// dependent reads and two exchanges.
+// 160 rows of 151936 take 40.0 us (4.9 TB/s, 0.73 of a copy's rate: clusters of
+// 8 are 1280 blocks, 4.2 rounds of the 304 that run at once); one row 4.2 us.  A
+// verification reads the row or two that its draw needs, not the others: 32 of
+// them with up to five drafts take 12.3 us, one 5.8 us, a chain of five
+// dependent reads and two exchanges.  At vocabularies that are no multiple of 4
+// it reads element by element (32 requests whose first draft is refused: 12.6 us
+// of 151935, 9.9 of 151936).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <math.h>
