@@ -558,6 +558,8 @@ int mk_chunk_sync(mk_chunk* c, mk_stream stream);
  * rows, rows to join, CTAs planned for]: writes up to n ints. */
 int mk_chunk_info(const mk_chunk* c, int* out, int n);
 
+/* Waits for the chunk's work.  Graphs that captured its calls are not to be
+ * replayed any more. */
 void mk_chunk_destroy(mk_chunk* c);
 
 /* Host only (no CUDA call): the attention tasks a chunk of these lengths would

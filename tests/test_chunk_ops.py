@@ -1021,3 +1021,144 @@ def test_verify_one_request_in_its_drafts_place(mk):
         tokens[0, :4] = x[0].cuda()
         mk.verify(t.cuda(), d.cuda(), tokens[:, :4], u.cuda(), r.cuda(), tokens, accepted)
         assert torch.equal(tokens.cpu(), torch.from_numpy(ref_t)) and torch.equal(accepted.cpu(), torch.from_numpy(ref_a))
+
+
+# ---- captures, and sizes at their limits ----
+
+FIRST_CALLS = """
+import sys, torch
+sys.path.insert(0, {root!r})
+from tests import chunk_util as cu
+from persistent_moe_decode_02_gb300 import mk
+D, batch = cu.dims(8, 2, 128), cu.Batch([5000], [3], seed=1)
+chunk = mk.Chunk(D, "bf16", batch.num_pages, batch.cached, batch.new, batch.flat, batch.width)
+pool = cu.make_pool("bf16", batch.num_pages, 2, 128, 3).cuda()
+qkv = cu.normal((3, 2, 6, 128), 4).bfloat16().cuda()
+new = lambda *s, t=torch.bfloat16: torch.zeros(s, dtype=t, device="cuda")
+logits = cu.normal((3, 40000), 5).cuda()
+x, u, r = new(1, 2, t=torch.int32), torch.full((1, 2), 2.0, device="cuda"), torch.full((1,), 0.5, device="cuda")
+
+def calls():
+    q, out, back = new(3, 8, 128), new(3, 8, 128), new(5003, 2, 2, 128)
+    p, tokens, accepted = torch.zeros_like(logits), new(1, 3, t=torch.int32), new(1, t=torch.int32)
+    chunk.append(qkv, pool, q)
+    chunk.attend(q, pool, out)
+    chunk.read(pool, back)
+    mk.probs(logits, 0.9, p)
+    mk.verify(p.view(1, 3, -1), None, x, u, r, tokens, accepted)
+    return q, out, back, p, tokens, accepted
+
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = calls()
+graph.replay()
+assert chunk.sync() == mk.MK_OK
+want = calls()
+assert chunk.sync() == mk.MK_OK
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and got[1].abs().max() > 0 and int(want[4][0, 0]) > 0
+print("the same")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture(mk):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "the same" in run.stdout, run.stderr[-2000:]
+
+
+def test_capture_over_two_streams(mk):
+    # a captured fork: two chunks' calls on streams of their own, joined, and a call after the join
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    work = []
+    for lens, seed in (("drafts", 4), ("behind_cache", 6)):
+        D, b, c = make(mk, "g8", "bf16", lens, seed=seed, theta=0.0)
+        work.append(dict(b=b, c=c, pool=cu.make_pool("bf16", b.num_pages, 4, 128, 9).cuda(),
+                         qkv=torch.zeros(b.rows, 4, 10, 128, dtype=torch.bfloat16, device="cuda"),
+                         q=torch.empty(b.rows, 32, 128, dtype=torch.bfloat16, device="cuda"),
+                         out=torch.empty(b.rows, 32, 128, dtype=torch.bfloat16, device="cuda")))
+    back = torch.empty(sum(work[1]["b"].total), 4, 2, 128, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=one):
+        two.wait_stream(one)
+        for w, s in zip(work, (one, two)):
+            w["c"].append(w["qkv"], w["pool"], w["q"], stream=s)
+            w["c"].attend(w["q"], w["pool"], w["out"], stream=s)
+        one.wait_stream(two)
+        work[1]["c"].read(work[1]["pool"], back, stream=one)
+    for turn in range(3):
+        x = [cu.normal(w["qkv"].shape, 20 + turn + i).bfloat16() for i, w in enumerate(work)]
+        with torch.cuda.stream(one):
+            for w, t in zip(work, x):
+                w["qkv"].copy_(t)
+            graph.replay()
+        assert all(w["c"].sync(one) == mk.MK_OK for w in work)
+        for w, t in zip(work, x):
+            assert torch.equal(w["q"].cpu(), t[:, :, :8].flatten(1, 2))
+            ref, mag = cu.attend(w["q"].cpu(), w["pool"].cpu(), "bf16", w["b"], 4)
+            assert ((w["out"].cpu().double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
+        b = work[1]["b"]
+        assert torch.equal(back.cpu(), torch.cat([cu.rows_of(work[1]["pool"].cpu(), "bf16", b, i) for i in range(2)]).bfloat16())
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_the_largest_batch(mk, kv):
+    # 65535 requests of one new token behind 0 to 3 cached ones; one more is refused
+    n, D = 65535, cu.dims(2, 1, 64, 0.0)
+    cached = torch.arange(n) % 4
+    table = torch.randperm(n, generator=torch.Generator().manual_seed(1))
+    chunk = mk.Chunk(D, kv, n, cached.numpy(), torch.ones(n, dtype=torch.int64).numpy(), table.numpy(), 1)
+    pool = cu.make_pool(kv, n, 1, 64, 5)
+    x = cu.normal((n, 1, 4, 64), 6).bfloat16()
+    gpool, q = pool.cuda(), torch.empty(n, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out, back = torch.empty_like(q), torch.empty(int(cached.sum()) + n, 1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    chunk.append(x.cuda(), gpool, q)
+    chunk.attend(q, gpool, out)
+    chunk.read(gpool, back)
+    assert chunk.sync() == mk.MK_OK
+    assert torch.equal(q.cpu(), x[:, 0, :2])
+    rows = cu.values(gpool.cpu(), kv)[table][:, 0].permute(0, 3, 1, 2)[:, :4]         # [n, 4 slots, 2, 64]
+    assert torch.equal(rows[torch.arange(n), cached].bfloat16(), stored(kv, x[:, 0, 2:]))
+    seen = torch.arange(4) <= cached.unsqueeze(1)
+    assert torch.equal(back.cpu(), rows[seen].unsqueeze(1).bfloat16())
+    s = torch.einsum("nhd,ntd->nht", q.cpu().double(), rows[:, :, 0]) / 8
+    p = torch.softmax(s.masked_fill(~seen.unsqueeze(1), -math.inf), -1)
+    ref, mag = torch.einsum("nht,ntd->nhd", p, rows[:, :, 1]), torch.einsum("nht,ntd->nhd", p, rows[:, :, 1].abs())
+    assert ((out.cpu().double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
+    with pytest.raises(mk.MkError) as e:
+        mk.Chunk(D, kv, n + 1, [0] * (n + 1), [1] * (n + 1), list(range(n + 1)), 1)
+    assert e.value.code == mk.MK_ERR_UNSUPPORTED
+
+
+def test_rows_beyond_4_gb(mk):
+    # a request of 4.4 million tokens: rows, queries and what is read back pass 2^32 bytes
+    n, D = 4_400_003, cu.dims(8, 1, 64)
+    pages = -(-n // 16)
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(2))
+    qkv = torch.empty(n, 1, 10, 64, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(3))
+    q = torch.empty(n, 8, 64, dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros(pages, 1, 2, 64, 16, dtype=torch.bfloat16, device="cuda")
+    chunk = mk.Chunk(D, "bf16", pages, [0], [n], table.numpy(), pages)
+    chunk.append(qkv, pool, q)
+    assert chunk.sync() == mk.MK_OK
+    last = torch.cat([torch.arange(0, 3), torch.arange(n - 50, n)])
+    x = qkv[last.cuda()].cpu()
+    turned = cu.rotate(x[:, :, :9], last, D.rope_theta)
+    slack = 4 * 2.0 ** -24 * (x[:, :, :9].double()[..., :32].abs() + x[:, :, :9].double()[..., 32:].abs()).repeat(1, 1, 1, 2)
+    bound = cu.BF16 * turned.abs() + 1.01 * slack
+    assert ((q[last.cuda()].cpu().double() - turned[:, 0, :8]).abs() <= bound[:, 0, :8]).all()
+    got = pool[table[last // 16].cuda()].cpu()[torch.arange(len(last)), 0, :, :, last % 16]
+    assert torch.equal(got[:, 1], x[:, 0, 9]) and ((got[:, 0].double() - turned[:, 0, 8]).abs() <= bound[:, 0, 8]).all()
+    chunk.close()
+    del qkv
+    copies = 4                             # the same pages four times over: 17.6 million tokens of 256 bytes
+    reader = mk.Chunk(D, "bf16", pages, [pages * 16] * copies, [0] * copies, table.repeat(copies).numpy(), pages)
+    back = torch.empty(pages * 16 * copies, 1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    reader.read(pool, back)
+    assert reader.sync() == mk.MK_OK
+    want = pool[table.cuda()].squeeze(1).permute(0, 3, 1, 2).reshape(-1, 2, 64)
+    for i in range(copies):
+        assert torch.equal(back[i * pages * 16:(i + 1) * pages * 16, 0], want)
