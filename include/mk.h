@@ -506,11 +506,12 @@ int mk_chunk_create(const mk_model_dims* dims, int kv_type, int num_pages, int b
  * uploaded on `stream`.  Work already enqueued on other streams must be
  * ordered before it.  The host arrays are free when it returns, and it does
  * not wait for the work in front of it, except for the upload of the update
- * before last and where memory has to grow.  On an error the chunk keeps its batch; after an
- * MK_ERR_CUDA of the upload itself it has none until an update succeeds.  Not
- * during a stream capture (MK_ERR_INVALID).  Graphs that captured calls for an
- * earlier batch have to be captured again: replayed all the same, those calls
- * write nothing and mk_chunk_sync returns MK_ERR_INVALID. */
+ * before last and where memory has to grow.  On an error the chunk keeps its
+ * batch; after an MK_ERR_CUDA of the upload itself it has none until an update
+ * succeeds.  Not on a stream that is being captured (MK_ERR_INVALID).  Graphs
+ * that captured calls for an earlier batch have to be captured again: replayed
+ * all the same, those calls write nothing and mk_chunk_sync returns
+ * MK_ERR_INVALID. */
 int mk_chunk_update(mk_chunk* c, int batch, const int* seq_lens, const int* new_lens, const int* page_table,
                     int max_pages_per_seq, mk_stream stream);
 
@@ -533,19 +534,19 @@ int mk_chunk_append(mk_chunk* c, const void* qkv, int rows_type, long long row_s
  * head_dim], 16-byte aligned; scores are scaled by 1 / sqrt(head_dim), softmax
  * statistics and sums are fp32.  A weight meets its value rounded to bf16, and
  * the queries are bf16 as given; the decode step's attention keeps both close
- * to fp32, so the two differ by about a rounding to bf16.  The cached values of the positions below
- * seq_lens[b] + new_lens[b] must be finite; slots behind them may hold
- * anything.  out may be q itself, but may not overlap it otherwise, nor the
- * pool.  Calls on one chunk share its space for
- * split rows: enqueue them on one stream, or one after another, replays of
- * graphs that captured them among them (chunks of their own run at the same
- * time).  MK_ERR_UNSUPPORTED for a bf16 pool of 256 GB or more. */
+ * to fp32, so the two differ by about a rounding to bf16.  The cached values
+ * of the positions below seq_lens[b] + new_lens[b] must be finite; slots
+ * behind them may hold anything.  out may be q itself, but may not overlap it
+ * otherwise, nor the pool.  Calls on one chunk share its space for split rows:
+ * enqueue them on one stream, or one after another, replays of graphs that
+ * captured them among them (chunks of their own run at the same time).
+ * MK_ERR_UNSUPPORTED for a bf16 pool of 256 GB or more. */
 int mk_chunk_attend(mk_chunk* c, const void* q, const void* kv_pool, void* out, mk_stream stream);
 
 /* Read the cache back: every position below seq_lens[b] + new_lens[b] of every
  * request, packed (request 0's first), as bf16 [tokens, n_kv_heads, 2,
- * head_dim] (K, then V; 16-byte aligned, not in the pool).  A chunk with n_q_heads 0 and
- * rope_theta 0 appends such rows to another pool. */
+ * head_dim] (K, then V; 16-byte aligned, not in the pool).  A chunk with
+ * n_q_heads 0 and rope_theta 0 appends such rows to another pool. */
 int mk_chunk_read(mk_chunk* c, const void* kv_pool, void* out, mk_stream stream);
 
 /* Wait for `stream`, then return the device status: MK_OK, or

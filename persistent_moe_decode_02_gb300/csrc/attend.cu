@@ -11,9 +11,9 @@
 // tensor memory, softmax in registers (one thread a row), P back to tensor
 // memory as bf16 (half a step of bf16 off; the decode step, which waits for
 // memory anyway, multiplies queries and weights as pairs of bf16 instead: here
-// a pair would double the products of P V), O += P V.  Each query tile has two S buffers, so the next
-// tile's scores are there when a softmax ends, whatever its latency.  (Tiles of
-// 128 keys with one S buffer, whose products take a fifth less of the pipe's
+// a pair would double the products of P V), O += P V.  Each query tile has two
+// S buffers, so the next tile's scores are there when a softmax ends, whatever
+// its latency.  (Tiles of 128 keys with one S buffer, whose products take a fifth less of the pipe's
 // time, took 997 us for the chunk below: a softmax then waits for the scores
 // and the scores for it.)
 //
@@ -43,12 +43,12 @@
 // turned into that layout by warps of their own: a code times a power of two is
 // a bf16 number, so nothing is rounded (outside bf16's normal range).  A tile
 // then passes one step more before its products, and no pipe is full: of few
-// rows the issue slots are half taken, shared memory's two ports together 0.6,
-// the ALUs 0.36, the conversions' own unit 0.08.  37 rows over 109594 tokens
-// take 43.3 us (the same over bf16 pages, twice the bytes, 42.6), 1024 rows over
-// 30000 cached ones 428 us.  The 15 warps' 128 registers a thread spill 60 bytes
-// at head_dim 128 and 52 at 64; 11 warps of bf16 have 168 and spill none at 128,
-// 4 at 64.
+// rows the issue slots are half taken, shared memory's data pipe 0.6 (warps and
+// matrix instructions together), the ALUs 0.36, XU 0.08.  37 rows over 109594
+// tokens take 43.3 us (the same over bf16 pages, twice the bytes, 42.6), 1024
+// rows over 30000 cached ones 428 us.  The 15 warps' 128 registers a thread
+// spill 60 bytes at head_dim 128 and 52 at 64; the 11 warps of bf16 have 168
+// and spill none at 128, 4 at 64.
 // (K's codes fed to 8-bit products as they lie, with Q in two parts and the
 // scales on the scores, left V alone to convert, and took 75 and 546 us with
 // 57 and 580 at the time: the softmax then had the scales' work.)

@@ -9,9 +9,9 @@
 // enter bf16 pages in 27.5 us (6.0 TB/s, 0.89 of a copy's rate), 8144 fp32 rows
 // 8-bit pages in 43.6 us (5.5 TB/s); 65000 tokens come back from bf16 pages in
 // 42.0 us (6.3 TB/s), 55395 from 8 bits in 27.4 us (6.2 TB/s).  A few rows take
-// 1.5 to 3.5 us, a launch and its chain of loads.  Grids hold the pages that are there: with the
-// longest request's for each, a ragged batch (14700 tokens and three short
-// ones) took 16.4 us to read, 11 so.
+// 1.5 to 3.5 us, a launch and its chain of loads.  Grids hold the pages that
+// are there: with the longest request's for each, a ragged batch (14700 tokens
+// and three short ones) took 16.4 us to read, 11 so.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math.h>

@@ -11,7 +11,7 @@ namespace mk {
 // does (launch_kernel).  Such memory is read with plain loads behind it: the
 // read-only path (__ldg) is for what nobody writes while a kernel runs, and
 // these kernels run before their inputs' last writer has ended.  Tables that
-// the host uploads may take it: a copy and a kernel never overlap.
+// the host uploads may take it: a stream's copies and kernels never overlap.
 __device__ __forceinline__ void await_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // The next kernel may be launched; its own await_stream() still waits for this
 // one's end.
