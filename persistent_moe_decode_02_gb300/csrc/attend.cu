@@ -13,9 +13,9 @@
 // memory anyway, multiplies queries and weights as pairs of bf16 instead: here
 // a pair would double the products of P V), O += P V.  Each query tile has two
 // S buffers, so the next tile's scores are there when a softmax ends, whatever
-// its latency.  (Tiles of 128 keys with one S buffer, whose products take a fifth less of the pipe's
-// time, took 997 us for the chunk below: a softmax then waits for the scores
-// and the scores for it.)
+// its latency.  (Tiles of 128 keys with one S buffer, whose products take a
+// fifth less of the pipe's time, took 997 us for the chunk below: a softmax then
+// waits for the scores and the scores for it.)
 //
 // What bounds it.  Two query tiles take about 1440 cycles a key tile, of which
 // the products need 1280 (Q K^T with 64 keys reads Q from shared memory for

@@ -286,6 +286,14 @@ struct mk_chunk {
 
 namespace {
 
+// Allocations of this thread while it captures some other stream: without it
+// they would fail, and end that capture.
+struct BesideCaptures {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  BesideCaptures() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~BesideCaptures() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
 cudaError_t grow(mk_chunk* c, size_t need) {
@@ -473,6 +481,7 @@ int mk_chunk_update(mk_chunk* c, int batch, const int* seq_lens, const int* new_
     if (e != cudaSuccess) return fail_cuda("mk_chunk_update", e);
     if (cap != cudaStreamCaptureStatusNone) return fail(MK_ERR_INVALID, "mk_chunk_update: the stream is being captured");
     set_tasks(c->s, c->ctas, b);
+    BesideCaptures relaxed;
     return commit(c, std::move(b), (cudaStream_t)stream, false);
   });
 }

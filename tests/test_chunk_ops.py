@@ -1162,3 +1162,24 @@ def test_rows_beyond_4_gb(mk):
     want = pool[table.cuda()].squeeze(1).permute(0, 3, 1, 2).reshape(-1, 2, 64)
     for i in range(copies):
         assert torch.equal(back[i * pages * 16:(i + 1) * pages * 16, 0], want)
+
+
+def test_update_beside_a_capture(mk):
+    # one chunk's calls are captured on a stream while another's batch changes, and grows, on a second one
+    D, batch, chunk = make(mk, "g8", "bf16", "drafts", seed=4)
+    b2 = cu.Batch(*LENS["prompts"], seed=5)
+    other = mk.Chunk(D, "bf16", b2.num_pages, [0], [1], [0], 1)
+    pool, pool2 = (cu.make_pool("bf16", b.num_pages, 4, 128, 9) for b in (batch, b2))
+    q, q2 = (cu.normal((b.rows, 32, 128), 3).bfloat16() for b in (batch, b2))
+    on = [(x.cuda(), y.cuda(), torch.zeros_like(x, device="cuda")) for x, y in ((q, pool), (q2, pool2))]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        chunk.attend(*on[0])
+        other.update(b2.cached, b2.new, b2.flat, b2.width, stream=side)
+        other.attend(*on[1], stream=side)
+    graph.replay()
+    assert chunk.sync() == mk.MK_OK and other.sync(side) == mk.MK_OK
+    for x, y, b, (_, _, out) in ((q, pool, batch, on[0]), (q2, pool2, b2, on[1])):
+        ref, mag = cu.attend(x, y, "bf16", b, 4)
+        assert ((out.cpu().double() - ref).abs() <= cu.attend_bound(ref, mag)).all()
