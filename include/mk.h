@@ -478,7 +478,12 @@ int mk_serve_step(mk_sched* s, mk_plan** plan, const mk_model_dims* dims, const 
  *               (which a vector of zeros has), so reading back is exact in
  *               bf16 unless the value underflows or overflows there */
 enum { MK_KV_BF16 = 0, MK_KV_E4M3 = 1 };
-enum { MK_ROWS_BF16 = 0, MK_ROWS_F32 = 1 };
+/* Rows outside the cache.  MK_ROWS_E4M3: bytes [rows, n], e4m3 codes, and beside
+ * them uint8 [rows, n / 32], the E8M0 scale (k + 127) of every 32 consecutive
+ * values of a row: the smallest power of two with |value| <= 448 * 2^k, -127 at
+ * least.  (mk_norm, mk_quantize and mk_experts_* take it, mk_chunk_append does
+ * not.) */
+enum { MK_ROWS_BF16 = 0, MK_ROWS_F32 = 1, MK_ROWS_E4M3 = 2 };
 
 /* A chunk: `batch` requests, request b with seq_lens[b] >= 0 cached tokens and
  * new_lens[b] >= 0 new ones at positions seq_lens[b] .. seq_lens[b] +
@@ -607,6 +612,102 @@ int mk_probs(const float* logits, int rows, int vocab, long long row_stride, flo
  * batch 1. */
 int mk_verify(int batch, int max_draft, int vocab, const float* target, const float* draft, const int* drafts,
               const int* n_draft, const float* u, const float* r, int* tokens, int* accepted, mk_stream stream);
+
+/* ---- The mixture of experts over a chunk's rows ----
+ *
+ * The other half of a layer for chunks of any length, with the pieces that the
+ * decode step runs inside its launch: norm, (the caller's) router product, top-k
+ * and sort, the experts' gate and up, their down, and their sum in the next norm.
+ * They are enqueued on `stream` and can be captured into a graph, except where
+ * said otherwise; rows 0 is allowed everywhere and does nothing.  Results may not
+ * overlap any other buffer of the call (MK_ERR_INVALID), except where said. */
+
+/* Norm with the addition in front of it: t = x + sum_j add[r, j, :] in fp32, j
+ * in order, and out = t / sqrt(mean(t^2) + eps) * gamma from that fp32 t.
+ *   x      device [rows, n] (MK_ROWS_BF16 or F32), rows x_stride elements apart
+ *   add    device [rows, terms, n] (MK_ROWS_BF16 or F32; unused with terms 0):
+ *          the O projection's rows, or the experts' (mk_experts_down)
+ *   gamma  device bf16 [n], NULL: 1
+ *   total  device [rows, n] of x's type, packed: t, rounded to that type; NULL:
+ *          not wanted.  May be x's own packed buffer
+ *   out    device [rows, n] of out_type (MK_ROWS_BF16, F32 or E4M3 with scales
+ *          uint8 [rows, n / 32]); NULL: the sum alone
+ * n a multiple of 8 (E4M3: of 32), at most 16384 (MK_ERR_UNSUPPORTED); x_stride
+ * times the element's size a multiple of 16; buffers 16-byte aligned (scales:
+ * any).  A NaN in a row makes the row's out NaN. */
+int mk_norm(int rows, int n, const void* x, int x_type, long long x_stride, const void* add, int add_type, int terms,
+            const void* gamma, float eps, void* total, void* out, int out_type, uint8_t* scales, mk_stream stream);
+
+/* Rows to 8 bits (MK_ROWS_E4M3): weights once, or rows that come from elsewhere.
+ * x device [rows, n] (MK_ROWS_BF16 or F32), rows x_stride elements apart (times
+ * the element's size a multiple of 16), n a multiple of 32; codes [rows, n]
+ * 16-byte aligned, scales [rows, n / 32].  A NaN stays one and does not change
+ * its group's scale; an infinity takes the scale 2^127 and the largest code. */
+int mk_quantize(int rows, int n, const void* x, int x_type, long long x_stride, uint8_t* codes, uint8_t* scales,
+                mk_stream stream);
+
+/* Routing: each row's top_k largest logits (device fp32 [rows, n_experts], rows
+ * row_stride elements apart; the lowest index of equal ones), the decode step's
+ * choice.
+ *   ids    device int32 [rows, top_k], by falling logit
+ *   gates  device fp32 [rows, top_k], the softmax over the chosen logits
+ *   first  device int32 [n_experts + 1], order device int32 [rows * top_k]: pair
+ *          p = r * top_k + j is row r's choice j; order lists the pairs by
+ *          expert, and by p within one; expert e's are order[first[e]] ..
+ *          order[first[e + 1] - 1]
+ * An expert with a logit of -infinity or NaN is not chosen; a row with fewer
+ * others than top_k has id -1 and gate 0 in the places left, and those pairs lie
+ * behind first[n_experts].  Gates of a row with a NaN or a +infinity are NaN.
+ * n_experts at most 256, top_k at most 8 (MK_ERR_UNSUPPORTED). */
+int mk_route(int rows, int n_experts, int top_k, const float* logits, long long row_stride, int* ids, float* gates,
+             int* first, int* order, mk_stream stream);
+
+/* The experts' products.  One object serves every layer of a model; it holds the
+ * sizes and a status word, so calls on several streams may run at the same time. */
+typedef struct mk_experts mk_experts;
+
+/* Of dims only hidden, n_experts, top_k and expert_ffn are read.  rows_type:
+ * MK_ROWS_BF16 (hidden and expert_ffn multiples of 8) or MK_ROWS_E4M3 (of 32).
+ * At most 256 experts, top_k 8, hidden and expert_ffn 32768, 2^26 pairs.  Belongs
+ * to the current device, where all later calls must run; not while a stream is
+ * captured. */
+int mk_experts_create(const mk_model_dims* dims, int rows_type, mk_experts** out);
+
+/* h[i] = silu(g) * u for each pair in the sorted order, (g, u) = the gate and up
+ * products of row order[i] / top_k of x with the weights of the expert that has i
+ * in first[e] .. first[e + 1] - 1.  Sums are fp32, h is rounded once.
+ *   x     device [rows, hidden] of rows_type (8 bits: x_scales)
+ *   w     device [n_experts, 2 * expert_ffn, hidden] of rows_type, rows
+ *         interleaved as w_gate_up of mk_weights (8 bits: w_scales)
+ *   first, order  of mk_route
+ *   h     device [rows * top_k, expert_ffn] of rows_type (8 bits: h_scales);
+ *         rows from first[n_experts] on are left as they were
+ * Buffers 16-byte aligned, x_scales and w_scales 4.  first and order may hold
+ * anything: an entry out of range is read as none. */
+int mk_experts_up(mk_experts* m, int rows, const void* x, const uint8_t* x_scales, const void* w, const uint8_t* w_scales,
+                  const int* first, const int* order, void* h, uint8_t* h_scales, mk_stream stream);
+
+/* y[p] = gates[p] * (down product of h[i] with the weights of i's expert), p =
+ * order[i]: row r's top_k terms side by side, for mk_norm to add.  Sums and gates
+ * fp32, y rounded once.
+ *   h      device [rows * top_k, expert_ffn] of rows_type, in the sorted order
+ *   w      MK_ROWS_BF16: device [n_experts, expert_ffn, hidden], w_down of
+ *          mk_weights; MK_ROWS_E4M3: device [n_experts, hidden, expert_ffn] (a
+ *          scale belongs to 32 values along the product's sum)
+ *   gates  device fp32 [rows * top_k], NULL: 1
+ *   y      device bf16 [rows, top_k, hidden]; pairs from first[n_experts] on in
+ *          the order (no expert): zeros */
+int mk_experts_down(mk_experts* m, int rows, const void* h, const uint8_t* h_scales, const void* w, const uint8_t* w_scales,
+                    const int* first, const int* order, const float* gates, void* y, mk_stream stream);
+
+/* Wait for `stream`, then return the device status and clear it: MK_OK, or
+ * MK_ERR_DEP_TIMEOUT when a bounded wait inside a product ran out (its results
+ * are then void). */
+int mk_experts_sync(mk_experts* m, mk_stream stream);
+
+/* Waits for the device's work.  Graphs that captured its calls are not to be
+ * replayed any more. */
+void mk_experts_destroy(mk_experts* m);
 
 #ifdef __cplusplus
 }

@@ -17,6 +17,7 @@
 #include <math.h>
 
 #include "chunk.h"
+#include "eights.cuh"
 
 namespace mk {
 namespace {
@@ -102,19 +103,6 @@ __global__ void k_chunk_rope(const ChunkReq* reqs, int half, const __grid_consta
     }
   }
 }
-
-// Smallest k with amax <= 448 * 2^k (448 = 0.875 * 2^9, the largest e4m3
-// value), from the bits of amax: exact, no rounding of a logarithm.
-__device__ __forceinline__ int scale_exp(float amax) {
-  if (amax == 0.f) return -127;
-  int e;
-  const float m = frexpf(amax, &e);              // amax = m 2^e, m in [0.5, 1)
-  if (!isfinite(amax)) return 127;
-  const int k = m <= 0.875f ? e - 9 : e - 8;
-  return k < -127 ? -127 : k;
-}
-
-__device__ __forceinline__ float pow2(int k) { return __int_as_float((k + 127) << 23); }   // k in [-126, 127]
 
 // Append: grid (pages that receive rows, KV heads).  A thread has one
 // token and the same 8 dimensions of either half of a head: its angles are read

@@ -1,0 +1,643 @@
+// The experts' products over a chunk's rows (mk_experts_* in include/mk.h): gate
+// and up with SwiGLU, and down with the gates, for each expert over the rows
+// that were routed to it.
+//
+// C[rows of e, n] = A[rows of e, :] . W_e, on the tensor cores: tiles of 128 rows
+// of one expert by NT columns, K in steps of 128 bytes.  A tile's rows are
+// gathered by their token numbers on the way to shared memory (up), or lie side
+// by side (down); its weights are one box of a tensor map.  A block works through
+// the tiles t, t + blocks, ... of all experts; neighbours in that order share an
+// expert's weights, which so come from device memory once.  One accumulator in
+// tensor memory is read (SwiGLU or gates, rounding, stores) while the next one
+// is summed.
+//
+// 8 bits: codes and scales are what the block-scaled matrix instructions take.
+// The scales pass through shared memory to tensor memory; up's epilogue has a
+// thread for each row, so its groups of 32 results and their scale stay within a
+// thread.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <new>
+
+#include "eights.cuh"
+#include "host.h"
+#include "launch.cuh"
+#include "mk.h"
+#include "ptx.cuh"
+
+struct mk_experts {
+  int hidden, experts, k, ffn;
+  bool e4m3;
+  int device;
+  int* status;                   // first recorded error
+};
+
+namespace mk {
+namespace {
+
+using namespace ptx;
+
+constexpr unsigned FULL = 0xffffffffu;
+constexpr int M_TILE = 128, MAX_EXPERTS = 256, MAX_STAGES = 12, SMEM_MOST = 232448;
+constexpr unsigned long long WAIT_NS = 2000000000ull;   // limit of every wait
+
+struct Ctl {
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], drain;
+  uint32_t tmem;
+  int fail;
+  int row0[MAX_EXPERTS + 1];     // an expert's first row in the sorted order
+  int tile0[MAX_EXPERTS + 1];    // and its first tile of rows
+};
+constexpr int CTL = 3072;
+static_assert(sizeof(Ctl) <= CTL, "control words");
+
+// Warps: 0 copies, 1 matrix instructions, 2 tensor memory, 4-7 results, 8-11
+// (8 bits) scales, a stage each in turn.
+template <bool E4M3, bool UP, int NT>
+struct Cfg {
+  static constexpr bool MN = !E4M3 && !UP;                    // weights lie along the columns
+  static constexpr int THREADS = (E4M3 ? 12 : 8) * 32;
+  static constexpr int KE = E4M3 ? 128 : 64;                  // elements of a stage
+  static constexpr int A_BYTES = M_TILE * 128, B_BYTES = NT * 128, STAGE = A_BYTES + B_BYTES;
+  static constexpr int SF_B = (NT + 127) / 128, SF = E4M3 ? 512 * (1 + SF_B) : 0;
+  static constexpr int FIT = (SMEM_MOST - CTL - 1024) / (STAGE + SF), NST = FIT < MAX_STAGES ? FIT : MAX_STAGES;
+  static constexpr int OFF_SF = NST * STAGE, OFF_CTL = OFF_SF + NST * SF, SMEM = OFF_CTL + CTL + 1024;
+  static constexpr int T_SF = 2 * NT, T_COLS = 512;           // tensor memory: two accumulators, each stage's scales
+  static_assert(T_SF + (E4M3 ? NST * 16 : 0) <= T_COLS, "tensor memory");
+  static_assert(SMEM <= SMEM_MOST, "shared memory");
+  static_assert(NT % 64 == 0, "columns of a tile");
+};
+
+struct Args {
+  const int *first, *order;
+  const float* gates;
+  const uint8_t *a_scales, *b_scales;
+  uint8_t* out;
+  uint8_t* out_scales;
+  int* status;
+  int pairs, rows, top_k, experts;
+  int k, n;                      // elements of a row of A; columns of C
+  int ntiles;                    // tiles of columns
+  bool wide;                     // rows of results are 32-byte aligned
+};
+
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Ctl* ctl, int* status) {
+  const unsigned long long t0 = now_ns();
+  while (!mbar_try(bar, parity)) {
+    if (*(volatile int*)&ctl->fail) return false;
+    if (now_ns() - t0 > WAIT_NS) {
+      *(volatile int*)&ctl->fail = 1;
+      atomicCAS(status, 0, MK_ERR_DEP_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, Ctl* ctl, int* status) {
+  return mbar_try(bar, parity) || wait_slow(bar, parity, ctl, status);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* ctl, int* status) {
+  return __all_sync(FULL, wait_one(bar, parity, ctl, status));
+}
+
+// Each expert's rows and tiles from `first`, by one warp; entries out of order or
+// out of range are moved into it, so whatever they hold, the rows stay within
+// the pairs and no row is counted twice.
+__device__ __forceinline__ void set_tables(const Args& a, Ctl* ctl) {
+  constexpr int PER = MAX_EXPERTS / 32;
+  const int lane = threadIdx.x % 32;
+  int f[PER], top = 0;           // ends of the lane's experts, the largest so far
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane * PER + i;
+    f[i] = e < a.experts ? min(max(a.first[e + 1], 0), a.pairs) : 0;
+  }
+  const int f0 = min(max(a.first[0], 0), a.pairs);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) f[i] = top = max(top, f[i]);
+  int before = top;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(FULL, before, o);
+    if (lane >= o) before = max(before, v);
+  }
+  before = __shfl_up_sync(FULL, before, 1);
+  if (lane == 0) before = 0;
+  before = max(before, f0);
+  int tiles = 0, from = before;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    f[i] = max(f[i], before);
+    tiles += (f[i] - from + M_TILE - 1) / M_TILE;
+    from = f[i];
+  }
+  int at = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(FULL, at, o);
+    if (lane >= o) at += v;
+  }
+  at -= tiles;
+  from = before;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane * PER + i;
+    if (e <= a.experts) {
+      ctl->row0[e] = from;
+      ctl->tile0[e] = at;
+    }
+    at += (f[i] - from + M_TILE - 1) / M_TILE;
+    from = f[i];
+  }
+  if (lane == 31 && a.experts == MAX_EXPERTS) {
+    ctl->row0[MAX_EXPERTS] = from;
+    ctl->tile0[MAX_EXPERTS] = at;
+  }
+}
+
+struct Tile {
+  int e, row0, rows, n0;         // expert, first row in the sorted order, rows, first column
+};
+template <int NT>
+__device__ __forceinline__ Tile tile_at(const Args& a, const Ctl* ctl, int t) {
+  const int g = t / a.ntiles;    // an expert's tiles are side by side, those of its columns in turn
+  int lo = 0, hi = a.experts - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (ctl->tile0[mid] <= g) lo = mid;
+    else hi = mid - 1;
+  }
+  const int mt = ctl->tile0[lo + 1] - ctl->tile0[lo], in = t - ctl->tile0[lo] * a.ntiles;
+  const int n = in / mt, row0 = ctl->row0[lo] + (in - n * mt) * M_TILE;
+  return {lo, row0, min(M_TILE, ctl->row0[lo + 1] - row0), n * NT};
+}
+
+// A pair's row of x; one that is none reads zeros.
+__device__ __forceinline__ int token_of(const Args& a, int at) {
+  const int p = a.order[at];
+  return p >= 0 && p < a.pairs ? p / a.top_k : a.rows;
+}
+
+// 32 bytes of a thread: a whole sector in one store where the address allows it.
+__device__ __forceinline__ void store32(void* p, const uint32_t* v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+// 16 bf16 numbers, of which `left` (a multiple of 8) are there.
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const float* v, int left, bool wide) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  if (left >= 16) store32(p, w, wide);
+  else if (left > 0) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float swiglu(float gate, float up) { return __fdividef(gate, 1.f + __expf(-gate)) * up; }
+
+// 64 columns of a row: up's 32 results (gate and up columns in turn), or down's
+// 64.  n: the first column.
+template <bool E4M3, bool UP>
+__device__ __forceinline__ void store_piece(const Args& a, const uint32_t* acc, size_t at, float gate, int n) {
+  if constexpr (UP) {
+    const int f = a.n / 2, u = n / 2;
+    float h[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) h[i] = swiglu(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1]));
+    if constexpr (E4M3) {
+      if (u >= f) return;
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(h[i]));
+      const int k = scale_exp(m);
+      const Factors s = factors(k);
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = codes4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3], s.f, s.g);
+      store32(a.out + at * f + u, w, a.wide);
+      a.out_scales[at * (f / GROUP) + u / GROUP] = (uint8_t)(k + 127);
+    } else {
+      __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + at * f + u;
+      store16(p, h, f - u, a.wide);
+      store16(p + 16, h + 16, f - u - 16, a.wide);
+    }
+  } else {
+    __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + at * a.n + n;
+#pragma unroll
+    for (int i = 0; i < 64; i += 16) {
+      float y[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(acc[i + j]) * gate;
+      store16(p + i, y, a.n - n - i, a.wide);
+    }
+  }
+}
+
+// Four scales of a row, those of the 128 values from 128 kb on.
+__device__ __forceinline__ uint32_t scales4(const uint8_t* row, int groups, int kb) {
+  if (groups % 4 == 0) return *reinterpret_cast<const uint32_t*>(row + kb * 4);
+  uint32_t v = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v |= (uint32_t)(kb * 4 + i < groups ? row[kb * 4 + i] : 127) << (8 * i);
+  return v;
+}
+
+template <bool E4M3, bool UP, int NT>
+__global__ void __launch_bounds__(Cfg<E4M3, UP, NT>::THREADS, 1)
+    k_experts(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
+  using C = Cfg<E4M3, UP, NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::OFF_CTL);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  int* status = a.status;
+  if (tid == 0) {
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(&ctl->full[i], E4M3 ? 2 : 1);    // the copies' issue; the scales
+      mbar_init(&ctl->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->acc_full[i], 1);
+      mbar_init(&ctl->acc_empty[i], 4);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->fail = 0;
+    fence_barrier_init();
+  }
+  if (warp == 2) tmem_alloc<C::T_COLS>(&ctl->tmem);
+  await_stream();
+  allow_next();
+  if (warp == 3) set_tables(a, ctl);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = ctl->tmem;
+  const int tiles = ctl->tile0[a.experts] * a.ntiles, kbs = (a.k + C::KE - 1) / C::KE;
+
+  if (warp == 0) {                               // ---- copies
+    int s = 0, sent = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    auto rows_of = [&](const Tile& t) {          // the lane's four rows of x
+      int4 r = make_int4(a.rows, a.rows, a.rows, a.rows);
+      if (UP && lane * 4 < t.rows) {
+        r.x = token_of(a, t.row0 + lane * 4);
+        if (lane * 4 + 1 < t.rows) r.y = token_of(a, t.row0 + lane * 4 + 1);
+        if (lane * 4 + 2 < t.rows) r.z = token_of(a, t.row0 + lane * 4 + 2);
+        if (lane * 4 + 3 < t.rows) r.w = token_of(a, t.row0 + lane * 4 + 3);
+      }
+      return r;
+    };
+    Tile next = {};
+    int4 next_rows = {};
+    if ((int)blockIdx.x < tiles) {
+      next = tile_at<NT>(a, ctl, blockIdx.x);
+      next_rows = rows_of(next);
+    }
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      const Tile tile = next;
+      const int4 rows = next_rows;
+      if (t + (int)gridDim.x < tiles) {
+        next = tile_at<NT>(a, ctl, t + gridDim.x);
+        next_rows = rows_of(next);
+      }
+      // four rows of x at a time, or 16 that lie side by side
+      const int parts = UP ? (tile.rows + 3) / 4 : (tile.rows + 15) / 16;
+      const uint32_t bytes = parts * (UP ? 512 : 2048) + C::B_BYTES;
+      for (int kb = 0; kb < kbs; ++kb) {
+        if (!(ok = wait(&ctl->empty[s], ph ^ 1, ctl, status))) break;
+        uint8_t* dst = smem + s * C::STAGE;
+        if (elect_one()) {
+          mbar_arrive_tx(&ctl->full[s], bytes);
+          if constexpr (C::MN) {
+#pragma unroll
+            for (int j = 0; j < NT / 64; ++j)
+              tma_3d(dst + C::A_BYTES + j * 8192, &map_b, tile.n0 + j * 64, kb * C::KE, tile.e, &ctl->full[s]);
+          } else {
+            tma_3d(dst + C::A_BYTES, &map_b, kb * C::KE, tile.n0, tile.e, &ctl->full[s]);
+          }
+        }
+        __syncwarp();
+        if (lane < parts) {
+          if constexpr (UP) tma_gather4(dst + lane * 512, &map_a, kb * C::KE, rows, &ctl->full[s]);
+          else tma_2d(dst + lane * 2048, &map_a, kb * C::KE, tile.row0 + lane * 16, &ctl->full[s]);
+        }
+        __syncwarp();
+        ++sent;
+        if (++s == C::NST) { s = 0; ph ^= 1; }
+      }
+    }
+    if (!ok)                                     // given up: what is in flight still lands before the block ends
+      for (int u = max(0, sent - C::NST); u < sent; ++u) {
+        const unsigned long long since = now_ns();
+        while (!mbar_try(&ctl->full[u % C::NST], u / C::NST & 1) && now_ns() - since < WAIT_NS) {}
+      }
+  } else if (warp == 1) {                        // ---- matrix instructions, by one thread
+    if (elect_one()) {
+      constexpr uint32_t IDESC = umma_idesc(M_TILE, NT, C::MN);
+      const uint64_t a_desc = umma_desc(smem_u32(smem), 16, 1024, 2);
+      const uint64_t b_desc = umma_desc(smem_u32(smem + C::A_BYTES), C::MN ? 8192 : 16, 1024, 2);
+      const uint64_t s_desc = umma_desc(smem_u32(smem + C::OFF_SF), 16, 128, 0);
+      int s = 0, i = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
+        const uint32_t acc = tmem + (i & 1) * NT;
+        if (!(ok = wait_one(&ctl->acc_empty[i & 1], (i >> 1 & 1) ^ 1, ctl, status))) break;
+        tc_after();
+        for (int kb = 0; kb < kbs; ++kb) {
+          if (!(ok = wait_one(&ctl->full[s], ph, ctl, status))) break;
+          tc_after();
+          const uint64_t ad = a_desc + (uint32_t)(s * C::STAGE >> 4), bd = b_desc + (uint32_t)(s * C::STAGE >> 4);
+          if constexpr (E4M3) {
+            const uint64_t sd = s_desc + (uint32_t)(s * C::SF >> 4);
+            const uint32_t sf = tmem + C::T_SF + s * 16;
+#pragma unroll
+            for (int j = 0; j < 1 + C::SF_B; ++j) tmem_scales(sf + 4 * j, sd + (512 * j >> 4));
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_mx8(acc, ad + 2 * k, bd + 2 * k, umma_idesc_mx8(M_TILE, NT, k), sf, sf + 4, kb > 0 || k > 0);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_ss(acc, ad + 2 * k, bd + (C::MN ? 2048 * k >> 4 : 2 * k), IDESC, kb > 0 || k > 0);
+          }
+          umma_commit(&ctl->empty[s]);
+          if (kb == kbs - 1) umma_commit(&ctl->acc_full[i & 1]);
+          if (++s == C::NST) { s = 0; ph ^= 1; }
+        }
+      }
+      // Products and their arrivals are done before the block's memory is given
+      // back, after a wait that gave up too.
+      umma_commit(&ctl->drain);
+      const unsigned long long since = now_ns();
+      while (!mbar_try(&ctl->drain, 0) && now_ns() - since < WAIT_NS) {}
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 8) {            // ---- results: one thread a row
+    const int row = (warp - 4) * 32 + lane;
+    int i = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
+      const Tile tile = tile_at<NT>(a, ctl, t);
+      const bool live = (warp - 4) * 32 < tile.rows;
+      bool here = row < tile.rows;
+      size_t at = tile.row0 + row;
+      float gate = 1.f;
+      if (!UP && here) {
+        const int p = a.order[tile.row0 + row];
+        here = p >= 0 && p < a.pairs;
+        at = here ? p : 0;
+        if (a.gates) gate = a.gates[at];
+      }
+      if (!wait(&ctl->acc_full[i & 1], i >> 1 & 1, ctl, status)) break;
+      tc_after();
+      const uint32_t acc = tmem + (i & 1) * NT + ((uint32_t)((warp - 4) * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < NT; c += 64) {
+        uint32_t r[64];
+        if (live) {
+          tmem_ld32(acc + c, r);
+          tmem_ld32(acc + c + 32, r + 32);
+          tmem_wait_ld();
+        }
+        if (c == NT - 64) {                      // all of it read: the accumulator may be summed into again
+          tc_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->acc_empty[i & 1]);
+        }
+        if (here) store_piece<E4M3, UP>(a, r, at, gate, tile.n0 + c);
+      }
+    }
+    if constexpr (!UP) {                         // pairs without an expert
+      for (int x = ctl->row0[a.experts] + blockIdx.x; x < a.pairs; x += gridDim.x) {
+        const int p = a.order[x];
+        if (p >= 0 && p < a.pairs)
+          for (int n = row * 8; n < a.n; n += 1024)
+            *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)p * a.n + n) = make_uint4(0, 0, 0, 0);
+      }
+    }
+  } else if (E4M3 && warp >= 8) {                // ---- scales: stages warp - 8, warp - 4, ...
+    const int groups = a.k / GROUP;
+    int u = 0;                                   // stages of the tiles before
+    bool ok = true;
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, u += kbs) {
+      const Tile tile = tile_at<NT>(a, ctl, t);
+      const uint8_t* ra[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = lane + 32 * j;
+        int from = a.rows;
+        if (r < tile.rows) from = UP ? token_of(a, tile.row0 + r) : tile.row0 + r;
+        ra[j] = from < (UP ? a.rows : a.pairs) ? a.a_scales + (size_t)from * groups : nullptr;
+      }
+      const uint8_t* rb = a.b_scales + ((size_t)tile.e * a.n + tile.n0 + lane) * groups;
+      for (int kb = ((warp - 8) - u % 4 + 4) % 4; kb < kbs; kb += 4) {
+        const int s = (u + kb) % C::NST;
+        uint32_t va[4], vb[NT / 32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) va[j] = ra[j] ? scales4(ra[j], groups, kb) : 0x7f7f7f7fu;
+#pragma unroll
+        for (int j = 0; j < NT / 32; ++j)
+          vb[j] = tile.n0 + lane + 32 * j < a.n ? scales4(rb + (size_t)(32 * j) * groups, groups, kb) : 0x7f7f7f7fu;
+        if (!(ok = wait(&ctl->empty[s], ((u + kb) / C::NST & 1) ^ 1, ctl, status))) break;
+        uint4* dst = reinterpret_cast<uint4*>(smem + C::OFF_SF + s * C::SF) + lane;
+        dst[0] = make_uint4(va[0], va[1], va[2], va[3]);
+#pragma unroll
+        for (int j = 0; j < NT / 128; ++j) dst[32 + 32 * j] = make_uint4(vb[4 * j], vb[4 * j + 1], vb[4 * j + 2], vb[4 * j + 3]);
+        if constexpr (NT % 128 != 0) dst[32 + NT / 128 * 32] = make_uint4(vb[NT / 32 - 2], vb[NT / 32 - 1], 0, 0);
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->full[s]);
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 2) tmem_free<C::T_COLS>(tmem);
+}
+
+// A matrix (or one for each expert) as boxes of 128-byte rows.
+cudaError_t tensor_map(CUtensorMap* map, bool e4m3, const void* base, int dims, const cuuint64_t* dim, const cuuint32_t* box) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t el = e4m3 ? 1 : 2, stride[2] = {dim[0] * el, dim[0] * dim[1] * el};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, const_cast<void*>(base), dim,
+                stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <bool E4M3, bool UP, int NT>
+cudaError_t launch(Args a, const void* rows, const void* w, int sms, cudaStream_t st) {
+  using C = Cfg<E4M3, UP, NT>;
+  a.ntiles = (a.n + NT - 1) / NT;
+  const cuuint64_t ke = C::KE, dim_a[2] = {(cuuint64_t)a.k, (cuuint64_t)(UP ? a.rows : a.pairs)};
+  const cuuint32_t box_a[2] = {(cuuint32_t)ke, UP ? 1u : 16u};
+  const cuuint64_t dim_b[3] = {(cuuint64_t)(C::MN ? a.n : a.k), (cuuint64_t)(C::MN ? a.k : a.n), (cuuint64_t)a.experts};
+  const cuuint32_t box_b[3] = {(cuuint32_t)ke, C::MN ? 64u : (cuuint32_t)NT, 1};
+  CUtensorMap map_a, map_b;
+  cudaError_t e = tensor_map(&map_a, E4M3, rows, 2, dim_a, box_a);
+  if (e == cudaSuccess) e = tensor_map(&map_b, E4M3, w, 3, dim_b, box_b);
+  if (e == cudaSuccess) e = allow((const void*)k_experts<E4M3, UP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const long long most = ((long long)a.pairs / M_TILE + (a.pairs < a.experts ? a.pairs : a.experts)) * a.ntiles;
+  return launch_kernel(k_experts<E4M3, UP, NT>, dim3((unsigned)(most < sms ? most : sms)), C::THREADS, C::SMEM, 1, st, a, map_a,
+                       map_b);
+}
+
+template <bool E4M3, bool UP>
+cudaError_t launch(const Args& a, const void* rows, const void* w, cudaStream_t st) {
+  int sms = 0;
+  const cudaError_t e = multiprocessors(&sms);
+  if (e != cudaSuccess) return e;
+  constexpr int WIDE = E4M3 ? 192 : 256;
+  const long long mt = a.pairs / M_TILE + (a.pairs < a.experts ? a.pairs : a.experts);
+  auto tiles = [&](int nt) { return mt * ((a.n + nt - 1) / nt); };
+  if (tiles(WIDE) >= 6 * sms) return launch<E4M3, UP, WIDE>(a, rows, w, sms, st);
+  if (tiles(128) >= 4 * sms) return launch<E4M3, UP, 128>(a, rows, w, sms, st);
+  return launch<E4M3, UP, 64>(a, rows, w, sms, st);
+}
+
+int check_device(const mk_experts* m) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail_cuda("mk_experts: current device", e);
+  return dev == m->device ? MK_OK : fail(MK_ERR_INVALID, "mk_experts: the object belongs to another device than the current one");
+}
+
+}  // namespace
+}  // namespace mk
+
+extern "C" {
+
+int mk_experts_create(const mk_model_dims* dims, int rows_type, mk_experts** out) {
+  using namespace mk;
+  if (!out) return fail(MK_ERR_INVALID, "mk_experts_create: out is NULL");
+  *out = nullptr;
+  if (!dims) return fail(MK_ERR_INVALID, "mk_experts_create: dims is NULL");
+  if (rows_type != MK_ROWS_BF16 && rows_type != MK_ROWS_E4M3) return fail(MK_ERR_INVALID, "mk_experts_create: rows_type");
+  const bool e4m3 = rows_type == MK_ROWS_E4M3;
+  const int h = dims->hidden, f = dims->expert_ffn, of = e4m3 ? GROUP : 8;
+  if (h < 1 || f < 1 || dims->n_experts < 1 || dims->top_k < 1 || dims->top_k > dims->n_experts)
+    return fail(MK_ERR_INVALID, "mk_experts_create: hidden, expert_ffn, n_experts or top_k");
+  if (h % of || f % of)
+    return fail(MK_ERR_UNSUPPORTED, "mk_experts_create: hidden and expert_ffn must be multiples of 8 (8 bits: of 32)");
+  if (dims->n_experts > MAX_EXPERTS || dims->top_k > 8 || h > 32768 || f > 32768)
+    return fail(MK_ERR_UNSUPPORTED, "mk_experts_create: at most 256 experts, 8 of them a row, hidden and expert_ffn at most 32768");
+  mk_experts* m = new (std::nothrow) mk_experts();
+  if (!m) return fail(MK_ERR_CAPACITY, "out of host memory");
+  m->hidden = h; m->ffn = f; m->experts = dims->n_experts; m->k = dims->top_k; m->e4m3 = e4m3;
+  cudaError_t e = cudaGetDevice(&m->device);
+  if (e == cudaSuccess) e = cudaMalloc((void**)&m->status, sizeof(int));
+  if (e == cudaSuccess) {
+    e = cudaMemset(m->status, 0, sizeof(int));
+    if (e == cudaSuccess) e = cudaStreamSynchronize(0);
+    if (e != cudaSuccess) cudaFree(m->status);
+  }
+  if (e != cudaSuccess) {
+    delete m;
+    return fail_cuda("mk_experts_create", e);
+  }
+  *out = m;
+  return MK_OK;
+}
+
+int mk_experts_up(mk_experts* m, int rows, const void* x, const uint8_t* x_scales, const void* w, const uint8_t* w_scales,
+                  const int* first, const int* order, void* h, uint8_t* h_scales, mk_stream stream) {
+  using namespace mk;
+  if (!m) return fail(MK_ERR_INVALID, "mk_experts_up: experts is NULL");
+  if (rows < 0) return fail(MK_ERR_INVALID, "mk_experts_up: rows");
+  if (rows > (1 << 26) / m->k) return fail(MK_ERR_UNSUPPORTED, "mk_experts_up: more than 2^26 pairs");
+  if (rows == 0) return check_device(m);
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(h, 16) || !aligned(first, 4) || !aligned(order, 4) ||
+      (m->e4m3 && (!aligned(x_scales, 4) || !aligned(w_scales, 4) || !h_scales)))
+    return fail(MK_ERR_INVALID, "mk_experts_up: a buffer is NULL or not aligned (rows and weights 16 bytes, scales 4)");
+  const size_t el = m->e4m3 ? 1 : 2, t = rows, p = t * m->k, wide = m->hidden, f = m->ffn, e = m->experts;
+  const bool s8 = m->e4m3;
+  const Span s[8] = {{h, p * f * el},
+                     {s8 ? h_scales : nullptr, p * f / GROUP},
+                     {x, t * wide * el},
+                     {s8 ? x_scales : nullptr, t * wide / GROUP},
+                     {w, e * 2 * f * wide * el},
+                     {s8 ? w_scales : nullptr, e * 2 * f * wide / GROUP},
+                     {first, 4 * (e + 1)},
+                     {order, 4 * p}};
+  if (clash(s, 2, 8)) return fail(MK_ERR_INVALID, "mk_experts_up: a result overlaps another buffer");
+  const int rc = check_device(m);
+  if (rc != MK_OK) return rc;
+  Args a = {first, order, nullptr, x_scales, w_scales, (uint8_t*)h, h_scales, m->status, (int)p, rows, m->k, m->experts,
+            m->hidden, 2 * m->ffn, 0, (uintptr_t)h % 32 == 0 && f * el % 32 == 0};
+  const cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t err = s8 ? launch<true, true>(a, x, w, st) : launch<false, true>(a, x, w, st);
+  return err == cudaSuccess ? MK_OK : fail_cuda("mk_experts_up", err);
+}
+
+int mk_experts_down(mk_experts* m, int rows, const void* h, const uint8_t* h_scales, const void* w, const uint8_t* w_scales,
+                    const int* first, const int* order, const float* gates, void* y, mk_stream stream) {
+  using namespace mk;
+  if (!m) return fail(MK_ERR_INVALID, "mk_experts_down: experts is NULL");
+  if (rows < 0) return fail(MK_ERR_INVALID, "mk_experts_down: rows");
+  if (rows > (1 << 26) / m->k) return fail(MK_ERR_UNSUPPORTED, "mk_experts_down: more than 2^26 pairs");
+  if (rows == 0) return check_device(m);
+  if (!aligned(h, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(first, 4) || !aligned(order, 4) ||
+      (gates && !aligned(gates, 4)) || (m->e4m3 && (!aligned(h_scales, 4) || !aligned(w_scales, 4))))
+    return fail(MK_ERR_INVALID, "mk_experts_down: a buffer is NULL or not aligned (rows and weights 16 bytes, scales 4)");
+  const size_t el = m->e4m3 ? 1 : 2, p = (size_t)rows * m->k, wide = m->hidden, f = m->ffn, e = m->experts;
+  const bool s8 = m->e4m3;
+  const Span s[8] = {{y, p * wide * 2},
+                     {h, p * f * el},
+                     {s8 ? h_scales : nullptr, p * f / GROUP},
+                     {w, e * f * wide * el},
+                     {s8 ? w_scales : nullptr, e * f * wide / GROUP},
+                     {first, 4 * (e + 1)},
+                     {order, 4 * p},
+                     {gates, 4 * p}};
+  if (clash(s, 1, 8)) return fail(MK_ERR_INVALID, "mk_experts_down: y overlaps another buffer");
+  const int rc = check_device(m);
+  if (rc != MK_OK) return rc;
+  Args a = {first, order, gates, h_scales, w_scales, (uint8_t*)y, nullptr, m->status, (int)p, rows, m->k, m->experts,
+            m->ffn, m->hidden, 0, (uintptr_t)y % 32 == 0 && wide % 16 == 0};
+  const cudaStream_t st = (cudaStream_t)stream;
+  const cudaError_t err = s8 ? launch<true, false>(a, h, w, st) : launch<false, false>(a, h, w, st);
+  return err == cudaSuccess ? MK_OK : fail_cuda("mk_experts_down", err);
+}
+
+int mk_experts_sync(mk_experts* m, mk_stream stream) {
+  using namespace mk;
+  if (!m) return fail(MK_ERR_INVALID, "mk_experts_sync: experts is NULL");
+  const int rc = check_device(m);
+  if (rc != MK_OK) return rc;
+  int st = 0;
+  cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&st, m->status, sizeof(int), cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+  if (e == cudaSuccess && st) e = cudaMemsetAsync(m->status, 0, sizeof(int), (cudaStream_t)stream);
+  return e == cudaSuccess ? st : fail_cuda("mk_experts_sync", e);
+}
+
+void mk_experts_destroy(mk_experts* m) {
+  if (!m) return;
+  cudaFree(m->status);
+  delete m;
+}
+
+}  // extern "C"

@@ -44,6 +44,22 @@ __device__ __forceinline__ void tma_2d(void* dst, const void* map, int x, int y,
       "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ void tma_3d(void* dst, const void* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// Four rows of a matrix from the column x on, one behind the other (the map's
+// box is one row high); a row past the end reads zeros.
+__device__ __forceinline__ void tma_gather4(void* dst, const void* map, int x, int4 rows, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+      "%6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z), "r"(rows.w), "r"(smem_u32(bar))
+      : "memory");
+}
 __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    smem_u32(dst)),
@@ -86,6 +102,25 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint
       "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
       : "memory");
+}
+// Block-scaled 8-bit products (e4m3, a power-of-two scale for 32 values of a
+// row): A and B K-major in shared memory, their scales in tensor memory.  A
+// scale column holds the scales of a row's next 128 values, `part` says which
+// 32 of them.
+__host__ __device__ constexpr uint32_t umma_idesc_mx8(int m, int n, int part) {
+  return (uint32_t)part << 4 | (uint32_t)(n >> 3) << 17 | 1u << 23 | (uint32_t)(m >> 4) << 24 | (uint32_t)part << 29;
+}
+__device__ __forceinline__ void umma_mx8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa, uint32_t sb, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %6, 0;\n tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)add)
+      : "memory");
+}
+// The scales of 128 rows (32 rows of 16 bytes: row r's four at r % 32, r / 32)
+// to four columns of tensor memory, behind the matrix instructions before it.
+__device__ __forceinline__ void tmem_scales(uint32_t dst, uint64_t src) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(dst), "l"(src) : "memory");
 }
 // Arrive once every matrix instruction that this thread issued is done.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {

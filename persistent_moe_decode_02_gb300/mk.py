@@ -28,10 +28,12 @@ EXPORTS = [
     "mk_sched_commit", "mk_sched_abandon", "mk_sched_result", "mk_sched_forget", "mk_sched_stats",
     "mk_sched_destroy", "mk_serve_step", "mk_sched_next_rows", "mk_sched_set_prefill", "mk_plan_update_rows",
     "mk_sched_peek_rows", "mk_chunk_create", "mk_chunk_update", "mk_chunk_append", "mk_chunk_attend", "mk_chunk_read",
-    "mk_chunk_sync", "mk_chunk_info", "mk_chunk_destroy", "mk_chunk_inspect", "mk_probs", "mk_verify",
+    "mk_chunk_sync", "mk_chunk_info", "mk_chunk_destroy", "mk_chunk_inspect", "mk_probs", "mk_verify", "mk_norm",
+    "mk_quantize", "mk_route", "mk_experts_create", "mk_experts_up", "mk_experts_down", "mk_experts_sync",
+    "mk_experts_destroy",
 ]
 MK_KV_BF16, MK_KV_E4M3 = 0, 1
-MK_ROWS_BF16, MK_ROWS_F32 = 0, 1
+MK_ROWS_BF16, MK_ROWS_F32, MK_ROWS_E4M3 = 0, 1, 2
 
 
 class MkModelDims(ctypes.Structure):
@@ -128,13 +130,23 @@ def lib():
         L.mk_chunk_inspect.argtypes = [ctypes.POINTER(MkModelDims), i32, p_int, p_int, i32, p_int, i32]
         L.mk_probs.argtypes = [vp, i32, i32, i64, ctypes.c_float, vp, vp]
         L.mk_verify.argtypes = [i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.mk_norm.argtypes = [i32, i32, vp, i32, i64, vp, i32, i32, vp, ctypes.c_float, vp, vp, i32, vp, vp]
+        L.mk_quantize.argtypes = [i32, i32, vp, i32, i64, vp, vp, vp]
+        L.mk_route.argtypes = [i32, i32, i32, vp, i64, vp, vp, vp, vp, vp]
+        L.mk_experts_create.argtypes = [ctypes.POINTER(MkModelDims), i32, ctypes.POINTER(vp)]
+        L.mk_experts_up.argtypes = [vp, i32] + [vp] * 9
+        L.mk_experts_down.argtypes = [vp, i32] + [vp] * 9
+        L.mk_experts_sync.argtypes = [vp, vp]
+        L.mk_experts_destroy.argtypes = [vp]
+        L.mk_experts_destroy.restype = None
         for f in ("mk_plan_create", "mk_decode_step", "mk_decode_steps", "mk_decode_step_host", "mk_plan_update", "mk_plan_sync",
                   "mk_plan_read_debug", "mk_plan_info", "mk_plan_inspect", "mk_decode_step_noalloc",
                   "mk_plan_set_sampling", "mk_plan_set_top_p", "mk_sched_create", "mk_sched_submit", "mk_sched_next", "mk_sched_commit", "mk_sched_abandon",
                   "mk_sched_result", "mk_sched_forget", "mk_sched_stats", "mk_serve_step", "mk_sched_next_rows",
                   "mk_sched_set_prefill", "mk_plan_update_rows", "mk_sched_peek_rows", "mk_chunk_create",
                   "mk_chunk_update", "mk_chunk_append", "mk_chunk_attend", "mk_chunk_read", "mk_chunk_sync",
-                  "mk_chunk_info", "mk_chunk_inspect", "mk_probs", "mk_verify"):
+                  "mk_chunk_info", "mk_chunk_inspect", "mk_probs", "mk_verify", "mk_norm", "mk_quantize", "mk_route",
+                  "mk_experts_create", "mk_experts_up", "mk_experts_down", "mk_experts_sync"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -690,3 +702,170 @@ def verify(target: torch.Tensor, draft: Optional[torch.Tensor], drafts: torch.Te
                          _on(stream, dev))
     if rc != MK_OK:
         raise MkError("mk_verify", rc)
+
+
+_E4M3 = torch.float8_e4m3fn
+_ROWS = {_BF16: MK_ROWS_BF16, _F32: MK_ROWS_F32}
+
+
+def _rows(name: str, t: torch.Tensor, dev: int):
+    """Address, type and row stride of bf16 or float32 rows [rows, n] that may lie apart."""
+    if t.dim() != 2 or t.dtype not in _ROWS or t.get_device() != dev or (t.numel() and t.stride(1) != 1 and t.shape[1] != 1):
+        raise ValueError(f"{name}: bf16 or float32 rows [rows, n] of the current CUDA device are wanted")
+    return t.data_ptr(), _ROWS[t.dtype], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _codes(name: str, codes: torch.Tensor, scales: Optional[torch.Tensor], shape, dev: int):
+    """Addresses of 8-bit rows: codes float8_e4m3fn, scales uint8 of a 32nd of the last dimension."""
+    if scales is None:
+        raise ValueError(f"{name}: 8-bit rows come with their scales")
+    return _here(name, codes, _E4M3, shape, dev), _here(f"{name}'s scales", scales, _U8, (*shape[:-1], shape[-1] // 32), dev)
+
+
+def norm(x: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, out: Optional[torch.Tensor],
+         add: Optional[torch.Tensor] = None, total: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+         stream=None) -> None:
+    """t = x + add summed over its terms (fp32), out = t / sqrt(mean(t^2) + eps) * gamma (include/mk.h).  x bf16 or
+    float32 [rows, n] (rows may lie apart); add bf16 or float32 [rows, n] or [rows, terms, n]; gamma bf16 [n] or None;
+    out bf16, float32 or (with scales uint8 [rows, n / 32]) float8_e4m3fn [rows, n], or None; total like x, packed, or
+    None; it may be x itself."""
+    dev = _device()
+    at, kind, stride = _rows("x", x, dev)
+    rows, n = x.shape
+    terms, a, a_kind = 0, None, 0
+    if add is not None:
+        if add.dtype not in _ROWS or add.dim() not in (2, 3):
+            raise ValueError("add: bf16 or float32 [rows, n] or [rows, terms, n] is wanted")
+        terms, a_kind = add.shape[1] if add.dim() == 3 else 1, _ROWS[add.dtype]
+        a = _here("add", add, add.dtype, (rows, n) if add.dim() == 2 else (rows, terms, n), dev)
+    o, s, o_kind = None, None, 0
+    if out is not None and out.dtype is _E4M3:
+        (o, s), o_kind = _codes("out", out, scales, (rows, n), dev), MK_ROWS_E4M3
+    elif scales is not None:
+        raise ValueError("scales: only with an 8-bit out")
+    elif out is not None:
+        if out.dtype not in _ROWS:
+            raise ValueError("out: bf16, float32 or float8_e4m3fn is wanted")
+        o, o_kind = _here("out", out, out.dtype, x.shape, dev), _ROWS[out.dtype]
+    if not rows:
+        return
+    rc = lib().mk_norm(rows, n, at, kind, stride, a, a_kind, terms,
+                       None if gamma is None else _here("gamma", gamma, _BF16, (n,), dev), float(eps),
+                       None if total is None else _here("total", total, x.dtype, x.shape, dev), o, o_kind, s,
+                       _on(stream, dev))
+    if rc != MK_OK:
+        raise MkError("mk_norm", rc)
+
+
+def quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """Rows x [rows, n] (bf16 or float32, rows may lie apart) to 8 bits: codes float8_e4m3fn [rows, n], scales uint8
+    [rows, n / 32] (include/mk.h).  Contiguous weights of more dimensions go as x.view(-1, n)."""
+    dev = _device()
+    at, kind, stride = _rows("x", x, dev)
+    rows, n = x.shape
+    c, s = _codes("codes", codes, scales, x.shape, dev)
+    if not rows:
+        return
+    rc = lib().mk_quantize(rows, n, at, kind, stride, c, s, _on(stream, dev))
+    if rc != MK_OK:
+        raise MkError("mk_quantize", rc)
+
+
+def route(logits: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor, first: torch.Tensor, order: torch.Tensor,
+          stream=None) -> None:
+    """Each row's experts and the rows of each expert (include/mk.h): logits float32 [rows, experts] (rows may lie
+    apart); out: ids int32 and gates float32 [rows, top_k], first int32 [experts + 1], order int32 [rows * top_k]."""
+    dev = _device()
+    if logits.dim() != 2 or logits.dtype is not _F32 or logits.get_device() != dev or (
+            logits.numel() and logits.stride(1) != 1 and logits.shape[1] != 1):
+        raise ValueError("logits: float32 rows [rows, experts] of the current CUDA device are wanted")
+    if ids.dim() != 2:
+        raise ValueError("ids: int32 [rows, top_k] is wanted")
+    (rows, experts), k = logits.shape, ids.shape[1]
+    args = (_here("ids", ids, _I32, (rows, k), dev), _here("gates", gates, _F32, (rows, k), dev),
+            _here("first", first, _I32, (experts + 1,), dev), _here("order", order, _I32, (rows * k,), dev))
+    rc = lib().mk_route(rows, experts, k, logits.data_ptr() if rows else None, logits.stride(0) if rows > 1 else experts,
+                        *args, _on(stream, dev))
+    if rc != MK_OK:
+        raise MkError("mk_route", rc)
+
+
+class Experts:
+    """Owns an mk_experts: the experts' products over a chunk's rows
+    (include/mk.h).
+
+    D: dims with hidden, n_experts, top_k and expert_ffn.  rows_type: "bf16", or
+    "e4m3" (rows, weights and up's results as float8_e4m3fn codes with uint8
+    scales of a 32nd of their last dimension)."""
+
+    def __init__(self, D, rows_type: str):
+        kinds = {"bf16": MK_ROWS_BF16, "e4m3": MK_ROWS_E4M3}
+        if rows_type not in kinds:
+            raise ValueError(f"rows_type: {rows_type!r}, wanted one of {tuple(kinds)}")
+        dims = MkModelDims(hidden=D.hidden, n_experts=D.n_experts, top_k=D.top_k, expert_ffn=D.expert_ffn)
+        h = ctypes.c_void_p()
+        rc = lib().mk_experts_create(ctypes.byref(dims), kinds[rows_type], ctypes.byref(h))
+        if rc != MK_OK:
+            raise MkError("mk_experts_create", rc)
+        self.h, self.e4m3 = h, rows_type == "e4m3"
+        self.hidden, self.experts, self.top_k, self.ffn = D.hidden, D.n_experts, D.top_k, D.expert_ffn
+
+    def _two(self, name, t, scales, shape, dev):
+        if self.e4m3:
+            return _codes(name, t, scales, shape, dev)
+        if scales is not None:
+            raise ValueError(f"{name}: scales are of 8-bit rows")
+        return _here(name, t, _BF16, shape, dev), None
+
+    def _lists(self, first, order, dev):
+        pairs = order.numel()
+        if pairs % self.top_k:
+            raise ValueError(f"order: {pairs} pairs, wanted a multiple of {self.top_k}")
+        return pairs, _here("first", first, _I32, (self.experts + 1,), dev), _here("order", order, _I32, (pairs,), dev)
+
+    def up(self, x: torch.Tensor, w: torch.Tensor, first: torch.Tensor, order: torch.Tensor, h: torch.Tensor,
+           x_scales: Optional[torch.Tensor] = None, w_scales: Optional[torch.Tensor] = None,
+           h_scales: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Gate and up products with SwiGLU: x [rows, hidden], w [experts, 2 ffn, hidden] (rows interleaved), first and
+        order of route(); h [rows * top_k, ffn] in the sorted order."""
+        dev = _device()
+        pairs, f, o = self._lists(first, order, dev)
+        rows = pairs // self.top_k
+        a, sa = self._two("x", x, x_scales, (rows, self.hidden), dev)
+        b, sb = self._two("w", w, w_scales, (self.experts, 2 * self.ffn, self.hidden), dev)
+        c, sc = self._two("h", h, h_scales, (pairs, self.ffn), dev)
+        rc = lib().mk_experts_up(self.h, rows, a, sa, b, sb, f, o, c, sc, _on(stream, dev))
+        if rc != MK_OK:
+            raise MkError("mk_experts_up", rc)
+
+    def down(self, h: torch.Tensor, w: torch.Tensor, first: torch.Tensor, order: torch.Tensor,
+             gates: Optional[torch.Tensor], y: torch.Tensor, h_scales: Optional[torch.Tensor] = None,
+             w_scales: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Down products times the gates: h [rows * top_k, ffn] of up(), w [experts, ffn, hidden] (8 bits: [experts,
+        hidden, ffn]), gates float32 [rows, top_k] or None; y bf16 [rows, top_k, hidden] (or [rows * top_k, hidden])."""
+        dev = _device()
+        pairs, f, o = self._lists(first, order, dev)
+        rows = pairs // self.top_k
+        a, sa = self._two("h", h, h_scales, (pairs, self.ffn), dev)
+        b, sb = self._two("w", w, w_scales,
+                          (self.experts, self.hidden, self.ffn) if self.e4m3 else (self.experts, self.ffn, self.hidden), dev)
+        g = None if gates is None else _here("gates", gates, _F32, (rows, self.top_k), dev)
+        c = _here("y", y, _BF16, (rows, self.top_k, self.hidden) if y.dim() == 3 else (pairs, self.hidden), dev)
+        rc = lib().mk_experts_down(self.h, rows, a, sa, b, sb, f, o, g, c, _on(stream, dev))
+        if rc != MK_OK:
+            raise MkError("mk_experts_down", rc)
+
+    def sync(self, stream=None) -> int:
+        """Wait for the stream; the device status, which it clears."""
+        return lib().mk_experts_sync(self.h, _stream(stream))
+
+    def close(self):
+        if getattr(self, "h", None):
+            lib().mk_experts_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
