@@ -4,8 +4,9 @@
 //
 // C[rows of e, n] = A[rows of e, :] . W_e, on the tensor cores: tiles of 128 rows
 // of one expert by NT columns, K in steps of 128 bytes.  A tile's rows are
-// gathered by their token numbers on the way to shared memory (up), or lie side
-// by side (down); its weights are one box of a tensor map.  A block works through
+// gathered by their token numbers on the way to shared memory (up: 16-byte
+// copies of four warps), or lie side by side (down: boxes of a tensor map); its
+// weights are one box of a tensor map.  A block works through
 // the tiles t, t + blocks, ... of all experts; neighbours in that order share an
 // expert's weights, which so come from device memory once.  One accumulator in
 // tensor memory is read (SwiGLU or gates, rounding, stores) while the next one
@@ -53,12 +54,13 @@ struct Ctl {
 constexpr int CTL = 3072;
 static_assert(sizeof(Ctl) <= CTL, "control words");
 
-// Warps: 0 copies, 1 matrix instructions, 2 tensor memory, 4-7 results, 8-11
-// (8 bits) scales, a stage each in turn.
+// Warps: 0 boxes of tensor maps, 1 matrix instructions, 2 tensor memory, 4-7
+// results, 8-11 gathered rows and scales.
 template <bool E4M3, bool UP, int NT>
 struct Cfg {
   static constexpr bool MN = !E4M3 && !UP;                    // weights lie along the columns
-  static constexpr int THREADS = (E4M3 ? 12 : 8) * 32;
+  static constexpr bool LOAD = UP || E4M3;                    // rows or scales come by the threads' own copies
+  static constexpr int THREADS = (LOAD ? 12 : 8) * 32;
   static constexpr int KE = E4M3 ? 128 : 64;                  // elements of a stage
   static constexpr int A_BYTES = M_TILE * 128, B_BYTES = NT * 128, STAGE = A_BYTES + B_BYTES;
   static constexpr int SF_B = (NT + 127) / 128, SF = E4M3 ? 512 * (1 + SF_B) : 0;
@@ -73,7 +75,7 @@ struct Cfg {
 struct Args {
   const int *first, *order;
   const float* gates;
-  const uint8_t *a_scales, *b_scales;
+  const uint8_t *x, *a_scales, *b_scales;   // x: rows to gather (up)
   uint8_t* out;
   uint8_t* out_scales;
   int* status;
@@ -242,11 +244,13 @@ __device__ __forceinline__ void store_piece(const Args& a, const uint32_t* acc, 
 
 // Four scales of a row, those of the 128 values from 128 kb on.
 __device__ __forceinline__ uint32_t scales4(const uint8_t* row, int groups, int kb) {
-  if (groups % 4 == 0) return *reinterpret_cast<const uint32_t*>(row + kb * 4);
   uint32_t v = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v |= (uint32_t)(kb * 4 + i < groups ? row[kb * 4 + i] : 127) << (8 * i);
+  for (int i = 0; i < 4; ++i) v |= (uint32_t)(kb * 4 + i < groups ? row[kb * 4 + i] : 0) << (8 * i);
   return v;
+}
+__device__ __forceinline__ void store4(uint32_t dst, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
 }
 
 template <bool E4M3, bool UP, int NT>
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, NT>::THREADS, 1)
   int* status = a.status;
   if (tid == 0) {
     for (int i = 0; i < C::NST; ++i) {
-      mbar_init(&ctl->full[i], E4M3 ? 2 : 1);    // the copies' issue; the scales
+      mbar_init(&ctl->full[i], C::LOAD ? 129 : 1);   // the boxes' issue; the gathering threads
       mbar_init(&ctl->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -285,37 +289,14 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, NT>::THREADS, 1)
     int s = 0, sent = 0;
     uint32_t ph = 0;
     bool ok = true;
-    auto rows_of = [&](const Tile& t) {          // the lane's four rows of x
-      int4 r = make_int4(a.rows, a.rows, a.rows, a.rows);
-      if (UP && lane * 4 < t.rows) {
-        r.x = token_of(a, t.row0 + lane * 4);
-        if (lane * 4 + 1 < t.rows) r.y = token_of(a, t.row0 + lane * 4 + 1);
-        if (lane * 4 + 2 < t.rows) r.z = token_of(a, t.row0 + lane * 4 + 2);
-        if (lane * 4 + 3 < t.rows) r.w = token_of(a, t.row0 + lane * 4 + 3);
-      }
-      return r;
-    };
-    Tile next = {};
-    int4 next_rows = {};
-    if ((int)blockIdx.x < tiles) {
-      next = tile_at<NT>(a, ctl, blockIdx.x);
-      next_rows = rows_of(next);
-    }
     for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile tile = next;
-      const int4 rows = next_rows;
-      if (t + (int)gridDim.x < tiles) {
-        next = tile_at<NT>(a, ctl, t + gridDim.x);
-        next_rows = rows_of(next);
-      }
-      // four rows of x at a time, or 16 that lie side by side
-      const int parts = UP ? (tile.rows + 3) / 4 : (tile.rows + 15) / 16;
-      const uint32_t bytes = parts * (UP ? 512 : 2048) + C::B_BYTES;
+      const Tile tile = tile_at<NT>(a, ctl, t);
+      const int boxes = UP ? 0 : (tile.rows + 15) / 16;   // of rows that lie side by side
       for (int kb = 0; kb < kbs; ++kb) {
         if (!(ok = wait(&ctl->empty[s], ph ^ 1, ctl, status))) break;
         uint8_t* dst = smem + s * C::STAGE;
         if (elect_one()) {
-          mbar_arrive_tx(&ctl->full[s], bytes);
+          mbar_arrive_tx(&ctl->full[s], boxes * 2048 + C::B_BYTES);
           if constexpr (C::MN) {
 #pragma unroll
             for (int j = 0; j < NT / 64; ++j)
@@ -325,10 +306,7 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, NT>::THREADS, 1)
           }
         }
         __syncwarp();
-        if (lane < parts) {
-          if constexpr (UP) tma_gather4(dst + lane * 512, &map_a, kb * C::KE, rows, &ctl->full[s]);
-          else tma_2d(dst + lane * 2048, &map_a, kb * C::KE, tile.row0 + lane * 16, &ctl->full[s]);
-        }
+        if (lane < boxes) tma_2d(dst + lane * 2048, &map_a, kb * C::KE, tile.row0 + lane * 16, &ctl->full[s]);
         __syncwarp();
         ++sent;
         if (++s == C::NST) { s = 0; ph ^= 1; }
@@ -354,6 +332,7 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, NT>::THREADS, 1)
         tc_after();
         for (int kb = 0; kb < kbs; ++kb) {
           if (!(ok = wait_one(&ctl->full[s], ph, ctl, status))) break;
+          if (C::LOAD) fence_async();            // the threads' copies, before the matrix instructions read them
           tc_after();
           const uint64_t ad = a_desc + (uint32_t)(s * C::STAGE >> 4), bd = b_desc + (uint32_t)(s * C::STAGE >> 4);
           if constexpr (E4M3) {
@@ -423,40 +402,77 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, NT>::THREADS, 1)
             *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)p * a.n + n) = make_uint4(0, 0, 0, 0);
       }
     }
-  } else if (E4M3 && warp >= 8) {                // ---- scales: stages warp - 8, warp - 4, ...
-    const int groups = a.k / GROUP;
-    int u = 0;                                   // stages of the tiles before
+  } else if (C::LOAD && warp >= 8) {             // ---- gathered rows, scales: a warp has 32 rows of a stage
+    const int w = warp - 8, groups = a.k / GROUP, el = E4M3 ? 1 : 2, piece = lane % 8;
+    const size_t pitch = (size_t)a.k * el;
+    const bool words = groups % 4 == 0;          // a row's scales of a stage are an aligned word
+    // rows 4 i + lane / 8 of the warp's: a row's 8 pieces by neighbours, swizzled as the tensor maps do
+    uint32_t to[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = 4 * i + lane / 8;
+      to[i] = smem_u32(smem) + (w * 32 + row) * 128 + (piece ^ row) * 16;
+    }
+    int s = 0;
+    uint32_t ph = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, u += kbs) {
+    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
       const Tile tile = tile_at<NT>(a, ctl, t);
-      const uint8_t* ra[4];
+      const int mine = min(32, max(0, tile.rows - w * 32));   // rows of this warp
+      int from = UP ? a.rows : a.pairs;          // the lane's row
+      if (lane < mine) from = UP ? token_of(a, tile.row0 + w * 32 + lane) : tile.row0 + w * 32 + lane;
+      const bool there = from < (UP ? a.rows : a.pairs);
+      const uint8_t* src[8];
+      uint32_t some = 0;
+      if constexpr (UP) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = lane + 32 * j;
-        int from = a.rows;
-        if (r < tile.rows) from = UP ? token_of(a, tile.row0 + r) : tile.row0 + r;
-        ra[j] = from < (UP ? a.rows : a.pairs) ? a.a_scales + (size_t)from * groups : nullptr;
+        for (int i = 0; i < 8; ++i) {
+          const int r = __shfl_sync(FULL, from, 4 * i + lane / 8);
+          some |= (uint32_t)(r < a.rows) << i;
+          src[i] = a.x + (r < a.rows ? r * pitch : 0) + piece * 16;
+        }
       }
-      const uint8_t* rb = a.b_scales + ((size_t)tile.e * a.n + tile.n0 + lane) * groups;
-      for (int kb = ((warp - 8) - u % 4 + 4) % 4; kb < kbs; kb += 4) {
-        const int s = (u + kb) % C::NST;
-        uint32_t va[4], vb[NT / 32];
+      const uint8_t* sa = E4M3 ? a.a_scales + (there ? (size_t)from * groups : 0) : nullptr;
+      const uint8_t* sb = E4M3 ? a.b_scales + ((size_t)tile.e * a.n + min(tile.n0 + w * 32 + lane, a.n - 1)) * groups : nullptr;
+      for (int kb = 0; kb < kbs; ++kb) {
+        if (!(ok = wait(&ctl->empty[s], ph ^ 1, ctl, status))) break;
+        if constexpr (UP) {
+          const bool in = kb * 128 + piece * 16 < (int)pitch;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) va[j] = ra[j] ? scales4(ra[j], groups, kb) : 0x7f7f7f7fu;
+          for (int i = 0; i < 8; ++i)
+            if (4 * i < mine)
+              copy16(to[i & 1] + s * C::STAGE + (i >> 1) * 1024, src[i] + (in ? kb * 128 : 0), in && (some >> i & 1));
+        }
+        if constexpr (E4M3) {
+          // row r's word lies at r % 32, r / 32 of its 128 rows
+          const uint32_t dst = smem_u32(smem + C::OFF_SF + s * C::SF) + lane * 16 + w * 4;
+          if (words) {
+            copy4(dst, sa + kb * 4, there);
 #pragma unroll
-        for (int j = 0; j < NT / 32; ++j)
-          vb[j] = tile.n0 + lane + 32 * j < a.n ? scales4(rb + (size_t)(32 * j) * groups, groups, kb) : 0x7f7f7f7fu;
-        if (!(ok = wait(&ctl->empty[s], ((u + kb) / C::NST & 1) ^ 1, ctl, status))) break;
-        uint4* dst = reinterpret_cast<uint4*>(smem + C::OFF_SF + s * C::SF) + lane;
-        dst[0] = make_uint4(va[0], va[1], va[2], va[3]);
+            for (int j = 0; j < C::SF_B; ++j)
+              if (NT % 128 == 0 || j * 128 + w * 32 < NT) {
+                const bool in = tile.n0 + j * 128 + w * 32 + lane < a.n;
+                copy4(dst + 512 + j * 512, in ? sb + (size_t)j * 128 * groups + kb * 4 : sa, in);
+              }
+          } else {
+            store4(dst, there ? scales4(sa, groups, kb) : 0);
 #pragma unroll
-        for (int j = 0; j < NT / 128; ++j) dst[32 + 32 * j] = make_uint4(vb[4 * j], vb[4 * j + 1], vb[4 * j + 2], vb[4 * j + 3]);
-        if constexpr (NT % 128 != 0) dst[32 + NT / 128 * 32] = make_uint4(vb[NT / 32 - 2], vb[NT / 32 - 1], 0, 0);
-        fence_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->full[s]);
+            for (int j = 0; j < C::SF_B; ++j)
+              if (NT % 128 == 0 || j * 128 + w * 32 < NT)
+                store4(dst + 512 + j * 512,
+                       tile.n0 + j * 128 + w * 32 + lane < a.n ? scales4(sb + (size_t)j * 128 * groups, groups, kb) : 0);
+          }
+        }
+        if (E4M3 && !words) {
+          copies_done();
+          mbar_arrive(&ctl->full[s]);
+        } else {
+          mbar_arrive_copies(&ctl->full[s]);
+        }
+        if (++s == C::NST) { s = 0; ph ^= 1; }
       }
     }
+    copies_done();                               // nothing lands after the block's end
   }
 
   __syncwarp();
@@ -490,12 +506,12 @@ template <bool E4M3, bool UP, int NT>
 cudaError_t launch(Args a, const void* rows, const void* w, int sms, cudaStream_t st) {
   using C = Cfg<E4M3, UP, NT>;
   a.ntiles = (a.n + NT - 1) / NT;
-  const cuuint64_t ke = C::KE, dim_a[2] = {(cuuint64_t)a.k, (cuuint64_t)(UP ? a.rows : a.pairs)};
-  const cuuint32_t box_a[2] = {(cuuint32_t)ke, UP ? 1u : 16u};
+  const cuuint64_t ke = C::KE, dim_a[2] = {(cuuint64_t)a.k, (cuuint64_t)a.pairs};
+  const cuuint32_t box_a[2] = {(cuuint32_t)ke, 16};
   const cuuint64_t dim_b[3] = {(cuuint64_t)(C::MN ? a.n : a.k), (cuuint64_t)(C::MN ? a.k : a.n), (cuuint64_t)a.experts};
   const cuuint32_t box_b[3] = {(cuuint32_t)ke, C::MN ? 64u : (cuuint32_t)NT, 1};
-  CUtensorMap map_a, map_b;
-  cudaError_t e = tensor_map(&map_a, E4M3, rows, 2, dim_a, box_a);
+  CUtensorMap map_a = {}, map_b;
+  cudaError_t e = UP ? cudaSuccess : tensor_map(&map_a, E4M3, rows, 2, dim_a, box_a);
   if (e == cudaSuccess) e = tensor_map(&map_b, E4M3, w, 3, dim_b, box_b);
   if (e == cudaSuccess) e = allow((const void*)k_experts<E4M3, UP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
@@ -584,7 +600,7 @@ int mk_experts_up(mk_experts* m, int rows, const void* x, const uint8_t* x_scale
   if (clash(s, 2, 8)) return fail(MK_ERR_INVALID, "mk_experts_up: a result overlaps another buffer");
   const int rc = check_device(m);
   if (rc != MK_OK) return rc;
-  Args a = {first, order, nullptr, x_scales, w_scales, (uint8_t*)h, h_scales, m->status, (int)p, rows, m->k, m->experts,
+  Args a = {first, order, nullptr, (const uint8_t*)x, x_scales, w_scales, (uint8_t*)h, h_scales, m->status, (int)p, rows, m->k, m->experts,
             m->hidden, 2 * m->ffn, 0, (uintptr_t)h % 32 == 0 && f * el % 32 == 0};
   const cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t err = s8 ? launch<true, true>(a, x, w, st) : launch<false, true>(a, x, w, st);
@@ -614,7 +630,7 @@ int mk_experts_down(mk_experts* m, int rows, const void* h, const uint8_t* h_sca
   if (clash(s, 1, 8)) return fail(MK_ERR_INVALID, "mk_experts_down: y overlaps another buffer");
   const int rc = check_device(m);
   if (rc != MK_OK) return rc;
-  Args a = {first, order, gates, h_scales, w_scales, (uint8_t*)y, nullptr, m->status, (int)p, rows, m->k, m->experts,
+  Args a = {first, order, gates, nullptr, h_scales, w_scales, (uint8_t*)y, nullptr, m->status, (int)p, rows, m->k, m->experts,
             m->ffn, m->hidden, 0, (uintptr_t)y % 32 == 0 && wide % 16 == 0};
   const cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t err = s8 ? launch<true, false>(a, h, w, st) : launch<false, false>(a, h, w, st);
