@@ -668,7 +668,7 @@ typedef struct mk_experts mk_experts;
 
 /* Of dims only hidden, n_experts, top_k and expert_ffn are read.  rows_type:
  * MK_ROWS_BF16 (hidden and expert_ffn multiples of 8) or MK_ROWS_E4M3 (of 32).
- * At most 256 experts, top_k 8, hidden and expert_ffn 32768, 2^26 pairs.  Belongs
+ * At most 256 experts, top_k 8, hidden and expert_ffn 32768, 2^25 pairs.  Belongs
  * to the current device, where all later calls must run; not while a stream is
  * captured. */
 int mk_experts_create(const mk_model_dims* dims, int rows_type, mk_experts** out);
@@ -682,7 +682,7 @@ int mk_experts_create(const mk_model_dims* dims, int rows_type, mk_experts** out
  *   first, order  of mk_route
  *   h     device [rows * top_k, expert_ffn] of rows_type (8 bits: h_scales);
  *         rows from first[n_experts] on are left as they were
- * Buffers 16-byte aligned, x_scales and w_scales 4.  first and order may hold
+ * Buffers 16-byte aligned (scales: any).  first and order may hold
  * anything: an entry out of range is read as none. */
 int mk_experts_up(mk_experts* m, int rows, const void* x, const uint8_t* x_scales, const void* w, const uint8_t* w_scales,
                   const int* first, const int* order, void* h, uint8_t* h_scales, mk_stream stream);

@@ -41,35 +41,46 @@ namespace {
 using namespace ptx;
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int M_TILE = 128, MAX_EXPERTS = 256, MAX_STAGES = 12, SMEM_MOST = 232448;
+constexpr int MAX_EXPERTS = 256, MAX_STAGES = 12, SMEM_MOST = 232448;
 constexpr unsigned long long WAIT_NS = 2000000000ull;   // limit of every wait
 
 struct Ctl {
-  uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], drain;
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], list_full[2], list_free[2], drain;
   uint32_t tmem;
   int fail;
+  int4 list[2][32];              // the block's next tiles, as they are planned
+  int width, columns;            // columns of a tile, tiles of columns
   int row0[MAX_EXPERTS + 1];     // an expert's first row in the sorted order
   int tile0[MAX_EXPERTS + 1];    // and its first tile of rows
 };
-constexpr int CTL = 3072;
+constexpr int CTL = 4096;
 static_assert(sizeof(Ctl) <= CTL, "control words");
 
-// Warps: 0 boxes of tensor maps, 1 matrix instructions, 2 tensor memory, 4-7
-// results, 8-11 gathered rows and scales.
-template <bool E4M3, bool UP, int NT>
+// Warps: 0 boxes of tensor maps, 1 matrix instructions, 2 tensor memory, 3 the
+// list of tiles, 4-7 results, then four for gathered rows (up) and four for scales
+// (8 bits).
+//
+// AM: rows of a tile in shared memory.  The instructions take 128; what lies
+// behind a tile's rows (an older stage, weights) is multiplied too, into rows
+// that nobody reads.  NT: columns of a tile at most, G: what their number is a
+// multiple of.
+template <bool E4M3, bool UP, int AM, int NT>
 struct Cfg {
   static constexpr bool MN = !E4M3 && !UP;                    // weights lie along the columns
-  static constexpr bool LOAD = UP || E4M3;                    // rows or scales come by the threads' own copies
-  static constexpr int THREADS = (LOAD ? 12 : 8) * 32;
+  static constexpr int NGW = UP ? 4 : 0, NSW = E4M3 ? 4 : 0;   // warps that gather rows, scales
+  static constexpr int THREADS = (8 + NGW + NSW) * 32;
+  static constexpr int G = MN || (E4M3 && UP) ? 64 : 16;      // a swizzled row of columns; 32 results that share a scale
   static constexpr int KE = E4M3 ? 128 : 64;                  // elements of a stage
-  static constexpr int A_BYTES = M_TILE * 128, B_BYTES = NT * 128, STAGE = A_BYTES + B_BYTES;
+  static constexpr int A_BYTES = AM * 128, B_BYTES = NT * 128, STAGE = A_BYTES + B_BYTES;
+  static constexpr int BOX = AM < 64 ? 16 : 64;               // rows of a box of rows that lie side by side
   static constexpr int SF_B = (NT + 127) / 128, SF = E4M3 ? 512 * (1 + SF_B) : 0;
   static constexpr int FIT = (SMEM_MOST - CTL - 1024) / (STAGE + SF), NST = FIT < MAX_STAGES ? FIT : MAX_STAGES;
   static constexpr int OFF_SF = NST * STAGE, OFF_CTL = OFF_SF + NST * SF, SMEM = OFF_CTL + CTL + 1024;
   static constexpr int T_SF = 2 * NT, T_COLS = 512;           // tensor memory: two accumulators, each stage's scales
+  static constexpr int ARRIVALS = 1 + NGW * 32 + NSW;   // the boxes' issue, rows by thread, scales by warp
   static_assert(T_SF + (E4M3 ? NST * 16 : 0) <= T_COLS, "tensor memory");
   static_assert(SMEM <= SMEM_MOST, "shared memory");
-  static_assert(NT % 64 == 0, "columns of a tile");
+  static_assert(NT % 64 == 0 && AM % 32 == 0 && STAGE >= 128 * 128, "a tile");
 };
 
 struct Args {
@@ -81,7 +92,8 @@ struct Args {
   int* status;
   int pairs, rows, top_k, experts;
   int k, n;                      // elements of a row of A; columns of C
-  int ntiles;                    // tiles of columns
+  int extra;                     // what a tile costs beside its columns, in columns
+  int a_wide, b_wide;            // bytes that a row's scales may be read by
   bool wide;                     // rows of results are 32-byte aligned
 };
 
@@ -107,6 +119,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* ctl, i
 // Each expert's rows and tiles from `first`, by one warp; entries out of order or
 // out of range are moved into it, so whatever they hold, the rows stay within
 // the pairs and no row is counted twice.
+template <int AM, int NT, int G>
 __device__ __forceinline__ void set_tables(const Args& a, Ctl* ctl) {
   constexpr int PER = MAX_EXPERTS / 32;
   const int lane = threadIdx.x % 32;
@@ -132,7 +145,7 @@ __device__ __forceinline__ void set_tables(const Args& a, Ctl* ctl) {
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     f[i] = max(f[i], before);
-    tiles += (f[i] - from + M_TILE - 1) / M_TILE;
+    tiles += (f[i] - from + AM - 1) / AM;
     from = f[i];
   }
   int at = tiles;
@@ -150,31 +163,78 @@ __device__ __forceinline__ void set_tables(const Args& a, Ctl* ctl) {
       ctl->row0[e] = from;
       ctl->tile0[e] = at;
     }
-    at += (f[i] - from + M_TILE - 1) / M_TILE;
+    at += (f[i] - from + AM - 1) / AM;
     from = f[i];
   }
   if (lane == 31 && a.experts == MAX_EXPERTS) {
     ctl->row0[MAX_EXPERTS] = from;
     ctl->tile0[MAX_EXPERTS] = at;
   }
+  // The width: rounds of tiles that the blocks take, times what one takes.
+  const int all = __shfl_sync(FULL, at, 31), width = G * (lane + 1);
+  const int columns = (a.n + width - 1) / width;
+  const int rounds = (int)(((long long)all * columns + gridDim.x - 1) / gridDim.x);
+  const unsigned cost = width <= NT ? (unsigned)min((long long)rounds * (width + a.extra), 0x7fffffffll) : 0xffffffffu;
+  const unsigned best = __reduce_min_sync(FULL, cost);
+  const int who = __reduce_max_sync(FULL, cost == best ? lane : 0);
+  if (lane == who) {
+    ctl->width = width;
+    ctl->columns = columns;
+  }
 }
 
 struct Tile {
-  int e, row0, rows, n0;         // expert, first row in the sorted order, rows, first column
+  int e, row0, rows, n0, width;  // expert, first row in the sorted order, rows, first column, columns
 };
-template <int NT>
-__device__ __forceinline__ Tile tile_at(const Args& a, const Ctl* ctl, int t) {
-  const int g = t / a.ntiles;    // an expert's tiles are side by side, those of its columns in turn
-  int lo = 0, hi = a.experts - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (ctl->tile0[mid] <= g) lo = mid;
-    else hi = mid - 1;
+// A block's tiles are t, t + blocks, ...: neighbours share an expert's weights
+// in L2.  One warp plans 32 at a time (a search and divisions, which took the
+// issuing thread 500 cycles a tile) and the others read them.  (Sharing the last
+// tiles out by columns cost more than it gave: a tile takes its steps of K
+// however narrow it is.)
+template <int AM, int G>
+__device__ __forceinline__ void plan_tiles(const Args& a, Ctl* ctl) {
+  const int lane = threadIdx.x % 32, columns = ctl->columns, width = ctl->width, tiles = ctl->tile0[a.experts] * columns;
+  for (int c = 0;; ++c) {
+    if (!wait(&ctl->list_free[c & 1], (c >> 1 & 1) ^ 1, ctl, a.status)) return;
+    const int t = (c * 32 + lane) * (int)gridDim.x + (int)blockIdx.x;
+    int4 v = make_int4(0, 0, 0, 0);
+    if (t < tiles) {
+      const int g = t / columns; // an expert's tiles are side by side, those of its columns in turn
+      int lo = 0, hi = a.experts - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (ctl->tile0[mid] <= g) lo = mid;
+        else hi = mid - 1;
+      }
+      const int mt = ctl->tile0[lo + 1] - ctl->tile0[lo], in = t - ctl->tile0[lo] * columns;
+      const int n = in / mt, row0 = ctl->row0[lo] + (in - n * mt) * AM;
+      v = make_int4(lo | min(AM, ctl->row0[lo + 1] - row0) << 16, row0, n * width, min(width, (a.n - n * width + G - 1) / G * G));
+    }
+    ctl->list[c & 1][lane] = v;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ctl->list_full[c & 1]);
+    if (!__all_sync(FULL, t < tiles)) return;    // an entry without rows is behind the last one
   }
-  const int mt = ctl->tile0[lo + 1] - ctl->tile0[lo], in = t - ctl->tile0[lo] * a.ntiles;
-  const int n = in / mt, row0 = ctl->row0[lo] + (in - n * mt) * M_TILE;
-  return {lo, row0, min(M_TILE, ctl->row0[lo + 1] - row0), n * NT};
 }
+// The next tile of the list, for a thread (or a warp: the same for all its
+// lanes); one arrival frees 32 of them.
+struct Reader {
+  int i = 0;
+  template <bool WARP>
+  __device__ __forceinline__ bool next(Ctl* ctl, int* status, Tile& t) {
+    const int c = i / 32;
+    uint64_t* full = &ctl->list_full[c & 1];
+    if (i % 32 == 0 && !(WARP ? wait(full, c >> 1 & 1, ctl, status) : wait_one(full, c >> 1 & 1, ctl, status))) return false;
+    const int4 v = ctl->list[c & 1][i % 32];
+    if (v.x >> 16 == 0) return false;
+    if (++i % 32 == 0) {
+      if (WARP) __syncwarp();
+      if (!WARP || threadIdx.x % 32 == 0) mbar_arrive(&ctl->list_free[c & 1]);
+    }
+    t = {v.x & 0xffff, v.y, v.x >> 16, v.z, v.w};
+    return true;
+  }
+};
 
 // A pair's row of x; one that is none reads zeros.
 __device__ __forceinline__ int token_of(const Args& a, int at) {
@@ -204,17 +264,16 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const float* v, int le
 
 __device__ __forceinline__ float swiglu(float gate, float up) { return __fdividef(gate, 1.f + __expf(-gate)) * up; }
 
-// 64 columns of a row: up's 32 results (gate and up columns in turn), or down's
-// 64.  n: the first column.
+// 64 columns of a row from n on, those before `end`: up's 32 results (gate and up
+// columns in turn), or down's 64.
 template <bool E4M3, bool UP>
-__device__ __forceinline__ void store_piece(const Args& a, const uint32_t* acc, size_t at, float gate, int n) {
+__device__ __forceinline__ void store_piece(const Args& a, const uint32_t* acc, size_t at, float gate, int n, int end) {
   if constexpr (UP) {
     const int f = a.n / 2, u = n / 2;
     float h[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) h[i] = swiglu(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1]));
     if constexpr (E4M3) {
-      if (u >= f) return;
       float m = 0.f;
 #pragma unroll
       for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(h[i]));
@@ -227,8 +286,8 @@ __device__ __forceinline__ void store_piece(const Args& a, const uint32_t* acc, 
       a.out_scales[at * (f / GROUP) + u / GROUP] = (uint8_t)(k + 127);
     } else {
       __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + at * f + u;
-      store16(p, h, f - u, a.wide);
-      store16(p + 16, h + 16, f - u - 16, a.wide);
+      store16(p, h, end / 2 - u, a.wide);
+      store16(p + 16, h + 16, end / 2 - u - 16, a.wide);
     }
   } else {
     __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + at * a.n + n;
@@ -237,26 +296,43 @@ __device__ __forceinline__ void store_piece(const Args& a, const uint32_t* acc, 
       float y[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(acc[i + j]) * gate;
-      store16(p + i, y, a.n - n - i, a.wide);
+      store16(p + i, y, end - n - i, a.wide);
     }
   }
 }
 
-// Four scales of a row, those of the 128 values from 128 kb on.
-__device__ __forceinline__ uint32_t scales4(const uint8_t* row, int groups, int kb) {
-  uint32_t v = 0;
+// A row's scales of four stages from kb on, a word each; `wide` bytes at a time.
+__device__ __forceinline__ uint4 scales16(const uint8_t* row, int groups, int kb, int wide) {
+  const uint8_t* p = row + kb * 4;
+  const int left = groups - kb * 4;
+  if (wide == 16) return *reinterpret_cast<const uint4*>(p);
+  uint32_t v[4] = {0, 0, 0, 0};
+  if (wide == 8) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v |= (uint32_t)(kb * 4 + i < groups ? row[kb * 4 + i] : 0) << (8 * i);
-  return v;
+    for (int i = 0; i < 2; ++i)
+      if (8 * i < left) {
+        const uint2 w = reinterpret_cast<const uint2*>(p)[i];
+        v[2 * i] = w.x;
+        v[2 * i + 1] = w.y;
+      }
+  } else if (wide == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (4 * i < left) v[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < left) v[i / 4] |= (uint32_t)p[i] << (i % 4 * 8);
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
 }
-__device__ __forceinline__ void store4(uint32_t dst, uint32_t v) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(v) : "memory");
-}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-template <bool E4M3, bool UP, int NT>
-__global__ void __launch_bounds__(Cfg<E4M3, UP, NT>::THREADS, 1)
-    k_experts(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b) {
-  using C = Cfg<E4M3, UP, NT>;
+template <bool E4M3, bool UP, int AM, int NT>
+__global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
+    k_experts(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+              const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_d) {
+  using C = Cfg<E4M3, UP, AM, NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023);
   Ctl* ctl = reinterpret_cast<Ctl*>(smem + C::OFF_CTL);
@@ -264,12 +340,16 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, NT>::THREADS, 1)
   int* status = a.status;
   if (tid == 0) {
     for (int i = 0; i < C::NST; ++i) {
-      mbar_init(&ctl->full[i], C::LOAD ? 129 : 1);   // the boxes' issue; the gathering threads
+      mbar_init(&ctl->full[i], C::ARRIVALS);
       mbar_init(&ctl->empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->acc_full[i], 1);
       mbar_init(&ctl->acc_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->list_full[i], 1);
+      mbar_init(&ctl->list_free[i], 6 + C::NGW + C::NSW);   // the reading warps
     }
     mbar_init(&ctl->drain, 1);
     ctl->fail = 0;
@@ -278,61 +358,66 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, NT>::THREADS, 1)
   if (warp == 2) tmem_alloc<C::T_COLS>(&ctl->tmem);
   await_stream();
   allow_next();
-  if (warp == 3) set_tables(a, ctl);
+  if (warp == 3) set_tables<AM, NT, C::G>(a, ctl);
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = ctl->tmem;
-  const int tiles = ctl->tile0[a.experts] * a.ntiles, kbs = (a.k + C::KE - 1) / C::KE;
+  const int kbs = (a.k + C::KE - 1) / C::KE;
+  Reader list;
+  Tile tile;
 
-  if (warp == 0) {                               // ---- copies
-    int s = 0, sent = 0;
-    uint32_t ph = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile tile = tile_at<NT>(a, ctl, t);
-      const int boxes = UP ? 0 : (tile.rows + 15) / 16;   // of rows that lie side by side
-      for (int kb = 0; kb < kbs; ++kb) {
-        if (!(ok = wait(&ctl->empty[s], ph ^ 1, ctl, status))) break;
-        uint8_t* dst = smem + s * C::STAGE;
-        if (elect_one()) {
-          mbar_arrive_tx(&ctl->full[s], boxes * 2048 + C::B_BYTES);
+  if (warp == 0) {                               // ---- boxes: weights, rows that lie side by side; by one thread
+    if (elect_one()) {
+      int s = 0, sent = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      while (ok && list.next<false>(ctl, status, tile)) {
+        const int boxes = UP ? 0 : (tile.rows + C::BOX - 1) / C::BOX;
+        const uint32_t bytes = (boxes * C::BOX + tile.width) * 128;
+        for (int kb = 0; kb < kbs; ++kb) {
+          uint64_t *full = &ctl->full[s], *empty = &ctl->empty[s];
+          if (!(ok = wait_one(empty, ph ^ 1, ctl, status))) break;
+          uint8_t *dst = smem + s * C::STAGE, *w = dst + C::A_BYTES;
+          mbar_arrive_tx(full, bytes);
           if constexpr (C::MN) {
-#pragma unroll
-            for (int j = 0; j < NT / 64; ++j)
-              tma_3d(dst + C::A_BYTES + j * 8192, &map_b, tile.n0 + j * 64, kb * C::KE, tile.e, &ctl->full[s]);
+            for (int n = 0; n < tile.width; n += 64) tma_3d(w + n * 128, &map_c, tile.n0 + n, kb * C::KE, tile.e, full);
+          } else if (tile.width == NT) {
+            tma_3d(w, &map_b, kb * C::KE, tile.n0, tile.e, full);
           } else {
-            tma_3d(dst + C::A_BYTES, &map_b, kb * C::KE, tile.n0, tile.e, &ctl->full[s]);
+            int n = 0;
+            for (; n + 64 <= tile.width; n += 64) tma_3d(w + n * 128, &map_c, kb * C::KE, tile.n0 + n, tile.e, full);
+            if constexpr (C::G < 64)
+              for (; n < tile.width; n += 16) tma_3d(w + n * 128, &map_d, kb * C::KE, tile.n0 + n, tile.e, full);
           }
+          for (int i = 0; i < boxes; ++i) tma_2d(dst + i * C::BOX * 128, &map_a, kb * C::KE, tile.row0 + i * C::BOX, full);
+          ++sent;
+          if (++s == C::NST) { s = 0; ph ^= 1; }
         }
-        __syncwarp();
-        if (lane < boxes) tma_2d(dst + lane * 2048, &map_a, kb * C::KE, tile.row0 + lane * 16, &ctl->full[s]);
-        __syncwarp();
-        ++sent;
-        if (++s == C::NST) { s = 0; ph ^= 1; }
       }
+      if (!ok)                                   // given up: what is in flight still lands before the block ends
+        for (int u = max(0, sent - C::NST); u < sent; ++u) {
+          const unsigned long long since = now_ns();
+          while (!mbar_try(&ctl->full[u % C::NST], u / C::NST & 1) && now_ns() - since < WAIT_NS) {}
+        }
     }
-    if (!ok)                                     // given up: what is in flight still lands before the block ends
-      for (int u = max(0, sent - C::NST); u < sent; ++u) {
-        const unsigned long long since = now_ns();
-        while (!mbar_try(&ctl->full[u % C::NST], u / C::NST & 1) && now_ns() - since < WAIT_NS) {}
-      }
+    __syncwarp();
   } else if (warp == 1) {                        // ---- matrix instructions, by one thread
     if (elect_one()) {
-      constexpr uint32_t IDESC = umma_idesc(M_TILE, NT, C::MN);
       const uint64_t a_desc = umma_desc(smem_u32(smem), 16, 1024, 2);
       const uint64_t b_desc = umma_desc(smem_u32(smem + C::A_BYTES), C::MN ? 8192 : 16, 1024, 2);
       const uint64_t s_desc = umma_desc(smem_u32(smem + C::OFF_SF), 16, 128, 0);
       int s = 0, i = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
+      for (; ok && list.next<false>(ctl, status, tile); ++i) {
         const uint32_t acc = tmem + (i & 1) * NT;
+        const uint32_t columns = (uint32_t)(tile.width >> 3) << 17;
         if (!(ok = wait_one(&ctl->acc_empty[i & 1], (i >> 1 & 1) ^ 1, ctl, status))) break;
         tc_after();
         for (int kb = 0; kb < kbs; ++kb) {
           if (!(ok = wait_one(&ctl->full[s], ph, ctl, status))) break;
-          if (C::LOAD) fence_async();            // the threads' copies, before the matrix instructions read them
+          if (UP) fence_async();                 // the threads' copies, before the matrix instructions read them
           tc_after();
           const uint64_t ad = a_desc + (uint32_t)(s * C::STAGE >> 4), bd = b_desc + (uint32_t)(s * C::STAGE >> 4);
           if constexpr (E4M3) {
@@ -342,11 +427,11 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, NT>::THREADS, 1)
             for (int j = 0; j < 1 + C::SF_B; ++j) tmem_scales(sf + 4 * j, sd + (512 * j >> 4));
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_mx8(acc, ad + 2 * k, bd + 2 * k, umma_idesc_mx8(M_TILE, NT, k), sf, sf + 4, kb > 0 || k > 0);
+              umma_mx8(acc, ad + 2 * k, bd + 2 * k, umma_idesc_mx8(128, 0, k) | columns, sf, sf + 4, kb > 0 || k > 0);
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              umma_ss(acc, ad + 2 * k, bd + (C::MN ? 2048 * k >> 4 : 2 * k), IDESC, kb > 0 || k > 0);
+              umma_ss(acc, ad + 2 * k, bd + (C::MN ? 2048 * k >> 4 : 2 * k), umma_idesc(128, 0, C::MN) | columns, kb > 0 || k > 0);
           }
           umma_commit(&ctl->empty[s]);
           if (kb == kbs - 1) umma_commit(&ctl->acc_full[i & 1]);
@@ -360,11 +445,11 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, NT>::THREADS, 1)
       while (!mbar_try(&ctl->drain, 0) && now_ns() - since < WAIT_NS) {}
     }
     __syncwarp();
+  } else if (warp == 3) {                        // ---- the list of tiles
+    plan_tiles<AM, C::G>(a, ctl);
   } else if (warp >= 4 && warp < 8) {            // ---- results: one thread a row
     const int row = (warp - 4) * 32 + lane;
-    int i = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
-      const Tile tile = tile_at<NT>(a, ctl, t);
+    for (int i = 0; list.next<true>(ctl, status, tile); ++i) {
       const bool live = (warp - 4) * 32 < tile.rows;
       bool here = row < tile.rows;
       size_t at = tile.row0 + row;
@@ -378,20 +463,21 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, NT>::THREADS, 1)
       if (!wait(&ctl->acc_full[i & 1], i >> 1 & 1, ctl, status)) break;
       tc_after();
       const uint32_t acc = tmem + (i & 1) * NT + ((uint32_t)((warp - 4) * 32) << 16);
+      const int end = min(a.n, tile.n0 + tile.width);
 #pragma unroll 1
-      for (int c = 0; c < NT; c += 64) {
+      for (int c = 0; c < tile.width; c += 64) {
         uint32_t r[64];
         if (live) {
           tmem_ld32(acc + c, r);
           tmem_ld32(acc + c + 32, r + 32);
           tmem_wait_ld();
         }
-        if (c == NT - 64) {                      // all of it read: the accumulator may be summed into again
+        if (c + 64 >= tile.width) {              // all of it read: the accumulator may be summed into again
           tc_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->acc_empty[i & 1]);
         }
-        if (here) store_piece<E4M3, UP>(a, r, at, gate, tile.n0 + c);
+        if (here) store_piece<E4M3, UP>(a, r, at, gate, tile.n0 + c, end);
       }
     }
     if constexpr (!UP) {                         // pairs without an expert
@@ -402,77 +488,107 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, NT>::THREADS, 1)
             *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)p * a.n + n) = make_uint4(0, 0, 0, 0);
       }
     }
-  } else if (C::LOAD && warp >= 8) {             // ---- gathered rows, scales: a warp has 32 rows of a stage
-    const int w = warp - 8, groups = a.k / GROUP, el = E4M3 ? 1 : 2, piece = lane % 8;
-    const size_t pitch = (size_t)a.k * el;
-    const bool words = groups % 4 == 0;          // a row's scales of a stage are an aligned word
+  } else if (UP && warp >= 8 && warp < 8 + C::NGW) {   // ---- gathered rows
+    constexpr int RW = AM / (UP ? C::NGW : 1), NI = RW / 4;   // the warp's rows of a stage, its copies of 4 rows
+    const int w = warp - 8, piece = lane % 8;
+    const size_t pitch = (size_t)a.k * (E4M3 ? 1 : 2);
     // rows 4 i + lane / 8 of the warp's: a row's 8 pieces by neighbours, swizzled as the tensor maps do
     uint32_t to[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int row = 4 * i + lane / 8;
-      to[i] = smem_u32(smem) + (w * 32 + row) * 128 + (piece ^ row) * 16;
+      const int row = w * RW + 4 * i + lane / 8;
+      to[i] = smem_u32(smem) + row * 128 + (piece ^ (row & 7)) * 16;
     }
+    int from[(RW + 31) / 32];                    // the lane's rows of x, of the tile to come
+    auto rows_of = [&](const Tile& t) {
+#pragma unroll
+      for (int j = 0; j < (RW + 31) / 32; ++j) {
+        const int r = j * 32 + lane;
+        from[j] = r < RW && w * RW + r < t.rows ? token_of(a, t.row0 + w * RW + r) : a.rows;
+      }
+    };
     int s = 0;
     uint32_t ph = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-      const Tile tile = tile_at<NT>(a, ctl, t);
-      const int mine = min(32, max(0, tile.rows - w * 32));   // rows of this warp
-      int from = UP ? a.rows : a.pairs;          // the lane's row
-      if (lane < mine) from = UP ? token_of(a, tile.row0 + w * 32 + lane) : tile.row0 + w * 32 + lane;
-      const bool there = from < (UP ? a.rows : a.pairs);
-      const uint8_t* src[8];
+    bool ok = true, more = list.next<true>(ctl, status, tile);
+    if (more) rows_of(tile);
+    while (ok && more) {
+      const int mine = min(RW, max(0, tile.rows - w * RW));
+      const uint8_t* src[NI];
       uint32_t some = 0;
-      if constexpr (UP) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = __shfl_sync(FULL, from, 4 * i + lane / 8);
-          some |= (uint32_t)(r < a.rows) << i;
-          src[i] = a.x + (r < a.rows ? r * pitch : 0) + piece * 16;
-        }
+      for (int i = 0; i < NI; ++i) {
+        const int r = __shfl_sync(FULL, from[i / 8], 4 * i % 32 + lane / 8);
+        some |= (uint32_t)(r < a.rows) << i;
+        src[i] = a.x + (r < a.rows ? r * pitch : 0) + piece * 16;
       }
-      const uint8_t* sa = E4M3 ? a.a_scales + (there ? (size_t)from * groups : 0) : nullptr;
-      const uint8_t* sb = E4M3 ? a.b_scales + ((size_t)tile.e * a.n + min(tile.n0 + w * 32 + lane, a.n - 1)) * groups : nullptr;
+      if ((more = list.next<true>(ctl, status, tile))) rows_of(tile);
       for (int kb = 0; kb < kbs; ++kb) {
         if (!(ok = wait(&ctl->empty[s], ph ^ 1, ctl, status))) break;
-        if constexpr (UP) {
-          const bool in = kb * 128 + piece * 16 < (int)pitch;
+        const bool in = kb * 128 + piece * 16 < (int)pitch;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (4 * i < mine)
-              copy16(to[i & 1] + s * C::STAGE + (i >> 1) * 1024, src[i] + (in ? kb * 128 : 0), in && (some >> i & 1));
-        }
-        if constexpr (E4M3) {
-          // row r's word lies at r % 32, r / 32 of its 128 rows
-          const uint32_t dst = smem_u32(smem + C::OFF_SF + s * C::SF) + lane * 16 + w * 4;
-          if (words) {
-            copy4(dst, sa + kb * 4, there);
-#pragma unroll
-            for (int j = 0; j < C::SF_B; ++j)
-              if (NT % 128 == 0 || j * 128 + w * 32 < NT) {
-                const bool in = tile.n0 + j * 128 + w * 32 + lane < a.n;
-                copy4(dst + 512 + j * 512, in ? sb + (size_t)j * 128 * groups + kb * 4 : sa, in);
-              }
-          } else {
-            store4(dst, there ? scales4(sa, groups, kb) : 0);
-#pragma unroll
-            for (int j = 0; j < C::SF_B; ++j)
-              if (NT % 128 == 0 || j * 128 + w * 32 < NT)
-                store4(dst + 512 + j * 512,
-                       tile.n0 + j * 128 + w * 32 + lane < a.n ? scales4(sb + (size_t)j * 128 * groups, groups, kb) : 0);
-          }
-        }
-        if (E4M3 && !words) {
-          copies_done();
-          mbar_arrive(&ctl->full[s]);
-        } else {
-          mbar_arrive_copies(&ctl->full[s]);
-        }
+        for (int i = 0; i < NI; ++i)
+          if (4 * i < mine)
+            copy16(to[i & 1] + s * C::STAGE + (i >> 1) * 1024, src[i] + (in ? kb * 128 : 0), in && (some >> i & 1));
+        mbar_arrive_copies(&ctl->full[s]);
         if (++s == C::NST) { s = 0; ph ^= 1; }
       }
     }
     copies_done();                               // nothing lands after the block's end
+  } else if (E4M3 && warp >= 8 + C::NGW) {       // ---- scales: a warp has a quarter of every stage's rows
+    // (Every warp passes every stage: a phase is told from its neighbours by its
+    // parity alone, so nobody may be two of them away from the one it waits for.)
+    constexpr int RW = AM / 4, SF_B = C::SF_B;
+    const int w = warp - 8 - C::NGW, groups = a.k / GROUP, r = w * RW + lane, c = w * 32 + lane;
+    // row r's scales of a stage are the word at r % 32, r / 32 of its 128 rows
+    uint8_t *const sf_a = smem + C::OFF_SF + r % 32 * 16 + r / 32 * 4, *const sf_b = smem + C::OFF_SF + 512 + lane * 16 + w * 4;
+    struct Four {                                // the lane's rows' scales of four stages
+      uint4 a, b[SF_B ? SF_B : 1];
+    };
+    const uint8_t *pa = nullptr, *pb = nullptr;  // the lane's rows of the tile that is being fetched
+    int kb = kbs;
+    auto fetch = [&](Four& f) {                  // the next four stages, of the next tile where need be
+      if (kb >= kbs) {
+        if (!list.next<true>(ctl, status, tile)) return false;
+        const int limit = UP ? a.rows : a.pairs;
+        const int from = lane >= RW || r >= tile.rows ? limit : UP ? token_of(a, tile.row0 + r) : tile.row0 + r;
+        pa = from < limit ? a.a_scales + (size_t)from * groups : nullptr;
+        pb = a.b_scales + ((size_t)tile.e * a.n + tile.n0 + c) * groups;
+        kb = 0;
+      }
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      f.a = pa ? scales16(pa, groups, kb, a.a_wide) : none;
+#pragma unroll
+      for (int j = 0; j < SF_B; ++j) {
+        const int n = j * 128 + c;
+        f.b[j] = n < tile.width && tile.n0 + n < a.n ? scales16(pb + (size_t)(j * 128) * groups, groups, kb, a.b_wide) : none;
+      }
+      kb += 4;
+      return true;
+    };
+    Four now, next, after;                       // two are on their way while one is stored
+    bool has = fetch(now), has_next = has && fetch(next), ok = true;
+    int s = 0, at = 0;
+    uint32_t ph = 0;
+    while (has && ok) {
+      const bool has_after = has_next && fetch(after);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (at + i >= kbs || !ok || !(ok = wait(&ctl->empty[s], ph ^ 1, ctl, status))) break;
+        if (lane < RW) *reinterpret_cast<uint32_t*>(sf_a + s * C::SF) = word(now.a, i);
+#pragma unroll
+        for (int j = 0; j < SF_B; ++j)
+          if (NT % 128 == 0 || j * 128 + w * 32 < NT) *reinterpret_cast<uint32_t*>(sf_b + s * C::SF + j * 512) = word(now.b[j], i);
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->full[s]);
+        if (++s == C::NST) { s = 0; ph ^= 1; }
+      }
+      at = at + 4 < kbs ? at + 4 : 0;
+      now = next;
+      next = after;
+      has = has_next;
+      has_next = has_after;
+    }
   }
 
   __syncwarp();
@@ -502,22 +618,32 @@ cudaError_t tensor_map(CUtensorMap* map, bool e4m3, const void* base, int dims, 
              : cudaErrorInvalidValue;
 }
 
-template <bool E4M3, bool UP, int NT>
+int scales_wide(const void* p, int groups) {
+  for (int w = 16; w > 2; w /= 2)
+    if (groups % w == 0 && (uintptr_t)p % w == 0) return w;
+  return 1;
+}
+
+template <bool E4M3, bool UP, int AM, int NT>
 cudaError_t launch(Args a, const void* rows, const void* w, int sms, cudaStream_t st) {
-  using C = Cfg<E4M3, UP, NT>;
-  a.ntiles = (a.n + NT - 1) / NT;
-  const cuuint64_t ke = C::KE, dim_a[2] = {(cuuint64_t)a.k, (cuuint64_t)a.pairs};
-  const cuuint32_t box_a[2] = {(cuuint32_t)ke, 16};
+  using C = Cfg<E4M3, UP, AM, NT>;
+  a.extra = AM;                  // the rows' bytes
+  a.a_wide = scales_wide(a.a_scales, a.k / GROUP);
+  a.b_wide = scales_wide(a.b_scales, a.k / GROUP);
+  const cuuint64_t dim_a[2] = {(cuuint64_t)a.k, (cuuint64_t)a.pairs};
+  const cuuint32_t box_a[2] = {C::KE, C::BOX};
   const cuuint64_t dim_b[3] = {(cuuint64_t)(C::MN ? a.n : a.k), (cuuint64_t)(C::MN ? a.k : a.n), (cuuint64_t)a.experts};
-  const cuuint32_t box_b[3] = {(cuuint32_t)ke, C::MN ? 64u : (cuuint32_t)NT, 1};
-  CUtensorMap map_a = {}, map_b;
+  const cuuint32_t box_b[3] = {C::KE, NT, 1}, box_c[3] = {C::KE, 64, 1}, box_d[3] = {C::KE, 16, 1};
+  CUtensorMap map_a = {}, map_b = {}, map_c, map_d = {};
   cudaError_t e = UP ? cudaSuccess : tensor_map(&map_a, E4M3, rows, 2, dim_a, box_a);
-  if (e == cudaSuccess) e = tensor_map(&map_b, E4M3, w, 3, dim_b, box_b);
-  if (e == cudaSuccess) e = allow((const void*)k_experts<E4M3, UP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e == cudaSuccess && !C::MN) e = tensor_map(&map_b, E4M3, w, 3, dim_b, box_b);
+  if (e == cudaSuccess) e = tensor_map(&map_c, E4M3, w, 3, dim_b, box_c);
+  if (e == cudaSuccess && C::G < 64) e = tensor_map(&map_d, E4M3, w, 3, dim_b, box_d);
+  if (e == cudaSuccess) e = allow((const void*)k_experts<E4M3, UP, AM, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const long long most = ((long long)a.pairs / M_TILE + (a.pairs < a.experts ? a.pairs : a.experts)) * a.ntiles;
-  return launch_kernel(k_experts<E4M3, UP, NT>, dim3((unsigned)(most < sms ? most : sms)), C::THREADS, C::SMEM, 1, st, a, map_a,
-                       map_b);
+  const long long most = ((long long)a.pairs / AM + (a.pairs < a.experts ? a.pairs : a.experts)) * ((a.n + C::G - 1) / C::G);
+  return launch_kernel(k_experts<E4M3, UP, AM, NT>, dim3((unsigned)(most < sms ? most : sms)), C::THREADS, C::SMEM, 1, st, a,
+                       map_a, map_b, map_c, map_d);
 }
 
 template <bool E4M3, bool UP>
@@ -525,12 +651,8 @@ cudaError_t launch(const Args& a, const void* rows, const void* w, cudaStream_t 
   int sms = 0;
   const cudaError_t e = multiprocessors(&sms);
   if (e != cudaSuccess) return e;
-  constexpr int WIDE = E4M3 ? 192 : 256;
-  const long long mt = a.pairs / M_TILE + (a.pairs < a.experts ? a.pairs : a.experts);
-  auto tiles = [&](int nt) { return mt * ((a.n + nt - 1) / nt); };
-  if (tiles(WIDE) >= 6 * sms) return launch<E4M3, UP, WIDE>(a, rows, w, sms, st);
-  if (tiles(128) >= 4 * sms) return launch<E4M3, UP, 128>(a, rows, w, sms, st);
-  return launch<E4M3, UP, 64>(a, rows, w, sms, st);
+  if (a.pairs <= 16 * a.experts) return launch<E4M3, UP, 32, 128>(a, rows, w, sms, st);
+  return launch<E4M3, UP, 128, E4M3 ? 192 : 256>(a, rows, w, sms, st);
 }
 
 int check_device(const mk_experts* m) {
@@ -582,11 +704,11 @@ int mk_experts_up(mk_experts* m, int rows, const void* x, const uint8_t* x_scale
   using namespace mk;
   if (!m) return fail(MK_ERR_INVALID, "mk_experts_up: experts is NULL");
   if (rows < 0) return fail(MK_ERR_INVALID, "mk_experts_up: rows");
-  if (rows > (1 << 26) / m->k) return fail(MK_ERR_UNSUPPORTED, "mk_experts_up: more than 2^26 pairs");
+  if (rows > (1 << 25) / m->k) return fail(MK_ERR_UNSUPPORTED, "mk_experts_up: more than 2^25 pairs");
   if (rows == 0) return check_device(m);
   if (!aligned(x, 16) || !aligned(w, 16) || !aligned(h, 16) || !aligned(first, 4) || !aligned(order, 4) ||
-      (m->e4m3 && (!aligned(x_scales, 4) || !aligned(w_scales, 4) || !h_scales)))
-    return fail(MK_ERR_INVALID, "mk_experts_up: a buffer is NULL or not aligned (rows and weights 16 bytes, scales 4)");
+      (m->e4m3 && (!x_scales || !w_scales || !h_scales)))
+    return fail(MK_ERR_INVALID, "mk_experts_up: a buffer is NULL or not aligned (rows and weights 16 bytes)");
   const size_t el = m->e4m3 ? 1 : 2, t = rows, p = t * m->k, wide = m->hidden, f = m->ffn, e = m->experts;
   const bool s8 = m->e4m3;
   const Span s[8] = {{h, p * f * el},
@@ -612,11 +734,11 @@ int mk_experts_down(mk_experts* m, int rows, const void* h, const uint8_t* h_sca
   using namespace mk;
   if (!m) return fail(MK_ERR_INVALID, "mk_experts_down: experts is NULL");
   if (rows < 0) return fail(MK_ERR_INVALID, "mk_experts_down: rows");
-  if (rows > (1 << 26) / m->k) return fail(MK_ERR_UNSUPPORTED, "mk_experts_down: more than 2^26 pairs");
+  if (rows > (1 << 25) / m->k) return fail(MK_ERR_UNSUPPORTED, "mk_experts_down: more than 2^25 pairs");
   if (rows == 0) return check_device(m);
   if (!aligned(h, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(first, 4) || !aligned(order, 4) ||
-      (gates && !aligned(gates, 4)) || (m->e4m3 && (!aligned(h_scales, 4) || !aligned(w_scales, 4))))
-    return fail(MK_ERR_INVALID, "mk_experts_down: a buffer is NULL or not aligned (rows and weights 16 bytes, scales 4)");
+      (gates && !aligned(gates, 4)) || (m->e4m3 && (!h_scales || !w_scales)))
+    return fail(MK_ERR_INVALID, "mk_experts_down: a buffer is NULL or not aligned (rows and weights 16 bytes)");
   const size_t el = m->e4m3 ? 1 : 2, p = (size_t)rows * m->k, wide = m->hidden, f = m->ffn, e = m->experts;
   const bool s8 = m->e4m3;
   const Span s[8] = {{y, p * wide * 2},

@@ -277,6 +277,15 @@ def test_products_full_size(mk, kind, rows):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_products_of_many_tiles(mk, kind):
+    # more than 64 tiles a block: the list of tiles is planned piece by piece, the rings turn over many times
+    c = Case(kind, (32, 256, 8, 2560), routed((32, 256, 8, 2560), 512), 21)
+    check_up(mk, c)
+    c = Case(kind, (5120, 256, 8, 32), routed((5120, 256, 8, 32), 512), 22)
+    check_down(mk, c)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("counts", [[0, 128, 0, 0], [127, 0, 1, 129], [0, 0, 0, 513], [256, 255, 257, 1], [16, 17, 15, 4]])
 def test_products_tile_borders(mk, kind, counts):
     D = DIMS["tail"]
