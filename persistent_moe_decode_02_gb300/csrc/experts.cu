@@ -74,8 +74,12 @@ struct Cfg {
   static constexpr int A_BYTES = AM * 128, B_BYTES = NT * 128, STAGE = A_BYTES + B_BYTES;
   static constexpr int BOX = AM < 64 ? 16 : 64;               // rows of a box of rows that lie side by side
   static constexpr int SF_B = (NT + 127) / 128, SF = E4M3 ? 512 * (1 + SF_B) : 0;
-  static constexpr int FIT = (SMEM_MOST - CTL - 1024) / (STAGE + SF), NST = FIT < MAX_STAGES ? FIT : MAX_STAGES;
-  static constexpr int OFF_SF = NST * STAGE, OFF_CTL = OFF_SF + NST * SF, SMEM = OFF_CTL + CTL + 1024;
+  // Results leave by rows of RB bytes that are put together in shared memory:
+  // whole lines instead of a sector of each of 32 rows.
+  static constexpr int RB = !E4M3 ? 128 : UP ? 96 : 64, PITCH = RB + 16, OUT = AM * PITCH;
+  static constexpr int STEP = UP ? 64 : RB / 2;               // columns at a time
+  static constexpr int FIT = (SMEM_MOST - CTL - 1024 - OUT) / (STAGE + SF), NST = FIT < MAX_STAGES ? FIT : MAX_STAGES;
+  static constexpr int OFF_SF = NST * STAGE, OFF_OUT = OFF_SF + NST * SF, OFF_CTL = OFF_OUT + OUT, SMEM = OFF_CTL + CTL + 1024;
   static constexpr int T_SF = 2 * NT, T_COLS = 512;           // tensor memory: two accumulators, each stage's scales
   static constexpr int ARRIVALS = 1 + NGW * 32 + NSW;   // the boxes' issue, rows by thread, scales by warp
   static_assert(T_SF + (E4M3 ? NST * 16 : 0) <= T_COLS, "tensor memory");
@@ -94,7 +98,6 @@ struct Args {
   int k, n;                      // elements of a row of A; columns of C
   int extra;                     // what a tile costs beside its columns, in columns
   int a_wide, b_wide;            // bytes that a row's scales may be read by
-  bool wide;                     // rows of results are 32-byte aligned
 };
 
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Ctl* ctl, int* status) {
@@ -242,62 +245,65 @@ __device__ __forceinline__ int token_of(const Args& a, int at) {
   return p >= 0 && p < a.pairs ? p / a.top_k : a.rows;
 }
 
-// 32 bytes of a thread: a whole sector in one store where the address allows it.
-__device__ __forceinline__ void store32(void* p, const uint32_t* v, bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-  }
-}
-// 16 bf16 numbers, of which `left` (a multiple of 8) are there.
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const float* v, int left, bool wide) {
-  uint32_t w[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-  if (left >= 16) store32(p, w, wide);
-  else if (left > 0) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 __device__ __forceinline__ float swiglu(float gate, float up) { return __fdividef(gate, 1.f + __expf(-gate)) * up; }
 
-// 64 columns of a row from n on, those before `end`: up's 32 results (gate and up
-// columns in turn), or down's 64.
-template <bool E4M3, bool UP>
-__device__ __forceinline__ void store_piece(const Args& a, const uint32_t* acc, size_t at, float gate, int n, int end) {
-  if constexpr (UP) {
-    const int f = a.n / 2, u = n / 2;
-    float h[32];
+// Behind a wait for loads: their registers are used after it, not before.
+template <int N>
+__device__ __forceinline__ void landed(uint32_t* r) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) h[i] = swiglu(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1]));
-    if constexpr (E4M3) {
-      float m = 0.f;
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+// Columns of a row as results, 16 bytes at a time: up's (gate and up columns in
+// turn; 8 bits: and the scale of 32 of them), or down's times the gate.
+__device__ __forceinline__ void put16(uint8_t* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+// up: 64 columns, 32 results.
+template <bool E4M3>
+__device__ __forceinline__ void put_up(uint32_t acc, uint8_t* to, uint8_t* scale) {
+  float v[32];
+  uint32_t r[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(h[i]));
-      const int k = scale_exp(m);
-      const Factors s = factors(k);
-      uint32_t w[8];
+  for (int c = 0; c < 64; c += 32) {
+    tmem_ld32(acc + c, r);
+    tmem_wait_ld();
+    landed<32>(r);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = codes4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3], s.f, s.g);
-      store32(a.out + at * f + u, w, a.wide);
-      a.out_scales[at * (f / GROUP) + u / GROUP] = (uint8_t)(k + 127);
-    } else {
-      __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + at * f + u;
-      store16(p, h, end / 2 - u, a.wide);
-      store16(p + 16, h + 16, end / 2 - u - 16, a.wide);
-    }
+    for (int i = 0; i < 16; ++i) v[c / 2 + i] = swiglu(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+  }
+  if constexpr (E4M3) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
+    const int k = scale_exp(m);
+    const Factors s = factors(k);
+#pragma unroll
+    for (int i = 0; i < 32; i += 16)
+      *reinterpret_cast<uint4*>(to + i) =
+          make_uint4(codes4(v[i], v[i + 1], v[i + 2], v[i + 3], s.f, s.g), codes4(v[i + 4], v[i + 5], v[i + 6], v[i + 7], s.f, s.g),
+                     codes4(v[i + 8], v[i + 9], v[i + 10], v[i + 11], s.f, s.g),
+                     codes4(v[i + 12], v[i + 13], v[i + 14], v[i + 15], s.f, s.g));
+    if (scale) *scale = (uint8_t)(k + 127);
   } else {
-    __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(a.out) + at * a.n + n;
 #pragma unroll
-    for (int i = 0; i < 64; i += 16) {
-      float y[16];
+    for (int i = 0; i < 32; i += 8) put16(to + 2 * i, v + i);
+  }
+}
+// down: N columns that are on their way to registers.
+template <int N>
+__device__ __forceinline__ void load_down(uint32_t acc, uint32_t* r) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(acc[i + j]) * gate;
-      store16(p + i, y, end - n - i, a.wide);
-    }
+  for (int c = 0; c < N; c += 32) tmem_ld32(acc + c, r + c);
+}
+template <int N>
+__device__ __forceinline__ void put_down(const uint32_t* r, uint8_t* to, float gate) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r[i + j]) * gate;
+    put16(to + 2 * i, v);
   }
 }
 
@@ -449,35 +455,75 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
     plan_tiles<AM, C::G>(a, ctl);
   } else if (warp >= 4 && warp < 8) {            // ---- results: one thread a row
     const int row = (warp - 4) * 32 + lane;
-    for (int i = 0; list.next<true>(ctl, status, tile); ++i) {
-      const bool live = (warp - 4) * 32 < tile.rows;
-      bool here = row < tile.rows;
-      size_t at = tile.row0 + row;
-      float gate = 1.f;
-      if (!UP && here) {
-        const int p = a.order[tile.row0 + row];
-        here = p >= 0 && p < a.pairs;
-        at = here ? p : 0;
-        if (a.gates) gate = a.gates[at];
-      }
+    constexpr int EL = E4M3 && UP ? 1 : 2, LANES = C::RB > 64 ? 8 : 4;   // bytes of a result; lanes that write a row's piece
+    const size_t pitch = (size_t)(UP ? a.n / 2 : a.n) * EL;
+    uint8_t* const mine = smem + C::OFF_OUT + row * C::PITCH;
+    // The row's place in the output, -1 for none, and its gate: those of the next
+    // tile are read while this one is worked on (two dependent loads).
+    auto place_of = [&](const Tile& t) {
+      if (row >= t.rows) return -1;
+      const int at = t.row0 + row;
+      return UP ? at : a.order[at];
+    };
+    auto gate_of = [&](int& at) {
+      if (UP) return 1.f;
+      if ((unsigned)at >= (unsigned)a.pairs) at = -1;
+      return at >= 0 && a.gates ? a.gates[at] : 1.f;
+    };
+    bool more = list.next<true>(ctl, status, tile);
+    int next_at = more ? place_of(tile) : -1;
+    float next_gate = gate_of(next_at);
+    for (int i = 0; more; ++i) {
+      const int rows = min(32, tile.rows - (warp - 4) * 32);   // of this warp
+      const int n0 = tile.n0, width = min(tile.width, a.n - tile.n0), at = next_at;
+      const float gate = next_gate;
+      if ((more = list.next<true>(ctl, status, tile))) next_at = place_of(tile);
       if (!wait(&ctl->acc_full[i & 1], i >> 1 & 1, ctl, status)) break;
       tc_after();
       const uint32_t acc = tmem + (i & 1) * NT + ((uint32_t)((warp - 4) * 32) << 16);
-      const int end = min(a.n, tile.n0 + tile.width);
+      constexpr int EACH = 32 / LANES;           // rows that the warp writes at a time
+      int place[LANES];
+#pragma unroll
+      for (int j = 0; j < LANES; ++j) place[j] = __shfl_sync(FULL, at, j * EACH + lane / LANES);
+      const int piece = lane % LANES * 16;
+      uint8_t* out = a.out + (size_t)(UP ? n0 / 2 : n0) * EL + piece;
+      const uint8_t* from = smem + C::OFF_OUT + ((warp - 4) * 32 + lane / LANES) * C::PITCH + piece;
+      uint32_t r[UP ? 1 : C::STEP];
+      if (!UP && rows > 0) load_down<C::STEP>(acc, r);
+      int fill = 0;                              // bytes of the rows' pieces
 #pragma unroll 1
-      for (int c = 0; c < tile.width; c += 64) {
-        uint32_t r[64];
-        if (live) {
-          tmem_ld32(acc + c, r);
-          tmem_ld32(acc + c + 32, r + 32);
+      for (int c = 0; c < width; c += C::STEP) {
+        const bool last = c + C::STEP >= width;
+        if (UP && rows > 0)
+          put_up<E4M3>(acc + c, mine + fill, E4M3 && at >= 0 ? a.out_scales + (size_t)at * (a.n / 2 / GROUP) + (n0 + c) / 64 : nullptr);
+        if constexpr (!UP) {
           tmem_wait_ld();
+          landed<C::STEP>(r);
         }
-        if (c + 64 >= tile.width) {              // all of it read: the accumulator may be summed into again
+        if (last) {                              // all of it read: the accumulator may be summed into again
           tc_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->acc_empty[i & 1]);
         }
-        if (here) store_piece<E4M3, UP>(a, r, at, gate, tile.n0 + c, end);
+        if (!UP && rows > 0) {
+          put_down<C::STEP>(r, mine, gate);
+          if (!last) load_down<C::STEP>(acc + c + C::STEP, r);
+        }
+        if (c == 0) next_gate = gate_of(next_at);
+        fill += (UP ? min(C::STEP, width - c) / 2 : min(C::STEP, width - c)) * EL;
+        if (fill < C::RB && !last) continue;
+        __syncwarp();
+        if (rows > 0) {
+          uint4 v[LANES];
+#pragma unroll
+          for (int j = 0; j < LANES; ++j) v[j] = *reinterpret_cast<const uint4*>(from + j * EACH * C::PITCH);
+#pragma unroll
+          for (int j = 0; j < LANES; ++j)
+            if (place[j] >= 0 && piece < fill) *reinterpret_cast<uint4*>(out + (size_t)place[j] * pitch) = v[j];
+        }
+        __syncwarp();
+        out += fill;
+        fill = 0;
       }
     }
     if constexpr (!UP) {                         // pairs without an expert
@@ -723,7 +769,7 @@ int mk_experts_up(mk_experts* m, int rows, const void* x, const uint8_t* x_scale
   const int rc = check_device(m);
   if (rc != MK_OK) return rc;
   Args a = {first, order, nullptr, (const uint8_t*)x, x_scales, w_scales, (uint8_t*)h, h_scales, m->status, (int)p, rows, m->k, m->experts,
-            m->hidden, 2 * m->ffn, 0, (uintptr_t)h % 32 == 0 && f * el % 32 == 0};
+            m->hidden, 2 * m->ffn};
   const cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t err = s8 ? launch<true, true>(a, x, w, st) : launch<false, true>(a, x, w, st);
   return err == cudaSuccess ? MK_OK : fail_cuda("mk_experts_up", err);
@@ -753,7 +799,7 @@ int mk_experts_down(mk_experts* m, int rows, const void* h, const uint8_t* h_sca
   const int rc = check_device(m);
   if (rc != MK_OK) return rc;
   Args a = {first, order, gates, nullptr, h_scales, w_scales, (uint8_t*)y, nullptr, m->status, (int)p, rows, m->k, m->experts,
-            m->ffn, m->hidden, 0, (uintptr_t)y % 32 == 0 && wide % 16 == 0};
+            m->ffn, m->hidden};
   const cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t err = s8 ? launch<true, false>(a, h, w, st) : launch<false, false>(a, h, w, st);
   return err == cudaSuccess ? MK_OK : fail_cuda("mk_experts_down", err);
