@@ -87,10 +87,13 @@ struct NormArgs {
 };
 
 // A row is the work of blockDim.x threads (a multiple of 32; blockDim.y rows a
-// block), 8 elements a thread and pass.
-template <class X, class A, int OUT, int PASSES>
-__global__ void __launch_bounds__(256) k_norm(const __grid_constant__ NormArgs a) {
-  __shared__ float part[8];
+// block), 8 elements a thread and pass, AHEAD terms in flight at a time.  Few
+// terms: 32 registers and all 2048 threads of an SM (8143 rows of 2048 with one
+// term to 8 bits take 32.8 us so, 36.8 with 46 registers).
+template <class X, class A, int OUT, int PASSES, int AHEAD, int MAX_NT>
+__global__ void __launch_bounds__(MAX_NT, PASSES > 1 ? 1 : (AHEAD == 1 ? 2048 : sizeof(A) == 4 ? 1024 : 1280) / MAX_NT)
+    k_norm(const __grid_constant__ NormArgs a) {
+  __shared__ float part[MAX_NT / 32];
   allow_next();
   const int tx = threadIdx.x, w0 = threadIdx.y * (blockDim.x / 32), warp = w0 + tx / 32;
   const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
@@ -105,13 +108,13 @@ __global__ void __launch_bounds__(256) k_norm(const __grid_constant__ NormArgs a
     if (live && i < a.n) {
       unpack8(load8((const X*)a.x + r * a.x_stride + i), t[p]);
       const A* add = (const A*)a.add + r * a.terms * a.n + i;
-      for (int j0 = 0; j0 < a.terms; j0 += 4) {
-        Raw8<A> raw[4];
+      for (int j0 = 0; j0 < a.terms; j0 += AHEAD) {
+        Raw8<A> raw[AHEAD];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < AHEAD; ++j)
           if (j0 + j < a.terms) raw[j] = load8(add + (size_t)(j0 + j) * a.n);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < AHEAD; ++j)
           if (j0 + j < a.terms) {
             float v[8];
             unpack8(raw[j], v);
@@ -185,14 +188,15 @@ __global__ void __launch_bounds__(256) k_quantize(const X* x, long long stride, 
 
 template <class X, class A, int OUT>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
-  // a row in one pass of up to 256 threads, several short rows in a block
-  const int want = (a.n / 8 + 31) / 32 * 32, passes = (want + 255) / 256;
-  const int tx = want < 256 ? want : 256, ty = 256 / tx;
+  // several short rows in a block of 256 threads, or one long row in up to 1024
+  const int want = (a.n / 8 + 31) / 32 * 32;
+  const int tx = want < 1024 ? want : 1024, ty = tx < 256 ? 256 / tx : 1;
   const dim3 grid((unsigned)((a.rows + ty - 1) / ty)), block(tx, ty);
-  auto k = passes <= 1   ? k_norm<X, A, OUT, 1>
-           : passes <= 2 ? k_norm<X, A, OUT, 2>
-           : passes <= 4 ? k_norm<X, A, OUT, 4>
-                         : k_norm<X, A, OUT, 8>;
+  const bool few = a.terms <= 1;
+  auto k = want > 1024  ? k_norm<X, A, OUT, 2, 1, 1024>
+           : want > 256 ? few ? k_norm<X, A, OUT, 1, 1, 1024> : k_norm<X, A, OUT, 1, 4, 1024>
+           : few        ? k_norm<X, A, OUT, 1, 1, 256>
+                        : k_norm<X, A, OUT, 1, 4, 256>;
   return launch_kernel(k, grid, block, 0, 1, st, a);
 }
 template <class X, class A>

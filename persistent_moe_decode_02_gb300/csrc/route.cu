@@ -9,7 +9,11 @@
 // its place, so the order is the pairs' own within an expert and the same on
 // every call.
 #include <cooperative_groups.h>
+#include <limits.h>
 #include <math.h>
+
+#include <type_traits>
+#include <utility>
 
 #include "host.h"
 #include "launch.cuh"
@@ -23,6 +27,7 @@ namespace {
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int MAX_EXPERTS = 256, MAX_TOP = 8;
 constexpr int NT = 1024, NW = NT / 32, BUCKETS = MAX_EXPERTS + 1;   // the last one: pairs without an expert
+constexpr int FEW_PAIRS = 128, HOLD = 8;
 
 struct RouteArgs {
   const float* logits;
@@ -44,45 +49,78 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
 }
 
-// One row's choice by a warp; V logits a lane.
+// One row's logits, V a lane, and a warp's choice among them: the lane's place
+// among the choices (lane < k) has the expert that is returned, -1 for none.
 template <int V>
-__device__ __forceinline__ void choose(const RouteArgs& a, int row) {
-  const int lane = threadIdx.x % 32;
+struct Row {
+  float x[V];
+};
+template <int V>
+__device__ __forceinline__ Row<V> load_row(const RouteArgs& a, int row) {
+  Row<V> r;
   const float* src = a.logits + row * a.stride;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = v * 32 + threadIdx.x % 32;
+    r.x[v] = e < a.experts && row < a.rows ? src[e] : -INFINITY;
+  }
+  return r;
+}
+template <int V>
+__device__ __forceinline__ int choose(const RouteArgs& a, int row, const Row<V>& r) {
+  const int lane = threadIdx.x % 32;
   uint32_t key[V];
   bool none = false;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = v * 32 + lane;
-    const float x = e < a.experts ? src[e] : -INFINITY;
-    none |= isnan(x);
-    key[v] = key_of(x);
+    none |= isnan(r.x[v]);
+    key[v] = key_of(r.x[v]);
   }
   const bool spoilt = __any_sync(FULL, none);
+  // The lane's own, the largest first and the lower index first among equal
+  // ones: a round then looks at one a lane.
+  int at[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) at[v] = v * 32 + lane;
+#pragma unroll
+  for (int n = V - 1; n > 0; --n)
+#pragma unroll
+    for (int v = 0; v < n; ++v)
+      if (key[v + 1] > key[v]) {
+        const uint32_t k0 = key[v];
+        const int a0 = at[v];
+        key[v] = key[v + 1];
+        at[v] = at[v + 1];
+        key[v + 1] = k0;
+        at[v + 1] = a0;
+      }
   int id = -1;
   uint32_t mine = 0;
   for (int j = 0; j < a.k; ++j) {
-    uint32_t best = key[0];
-    int at = lane;
-#pragma unroll
-    for (int v = 1; v < V; ++v)
-      if (key[v] > best) {
-        best = key[v];
-        at = v * 32 + lane;
-      }
-    const uint32_t top = __reduce_max_sync(FULL, best);
+    const uint32_t top = __reduce_max_sync(FULL, key[0]);
     if (top == 0) break;                         // nothing is left to choose
-    const int e = __reduce_min_sync(FULL, best == top ? at : 0x7fffffff);
+    const unsigned who = __ballot_sync(FULL, key[0] == top);
+    int winner = __ffs(who) - 1;
+    if (who & (who - 1)) {                       // equal ones: the lowest index
+      const int e = __reduce_min_sync(FULL, key[0] == top ? at[0] : 0x7fffffff);
+      winner = e % 32;
+    }
+    const int e = __shfl_sync(FULL, at[0], winner);
+    if (lane == winner) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (e == v * 32 + lane) key[v] = 0;
+      for (int v = 0; v + 1 < V; ++v) {
+        key[v] = key[v + 1];
+        at[v] = at[v + 1];
+      }
+      key[V - 1] = 0;
+    }
     if (lane == j) {
       id = e;
       mine = top;
     }
   }
   const float x = value_of(mine), m = __shfl_sync(FULL, x, 0);
-  float w = id >= 0 ? expf(x - m) : 0.f;         // +infinity, the row's largest: NaN
+  const float w = id >= 0 ? expf(x - m) : 0.f;   // +infinity, the row's largest: NaN
   float sum = w;
 #pragma unroll
   for (int o = 4; o; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
@@ -90,50 +128,111 @@ __device__ __forceinline__ void choose(const RouteArgs& a, int row) {
     a.ids[(size_t)row * a.k + lane] = id;
     a.gates[(size_t)row * a.k + lane] = id < 0 ? 0.f : spoilt ? NAN : w / sum;
   }
+  return id;
 }
-__device__ __forceinline__ void choose_rows(const RouteArgs& a, int warp, int warps) {
-  for (int row = warp; row < a.rows; row += warps) {
-    if (a.experts <= 32) choose<1>(a, row);
-    else if (a.experts <= 64) choose<2>(a, row);
-    else if (a.experts <= 128) choose<4>(a, row);
-    else choose<8>(a, row);
-  }
+// f(V) for the logits of a lane.
+template <class F>
+__device__ __forceinline__ void with_width(int experts, F&& f) {
+  if (experts <= 32) f(std::integral_constant<int, 1>());
+  else if (experts <= 64) f(std::integral_constant<int, 2>());
+  else if (experts <= 128) f(std::integral_constant<int, 4>());
+  else f(std::integral_constant<int, 8>());
 }
 
 __global__ void __launch_bounds__(256) k_choose(const __grid_constant__ RouteArgs a) {
   allow_next();
   await_stream();
-  choose_rows(a, (blockIdx.x * 256 + threadIdx.x) / 32, gridDim.x * 8);
+  const int row = (int)(((long long)blockIdx.x * 256 + threadIdx.x) / 32);
+  if (row < a.rows)
+    with_width(a.experts, [&](auto n) {
+      constexpr int V = decltype(n)::value;
+      choose<V>(a, row, load_row<V>(a, row));
+    });
 }
 
-// The sort, in one cluster; `all`: the choice too.
-__global__ void __launch_bounds__(NT) k_sort(const __grid_constant__ RouteArgs a, bool all) {
+// Few rows in one block: a pair's place is the number of pairs before it, an
+// expert's first the number of those of lower experts, counted one by one.
+__global__ void __launch_bounds__(1024) k_few(const __grid_constant__ RouteArgs a) {
+  __shared__ alignas(16) int keys[FEW_PAIRS];    // expert (the last one: none), pair
+  allow_next();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, pairs = a.rows * a.k, padded = (pairs + 3) / 4 * 4;
+  if ((int)threadIdx.x < padded - pairs) keys[pairs + threadIdx.x] = INT_MAX;
+  await_stream();
+  with_width(a.experts, [&](auto n) {
+    constexpr int V = decltype(n)::value;
+    const int warps = blockDim.x / 32;
+    Row<V> r = load_row<V>(a, warp);
+    for (int row = warp; row < a.rows; row += warps) {
+      const Row<V> now = r;
+      r = load_row<V>(a, row + warps);           // the next one is on its way
+      const int id = choose<V>(a, row, now);
+      if (lane < a.k) keys[row * a.k + lane] = (id < 0 ? a.experts : id) * FEW_PAIRS + row * a.k + lane;
+    }
+  });
+  __syncthreads();
+  for (int i = threadIdx.x; i < pairs + a.experts + 1; i += blockDim.x) {
+    const int key = i < pairs ? keys[i] : (i - pairs) * FEW_PAIRS;
+    int n = 0;
+#pragma unroll 8
+    for (int q = 0; q < padded; q += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(keys + q);
+      n += (v.x < key) + (v.y < key) + (v.z < key) + (v.w < key);
+    }
+    if (i < pairs) a.order[n] = i;
+    else a.first[i - pairs] = n;
+  }
+}
+
+// The lanes that have the same bucket as this one, by ballots over its bits
+// (a warp's match instruction takes 80 cycles of the SM: 22 us for 8143 rows).
+__device__ __forceinline__ unsigned same_bucket(int b, int bits) {
+  unsigned same = FULL;
+  for (int i = 0; i < bits; ++i) {
+    const bool one = b >> i & 1;
+    const unsigned with = __ballot_sync(FULL, one);
+    same &= one ? with : ~with;
+  }
+  return same;
+}
+
+// The sort, in one cluster.  A warp holds HOLD times 32 pairs of its run in
+// registers from the first pass to the second; longer runs are read twice.
+__global__ void __launch_bounds__(NT) k_sort(const __grid_constant__ RouteArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ int hist[NW][BUCKETS], total[BUCKETS], start[BUCKETS + 1];
   const int rank = cluster.block_rank(), blocks = cluster.num_blocks();
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, nb = a.experts + 1;
   allow_next();
   for (int i = tid; i < NW * BUCKETS; i += NT) (&hist[0][0])[i] = 0;
-  await_stream();
-  if (all) {
-    choose_rows(a, rank * NW + warp, blocks * NW);
-    __threadfence();
-    cluster.sync();
-  } else {
-    __syncthreads();
-  }
-  const long long pairs = (long long)a.rows * a.k;
-  const long long chunks = (pairs + 31) / 32, per = (chunks + blocks * NW - 1) / (blocks * NW);
-  const long long c0 = (rank * NW + warp) * per, c1 = min(chunks, c0 + per);
-  auto bucket = [&](long long p) {
-    const int id = p < pairs ? *(volatile const int*)(a.ids + p) : -1;
-    return p >= pairs ? BUCKETS : id < 0 ? a.experts : id;
+  const int pairs = a.rows * a.k, chunks = (pairs + 31) / 32, per = (chunks + blocks * NW - 1) / (blocks * NW);
+  const int c0 = min(chunks, (rank * NW + warp) * per), c1 = min(chunks, c0 + per);
+  const int bits = 32 - __clz(a.experts);        // (no pair is told from the others by its own ballot)
+  int b[HOLD];
+  unsigned same[HOLD];
+  auto fetch = [&](int c) {                      // the experts of the pairs from chunk c on; BUCKETS: no pair
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i) {
+      const int p = (c + i) * 32 + lane;
+      b[i] = BUCKETS;
+      if (c + i < c1 && p < pairs) {
+        const int id = a.ids[p];
+        b[i] = id < 0 ? a.experts : id;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i)
+      if (c + i < c1) same[i] = same_bucket(b[i], bits) & __ballot_sync(FULL, b[i] < BUCKETS);
   };
-  for (long long c = c0; c < c1; ++c) {
-    const int b = bucket(c * 32 + lane);
-    const unsigned same = __match_any_sync(FULL, b);
-    if (b < BUCKETS && lane == __ffs(same) - 1) hist[warp][b] += __popc(same);
-    __syncwarp();
+  __syncthreads();
+  await_stream();
+  for (int c = c0; c < c1; c += HOLD) {
+    fetch(c);
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i) {
+      if (c + i >= c1) break;
+      if (b[i] < BUCKETS && lane == __ffs(same[i]) - 1) hist[warp][b[i]] += __popc(same[i]);
+      __syncwarp();
+    }
   }
   __syncthreads();
   if (tid < nb) {                                // the warps before, within the block
@@ -147,22 +246,26 @@ __global__ void __launch_bounds__(NT) k_sort(const __grid_constant__ RouteArgs a
     total[tid] = sum;
   }
   cluster.sync();
-  int before = 0, whole = 0;
-  if (tid < nb)
+  int before = 0;
+  if (tid < nb) {
+    int whole = 0;
+#pragma unroll 8
     for (int r = 0; r < blocks; ++r) {           // the blocks before
       const int n = *cluster.map_shared_rank(&total[tid], r);
       before += r < rank ? n : 0;
       whole += n;
     }
-  if (tid < nb) start[tid] = whole;
+    start[tid] = whole;
+  }
+  auto read = cluster.barrier_arrive();
   __syncthreads();
   if (warp == 0) {                               // the experts before
     constexpr int PER = (BUCKETS + 31) / 32;
     int n[PER], sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int b = lane * PER + i;
-      n[i] = b < nb ? start[b] : 0;
+      const int e = lane * PER + i;
+      n[i] = e < nb ? start[e] : 0;
       sum += n[i];
     }
     int up = sum;
@@ -175,10 +278,10 @@ __global__ void __launch_bounds__(NT) k_sort(const __grid_constant__ RouteArgs a
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int b = lane * PER + i;
-      if (b < nb) {
-        start[b] = up;
-        if (rank == 0) a.first[b] = up;
+      const int e = lane * PER + i;
+      if (e < nb) {
+        start[e] = up;
+        if (rank == 0) a.first[e] = up;
       }
       up += n[i];
     }
@@ -190,19 +293,66 @@ __global__ void __launch_bounds__(NT) k_sort(const __grid_constant__ RouteArgs a
     for (int w = 0; w < NW; ++w) hist[w][tid] += before;
   }
   __syncthreads();
-  for (long long c = c0; c < c1; ++c) {
-    const long long p = c * 32 + lane;
-    const int b = bucket(p);
-    const unsigned same = __match_any_sync(FULL, b);
-    const int at = b < BUCKETS ? hist[warp][b] : 0;
-    __syncwarp();
-    if (b < BUCKETS) {
-      a.order[at + __popc(same & ((1u << lane) - 1))] = (int)p;
-      if (lane == __ffs(same) - 1) hist[warp][b] = at + __popc(same);
+  for (int c = c0; c < c1; c += HOLD) {
+    if (per > HOLD) fetch(c);
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i) {
+      if (c + i >= c1) break;
+      const int at = b[i] < BUCKETS ? hist[warp][b[i]] : 0;
+      __syncwarp();
+      if (b[i] < BUCKETS) {
+        a.order[at + __popc(same[i] & ((1u << lane) - 1))] = (c + i) * 32 + lane;
+        if (lane == __ffs(same[i]) - 1) hist[warp][b[i]] = at + __popc(same[i]);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
-  cluster.sync();                                // nobody leaves while its counts are read
+  cluster.barrier_wait(std::move(read));         // nobody leaves while its counts are read
+}
+
+// Whether the current device has room for a cluster of 16 (beyond what every
+// device has to offer), asked for once by each host thread.
+cudaError_t wide_cluster(bool* ok) {
+  thread_local int device = -1;
+  thread_local bool room = false;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev != device) {
+    e = cudaFuncSetAttribute(k_sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 16;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = 16;
+    cfg.blockDim = NT;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k_sort, &cfg) != cudaSuccess) {   // no room is an answer too
+      cudaGetLastError();
+      n = 0;
+    }
+    room = n > 0;
+    device = dev;
+  }
+  *ok = room;
+  return e;
+}
+
+// A block for every 1024 pairs, 16 of them at most.
+cudaError_t launch_sort(const RouteArgs& a, cudaStream_t st) {
+  const long long pairs = (long long)a.rows * a.k;
+  int blocks = 1;
+  while (blocks < 16 && pairs > blocks * 1024) blocks *= 2;
+  if (blocks == 16) {
+    bool ok = false;
+    const cudaError_t e = wide_cluster(&ok);
+    if (e != cudaSuccess) return e;
+    if (!ok) blocks = 8;
+  }
+  return launch_kernel(k_sort, blocks, NT, 0, blocks, st, a);
 }
 
 }  // namespace
@@ -226,14 +376,12 @@ extern "C" int mk_route(int rows, int n_experts, int top_k, const float* logits,
   if (clash(s, 4, 5)) return fail(MK_ERR_INVALID, "mk_route: two of the buffers overlap");
   const RouteArgs a = {logits, row_stride, rows, n_experts, top_k, ids, gates, first, order};
   const cudaStream_t st = (cudaStream_t)stream;
-  int sms = 0;
-  cudaError_t e = multiprocessors(&sms);
-  const bool all = rows <= 512;
-  if (e == cudaSuccess && !all) {
-    const int most = (rows + 7) / 8;
-    e = launch_kernel(k_choose, dim3(most < sms * 8 ? most : sms * 8), 256, 0, 1, st, a);
+  cudaError_t e;
+  if (pairs <= FEW_PAIRS) {
+    e = launch_kernel(k_few, 1, rows <= 8 ? 256 : 1024, 0, 1, st, a);
+  } else {
+    e = launch_kernel(k_choose, (rows + 7) / 8, 256, 0, 1, st, a);
+    if (e == cudaSuccess) e = launch_sort(a, st);
   }
-  const int blocks = pairs <= 1024 ? 1 : pairs <= 4096 ? 4 : 8;
-  if (e == cudaSuccess) e = launch_kernel(k_sort, dim3(blocks), NT, 0, blocks, st, a, all);
   return e == cudaSuccess ? MK_OK : fail_cuda("mk_route", e);
 }

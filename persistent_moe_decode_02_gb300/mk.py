@@ -710,16 +710,17 @@ _ROWS = {_BF16: MK_ROWS_BF16, _F32: MK_ROWS_F32}
 
 def _rows(name: str, t: torch.Tensor, dev: int):
     """Address, type and row stride of bf16 or float32 rows [rows, n] that may lie apart."""
-    if t.dim() != 2 or t.dtype not in _ROWS or t.get_device() != dev or (t.numel() and t.stride(1) != 1 and t.shape[1] != 1):
+    kind, shape, steps = _ROWS.get(t.dtype), t.shape, t.stride()
+    if kind is None or len(shape) != 2 or t.get_device() != dev or (steps[1] != 1 and shape[1] != 1 and shape[0]):
         raise ValueError(f"{name}: bf16 or float32 rows [rows, n] of the current CUDA device are wanted")
-    return t.data_ptr(), _ROWS[t.dtype], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), kind, steps[0] if shape[0] > 1 else shape[1]
 
 
-def _codes(name: str, codes: torch.Tensor, scales: Optional[torch.Tensor], shape, dev: int):
-    """Addresses of 8-bit rows: codes float8_e4m3fn, scales uint8 of a 32nd of the last dimension."""
-    if scales is None:
-        raise ValueError(f"{name}: 8-bit rows come with their scales")
-    return _here(name, codes, _E4M3, shape, dev), _here(f"{name}'s scales", scales, _U8, (*shape[:-1], shape[-1] // 32), dev)
+def _scales(t: Optional[torch.Tensor], shape, dev: int) -> int:
+    """The address of 8-bit rows' scales: uint8, a 32nd of the last dimension."""
+    if t is None:
+        raise ValueError("8-bit rows come with their scales")
+    return _here("scales", t, _U8, shape, dev)
 
 
 def norm(x: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, out: Optional[torch.Tensor],
@@ -731,27 +732,32 @@ def norm(x: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, out: Option
     None; it may be x itself."""
     dev = _device()
     at, kind, stride = _rows("x", x, dev)
-    rows, n = x.shape
+    shape = x.shape
+    rows, n = shape
     terms, a, a_kind = 0, None, 0
     if add is not None:
-        if add.dtype not in _ROWS or add.dim() not in (2, 3):
+        a_type = add.dtype
+        if a_type not in _ROWS or add.dim() not in (2, 3):
             raise ValueError("add: bf16 or float32 [rows, n] or [rows, terms, n] is wanted")
-        terms, a_kind = add.shape[1] if add.dim() == 3 else 1, _ROWS[add.dtype]
-        a = _here("add", add, add.dtype, (rows, n) if add.dim() == 2 else (rows, terms, n), dev)
+        terms, a_kind = add.shape[1] if add.dim() == 3 else 1, _ROWS[a_type]
+        a = _here("add", add, a_type, (rows, terms, n) if add.dim() == 3 else shape, dev)
     o, s, o_kind = None, None, 0
-    if out is not None and out.dtype is _E4M3:
-        (o, s), o_kind = _codes("out", out, scales, (rows, n), dev), MK_ROWS_E4M3
-    elif scales is not None:
-        raise ValueError("scales: only with an 8-bit out")
-    elif out is not None:
-        if out.dtype not in _ROWS:
+    if out is not None:
+        o_type = out.dtype
+        if o_type is _E4M3:
+            s, o_kind = _scales(scales, (rows, n // 32), dev), MK_ROWS_E4M3
+        elif o_type in _ROWS:
+            o_kind = _ROWS[o_type]
+        else:
             raise ValueError("out: bf16, float32 or float8_e4m3fn is wanted")
-        o, o_kind = _here("out", out, out.dtype, x.shape, dev), _ROWS[out.dtype]
+        o = _here("out", out, o_type, shape, dev)
+    if s is None and scales is not None:
+        raise ValueError("scales: only with an 8-bit out")
     if not rows:
         return
     rc = lib().mk_norm(rows, n, at, kind, stride, a, a_kind, terms,
-                       None if gamma is None else _here("gamma", gamma, _BF16, (n,), dev), float(eps),
-                       None if total is None else _here("total", total, x.dtype, x.shape, dev), o, o_kind, s,
+                       None if gamma is None else _here("gamma", gamma, _BF16, (n,), dev), eps,
+                       None if total is None else _here("total", total, x.dtype, shape, dev), o, o_kind, s,
                        _on(stream, dev))
     if rc != MK_OK:
         raise MkError("mk_norm", rc)
@@ -762,8 +768,8 @@ def quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=
     [rows, n / 32] (include/mk.h).  Contiguous weights of more dimensions go as x.view(-1, n)."""
     dev = _device()
     at, kind, stride = _rows("x", x, dev)
-    rows, n = x.shape
-    c, s = _codes("codes", codes, scales, x.shape, dev)
+    rows, n = shape = x.shape
+    c, s = _here("codes", codes, _E4M3, shape, dev), _scales(scales, (rows, n // 32), dev)
     if not rows:
         return
     rc = lib().mk_quantize(rows, n, at, kind, stride, c, s, _on(stream, dev))
@@ -812,7 +818,7 @@ class Experts:
 
     def _two(self, name, t, scales, shape, dev):
         if self.e4m3:
-            return _codes(name, t, scales, shape, dev)
+            return _here(name, t, _E4M3, shape, dev), _scales(scales, (*shape[:-1], shape[-1] // 32), dev)
         if scales is not None:
             raise ValueError(f"{name}: scales are of 8-bit rows")
         return _here(name, t, _BF16, shape, dev), None
