@@ -97,6 +97,7 @@ struct Args {
   int pairs, rows, top_k, experts;
   int k, n;                      // elements of a row of A; columns of C
   int extra;                     // what a tile costs beside its columns, in columns
+  int box;                       // columns of the large boxes
   int a_wide, b_wide;            // bytes that a row's scales may be read by
 };
 
@@ -117,6 +118,14 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, Ctl* ct
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* ctl, int* status) {
   return __all_sync(FULL, wait_one(bar, parity, ctl, status));
+}
+
+// What tiles of this width cost: their rounds over the blocks, times the columns
+// of one and what it takes beside them.  (At most 2^18 + 256 tiles of rows and
+// 2^12 of columns: 32 bits.)
+__host__ __device__ __forceinline__ unsigned cost_of(unsigned row_tiles, unsigned n, unsigned width, unsigned blocks, unsigned extra) {
+  const unsigned rounds = (row_tiles * ((n + width - 1) / width) + blocks - 1) / blocks;
+  return (rounds < 1u << 22 ? rounds : 1u << 22) * (width + extra);
 }
 
 // Each expert's rows and tiles from `first`, by one warp; entries out of order or
@@ -174,15 +183,13 @@ __device__ __forceinline__ void set_tables(const Args& a, Ctl* ctl) {
     ctl->tile0[MAX_EXPERTS] = at;
   }
   // The width: rounds of tiles that the blocks take, times what one takes.
-  const int all = __shfl_sync(FULL, at, 31), width = G * (lane + 1);
-  const int columns = (a.n + width - 1) / width;
-  const int rounds = (int)(((long long)all * columns + gridDim.x - 1) / gridDim.x);
-  const unsigned cost = width <= NT ? (unsigned)min((long long)rounds * (width + a.extra), 0x7fffffffll) : 0xffffffffu;
+  const int width = G * (lane + 1), all = __shfl_sync(FULL, at, 31);   // (by every lane)
+  const unsigned cost = width <= NT ? cost_of(all, a.n, width, gridDim.x, a.extra) : 0xffffffffu;
   const unsigned best = __reduce_min_sync(FULL, cost);
   const int who = __reduce_max_sync(FULL, cost == best ? lane : 0);
   if (lane == who) {
     ctl->width = width;
-    ctl->columns = columns;
+    ctl->columns = (a.n + width - 1) / width;
   }
 }
 
@@ -388,7 +395,7 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
           mbar_arrive_tx(full, bytes);
           if constexpr (C::MN) {
             for (int n = 0; n < tile.width; n += 64) tma_3d(w + n * 128, &map_c, tile.n0 + n, kb * C::KE, tile.e, full);
-          } else if (tile.width == NT) {
+          } else if (tile.width == a.box) {
             tma_3d(w, &map_b, kb * C::KE, tile.n0, tile.e, full);
           } else {
             int n = 0;
@@ -676,10 +683,17 @@ cudaError_t launch(Args a, const void* rows, const void* w, int sms, cudaStream_
   a.extra = AM;                  // the rows' bytes
   a.a_wide = scales_wide(a.a_scales, a.k / GROUP);
   a.b_wide = scales_wide(a.b_scales, a.k / GROUP);
+  const unsigned some = a.pairs < a.experts ? a.pairs : a.experts;   // experts with rows, if all the pairs' differ
+  const long long most = ((long long)a.pairs / AM + some) * ((a.n + C::G - 1) / C::G);
+  const unsigned blocks = (unsigned)(most < sms ? most : sms);
+  // The width that the blocks will choose if so: one box a stage then.
+  a.box = NT;
+  for (int w = NT; w > 0 && a.pairs <= a.experts; w -= C::G)
+    if (cost_of(some, a.n, w, blocks, a.extra) < cost_of(some, a.n, a.box, blocks, a.extra)) a.box = w;
   const cuuint64_t dim_a[2] = {(cuuint64_t)a.k, (cuuint64_t)a.pairs};
   const cuuint32_t box_a[2] = {C::KE, C::BOX};
   const cuuint64_t dim_b[3] = {(cuuint64_t)(C::MN ? a.n : a.k), (cuuint64_t)(C::MN ? a.k : a.n), (cuuint64_t)a.experts};
-  const cuuint32_t box_b[3] = {C::KE, NT, 1}, box_c[3] = {C::KE, 64, 1}, box_d[3] = {C::KE, 16, 1};
+  const cuuint32_t box_b[3] = {C::KE, (cuuint32_t)a.box, 1}, box_c[3] = {C::KE, 64, 1}, box_d[3] = {C::KE, 16, 1};
   CUtensorMap map_a = {}, map_b = {}, map_c, map_d = {};
   cudaError_t e = UP ? cudaSuccess : tensor_map(&map_a, E4M3, rows, 2, dim_a, box_a);
   if (e == cudaSuccess && !C::MN) e = tensor_map(&map_b, E4M3, w, 3, dim_b, box_b);
@@ -687,8 +701,7 @@ cudaError_t launch(Args a, const void* rows, const void* w, int sms, cudaStream_
   if (e == cudaSuccess && C::G < 64) e = tensor_map(&map_d, E4M3, w, 3, dim_b, box_d);
   if (e == cudaSuccess) e = allow((const void*)k_experts<E4M3, UP, AM, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  const long long most = ((long long)a.pairs / AM + (a.pairs < a.experts ? a.pairs : a.experts)) * ((a.n + C::G - 1) / C::G);
-  return launch_kernel(k_experts<E4M3, UP, AM, NT>, dim3((unsigned)(most < sms ? most : sms)), C::THREADS, C::SMEM, 1, st, a,
+  return launch_kernel(k_experts<E4M3, UP, AM, NT>, blocks, C::THREADS, C::SMEM, 1, st, a,
                        map_a, map_b, map_c, map_d);
 }
 
