@@ -369,12 +369,11 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
     fence_barrier_init();
   }
   if (warp == 2) tmem_alloc<C::T_COLS>(&ctl->tmem);
-  await_stream();
-  allow_next();
-  if (warp == 3) set_tables<AM, NT, C::G>(a, ctl);
   tc_before();
   __syncthreads();
   tc_after();
+  await_stream();
+  allow_next();
   const uint32_t tmem = ctl->tmem;
   const int kbs = (a.k + C::KE - 1) / C::KE;
   Reader list;
@@ -459,6 +458,8 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 3) {                        // ---- the list of tiles
+    set_tables<AM, NT, C::G>(a, ctl);
+    __syncwarp();
     plan_tiles<AM, C::G>(a, ctl);
   } else if (warp >= 4 && warp < 8) {            // ---- results: one thread a row
     const int row = (warp - 4) * 32 + lane;
