@@ -3,17 +3,15 @@
 // expert.
 //
 // A warp takes a row: its logits as integers in the order of their values, k
-// rounds of a warp's maximum and the lowest index that has it.  The sort counts:
-// each warp of one cluster counts its run of pairs by expert, the counts are
-// summed over warps, blocks and experts, and a second pass puts each pair at
-// its place, so the order is the pairs' own within an expert and the same on
-// every call.
+// rounds of a warp's maximum and the lowest index that has it.  The sort is one
+// cluster's: each block counts its rows' pairs by expert, the counts are summed
+// over blocks and experts, and each pair goes to its place, so the order is the
+// pairs' own within an expert and the same on every call.
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
 
 #include <type_traits>
-#include <utility>
 
 #include "host.h"
 #include "launch.cuh"
@@ -26,8 +24,8 @@ namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int MAX_EXPERTS = 256, MAX_TOP = 8;
-constexpr int NT = 1024, NW = NT / 32, BUCKETS = MAX_EXPERTS + 1;   // the last one: pairs without an expert
-constexpr int FEW_PAIRS = 128, HOLD = 8;
+constexpr int NT = 1024, BUCKETS = MAX_EXPERTS + 1;   // the last one: pairs without an expert
+constexpr int FEW_PAIRS = 128;
 
 struct RouteArgs {
   const float* logits;
@@ -42,8 +40,7 @@ struct RouteArgs {
 // which no row chooses.
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);   // (-0 is 0)
-  const uint32_t key = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return x == -INFINITY || isnan(x) ? 0u : key;
+  return x > -INFINITY ? b ^ ((uint32_t)((int)b >> 31) | 0x80000000u) : 0u;
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
@@ -183,131 +180,154 @@ __global__ void __launch_bounds__(1024) k_few(const __grid_constant__ RouteArgs 
   }
 }
 
-// The lanes that have the same bucket as this one, by ballots over its bits
-// (a warp's match instruction takes 80 cycles of the SM: 22 us for 8143 rows).
-__device__ __forceinline__ unsigned same_bucket(int b, int bits) {
-  unsigned same = FULL;
-  for (int i = 0; i < bits; ++i) {
-    const bool one = b >> i & 1;
-    const unsigned with = __ballot_sync(FULL, one);
-    same &= one ? with : ~with;
+// Exclusive sums of n <= BUCKETS numbers, by one warp.
+__device__ __forceinline__ void scan(const int* in, int* out, int n) {
+  constexpr int PER = (BUCKETS + 31) / 32;
+  const int lane = threadIdx.x % 32;
+  int v[PER], sum = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    v[i] = lane * PER + i < n ? in[lane * PER + i] : 0;
+    sum += v[i];
   }
-  return same;
+  int up = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(FULL, up, o);
+    if (lane >= o) up += x;
+  }
+  up -= sum;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (lane * PER + i < n) out[lane * PER + i] = up;
+    up += v[i];
+  }
 }
 
-// The sort, in one cluster.  A warp holds HOLD times 32 pairs of its run in
-// registers from the first pass to the second; longer runs are read twice.
-__global__ void __launch_bounds__(NT) k_sort(const __grid_constant__ RouteArgs a) {
+// The sort, in one cluster, a run of rows for each block.  A row has an expert
+// once, so an expert's pairs of 32 rows are a word with a bit for each row, and a
+// pair's place among them is the number of bits before its own.  (Places without
+// an expert: a word for each of the k.)  Blocks take BATCH rows at a time.
+constexpr int BATCH = 512, GROUPS = BATCH / 32, MAX_BLOCKS = 16;
+__global__ void __launch_bounds__(NT) k_sort(const __grid_constant__ RouteArgs a, int rows_per) {
   cg::cluster_group cluster = cg::this_cluster();
-  __shared__ int hist[NW][BUCKETS], total[BUCKETS], start[BUCKETS + 1];
+  __shared__ uint32_t word[GROUPS][MAX_EXPERTS + MAX_TOP];
+  __shared__ uint16_t pre[GROUPS][BUCKETS];      // pairs of the groups before
+  __shared__ int sorted[MAX_BLOCKS * BUCKETS];   // every block's totals; then expert, pair of the batch
+  __shared__ int count[BUCKETS], whole[BUCKETS], start[BUCKETS], local[BUCKETS], base[BUCKETS], none[GROUPS];
+  static_assert(MAX_BLOCKS * BUCKETS >= BATCH * MAX_TOP, "a batch's pairs");
   const int rank = cluster.block_rank(), blocks = cluster.num_blocks();
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, nb = a.experts + 1;
-  allow_next();
-  for (int i = tid; i < NW * BUCKETS; i += NT) (&hist[0][0])[i] = 0;
-  const int pairs = a.rows * a.k, chunks = (pairs + 31) / 32, per = (chunks + blocks * NW - 1) / (blocks * NW);
-  const int c0 = min(chunks, (rank * NW + warp) * per), c1 = min(chunks, c0 + per);
-  const int bits = 32 - __clz(a.experts);        // (no pair is told from the others by its own ballot)
-  int b[HOLD];
-  unsigned same[HOLD];
-  auto fetch = [&](int c) {                      // the experts of the pairs from chunk c on; BUCKETS: no pair
+  const int tid = threadIdx.x, warp = tid / 32, nb = a.experts + 1;
+  const int row0 = min(a.rows, rank * rows_per), row1 = min(a.rows, row0 + rows_per);
+  constexpr int MINE = BATCH * MAX_TOP / NT;
+  int id[MINE];                                  // of pairs tid, tid + NT, ... of the batch
+  const int inv = (65536 + a.k - 1) / a.k;       // p / k = p * inv >> 16 for p < 4096, k <= 8
+  auto build = [&](int r0) {
+    const int pairs = (min(row1, r0 + BATCH) - r0) * a.k;
+    const int* ids = a.ids + (size_t)r0 * a.k;
 #pragma unroll
-    for (int i = 0; i < HOLD; ++i) {
-      const int p = (c + i) * 32 + lane;
-      b[i] = BUCKETS;
-      if (c + i < c1 && p < pairs) {
-        const int id = a.ids[p];
-        b[i] = id < 0 ? a.experts : id;
+    for (int i = 0; i < MINE; ++i) {
+      const int p = i * NT + tid;
+      if (p < pairs) {
+        const int x = ids[p], r = p * inv >> 16;
+        id[i] = x < 0 ? a.experts + p - r * a.k : x;
+        atomicOr(&word[r / 32][id[i]], 1u << r % 32);
+        if (x < 0) atomicAdd(&none[r / 32], 1);
       }
     }
+    __syncthreads();
+    if (tid < nb) {
+      int n[GROUPS], sum = 0;
 #pragma unroll
-    for (int i = 0; i < HOLD; ++i)
-      if (c + i < c1) same[i] = same_bucket(b[i], bits) & __ballot_sync(FULL, b[i] < BUCKETS);
+      for (int g = 0; g < GROUPS; ++g) n[g] = tid == a.experts ? none[g] : (int)word[g][tid];
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) {
+        pre[g][tid] = (uint16_t)sum;
+        sum += tid == a.experts ? n[g] : __popc(n[g]);
+      }
+      count[tid] = sum;
+    }
   };
-  __syncthreads();
+  auto clear = [&] {
+    for (int i = tid; i < GROUPS * (MAX_EXPERTS + MAX_TOP); i += NT) (&word[0][0])[i] = 0;
+    if (tid < GROUPS) none[tid] = 0;
+    __syncthreads();
+  };
+  allow_next();
+  clear();
+  cluster.sync();                                // every block is there to be written to
   await_stream();
-  for (int c = c0; c < c1; c += HOLD) {
-    fetch(c);
-#pragma unroll
-    for (int i = 0; i < HOLD; ++i) {
-      if (c + i >= c1) break;
-      if (b[i] < BUCKETS && lane == __ffs(same[i]) - 1) hist[warp][b[i]] += __popc(same[i]);
-      __syncwarp();
+  int total = 0;
+  if (row0 == row1 && tid < nb) count[tid] = 0;
+  for (int r0 = row0; r0 < row1; r0 += BATCH) {
+    if (r0 > row0) {
+      __syncthreads();
+      clear();
     }
+    build(r0);
+    if (tid < nb) total += count[tid];
   }
-  __syncthreads();
-  if (tid < nb) {                                // the warps before, within the block
-    int sum = 0;
-#pragma unroll 8
-    for (int w = 0; w < NW; ++w) {
-      const int n = hist[w][tid];
-      hist[w][tid] = sum;
-      sum += n;
-    }
-    total[tid] = sum;
-  }
+  if (tid < nb)
+    for (int r = 0; r < blocks; ++r) *cluster.map_shared_rank(&sorted[rank * BUCKETS + tid], r) = total;
   cluster.sync();
-  int before = 0;
+  int before = 0;                                // the blocks before
   if (tid < nb) {
-    int whole = 0;
+    int all = 0;
 #pragma unroll 8
-    for (int r = 0; r < blocks; ++r) {           // the blocks before
-      const int n = *cluster.map_shared_rank(&total[tid], r);
+    for (int r = 0; r < blocks; ++r) {
+      const int n = sorted[r * BUCKETS + tid];
       before += r < rank ? n : 0;
-      whole += n;
+      all += n;
     }
-    start[tid] = whole;
+    whole[tid] = all;
   }
-  auto read = cluster.barrier_arrive();
   __syncthreads();
-  if (warp == 0) {                               // the experts before
-    constexpr int PER = (BUCKETS + 31) / 32;
-    int n[PER], sum = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = lane * PER + i;
-      n[i] = e < nb ? start[e] : 0;
-      sum += n[i];
-    }
-    int up = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(FULL, up, o);
-      if (lane >= o) up += v;
-    }
-    up -= sum;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = lane * PER + i;
-      if (e < nb) {
-        start[e] = up;
-        if (rank == 0) a.first[e] = up;
-      }
-      up += n[i];
-    }
-  }
+  if (warp == 0) scan(whole, start, nb);         // the experts before
+  if (warp == 1) scan(count, local, nb);
   __syncthreads();
   if (tid < nb) {
-    before += start[tid];
-#pragma unroll 8
-    for (int w = 0; w < NW; ++w) hist[w][tid] += before;
+    base[tid] = start[tid] + before;
+    if (rank == 0) a.first[tid] = start[tid];
   }
-  __syncthreads();
-  for (int c = c0; c < c1; c += HOLD) {
-    if (per > HOLD) fetch(c);
+  const bool once = row1 - row0 <= BATCH;        // the first pass's words are still there
+  for (int r0 = row0; r0 < row1; r0 += BATCH) {
+    if (!once) {
+      __syncthreads();
+      clear();
+      build(r0);
+      __syncthreads();
+      if (warp == 0) scan(count, local, nb);
+      __syncthreads();
+    }
+    const int pairs = (min(row1, r0 + BATCH) - r0) * a.k;
 #pragma unroll
-    for (int i = 0; i < HOLD; ++i) {
-      if (c + i >= c1) break;
-      const int at = b[i] < BUCKETS ? hist[warp][b[i]] : 0;
-      __syncwarp();
-      if (b[i] < BUCKETS) {
-        a.order[at + __popc(same[i] & ((1u << lane) - 1))] = (c + i) * 32 + lane;
-        if (lane == __ffs(same[i]) - 1) hist[warp][b[i]] = at + __popc(same[i]);
+    for (int i = 0; i < MINE; ++i) {
+      const int p = i * NT + tid;
+      if (p < pairs) {
+        const int r = p * inv >> 16, g = r / 32, e = min(id[i], a.experts);
+        const uint32_t less = (1u << r % 32) - 1;
+        int at = local[e] + pre[g][e];
+        if (id[i] < a.experts) {
+          at += __popc(word[g][e] & less);
+        } else {
+          for (int j = 0; j < a.k; ++j) {
+            const uint32_t w = word[g][a.experts + j];
+            at += __popc(w & less) + (a.experts + j < id[i] ? w >> r % 32 & 1 : 0);
+          }
+        }
+        sorted[at] = e << 16 | p;
       }
-      __syncwarp();
+    }
+    __syncthreads();
+    for (int l = tid; l < pairs; l += NT) {      // an expert's pairs side by side
+      const int v = sorted[l], e = v >> 16;
+      a.order[base[e] + l - local[e]] = r0 * a.k + (v & 0xffff);
+    }
+    if (!once) {
+      __syncthreads();
+      if (tid < nb) base[tid] += count[tid];
     }
   }
-  cluster.barrier_wait(std::move(read));         // nobody leaves while its counts are read
 }
 
 // Whether the current device has room for a cluster of 16 (beyond what every
@@ -341,18 +361,18 @@ cudaError_t wide_cluster(bool* ok) {
   return e;
 }
 
-// A block for every 1024 pairs, 16 of them at most.
+// A block for every 128 rows, 16 of them at most.
 cudaError_t launch_sort(const RouteArgs& a, cudaStream_t st) {
-  const long long pairs = (long long)a.rows * a.k;
   int blocks = 1;
-  while (blocks < 16 && pairs > blocks * 1024) blocks *= 2;
+  while (blocks < 16 && a.rows > blocks * 128) blocks *= 2;
   if (blocks == 16) {
     bool ok = false;
     const cudaError_t e = wide_cluster(&ok);
     if (e != cudaSuccess) return e;
     if (!ok) blocks = 8;
   }
-  return launch_kernel(k_sort, blocks, NT, 0, blocks, st, a);
+  const int rows_per = ((a.rows + blocks - 1) / blocks + 31) / 32 * 32;
+  return launch_kernel(k_sort, blocks, NT, 0, blocks, st, a, rows_per);
 }
 
 }  // namespace

@@ -151,7 +151,8 @@ def check_route(mk, logits, k, wide=None):
 
 
 @pytest.mark.parametrize("rows,experts,k", [(1, 128, 8), (37, 128, 8), (513, 128, 8), (1, 1, 1), (300, 1, 1), (700, 5, 3),
-                                            (64, 8, 8), (2000, 33, 4), (100, 64, 8), (129, 256, 8), (1500, 200, 1), (4097, 37, 3)])
+                                            (64, 8, 8), (2000, 33, 4), (100, 64, 8), (129, 256, 8), (1500, 200, 1), (4097, 37, 3),
+                                            (8192, 16, 8), (8193, 16, 8), (20011, 9, 2)])
 def test_route(mk, rows, experts, k):
     wide = mu.normal((rows, experts + 3), rows + experts, 0.9)
     check_route(mk, wide[:, :experts].contiguous(), k, wide)
@@ -172,6 +173,9 @@ def test_route_ties_and_masks(mk):
     check_route(mk, m, 6)
     check_route(mk, m[3:4].contiguous(), 6)
     check_route(mk, torch.full((3, 9), -math.inf), 2)
+    x = mu.normal((9000, 12), 8)                              # more than the sort holds at a time
+    x[torch.rand(9000, 12, generator=torch.Generator().manual_seed(9)) < 0.8] = -math.inf
+    check_route(mk, x, 5)
 
 
 def test_route_one_expert_for_all(mk):
