@@ -8,10 +8,11 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmk.so")
 SOURCES = ["megakernel.cu", "megakernel_nuc.cu", "plan.cu", "noalloc.cu", "serve.cu",
-           "chunk.cu", "cache.cu", "attend.cu", "verify.cu", "norm.cu", "route.cu", "experts.cu"]
+           "chunk.cu", "cache.cu", "attend.cu", "verify.cu", "norm.cu", "route.cu", "experts.cu", "experts_two.cu"]
 HEADERS = [os.path.join(CSRC, "mk_internal.h"), os.path.join(CSRC, "megakernel.cuh"),
            os.path.join(CSRC, "chunk.h"), os.path.join(CSRC, "ptx.cuh"), os.path.join(CSRC, "launch.cuh"),
            os.path.join(CSRC, "rows.h"), os.path.join(CSRC, "eights.cuh"), os.path.join(CSRC, "host.h"),
+           os.path.join(CSRC, "experts.cuh"),
            os.path.join(ROOT, "include", "mk.h")]
 NVFLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo",
            "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"), "-I", CSRC]

@@ -16,17 +16,9 @@
 // The scales pass through shared memory to tensor memory; up's epilogue has a
 // thread for each row, so its groups of 32 results and their scale stay within a
 // thread.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-#include <cuda_bf16.h>
-
 #include <new>
 
-#include "eights.cuh"
-#include "host.h"
-#include "launch.cuh"
-#include "mk.h"
-#include "ptx.cuh"
+#include "experts.cuh"
 
 struct mk_experts {
   int hidden, experts, k, ffn;
@@ -37,24 +29,6 @@ struct mk_experts {
 
 namespace mk {
 namespace {
-
-using namespace ptx;
-
-constexpr unsigned FULL = 0xffffffffu;
-constexpr int MAX_EXPERTS = 256, MAX_STAGES = 12, SMEM_MOST = 232448;
-constexpr unsigned long long WAIT_NS = 2000000000ull;   // limit of every wait
-
-struct Ctl {
-  uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], list_full[2], list_free[2], drain;
-  uint32_t tmem;
-  int fail;
-  int4 list[2][32];              // the block's next tiles, as they are planned
-  int width, columns;            // columns of a tile, tiles of columns
-  int row0[MAX_EXPERTS + 1];     // an expert's first row in the sorted order
-  int tile0[MAX_EXPERTS + 1];    // and its first tile of rows
-};
-constexpr int CTL = 4096;
-static_assert(sizeof(Ctl) <= CTL, "control words");
 
 // Warps: 0 boxes of tensor maps, 1 matrix instructions, 2 tensor memory, 3 the
 // list of tiles, 4-7 results, then four for gathered rows (up) and four for scales
@@ -87,39 +61,6 @@ struct Cfg {
   static_assert(NT % 64 == 0 && AM % 32 == 0 && STAGE >= 128 * 128, "a tile");
 };
 
-struct Args {
-  const int *first, *order;
-  const float* gates;
-  const uint8_t *x, *a_scales, *b_scales;   // x: rows to gather (up)
-  uint8_t* out;
-  uint8_t* out_scales;
-  int* status;
-  int pairs, rows, top_k, experts;
-  int k, n;                      // elements of a row of A; columns of C
-  int extra;                     // what a tile costs beside its columns, in columns
-  int box;                       // columns of the large boxes
-  int a_wide, b_wide;            // bytes that a row's scales may be read by
-};
-
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Ctl* ctl, int* status) {
-  const unsigned long long t0 = now_ns();
-  while (!mbar_try(bar, parity)) {
-    if (*(volatile int*)&ctl->fail) return false;
-    if (now_ns() - t0 > WAIT_NS) {
-      *(volatile int*)&ctl->fail = 1;
-      atomicCAS(status, 0, MK_ERR_DEP_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, Ctl* ctl, int* status) {
-  return mbar_try(bar, parity) || wait_slow(bar, parity, ctl, status);
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* ctl, int* status) {
-  return __all_sync(FULL, wait_one(bar, parity, ctl, status));
-}
-
 // What tiles of this width cost: their rounds over the blocks, times the columns
 // of one and what it takes beside them.  (At most 2^18 + 256 tiles of rows and
 // 2^12 of columns: 32 bits.)
@@ -128,63 +69,12 @@ __host__ __device__ __forceinline__ unsigned cost_of(unsigned row_tiles, unsigne
   return (rounds < 1u << 22 ? rounds : 1u << 22) * (width + extra);
 }
 
-// Each expert's rows and tiles from `first`, by one warp; entries out of order or
-// out of range are moved into it, so whatever they hold, the rows stay within
-// the pairs and no row is counted twice.
-template <int AM, int NT, int G>
-__device__ __forceinline__ void set_tables(const Args& a, Ctl* ctl) {
-  constexpr int PER = MAX_EXPERTS / 32;
-  const int lane = threadIdx.x % 32;
-  int f[PER], top = 0;           // ends of the lane's experts, the largest so far
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane * PER + i;
-    f[i] = e < a.experts ? min(max(a.first[e + 1], 0), a.pairs) : 0;
-  }
-  const int f0 = min(max(a.first[0], 0), a.pairs);
-#pragma unroll
-  for (int i = 0; i < PER; ++i) f[i] = top = max(top, f[i]);
-  int before = top;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(FULL, before, o);
-    if (lane >= o) before = max(before, v);
-  }
-  before = __shfl_up_sync(FULL, before, 1);
-  if (lane == 0) before = 0;
-  before = max(before, f0);
-  int tiles = 0, from = before;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    f[i] = max(f[i], before);
-    tiles += (f[i] - from + AM - 1) / AM;
-    from = f[i];
-  }
-  int at = tiles;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(FULL, at, o);
-    if (lane >= o) at += v;
-  }
-  at -= tiles;
-  from = before;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane * PER + i;
-    if (e <= a.experts) {
-      ctl->row0[e] = from;
-      ctl->tile0[e] = at;
-    }
-    at += (f[i] - from + AM - 1) / AM;
-    from = f[i];
-  }
-  if (lane == 31 && a.experts == MAX_EXPERTS) {
-    ctl->row0[MAX_EXPERTS] = from;
-    ctl->tile0[MAX_EXPERTS] = at;
-  }
-  // The width: rounds of tiles that the blocks take, times what one takes.
-  const int width = G * (lane + 1), all = __shfl_sync(FULL, at, 31);   // (by every lane)
-  const unsigned cost = width <= NT ? cost_of(all, a.n, width, gridDim.x, a.extra) : 0xffffffffu;
+// The width of all tiles: rounds of tiles that the blocks take, times what one
+// takes.
+template <int NT, int G>
+__device__ __forceinline__ void set_width(const Args& a, Ctl* ctl) {
+  const int lane = threadIdx.x % 32, width = G * (lane + 1);
+  const unsigned cost = width <= NT ? cost_of(ctl->tile0[a.experts], a.n, width, gridDim.x, a.extra) : 0xffffffffu;
   const unsigned best = __reduce_min_sync(FULL, cost);
   const int who = __reduce_max_sync(FULL, cost == best ? lane : 0);
   if (lane == who) {
@@ -193,9 +83,6 @@ __device__ __forceinline__ void set_tables(const Args& a, Ctl* ctl) {
   }
 }
 
-struct Tile {
-  int e, row0, rows, n0, width;  // expert, first row in the sorted order, rows, first column, columns
-};
 // A block's tiles are t, t + blocks, ...: neighbours share an expert's weights
 // in L2.  One warp plans 32 at a time (a search and divisions, which took the
 // issuing thread 500 cycles a tile) and the others read them.  (Sharing the last
@@ -226,41 +113,6 @@ __device__ __forceinline__ void plan_tiles(const Args& a, Ctl* ctl) {
     if (!__all_sync(FULL, t < tiles)) return;    // an entry without rows is behind the last one
   }
 }
-// The next tile of the list, for a thread (or a warp: the same for all its
-// lanes); one arrival frees 32 of them.
-struct Reader {
-  int i = 0;
-  template <bool WARP>
-  __device__ __forceinline__ bool next(Ctl* ctl, int* status, Tile& t) {
-    const int c = i / 32;
-    uint64_t* full = &ctl->list_full[c & 1];
-    if (i % 32 == 0 && !(WARP ? wait(full, c >> 1 & 1, ctl, status) : wait_one(full, c >> 1 & 1, ctl, status))) return false;
-    const int4 v = ctl->list[c & 1][i % 32];
-    if (v.x >> 16 == 0) return false;
-    if (++i % 32 == 0) {
-      if (WARP) __syncwarp();
-      if (!WARP || threadIdx.x % 32 == 0) mbar_arrive(&ctl->list_free[c & 1]);
-    }
-    t = {v.x & 0xffff, v.y, v.x >> 16, v.z, v.w};
-    return true;
-  }
-};
-
-// A pair's row of x; one that is none reads zeros.
-__device__ __forceinline__ int token_of(const Args& a, int at) {
-  const int p = a.order[at];
-  return p >= 0 && p < a.pairs ? p / a.top_k : a.rows;
-}
-
-__device__ __forceinline__ float swiglu(float gate, float up) { return __fdividef(gate, 1.f + __expf(-gate)) * up; }
-
-// Behind a wait for loads: their registers are used after it, not before.
-template <int N>
-__device__ __forceinline__ void landed(uint32_t* r) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
-
 // Columns of a row as results, 16 bytes at a time: up's (gate and up columns in
 // turn; 8 bits: and the scale of 32 of them), or down's times the gate.
 __device__ __forceinline__ void put16(uint8_t* p, const float* v) {
@@ -313,33 +165,6 @@ __device__ __forceinline__ void put_down(const uint32_t* r, uint8_t* to, float g
     put16(to + 2 * i, v);
   }
 }
-
-// A row's scales of four stages from kb on, a word each; `wide` bytes at a time.
-__device__ __forceinline__ uint4 scales16(const uint8_t* row, int groups, int kb, int wide) {
-  const uint8_t* p = row + kb * 4;
-  const int left = groups - kb * 4;
-  if (wide == 16) return *reinterpret_cast<const uint4*>(p);
-  uint32_t v[4] = {0, 0, 0, 0};
-  if (wide == 8) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (8 * i < left) {
-        const uint2 w = reinterpret_cast<const uint2*>(p)[i];
-        v[2 * i] = w.x;
-        v[2 * i + 1] = w.y;
-      }
-  } else if (wide == 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (4 * i < left) v[i] = reinterpret_cast<const uint32_t*>(p)[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < left) v[i / 4] |= (uint32_t)p[i] << (i % 4 * 8);
-  }
-  return make_uint4(v[0], v[1], v[2], v[3]);
-}
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
 template <bool E4M3, bool UP, int AM, int NT>
 __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
@@ -458,7 +283,9 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 3) {                        // ---- the list of tiles
-    set_tables<AM, NT, C::G>(a, ctl);
+    set_tables<AM>(a, ctl);
+    __syncwarp();
+    set_width<NT, C::G>(a, ctl);
     __syncwarp();
     plan_tiles<AM, C::G>(a, ctl);
   } else if (warp >= 4 && warp < 8) {            // ---- results: one thread a row
@@ -652,32 +479,6 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
   if (warp == 2) tmem_free<C::T_COLS>(tmem);
 }
 
-// A matrix (or one for each expert) as boxes of 128-byte rows.
-cudaError_t tensor_map(CUtensorMap* map, bool e4m3, const void* base, int dims, const cuuint64_t* dim, const cuuint32_t* box) {
-  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      fn = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }();
-  if (!encode) return cudaErrorNotSupported;
-  const cuuint64_t el = e4m3 ? 1 : 2, stride[2] = {dim[0] * el, dim[0] * dim[1] * el};
-  const cuuint32_t step[3] = {1, 1, 1};
-  return encode(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, const_cast<void*>(base), dim,
-                stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? cudaSuccess
-             : cudaErrorInvalidValue;
-}
-
-int scales_wide(const void* p, int groups) {
-  for (int w = 16; w > 2; w /= 2)
-    if (groups % w == 0 && (uintptr_t)p % w == 0) return w;
-  return 1;
-}
-
 template <bool E4M3, bool UP, int AM, int NT>
 cudaError_t launch(Args a, const void* rows, const void* w, int sms, cudaStream_t st) {
   using C = Cfg<E4M3, UP, AM, NT>;
@@ -711,6 +512,16 @@ cudaError_t launch(const Args& a, const void* rows, const void* w, cudaStream_t 
   int sms = 0;
   const cudaError_t e = multiprocessors(&sms);
   if (e != cudaSuccess) return e;
+  // bf16 with 128 rows an expert: tiles of two SMs (8143 rows of the full model:
+  // up 295 us, 311 with one; down 156 and 175; 2500 rows: 144 and 150, 82 and 85;
+  // 1200, 75 an expert: 135 and 130), where they are enough for four rounds of
+  // the SMs and little of their 256 columns is lost (hidden 1056: 28.6 us with
+  // one, 32.6).
+  const long long cols = (a.n + 255) / 256;
+  if (!E4M3 && a.pairs >= 128 * a.experts && (a.pairs / 256 + a.experts / 2) * cols >= 2 * sms && 10 * a.n >= 9 * 256 * cols)
+    return launch_two(UP, a, rows, w, sms, st);
+  // Few rows an expert: tiles of 32 rows leave the shared memory to the weights
+  // on their way.
   if (a.pairs <= 16 * a.experts) return launch<E4M3, UP, 32, 128>(a, rows, w, sms, st);
   return launch<E4M3, UP, 128, E4M3 ? 192 : 256>(a, rows, w, sms, st);
 }

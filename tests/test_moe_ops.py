@@ -289,6 +289,49 @@ def test_products_of_many_tiles(mk, kind):
     check_down(mk, c)
 
 
+TWO = [(2200, [1, 1, 1, 1]), (2311, [5, 0, 1, 3]), (2500, [0, 0, 1, 0]), (2250, [70, 1, 0, 30])]
+
+
+@pytest.mark.parametrize("rows,weights", TWO)
+@pytest.mark.parametrize("lost", [False, True])
+def test_products_of_two_sms(mk, rows, weights, lost):
+    # enough rows an expert and columns for tiles of two SMs: even, uneven, all with one expert, pairs without one
+    g = torch.Generator().manual_seed(rows)
+    ids = torch.multinomial(torch.tensor(weights).float(), rows * 2, replacement=True, generator=g).int().view(rows, 2)
+    if lost:
+        ids[torch.rand(rows, 2, generator=g) < 0.02] = -1
+    check_up(mk, Case("bf16", (72, 4, 2, 2040), ids, 31))
+    check_down(mk, Case("bf16", (4088, 4, 2, 72), ids, 32), gates=not lost)
+
+
+def test_products_of_two_sms_special(mk):
+    # a NaN stays with its rows; lists that hold anything read and write nothing outside
+    g = torch.Generator().manual_seed(5)
+    ids = torch.randint(0, 4, (2300, 2), generator=g).int()
+    c = Case("bf16", (64, 4, 2, 2048), ids, 33)
+    c.x[0][7] = math.nan
+    m = c.experts_of(mk)
+    x, w, first, order = c.x[0].cuda(), c.gu[0].cuda(), c.first.cuda(), c.order.cuda()
+    w_h, h = cuda_empty((c.pairs, c.ffn), BF16)
+    m.up(x, w, first, order, h)
+    bad = h.float().isnan().any(1).cpu()
+    assert m.sync() == mk.MK_OK and int(bad.sum()) == 2 and bad[(c.order == 14).nonzero()] and bad[(c.order == 15).nonzero()]
+    again = h.clone()
+    m.up(x, w, first, order, h)
+    assert m.sync() == mk.MK_OK and torch.equal(again.view(torch.int16), h.view(torch.int16))   # the same bits
+    d = Case("bf16", (4096, 4, 2, 64), ids, 34)
+    md, hh, dn = d.experts_of(mk), d.h[0].cuda(), d.dn[0].cuda()
+    big = 2 ** 31 - 1
+    for first, order in ([[0, 9000, -5, 100, 40], c.order], [[-big, big, big, 0, 300], c.order], [c.first, torch.full((4600,), big)],
+                         [c.first, torch.arange(4600) * 7 - 100], [[4000, 4100, 4050, 4600, 4580], c.order]):
+        first, order = torch.as_tensor(first).int().cuda(), order.int().cuda()
+        w_h, h = cuda_empty((c.pairs, c.ffn), BF16)
+        m.up(x, w, first, order, h)
+        w_y, y = cuda_empty((d.rows, 2, d.hidden), BF16)
+        md.down(hh, dn, first, order, d.gates.cuda(), y)
+        assert m.sync() == mk.MK_OK and md.sync() == mk.MK_OK and behind(w_h) and behind(w_y)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("counts", [[0, 128, 0, 0], [127, 0, 1, 129], [0, 0, 0, 513], [256, 255, 257, 1], [16, 17, 15, 4]])
 def test_products_tile_borders(mk, kind, counts):
@@ -427,9 +470,9 @@ class Layer:
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-@pytest.mark.parametrize("name,rows", [("tiny", 1), ("tiny", 200), ("odd", 37)])
+@pytest.mark.parametrize("name,rows", [("tiny", 1), ("tiny", 200), ("odd", 37), ("wide", 600)])
 def test_layer(mk, kind, name, rows):
-    layer = Layer(mk, kind, DIMS[name], rows)
+    layer = Layer(mk, kind, {**DIMS, "wide": (4096, 2, 2, 2048)}[name], rows)
     layer.run()
     layer.check()
     first = layer.out.clone()
