@@ -271,7 +271,7 @@ int mk_quantize(int rows, int n, const void* x, int x_type, long long x_stride, 
   int sms = 0;
   cudaError_t e = multiprocessors(&sms);
   if (e != cudaSuccess) return fail_cuda("mk_quantize", e);
-  const long long pieces = (long long)rows * (n / 8), most = (pieces + 1023) / 1024, full = (long long)sms * 8;
+  const long long pieces = (long long)rows * (n / 8), most = (pieces + 1023) / 1024, full = (long long)sms * 32;   // four rounds (one: 202 us below)
   const dim3 grid((unsigned)(most < full ? most : full));
   const cudaStream_t st = (cudaStream_t)stream;
   if (x_type == MK_ROWS_F32)
