@@ -516,3 +516,163 @@ def test_layers_on_two_streams(mk):
     torch.cuda.synchronize()
     for layer in (a, b, b_shared):
         layer.check()
+
+
+def test_layer_beside_a_capture_from_a_new_process(mk):
+    # a process's first calls, inside a capture
+    import subprocess
+    import sys
+
+    code = """
+import torch
+from persistent_moe_decode_02_gb300 import mk
+from tests import test_moe_ops as T
+layer = T.Layer(mk, "bf16", T.DIMS["tiny"], 300)
+layer.logits = torch.empty(300, 8, device="cuda")
+torch.mm(layer.w["x"], layer.w["router"])        # (the library's own first call)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    layer.run()
+g.replay()
+layer.check()
+print("fine")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+def test_nothing_to_do(mk):
+    m = mk.Experts(mu.dims(64, 4, 2, 32), "bf16")
+    e = lambda *s, t=BF16: torch.empty(*s, dtype=t, device="cuda")   # noqa: E731
+    first, order = torch.zeros(5, dtype=torch.int32, device="cuda"), e(0, t=torch.int32)
+    m.up(e(0, 64), e(4, 64, 64), first, order, e(0, 32))
+    m.down(e(0, 32), e(4, 32, 64), first, order, None, e(0, 2, 64))
+    mk.norm(e(0, 64), None, 1e-6, e(0, 64))
+    mk.quantize(e(0, 64), e(0, 64, t=E4M3), e(0, 2, t=U8))
+    assert m.sync() == mk.MK_OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("name,rows", [("odd", 77), ("odd", 600), ("tail", 300)])
+def test_products_between_alignments(mk, name, rows, kind):
+    # rows and weights 16 bytes past a larger alignment, scales at any byte
+    c = Case(kind, DIMS[name], routed(DIMS[name], rows), 41)
+    m = c.experts_of(mk)
+
+    def shifted(t, by):
+        if t is None:
+            return None
+        whole = torch.empty(t.numel() + by, dtype=t.dtype, device="cuda")
+        part = whole[by:].view(t.shape)
+        part.copy_(t.cuda())
+        return part
+
+    el = 1 if kind == "e4m3" else 2
+    (x, xs), (w, ws), (h, hs), (d, ds) = ((shifted(a, 16 // el), shifted(b, 3)) for a, b in (c.x, c.gu, c.h, c.dn))
+    out, s = shifted(torch.zeros(c.pairs, c.ffn).to(BF16 if kind == "bf16" else E4M3), 16 // el), shifted(
+        None if kind == "bf16" else torch.zeros(c.pairs, c.ffn // 32, dtype=U8), 5)
+    y = shifted(torch.zeros(c.rows, c.k, c.hidden, dtype=BF16), 8)
+    first, order, gates = shifted(c.first, 1), shifted(c.order, 1), shifted(c.gates, 1)
+    m.up(x, w, first, order, out, x_scales=xs, w_scales=ws, h_scales=s)
+    m.down(h, d, first, order, gates, y, h_scales=hs, w_scales=ds)
+    assert m.sync() == mk.MK_OK
+    ref, slack = mu.up(c.vx, c.vgu, c.first, c.order, c.k)
+    if kind == "bf16":
+        mu.within(out.cpu(), ref, slack)
+    else:
+        mu.check_eights(out.cpu(), s.cpu(), ref, slack)
+    ref, slack = mu.down(c.vh, c.vdn, c.first, c.order, c.gates)
+    mu.within(y.cpu().flatten(0, 1), ref, slack)
+
+
+def test_rows_beyond_4_gb(mk):
+    # the last rows of buffers of more than 4 GB: rows to 8 bits, norm, up and down
+    x = torch.zeros(70000, 32768, dtype=BF16, device="cuda")
+    some = mu.normal((3, 32768), 1).bfloat16()
+    x[-3:] = some.cuda()
+    codes, scales = torch.empty(70000, 32768, dtype=E4M3, device="cuda"), torch.empty(70000, 1024, dtype=U8, device="cuda")
+    mk.quantize(x, codes, scales)
+    want = mu.quantise(some)
+    assert torch.equal(codes[-3:].cpu().view(U8), want[0].view(U8)) and torch.equal(scales[-3:].cpu(), want[1])
+    del codes, scales
+    y = x.view(280000, 8192)
+    out = torch.empty_like(y)
+    mk.norm(y, None, 1e-6, out)
+    _, ref, _, slack = mu.norm(some.view(12, 8192), None, None, 1e-6)
+    mu.within(out[-12:].cpu(), ref, slack)
+    del x, y, out
+    D = (64, 2, 1, 4096)
+    rows = 600000
+    ids = (torch.arange(rows) % 2).int().unsqueeze(1)
+    order = torch.cat([torch.arange(0, rows, 2), torch.arange(1, rows, 2)]).int()
+    first = torch.tensor([0, rows // 2, rows], dtype=torch.int32)
+    xx, gu = mu.normal((rows, 64), 2).bfloat16(), mu.normal((2, 8192, 64), 3, 0.1).bfloat16()
+    m = mk.Experts(mu.dims(*D), "bf16")
+    h = torch.empty(rows, 4096, dtype=BF16, device="cuda")
+    m.up(xx.cuda(), gu.cuda(), first.cuda(), order.cuda(), h)
+    assert m.sync() == mk.MK_OK
+    last = order[-5:].long()
+    ref, slack = mu.up(xx[last].double(), gu.double(), torch.tensor([0, 0, 5]), torch.arange(5), 1)
+    mu.within(h[-5:].cpu(), ref, slack)
+    del h
+    D = (4096, 2, 1, 64)
+    hh, dn = mu.normal((rows, 64), 4).bfloat16(), mu.normal((2, 64, 4096), 5, 0.1).bfloat16()
+    m = mk.Experts(mu.dims(*D), "bf16")
+    y = torch.empty(rows, 4096, dtype=BF16, device="cuda")
+    m.down(hh.cuda(), dn.cuda(), first.cuda(), order.cuda(), None, y)
+    assert m.sync() == mk.MK_OK
+    ref, slack = mu.down(hh[-5:].double(), dn.double(), torch.tensor([0, 0, 5]), torch.arange(5), None)
+    mu.within(y[last.cuda()].cpu(), ref, slack)
+    assert int(ids[last[-1]]) == 1
+
+
+def test_refused_tensors(mk):
+    c = lambda *s, t=F32: torch.empty(*s, dtype=t, device="cuda")   # noqa: E731
+    x = c(4, 64)
+    with pytest.raises(ValueError):
+        mk.norm(x.cpu(), None, 1e-6, c(4, 64))
+    with pytest.raises(ValueError):
+        mk.norm(x.half(), None, 1e-6, c(4, 64))
+    with pytest.raises(ValueError):
+        mk.norm(x, None, 1e-6, c(4, 64, t=E4M3))                   # 8 bits without scales
+    with pytest.raises(ValueError):
+        mk.norm(x, None, 1e-6, c(4, 64), scales=c(4, 2, t=U8))
+    with pytest.raises(ValueError):
+        mk.norm(x, c(64), 1e-6, c(4, 64))                           # gamma is bf16
+    with pytest.raises(ValueError):
+        mk.norm(x, None, 1e-6, c(4, 64), add=c(4, 32))
+    with pytest.raises(ValueError):
+        mk.norm(x, None, 1e-6, c(4, 64), total=c(4, 64, t=BF16))
+    with pytest.raises(ValueError):
+        mk.norm(c(64, 4).t(), None, 1e-6, c(4, 64))                 # columns apart
+    with pytest.raises(mk.MkError):
+        mk.norm(x, None, 1e-6, x)                                   # onto its input
+    with pytest.raises(mk.MkError):
+        mk.norm(c(4, 68)[:, 1:65], None, 1e-6, c(4, 64))            # not 16-byte aligned
+    with pytest.raises(ValueError):
+        mk.quantize(x, c(4, 64, t=U8), c(4, 2, t=U8))
+    with pytest.raises(mk.MkError):
+        mk.quantize(c(4, 40), c(4, 40, t=E4M3), c(4, 1, t=U8))
+    i = lambda *s: c(*s, t=torch.int32)   # noqa: E731
+    with pytest.raises(ValueError):
+        mk.route(c(4, 8, t=BF16), i(4, 2), c(4, 2), i(9), i(8))
+    with pytest.raises(ValueError):
+        mk.route(c(4, 8), i(4, 2), c(4, 2), i(8), i(8))
+    with pytest.raises(mk.MkError):
+        mk.route(c(4, 8), i(4, 9), c(4, 9), i(9), i(36))
+    m, m8 = mk.Experts(mu.dims(64, 4, 2, 32), "bf16"), mk.Experts(mu.dims(64, 4, 2, 32), "e4m3")
+    b = lambda *s: c(*s, t=BF16)   # noqa: E731
+    with pytest.raises(ValueError):
+        m.up(b(3, 64), b(4, 64, 64), i(5), i(7), b(6, 32))          # pairs that are no rows
+    with pytest.raises(ValueError):
+        m.up(b(3, 64), b(4, 64, 32), i(5), i(6), b(6, 32))
+    with pytest.raises(ValueError):
+        m.up(b(3, 64), b(4, 64, 64), i(5), i(6), b(6, 32), x_scales=c(3, 2, t=U8))
+    with pytest.raises(ValueError):
+        m8.up(c(3, 64, t=E4M3), c(4, 64, 64, t=E4M3), i(5), i(6), c(6, 32, t=E4M3))
+    with pytest.raises(ValueError):
+        m.down(b(6, 32), b(4, 64, 32), i(5), i(6), c(3, 2), b(3, 2, 64))   # bf16 weights lie [experts, ffn, hidden]
+    h = b(6, 64)
+    with pytest.raises(mk.MkError):
+        m.down(h.view(-1)[:192].view(6, 32), b(4, 32, 64), i(5), i(6), None, h.view(3, 2, 64))   # y on its input
