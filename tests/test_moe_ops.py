@@ -6,6 +6,8 @@ import math
 import pytest
 import torch
 
+import synth
+from synth.device import DeviceModel, kv_pages_needed
 from tests import moe_util as mu
 
 pytestmark = pytest.mark.gpu
@@ -676,3 +678,61 @@ def test_refused_tensors(mk):
     h = b(6, 64)
     with pytest.raises(mk.MkError):
         m.down(h.view(-1)[:192].view(6, 32), b(4, 32, 64), i(5), i(6), None, h.view(3, 2, 64))   # y on its input
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_a_prompt_through_the_operators(mk, kind):
+    # a two-layer model's prompt by the chunk operators (dense products by torch) against the decode step's prefill
+    # rows: the same choice of experts from the same logits, and the hidden states of every layer
+    D, seed, n = synth.TINY, 5, 8
+    w = DeviceModel(D, seed).weights()
+    pages, width, table = kv_pages_needed(D, [16], 2) + 2, 3, [2, 0, 1]
+    pools = lambda: [torch.zeros(pages, D.n_kv_heads, 2, D.head_dim, 16, dtype=BF16, device="cuda") for _ in range(D.n_layers)]   # noqa: E731
+    tok = torch.tensor([(37 * i + 11) % D.vocab for i in range(n)], dtype=torch.int32, device="cuda")
+    plan = mk.Plan(D, w, pools(), [0], table, width, max_batch=8)
+    plan.update_rows(list(range(n)), table * n, width, [0] * n)
+    nxt = torch.empty(n, dtype=torch.int32, device="cuda")
+    assert plan.step(tok, nxt) == mk.MK_OK
+    c = lambda *s, t=F32: torch.empty(*s, dtype=t, device="cuda")   # noqa: E731
+    hid, ids, gates, logits = (plan.read_debug(what, c(n, D.n_layers, m, t=t)) for what, m, t in (
+        (mk.MK_DBG_HIDDEN, D.hidden, F32), (mk.MK_DBG_EXPERT_IDS, D.top_k, torch.int32), (mk.MK_DBG_GATES, D.top_k, F32),
+        (mk.MK_DBG_ROUTER_LOGITS, D.n_experts, F32)))
+    assert plan.sync() == mk.MK_OK
+    chunk = mk.Chunk(D, "bf16", pages, [0], [n], table, width)
+    m, mine, kv = mk.Experts(D, kind), pools(), None
+    e8 = kind == "e4m3"
+    x = w["embed"][tok.long()].float()
+    for l in range(D.n_layers):
+        nf, q = c(n, D.hidden), c(n, D.n_q_heads, D.head_dim, t=BF16)
+        mk.norm(x, w["attn_norm"][l], D.rms_eps, nf)
+        chunk.append(nf @ w["wqkv"][l].float().T, mine[l], q)
+        chunk.attend(q, mine[l], q)
+        o = q.float().flatten(1) @ w["wo"][l].float().T
+        x2, rows, s = c(n, D.hidden), c(n, D.hidden, t=E4M3 if e8 else BF16), c(n, D.hidden // 32, t=U8) if e8 else None
+        mk.norm(x, w["ffn_norm"][l], D.rms_eps, rows, add=o, total=x2, scales=s)
+        g_ids, g, first, order = c(n, D.top_k, t=torch.int32), c(n, D.top_k), c(D.n_experts + 1, t=torch.int32), c(n * D.top_k, t=torch.int32)
+        mk.route(logits[:, l], g_ids, g, first, order)             # the decode step's logits, which lie apart
+        assert torch.equal(g_ids, ids[:, l])
+        assert ((g - gates[:, l]).abs() < 1e-6).all()              # either a softmax in fp32
+        gu, dn = w["w_gate_up"][l], w["w_down"][l]
+        gu, gus, dn, dns = gu.view(D.n_experts, 2 * D.expert_ffn, D.hidden), None, dn.view(D.n_experts, D.expert_ffn, D.hidden), None
+        h, hs = c(n * D.top_k, D.expert_ffn, t=E4M3 if e8 else BF16), c(n * D.top_k, D.expert_ffn // 32, t=U8) if e8 else None
+        if e8:
+            def eight(t):
+                codes, scales = c(*t.shape, t=E4M3), c(*t.shape[:-1], t.shape[-1] // 32, t=U8)
+                k = t.shape[-1]
+                mk.quantize(t.reshape(-1, k), codes.view(-1, k), scales.view(-1, k // 32))
+                return codes, scales
+            (gu, gus), (dn, dns) = eight(gu), eight(dn.transpose(1, 2).contiguous())
+        y = c(n, D.top_k, D.hidden, t=BF16)
+        m.up(rows, gu, first, order, h, x_scales=s, w_scales=gus, h_scales=hs)
+        m.down(h, dn, first, order, g, y, h_scales=hs, w_scales=dns)
+        mk.norm(x2, None, 0.0, None, add=y, total=x2)
+        assert m.sync() == mk.MK_OK and chunk.sync() == mk.MK_OK
+        # bf16: the framework's own bound for hidden states; 8 bits: the experts' share of them is rounded to 4 bits
+        # three times (rows, weights, h), each to within 2^-4, and the layer before comes in
+        off = (x2 - hid[:, l]).norm() / hid[:, l].norm()
+        share = (x2 - x).norm() / hid[:, l].norm()
+        assert off < (1e-2 if not e8 else 1e-2 + 3 * 2 ** -4 * share * (l + 1)), (l, float(off), float(share))
+        x = x2
+    plan.close()
