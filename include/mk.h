@@ -619,8 +619,9 @@ int mk_verify(int batch, int max_draft, int vocab, const float* target, const fl
  * decode step runs inside its launch: norm, (the caller's) router product, top-k
  * and sort, the experts' gate and up, their down, and their sum in the next norm.
  * They are enqueued on `stream` and can be captured into a graph, except where
- * said otherwise; rows 0 is allowed everywhere and does nothing.  Results may not
- * overlap any other buffer of the call (MK_ERR_INVALID), except where said. */
+ * said otherwise; rows 0 is allowed everywhere and does nothing (mk_route still
+ * writes `first`).  Results may not overlap any other buffer of the call
+ * (MK_ERR_INVALID), except where said. */
 
 /* Norm with the addition in front of it: t = x + sum_j add[r, j, :] in fp32, j
  * in order, and out = t / sqrt(mean(t^2) + eps) * gamma from that fp32 t.
@@ -634,7 +635,8 @@ int mk_verify(int batch, int max_draft, int vocab, const float* target, const fl
  *          uint8 [rows, n / 32]); NULL: the sum alone
  * n a multiple of 8 (E4M3: of 32), at most 16384 (MK_ERR_UNSUPPORTED); x_stride
  * times the element's size a multiple of 16; buffers 16-byte aligned (scales:
- * any).  A NaN in a row makes the row's out NaN. */
+ * any).  A NaN in a row makes the row's out NaN; so does eps 0 for a row of
+ * zeros. */
 int mk_norm(int rows, int n, const void* x, int x_type, long long x_stride, const void* add, int add_type, int terms,
             const void* gamma, float eps, void* total, void* out, int out_type, uint8_t* scales, mk_stream stream);
 

