@@ -705,15 +705,19 @@ def verify(target: torch.Tensor, draft: Optional[torch.Tensor], drafts: torch.Te
 
 
 _E4M3 = torch.float8_e4m3fn
-_ROWS = {_BF16: MK_ROWS_BF16, _F32: MK_ROWS_F32}
+_ROWS, _F32_ROWS = {_BF16: MK_ROWS_BF16, _F32: MK_ROWS_F32}, {_F32: MK_ROWS_F32}
 
 
-def _rows(name: str, t: torch.Tensor, dev: int):
-    """Address, type and row stride of bf16 or float32 rows [rows, n] that may lie apart."""
-    kind, shape, steps = _ROWS.get(t.dtype), t.shape, t.stride()
-    if kind is None or len(shape) != 2 or t.get_device() != dev or (steps[1] != 1 and shape[1] != 1 and shape[0]):
-        raise ValueError(f"{name}: bf16 or float32 rows [rows, n] of the current CUDA device are wanted")
-    return t.data_ptr(), kind, steps[0] if shape[0] > 1 else shape[1]
+def _rows(name: str, t: torch.Tensor, kinds):
+    """Device, type, shape and row stride of rows [rows, n] that may lie apart."""
+    dev, kind, shape = t.get_device(), kinds.get(t.dtype), t.shape
+    if kind is not None and dev >= 0 and len(shape) == 2 and dev == torch._C._cuda_getDevice():
+        if t.is_contiguous():
+            return dev, kind, shape, shape[1]
+        steps = t.stride()
+        if steps[1] == 1 or shape[1] == 1:
+            return dev, kind, shape, steps[0] if shape[0] > 1 else shape[1]
+    raise ValueError(f"{name}: {' or '.join(str(k) for k in kinds)} rows [rows, n] of the current CUDA device are wanted")
 
 
 def _scales(t: Optional[torch.Tensor], shape, dev: int) -> int:
@@ -730,9 +734,7 @@ def norm(x: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, out: Option
     float32 [rows, n] (rows may lie apart); add bf16 or float32 [rows, n] or [rows, terms, n]; gamma bf16 [n] or None;
     out bf16, float32 or (with scales uint8 [rows, n / 32]) float8_e4m3fn [rows, n], or None; total like x, packed, or
     None; it may be x itself."""
-    dev = _device()
-    at, kind, stride = _rows("x", x, dev)
-    shape = x.shape
+    dev, kind, shape, stride = _rows("x", x, _ROWS)
     rows, n = shape
     terms, a, a_kind = 0, None, 0
     if add is not None:
@@ -755,7 +757,7 @@ def norm(x: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, out: Option
         raise ValueError("scales: only with an 8-bit out")
     if not rows:
         return
-    rc = lib().mk_norm(rows, n, at, kind, stride, a, a_kind, terms,
+    rc = lib().mk_norm(rows, n, x.data_ptr(), kind, stride, a, a_kind, terms,
                        None if gamma is None else _here("gamma", gamma, _BF16, (n,), dev), eps,
                        None if total is None else _here("total", total, x.dtype, shape, dev), o, o_kind, s,
                        _on(stream, dev))
@@ -766,13 +768,12 @@ def norm(x: torch.Tensor, gamma: Optional[torch.Tensor], eps: float, out: Option
 def quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
     """Rows x [rows, n] (bf16 or float32, rows may lie apart) to 8 bits: codes float8_e4m3fn [rows, n], scales uint8
     [rows, n / 32] (include/mk.h).  Contiguous weights of more dimensions go as x.view(-1, n)."""
-    dev = _device()
-    at, kind, stride = _rows("x", x, dev)
-    rows, n = shape = x.shape
+    dev, kind, shape, stride = _rows("x", x, _ROWS)
+    rows, n = shape
     c, s = _here("codes", codes, _E4M3, shape, dev), _scales(scales, (rows, n // 32), dev)
     if not rows:
         return
-    rc = lib().mk_quantize(rows, n, at, kind, stride, c, s, _on(stream, dev))
+    rc = lib().mk_quantize(rows, n, x.data_ptr(), kind, stride, c, s, _on(stream, dev))
     if rc != MK_OK:
         raise MkError("mk_quantize", rc)
 
@@ -781,17 +782,14 @@ def route(logits: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor, first: t
           stream=None) -> None:
     """Each row's experts and the rows of each expert (include/mk.h): logits float32 [rows, experts] (rows may lie
     apart); out: ids int32 and gates float32 [rows, top_k], first int32 [experts + 1], order int32 [rows * top_k]."""
-    dev = _device()
-    if logits.dim() != 2 or logits.dtype is not _F32 or logits.get_device() != dev or (
-            logits.numel() and logits.stride(1) != 1 and logits.shape[1] != 1):
-        raise ValueError("logits: float32 rows [rows, experts] of the current CUDA device are wanted")
+    dev, _, (rows, experts), stride = _rows("logits", logits, _F32_ROWS)
     if ids.dim() != 2:
         raise ValueError("ids: int32 [rows, top_k] is wanted")
-    (rows, experts), k = logits.shape, ids.shape[1]
-    args = (_here("ids", ids, _I32, (rows, k), dev), _here("gates", gates, _F32, (rows, k), dev),
-            _here("first", first, _I32, (experts + 1,), dev), _here("order", order, _I32, (rows * k,), dev))
-    rc = lib().mk_route(rows, experts, k, logits.data_ptr() if rows else None, logits.stride(0) if rows > 1 else experts,
-                        *args, _on(stream, dev))
+    k = ids.shape[1]
+    each = (rows, k)
+    rc = lib().mk_route(rows, experts, k, logits.data_ptr() if rows else None, stride, _here("ids", ids, _I32, each, dev),
+                        _here("gates", gates, _F32, each, dev), _here("first", first, _I32, (experts + 1,), dev),
+                        _here("order", order, _I32, (rows * k,), dev), _on(stream, dev))
     if rc != MK_OK:
         raise MkError("mk_route", rc)
 
@@ -814,33 +812,33 @@ class Experts:
         if rc != MK_OK:
             raise MkError("mk_experts_create", rc)
         self.h, self.e4m3 = h, rows_type == "e4m3"
-        self.hidden, self.experts, self.top_k, self.ffn = D.hidden, D.n_experts, D.top_k, D.expert_ffn
+        self.hidden, self.experts, self.top_k, self.ffn = e = D.hidden, D.n_experts, D.top_k, D.expert_ffn
+        self._first, self._up, self._down = (e[1] + 1,), (e[1], 2 * e[3], e[0]), (e[1], e[0], e[3]) if self.e4m3 else (e[1], e[3], e[0])
 
-    def _two(self, name, t, scales, shape, dev):
-        if self.e4m3:
-            return _here(name, t, _E4M3, shape, dev), _scales(scales, (*shape[:-1], shape[-1] // 32), dev)
-        if scales is not None:
-            raise ValueError(f"{name}: scales are of 8-bit rows")
-        return _here(name, t, _BF16, shape, dev), None
-
-    def _lists(self, first, order, dev):
-        pairs = order.numel()
-        if pairs % self.top_k:
-            raise ValueError(f"order: {pairs} pairs, wanted a multiple of {self.top_k}")
-        return pairs, _here("first", first, _I32, (self.experts + 1,), dev), _here("order", order, _I32, (pairs,), dev)
+    def _lists(self, first, order):
+        """Device, rows, pairs and the lists' addresses."""
+        dev, pairs = order.get_device(), order.numel()
+        if dev < 0 or dev != torch._C._cuda_getDevice() or pairs % self.top_k:
+            raise ValueError(f"order: a multiple of {self.top_k} pairs on the current CUDA device is wanted, got {pairs} on "
+                             f"{order.device}")
+        return (dev, pairs // self.top_k, pairs, _here("first", first, _I32, self._first, dev),
+                _here("order", order, _I32, (pairs,), dev))
 
     def up(self, x: torch.Tensor, w: torch.Tensor, first: torch.Tensor, order: torch.Tensor, h: torch.Tensor,
            x_scales: Optional[torch.Tensor] = None, w_scales: Optional[torch.Tensor] = None,
            h_scales: Optional[torch.Tensor] = None, stream=None) -> None:
         """Gate and up products with SwiGLU: x [rows, hidden], w [experts, 2 ffn, hidden] (rows interleaved), first and
         order of route(); h [rows * top_k, ffn] in the sorted order."""
-        dev = _device()
-        pairs, f, o = self._lists(first, order, dev)
-        rows = pairs // self.top_k
-        a, sa = self._two("x", x, x_scales, (rows, self.hidden), dev)
-        b, sb = self._two("w", w, w_scales, (self.experts, 2 * self.ffn, self.hidden), dev)
-        c, sc = self._two("h", h, h_scales, (pairs, self.ffn), dev)
-        rc = lib().mk_experts_up(self.h, rows, a, sa, b, sb, f, o, c, sc, _on(stream, dev))
+        dev, rows, pairs, f, o = self._lists(first, order)
+        h8, f8, kind, sa, sb, sc = self.hidden // 32, self.ffn // 32, _BF16, None, None, None
+        if self.e4m3:
+            kind, sa, sc = _E4M3, _scales(x_scales, (rows, h8), dev), _scales(h_scales, (pairs, f8), dev)
+            sb = _scales(w_scales, (self.experts, 2 * self.ffn, h8), dev)
+        elif x_scales is not None or w_scales is not None or h_scales is not None:
+            raise ValueError("scales are of 8-bit rows")
+        rc = lib().mk_experts_up(self.h, rows, _here("x", x, kind, (rows, self.hidden), dev), sa,
+                                 _here("w", w, kind, self._up, dev), sb, f, o,
+                                 _here("h", h, kind, (pairs, self.ffn), dev), sc, _on(stream, dev))
         if rc != MK_OK:
             raise MkError("mk_experts_up", rc)
 
@@ -849,15 +847,18 @@ class Experts:
              w_scales: Optional[torch.Tensor] = None, stream=None) -> None:
         """Down products times the gates: h [rows * top_k, ffn] of up(), w [experts, ffn, hidden] (8 bits: [experts,
         hidden, ffn]), gates float32 [rows, top_k] or None; y bf16 [rows, top_k, hidden] (or [rows * top_k, hidden])."""
-        dev = _device()
-        pairs, f, o = self._lists(first, order, dev)
-        rows = pairs // self.top_k
-        a, sa = self._two("h", h, h_scales, (pairs, self.ffn), dev)
-        b, sb = self._two("w", w, w_scales,
-                          (self.experts, self.hidden, self.ffn) if self.e4m3 else (self.experts, self.ffn, self.hidden), dev)
+        dev, rows, pairs, f, o = self._lists(first, order)
+        f8, kind, sa, sb = self.ffn // 32, _BF16, None, None
+        if self.e4m3:
+            kind, sa = _E4M3, _scales(h_scales, (pairs, f8), dev)
+            sb = _scales(w_scales, (self.experts, self.hidden, f8), dev)
+        elif h_scales is not None or w_scales is not None:
+            raise ValueError("scales are of 8-bit rows")
         g = None if gates is None else _here("gates", gates, _F32, (rows, self.top_k), dev)
-        c = _here("y", y, _BF16, (rows, self.top_k, self.hidden) if y.dim() == 3 else (pairs, self.hidden), dev)
-        rc = lib().mk_experts_down(self.h, rows, a, sa, b, sb, f, o, g, c, _on(stream, dev))
+        rc = lib().mk_experts_down(self.h, rows, _here("h", h, kind, (pairs, self.ffn), dev), sa,
+                                   _here("w", w, kind, self._down, dev), sb, f, o, g,
+                                   _here("y", y, _BF16, (rows, self.top_k, self.hidden) if y.dim() == 3 else (pairs, self.hidden),
+                                         dev), _on(stream, dev))
         if rc != MK_OK:
             raise MkError("mk_experts_down", rc)
 
