@@ -558,15 +558,15 @@ def test_nothing_to_do(mk):
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("name,rows", [("odd", 77), ("odd", 600), ("tail", 300)])
 def test_products_between_alignments(mk, name, rows, kind):
-    # rows and weights 16 bytes past a larger alignment, scales at any byte
+    # rows and weights 16 bytes past a larger alignment, scales at any byte, and no scale behind the last one
     c = Case(kind, DIMS[name], routed(DIMS[name], rows), 41)
     m = c.experts_of(mk)
 
     def shifted(t, by):
         if t is None:
             return None
-        whole = torch.empty(t.numel() + by, dtype=t.dtype, device="cuda")
-        part = whole[by:].view(t.shape)
+        whole = torch.full((t.numel() + by + 8,), 255 if t.dtype is U8 else 0, device="cuda").to(t.dtype)
+        part = whole[by:-8].view(t.shape)
         part.copy_(t.cuda())
         return part
 
