@@ -282,6 +282,16 @@ def test_products_full_size(mk, kind, rows):
     check_down(mk, c)
 
 
+@pytest.mark.parametrize("kind,D", [("bf16", (8, 1, 1, 8)), ("bf16", (16, 2, 2, 8)), ("bf16", (8, 256, 8, 16)), ("e4m3", (32, 1, 1, 32)),
+                                    ("bf16", (32768, 2, 1, 32)), ("e4m3", (32768, 2, 1, 32)), ("bf16", (32, 2, 1, 32768)),
+                                    ("e4m3", (32, 2, 1, 32768))])
+@pytest.mark.parametrize("rows", [1, 9, 300])
+def test_products_of_the_smallest_and_widest(mk, kind, D, rows):
+    c = Case(kind, D, routed(D, rows), rows + 40)
+    check_up(mk, c)
+    check_down(mk, c)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_products_of_many_tiles(mk, kind):
     # more than 64 tiles a block: the list of tiles is planned piece by piece, the rings turn over many times
