@@ -707,6 +707,13 @@ int mk_experts_down(mk_experts* m, int rows, const void* h, const uint8_t* h_sca
  * are then void). */
 int mk_experts_sync(mk_experts* m, mk_stream stream);
 
+/* Test hook, for the calls that follow: timeout_us, the limit of every device
+ * wait (0: 2,000,000, which is the largest), and drop, what stays away so that
+ * waits run out and the products give up with MK_ERR_DEP_TIMEOUT: 1 each
+ * block's list of tiles, 2 the copies behind a block's third step, 3 the
+ * accumulators' release (from a block's third tile on); 0 in production. */
+int mk_experts_set_debug(mk_experts* m, int timeout_us, int drop);
+
 /* Waits for the device's work.  Graphs that captured its calls are not to be
  * replayed any more. */
 void mk_experts_destroy(mk_experts* m);

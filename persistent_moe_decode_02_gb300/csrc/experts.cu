@@ -34,6 +34,8 @@ struct mk_experts {
   bool e4m3;
   int device;
   int* status;                   // first recorded error
+  unsigned long long limit;      // of every device wait, ns
+  int drop;
 };
 
 namespace mk {
@@ -200,6 +202,7 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
     }
     mbar_init(&ctl->drain, 1);
     ctl->fail = 0;
+    ctl->limit = a.limit;
     fence_barrier_init();
   }
   if (warp == 2) tmem_alloc<C::T_COLS>(&ctl->tmem);
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
         const uint32_t bytes = (boxes * C::BOX + tile.width) * 128;
         for (int kb = 0; kb < kbs; ++kb) {
           uint64_t *full = &ctl->full[s], *empty = &ctl->empty[s];
-          if (!(ok = wait_one(empty, ph ^ 1, ctl, status))) break;
+          if (!(ok = wait_one(empty, ph ^ 1, ctl, status) && !(a.drop == DROP_COPIES && sent == 3))) break;
           uint8_t *dst = smem + s * C::STAGE, *w = dst + C::A_BYTES;
           mbar_arrive_tx(full, bytes);
           if constexpr (C::MN) {
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
     __syncwarp();
     set_width<NT, C::G>(a, ctl);
     __syncwarp();
-    plan_tiles<AM, C::G>(a, ctl);
+    if (a.drop != DROP_LIST) plan_tiles<AM, C::G>(a, ctl);
   } else if (warp >= 4 && warp < 8) {            // ---- results: one thread a row
     const int row = (warp - 4) * 32 + lane;
     constexpr int EL = E4M3 && UP ? 1 : 2, LANES = C::RB > 64 ? 8 : 4;   // bytes of a result; lanes that write a row's piece
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
         if (last) {                              // all of it read: the accumulator may be summed into again
           tc_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->acc_empty[i & 1]);
+          if (lane == 0 && a.drop != DROP_ACC) mbar_arrive(&ctl->acc_empty[i & 1]);
         }
         if (!UP && rows > 0) {
           put_down<C::STEP>(r, mine, gate);
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
         fill = 0;
       }
     }
-    if constexpr (!UP) {                         // pairs without an expert
+    if (!UP && list.known) {                     // pairs without an expert
       for (int x = ctl->row0[a.experts] + blockIdx.x; x < a.pairs; x += gridDim.x) {
         const int p = a.order[x];
         if (p >= 0 && p < a.pairs)
@@ -566,7 +569,7 @@ int mk_experts_create(const mk_model_dims* dims, int rows_type, mk_experts** out
     return fail(MK_ERR_UNSUPPORTED, "mk_experts_create: at most 256 experts, 8 of them a row, hidden and expert_ffn at most 32768");
   mk_experts* m = new (std::nothrow) mk_experts();
   if (!m) return fail(MK_ERR_CAPACITY, "out of host memory");
-  m->hidden = h; m->ffn = f; m->experts = dims->n_experts; m->k = dims->top_k; m->e4m3 = e4m3;
+  m->hidden = h; m->ffn = f; m->experts = dims->n_experts; m->k = dims->top_k; m->e4m3 = e4m3; m->limit = WAIT_NS;
   cudaError_t e = cudaGetDevice(&m->device);
   if (e == cudaSuccess) e = cudaMalloc((void**)&m->status, sizeof(int));
   if (e == cudaSuccess) {
@@ -579,6 +582,16 @@ int mk_experts_create(const mk_model_dims* dims, int rows_type, mk_experts** out
     return fail_cuda("mk_experts_create", e);
   }
   *out = m;
+  return MK_OK;
+}
+
+int mk_experts_set_debug(mk_experts* m, int timeout_us, int drop) {
+  using namespace mk;
+  if (!m) return fail(MK_ERR_INVALID, "mk_experts_set_debug: experts is NULL");
+  if (timeout_us < 0 || timeout_us > 2000000 || drop < 0 || drop > DROP_ACC)
+    return fail(MK_ERR_INVALID, "mk_experts_set_debug: timeout_us (at most 2000000) or drop");
+  m->limit = timeout_us ? timeout_us * 1000ull : WAIT_NS;
+  m->drop = drop;
   return MK_OK;
 }
 
@@ -607,6 +620,8 @@ int mk_experts_up(mk_experts* m, int rows, const void* x, const uint8_t* x_scale
   if (rc != MK_OK) return rc;
   Args a = {first, order, nullptr, (const uint8_t*)x, x_scales, w_scales, (uint8_t*)h, h_scales, m->status, (int)p, rows, m->k, m->experts,
             m->hidden, 2 * m->ffn};
+  a.limit = m->limit;
+  a.drop = m->drop;
   const cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t err = s8 ? launch<true, true>(a, x, w, st) : launch<false, true>(a, x, w, st);
   return err == cudaSuccess ? MK_OK : fail_cuda("mk_experts_up", err);
@@ -637,6 +652,8 @@ int mk_experts_down(mk_experts* m, int rows, const void* h, const uint8_t* h_sca
   if (rc != MK_OK) return rc;
   Args a = {first, order, gates, nullptr, h_scales, w_scales, (uint8_t*)y, nullptr, m->status, (int)p, rows, m->k, m->experts,
             m->ffn, m->hidden};
+  a.limit = m->limit;
+  a.drop = m->drop;
   const cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t err = s8 ? launch<true, false>(a, h, w, st) : launch<false, false>(a, h, w, st);
   return err == cudaSuccess ? MK_OK : fail_cuda("mk_experts_down", err);

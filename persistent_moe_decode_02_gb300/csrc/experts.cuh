@@ -24,7 +24,10 @@ struct ExpertArgs {
   int extra;                     // what a tile costs beside its columns, in columns
   int box;                       // columns of the large boxes
   int a_wide, b_wide;            // bytes that a row's scales may be read by
+  int drop;                      // what stays away (mk_experts_set_debug)
+  unsigned long long limit;      // of every wait, ns
 };
+enum { DROP_LIST = 1, DROP_COPIES = 2, DROP_ACC = 3 };
 
 // Tiles of two SMs (experts_two.cu).
 cudaError_t launch_two(bool up, const ExpertArgs& a, const void* rows, const void* w, int sms, cudaStream_t st);
@@ -35,10 +38,11 @@ using namespace ptx;
 
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int MAX_EXPERTS = 256, MAX_STAGES = 12, SMEM_MOST = 232448;
-constexpr unsigned long long WAIT_NS = 2000000000ull;   // limit of every wait
+constexpr unsigned long long WAIT_NS = 2000000000ull;   // limit of every wait, if none is set; and of what is in flight at the end
 
 struct Ctl {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], list_full[2], list_free[2], drain;
+  unsigned long long limit;
   uint32_t tmem;
   int fail;
   int4 list[2][32];              // the block's next tiles, as they are planned
@@ -55,7 +59,7 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Ctl* ctl,
   const unsigned long long t0 = now_ns();
   while (!mbar_try(bar, parity)) {
     if (*(volatile int*)&ctl->fail) return false;
-    if (now_ns() - t0 > WAIT_NS) {
+    if (now_ns() - t0 > ctl->limit) {
       *(volatile int*)&ctl->fail = 1;
       atomicCAS(status, 0, MK_ERR_DEP_TIMEOUT);
       return false;
@@ -133,11 +137,13 @@ struct Tile {
 // lanes); one arrival frees 32 of them.
 struct Reader {
   int i = 0;
+  bool known = false;            // a part of the list has come, so the tables behind it are there
   template <bool WARP>
   __device__ __forceinline__ bool next(Ctl* ctl, int* status, Tile& t) {
     const int c = i / 32;
     uint64_t* full = &ctl->list_full[c & 1];
     if (i % 32 == 0 && !(WARP ? wait(full, c >> 1 & 1, ctl, status) : wait_one(full, c >> 1 & 1, ctl, status))) return false;
+    known = true;
     const int4 v = ctl->list[c & 1][i % 32];
     if (v.x >> 16 == 0) return false;
     if (++i % 32 == 0) {

@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(Two<UP>::THREADS, 1)
     }
     mbar_init(&ctl->drain, 1);
     ctl->fail = 0;
+    ctl->limit = a.limit;
     fence_barrier_init();
   }
   if (warp == 2) tmem2_alloc<C::T_COLS>(&ctl->tmem);
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(Two<UP>::THREADS, 1)
         const uint32_t bytes = C::A_BYTES + boxes * 2048;
         for (int kb = 0; kb < kbs; ++kb) {
           uint64_t *full = &ctl->full[s], *empty = &ctl->empty[s];
-          if (!(ok = wait_one(empty, ph ^ 1, ctl, status))) break;
+          if (!(ok = wait_one(empty, ph ^ 1, ctl, status) && !(a.drop == DROP_COPIES && rank == 1 && sent == 3))) break;
           uint8_t* dst = smem + s * C::STAGE;
           mbar_arrive_tx(full, bytes);
           if constexpr (!UP) {
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(Two<UP>::THREADS, 1)
   } else if (warp == 3) {                        // ---- the list of tiles
     set_tables<C::W>(a, ctl);
     __syncwarp();
-    plan_two<C::W>(a, ctl);
+    if (a.drop != DROP_LIST) plan_two<C::W>(a, ctl);
   } else if (warp >= 4 && warp < C::W_LOAD) {    // ---- results: a weight row a lane, a token a column
     const int group = (warp - 4) / 4, q = warp % 4, et = tid % 128;
     constexpr int TURN = C::GROUPS * C::TOKENS;
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(Two<UP>::THREADS, 1)
       auto release = [&] {                       // all of it read: the accumulator may be summed into again
         tc_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(&ctl->acc_empty[i & 1], 0);
+        if (lane == 0 && a.drop != DROP_ACC) mbar_arrive_at(&ctl->acc_empty[i & 1], 0);
       };
       if (group * C::TOKENS >= wide) release();
       else if (!UP) tmem_ld32(acc + group * C::TOKENS, r);
@@ -305,7 +306,7 @@ __global__ void __launch_bounds__(Two<UP>::THREADS, 1)
         group_sync(group);
       }
     }
-    if constexpr (!UP) {                         // pairs without an expert (their rows are known once the list is)
+    if (!UP && list.known) {                     // pairs without an expert
       for (int x = ctl->row0[a.experts] + blockIdx.x; x < a.pairs; x += gridDim.x) {
         const int p = a.order[x];
         if (p >= 0 && p < a.pairs)

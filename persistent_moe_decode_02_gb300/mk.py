@@ -30,7 +30,7 @@ EXPORTS = [
     "mk_sched_peek_rows", "mk_chunk_create", "mk_chunk_update", "mk_chunk_append", "mk_chunk_attend", "mk_chunk_read",
     "mk_chunk_sync", "mk_chunk_info", "mk_chunk_destroy", "mk_chunk_inspect", "mk_probs", "mk_verify", "mk_norm",
     "mk_quantize", "mk_route", "mk_experts_create", "mk_experts_up", "mk_experts_down", "mk_experts_sync",
-    "mk_experts_destroy",
+    "mk_experts_set_debug", "mk_experts_destroy",
 ]
 MK_KV_BF16, MK_KV_E4M3 = 0, 1
 MK_ROWS_BF16, MK_ROWS_F32, MK_ROWS_E4M3 = 0, 1, 2
@@ -137,6 +137,7 @@ def lib():
         L.mk_experts_up.argtypes = [vp, i32] + [vp] * 9
         L.mk_experts_down.argtypes = [vp, i32] + [vp] * 9
         L.mk_experts_sync.argtypes = [vp, vp]
+        L.mk_experts_set_debug.argtypes = [vp, i32, i32]
         L.mk_experts_destroy.argtypes = [vp]
         L.mk_experts_destroy.restype = None
         for f in ("mk_plan_create", "mk_decode_step", "mk_decode_steps", "mk_decode_step_host", "mk_plan_update", "mk_plan_sync",
@@ -146,7 +147,7 @@ def lib():
                   "mk_sched_set_prefill", "mk_plan_update_rows", "mk_sched_peek_rows", "mk_chunk_create",
                   "mk_chunk_update", "mk_chunk_append", "mk_chunk_attend", "mk_chunk_read", "mk_chunk_sync",
                   "mk_chunk_info", "mk_chunk_inspect", "mk_probs", "mk_verify", "mk_norm", "mk_quantize", "mk_route",
-                  "mk_experts_create", "mk_experts_up", "mk_experts_down", "mk_experts_sync"):
+                  "mk_experts_create", "mk_experts_up", "mk_experts_down", "mk_experts_sync", "mk_experts_set_debug"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -800,9 +801,10 @@ class Experts:
 
     D: dims with hidden, n_experts, top_k and expert_ffn.  rows_type: "bf16", or
     "e4m3" (rows, weights and up's results as float8_e4m3fn codes with uint8
-    scales of a 32nd of their last dimension)."""
+    scales of a 32nd of their last dimension).  timeout_us, debug_drop: limits
+    and losses for tests (mk_experts_set_debug)."""
 
-    def __init__(self, D, rows_type: str):
+    def __init__(self, D, rows_type: str, timeout_us: int = 0, debug_drop: int = 0):
         kinds = {"bf16": MK_ROWS_BF16, "e4m3": MK_ROWS_E4M3}
         if rows_type not in kinds:
             raise ValueError(f"rows_type: {rows_type!r}, wanted one of {tuple(kinds)}")
@@ -812,6 +814,10 @@ class Experts:
         if rc != MK_OK:
             raise MkError("mk_experts_create", rc)
         self.h, self.e4m3 = h, rows_type == "e4m3"
+        if timeout_us or debug_drop:
+            rc = lib().mk_experts_set_debug(h, timeout_us, debug_drop)
+            if rc != MK_OK:
+                raise MkError("mk_experts_set_debug", rc)
         self.hidden, self.experts, self.top_k, self.ffn = e = D.hidden, D.n_experts, D.top_k, D.expert_ffn
         self._first, self._up, self._down = (e[1] + 1,), (e[1], 2 * e[3], e[0]), (e[1], e[0], e[3]) if self.e4m3 else (e[1], e[3], e[0])
 
