@@ -244,11 +244,11 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
           if (++s == C::NST) { s = 0; ph ^= 1; }
         }
       }
-      if (!ok)                                   // given up: what is in flight still lands before the block ends
-        for (int u = max(0, sent - C::NST); u < sent; ++u) {
-          const unsigned long long since = now_ns();
+      if (!ok) {                                 // given up: what is in flight still lands before the block ends
+        const unsigned long long since = now_ns();
+        for (int u = max(0, sent - C::NST); u < sent; ++u)
           while (!mbar_try(&ctl->full[u % C::NST], u / C::NST & 1) && now_ns() - since < WAIT_NS) {}
-        }
+      }
     }
     __syncwarp();
   } else if (warp == 1) {                        // ---- matrix instructions, by one thread

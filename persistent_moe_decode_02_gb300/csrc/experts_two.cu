@@ -143,11 +143,11 @@ __global__ void __launch_bounds__(Two<UP>::THREADS, 1)
           if (++s == C::NST) { s = 0; ph ^= 1; }
         }
       }
+      const unsigned long long since = now_ns();
       for (int u = max(0, sent - C::NST); u < sent; ++u) {
         if (ok) {                                // the leader's last arrivals here, before the block ends
           wait_one(&ctl->empty[u % C::NST], u / C::NST & 1, ctl, status);
         } else {                                 // given up: what is in flight still lands
-          const unsigned long long since = now_ns();
           while (!mbar_try(&ctl->full[u % C::NST], u / C::NST & 1) && now_ns() - since < WAIT_NS) {}
         }
       }

@@ -125,3 +125,16 @@ def test_two_sms_give_up(mk, op, D, drop):
 def test_a_short_limit_that_nothing_runs_into(mk):
     # the limit is of a wait, not of a call
     Run(mk, "bf16", (2048, 8, 2, 768), T.routed((2048, 8, 2, 768), 500), timeout_us=LIMIT_US).check()
+
+
+@pytest.mark.gpu
+def test_giving_up_takes_one_limit(mk):
+    # the even block's stages never fill up (the odd one's copies stop): what is in flight is waited for once (2 s), not
+    # for each of five or six stages
+    import time
+    r = Run(mk, "bf16", (256, 4, 2, 2048), torch.randint(0, 4, (2600, 2), generator=torch.Generator().manual_seed(3)).int(),
+            timeout_us=LIMIT_US, debug_drop=2)
+    torch.cuda.synchronize()
+    t0 = time.monotonic()
+    assert r.up() == mk.MK_ERR_DEP_TIMEOUT
+    assert time.monotonic() - t0 < 3.9
