@@ -702,9 +702,10 @@ int mk_experts_up(mk_experts* m, int rows, const void* x, const uint8_t* x_scale
 int mk_experts_down(mk_experts* m, int rows, const void* h, const uint8_t* h_scales, const void* w, const uint8_t* w_scales,
                     const int* first, const int* order, const float* gates, void* y, mk_stream stream);
 
-/* Wait for `stream`, then return the device status and clear it: MK_OK, or
- * MK_ERR_DEP_TIMEOUT when a bounded wait inside a product ran out (its results
- * are then void). */
+/* Wait for `stream`, then return MK_OK, or MK_ERR_DEP_TIMEOUT when a bounded wait
+ * inside a product has run out (its results are then void) since this stream
+ * last asked.  The object does not know which stream's product it was: every
+ * stream that asks hears of it. */
 int mk_experts_sync(mk_experts* m, mk_stream stream);
 
 /* Test hook, for the calls that follow: timeout_us, the limit of every device

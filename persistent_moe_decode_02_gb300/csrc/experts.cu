@@ -25,7 +25,10 @@
 // The scales pass through shared memory to tensor memory; up's epilogue has a
 // thread for each row, so its groups of 32 results and their scale stay within a
 // thread.
+#include <mutex>
 #include <new>
+#include <utility>
+#include <vector>
 
 #include "experts.cuh"
 
@@ -33,9 +36,13 @@ struct mk_experts {
   int hidden, experts, k, ffn;
   bool e4m3;
   int device;
-  int* status;                   // first recorded error
+  int* status;                   // waits that ran out, counted
   unsigned long long limit;      // of every device wait, ns
   int drop;
+  // What each stream's mk_experts_sync has reported (none: 0).  The count itself is
+  // never cleared: another stream has yet to hear of it.
+  std::mutex lock;
+  std::vector<std::pair<cudaStream_t, int>> told;
 };
 
 namespace mk {
@@ -664,12 +671,25 @@ int mk_experts_sync(mk_experts* m, mk_stream stream) {
   if (!m) return fail(MK_ERR_INVALID, "mk_experts_sync: experts is NULL");
   const int rc = check_device(m);
   if (rc != MK_OK) return rc;
-  int st = 0;
-  cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(&st, m->status, sizeof(int), cudaMemcpyDeviceToHost, (cudaStream_t)stream);
-  if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
-  if (e == cudaSuccess && st) e = cudaMemsetAsync(m->status, 0, sizeof(int), (cudaStream_t)stream);
-  return e == cudaSuccess ? st : fail_cuda("mk_experts_sync", e);
+  const cudaStream_t st = (cudaStream_t)stream;
+  int n = 0;
+  cudaError_t e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(&n, m->status, sizeof(int), cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return fail_cuda("mk_experts_sync", e);
+  if (n == 0) return MK_OK;
+  try {
+    std::lock_guard<std::mutex> hold(m->lock);
+    for (auto& t : m->told)
+      if (t.first == st) {
+        const bool heard = t.second == n;
+        t.second = n;
+        return heard ? MK_OK : MK_ERR_DEP_TIMEOUT;
+      }
+    m->told.emplace_back(st, n);
+  } catch (...) {
+  }                              // (no memory for it: this stream hears of it again)
+  return MK_ERR_DEP_TIMEOUT;
 }
 
 void mk_experts_destroy(mk_experts* m) {

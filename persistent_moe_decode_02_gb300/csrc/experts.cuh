@@ -61,7 +61,7 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, Ctl* ctl,
     if (*(volatile int*)&ctl->fail) return false;
     if (now_ns() - t0 > ctl->limit) {
       *(volatile int*)&ctl->fail = 1;
-      atomicCAS(status, 0, MK_ERR_DEP_TIMEOUT);
+      atomicAdd(status, 1);
       return false;
     }
   }

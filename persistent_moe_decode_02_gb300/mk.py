@@ -869,7 +869,7 @@ class Experts:
             raise MkError("mk_experts_down", rc)
 
     def sync(self, stream=None) -> int:
-        """Wait for the stream; the device status, which it clears."""
+        """Wait for the stream; MK_OK, or MK_ERR_DEP_TIMEOUT if a wait of the products ran out since this stream last asked."""
         return lib().mk_experts_sync(self.h, _stream(stream))
 
     def close(self):

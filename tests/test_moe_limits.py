@@ -138,3 +138,32 @@ def test_giving_up_takes_one_limit(mk):
     t0 = time.monotonic()
     assert r.up() == mk.MK_ERR_DEP_TIMEOUT
     assert time.monotonic() - t0 < 3.9
+
+
+@pytest.mark.gpu
+def test_every_stream_hears_of_it_once(mk):
+    # a wait that runs out on one stream is not lost to it because another one asked first, and is told once
+    D, rows = (64, 4, 2, 64), 20
+    r = Run(mk, "bf16", D, T.routed(D, rows))
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    assert r.m.sync(a) == r.m.sync(b) == r.m.sync() == mk.MK_OK
+    limits = mk.lib().mk_experts_set_debug
+
+    def product(stream):
+        r.m.up(r.x, r.w, r.first, r.order, r.h, stream=stream)
+
+    torch.cuda.synchronize()
+    assert limits(r.m.h, LIMIT_US, 1) == mk.MK_OK
+    product(b)
+    assert limits(r.m.h, 0, 0) == mk.MK_OK
+    torch.cuda.synchronize()
+    assert r.m.sync(a) == mk.MK_ERR_DEP_TIMEOUT and r.m.sync(a) == mk.MK_OK
+    assert r.m.sync(b) == mk.MK_ERR_DEP_TIMEOUT and r.m.sync(b) == mk.MK_OK
+    assert r.m.sync() == mk.MK_ERR_DEP_TIMEOUT and r.m.sync() == mk.MK_OK
+    product(a)                                      # a good one
+    assert r.m.sync(a) == r.m.sync(b) == mk.MK_OK
+    assert limits(r.m.h, LIMIT_US, 1) == mk.MK_OK
+    product(a)                                      # and again a bad one
+    torch.cuda.synchronize()
+    assert r.m.sync(b) == mk.MK_ERR_DEP_TIMEOUT and r.m.sync(a) == mk.MK_ERR_DEP_TIMEOUT
+    assert r.m.sync(a) == r.m.sync(b) == mk.MK_OK
