@@ -225,15 +225,17 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
 
   if (warp == 0) {                               // ---- boxes: weights, rows that lie side by side; by one thread
     if (elect_one()) {
+      const int stop = a.drop == DROP_COPIES ? 3 : 0x7fffffff;
       int s = 0, sent = 0;
       uint32_t ph = 0;
       bool ok = true;
       while (ok && list.next<false>(ctl, status, tile)) {
         const int boxes = UP ? 0 : (tile.rows + C::BOX - 1) / C::BOX;
         const uint32_t bytes = (boxes * C::BOX + tile.width) * 128;
-        for (int kb = 0; kb < kbs; ++kb) {
+        const int steps = min(kbs, stop - sent);
+        for (int kb = 0; kb < steps; ++kb) {
           uint64_t *full = &ctl->full[s], *empty = &ctl->empty[s];
-          if (!(ok = wait_one(empty, ph ^ 1, ctl, status) && !(a.drop == DROP_COPIES && sent == 3))) break;
+          if (!(ok = wait_one(empty, ph ^ 1, ctl, status))) break;
           uint8_t *dst = smem + s * C::STAGE, *w = dst + C::A_BYTES;
           mbar_arrive_tx(full, bytes);
           if constexpr (C::MN) {
@@ -250,6 +252,7 @@ __global__ void __launch_bounds__(Cfg<E4M3, UP, AM, NT>::THREADS, 1)
           ++sent;
           if (++s == C::NST) { s = 0; ph ^= 1; }
         }
+        ok = ok && steps == kbs;
       }
       if (!ok) {                                 // given up: what is in flight still lands before the block ends
         const unsigned long long since = now_ns();

@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(Two<UP>::THREADS, 1)
 
   if (warp == 0) {                               // ---- boxes: weights, rows that lie side by side; by one thread
     if (elect_one()) {
+      const int stop = a.drop == DROP_COPIES && rank == 1 ? 3 : 0x7fffffff;
       int s = 0, sent = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -127,9 +128,10 @@ __global__ void __launch_bounds__(Two<UP>::THREADS, 1)
         const int half = tile.width / 2, mine = UP ? 0 : min(half, max(0, tile.rows - rank * half)), boxes = (mine + 15) / 16;
         const int n0 = tile.n0 + rank * 128, r0 = tile.row0 + rank * half;
         const uint32_t bytes = C::A_BYTES + boxes * 2048;
-        for (int kb = 0; kb < kbs; ++kb) {
+        const int steps = min(kbs, stop - sent);
+        for (int kb = 0; kb < steps; ++kb) {
           uint64_t *full = &ctl->full[s], *empty = &ctl->empty[s];
-          if (!(ok = wait_one(empty, ph ^ 1, ctl, status) && !(a.drop == DROP_COPIES && rank == 1 && sent == 3))) break;
+          if (!(ok = wait_one(empty, ph ^ 1, ctl, status))) break;
           uint8_t* dst = smem + s * C::STAGE;
           mbar_arrive_tx(full, bytes);
           if constexpr (!UP) {
@@ -142,6 +144,7 @@ __global__ void __launch_bounds__(Two<UP>::THREADS, 1)
           ++sent;
           if (++s == C::NST) { s = 0; ph ^= 1; }
         }
+        ok = ok && steps == kbs;
       }
       const unsigned long long since = now_ns();
       for (int u = max(0, sent - C::NST); u < sent; ++u) {
