@@ -684,7 +684,9 @@ int mk_experts_create(const mk_model_dims* dims, int rows_type, mk_experts** out
  *   first, order  of mk_route
  *   h     device [rows * top_k, expert_ffn] of rows_type (8 bits: h_scales);
  *         rows from first[n_experts] on are left as they were
- * Buffers 16-byte aligned (scales: any).  first and order may hold
+ * Buffers 16-byte aligned (scales: any; the products read them by aligned words
+ * of 4 bytes or more that hold a byte of theirs, so up to 3 bytes before
+ * and behind them too, which change nothing).  first and order may hold
  * anything: an entry out of range is read as none. */
 int mk_experts_up(mk_experts* m, int rows, const void* x, const uint8_t* x_scales, const void* w, const uint8_t* w_scales,
                   const int* first, const int* order, void* h, uint8_t* h_scales, mk_stream stream);
