@@ -56,6 +56,13 @@ def check_eights(codes, scales, ref, slack):
     assert not bad.any(), (int(bad.sum()), float(err.max()), bad.nonzero()[:5].tolist())
 
 
+def check_eights_strictly(codes, scales, ref, slack):
+    """check_eights for finite results: a NaN is none (a comparison with one is false, so it passes there)."""
+    v = values(codes, scales)
+    assert torch.isfinite(ref).all() and torch.isfinite(v).all(), (~torch.isfinite(v)).nonzero()[:5].tolist()
+    check_eights(codes, scales, ref, slack)
+
+
 def norm(x, add, gamma, eps):
     """(t, out, slack of t, slack of out) in 64 bits.  Each of the j sums in fp32 is off by half a step of what has
     been summed.  The square sum's error is that of t and of its own sums: a thread adds 64 squares one after another,

@@ -115,3 +115,25 @@ def test_the_quantised_form():
     assert (top <= 448 * unit).all() and (top > 448 * unit / 2).all()
     err = (mu.values(codes, scales) - x.double()).abs()
     assert (err <= mu.E4M3_STEP * x.double().abs() + mu.E4M3_MIN * unit.repeat_interleave(32, -1)).all()
+
+
+def test_the_check_of_8_bit_results():
+    # one code that is off, or none, is seen, wherever it lies in its group
+    ref = mu.normal((3, 64), 5).double()
+    codes, scales = mu.quantise(ref.float())
+    slack = torch.zeros_like(ref)
+    mu.check_eights_strictly(codes, scales, ref.float().double(), slack)
+    for at in ((0, 0), (1, 31), (2, 63)):
+        bad = codes.clone().view(torch.uint8)
+        bad[at] = 0x7f                                                     # NaN
+        with pytest.raises(AssertionError):
+            mu.check_eights_strictly(bad.view(torch.float8_e4m3fn), scales, ref, slack)
+        bad = codes.clone().view(torch.uint8)
+        bad[at] ^= 0x80                                                    # the other sign
+        with pytest.raises(AssertionError):
+            mu.check_eights_strictly(bad.view(torch.float8_e4m3fn), scales, ref, slack)
+        for s in (1, 255):                                                 # the next scale; a scale that is none
+            wrong = scales.clone()
+            wrong[at[0], at[1] // 32] = 255 if s == 255 else wrong[at[0], at[1] // 32] + 1
+            with pytest.raises(AssertionError):
+                mu.check_eights_strictly(codes, wrong, ref, slack)

@@ -1,5 +1,5 @@
 """More of the mixture-of-experts operators on a GPU against 64-bit CPU forms:
-gates where SiLU saturates."""
+gates where SiLU saturates, 8-bit results without a NaN."""
 import math
 
 import pytest
@@ -63,7 +63,7 @@ def test_gates_of_any_size(mk, kind, rows):
         bad = ~(err <= mu.BF16 * ref.abs() + 1.01 * slack + 2.0 ** -134)
         assert not bad.any(), (int(bad.sum()), bad.nonzero()[:5].tolist(), g[bad[0]][:5].tolist())
     else:
-        mu.check_eights(h.cpu(), s.cpu(), ref, slack)
+        mu.check_eights_strictly(h.cpu(), s.cpu(), ref, slack)
 
 
 @pytest.mark.parametrize("rows", [2600])
@@ -80,3 +80,66 @@ def test_gates_of_any_size_in_two_sms(mk, rows):
     err = (h[0].cpu().double() - ref).abs()
     bad = ~(err <= mu.BF16 * ref.abs() + 1.01 * slack + 2.0 ** -134)
     assert not bad.any(), (int(bad.sum()), g[bad][:5].tolist())
+
+
+# ---- 8-bit results hold no NaN ----
+
+@pytest.fixture
+def strict(monkeypatch):
+    """The tests of 8-bit results with the check that a NaN does not pass."""
+    monkeypatch.setattr(mu, "check_eights", _strictly(mu.check_eights))
+
+
+def _strictly(check):
+    def both(codes, scales, ref, slack):
+        v = mu.values(codes, scales)
+        assert torch.isfinite(v).all(), (~torch.isfinite(v)).nonzero()[:5].tolist()
+        check(codes, scales, ref, slack)
+    return both
+
+
+@pytest.mark.parametrize("case", [c for c in T.NORM if c[5] is E4M3], ids=str)
+def test_norm_to_8_bits(mk, strict, case):
+    T.test_norm(mk, *case)
+
+
+@pytest.mark.parametrize("name,rows", T.ROWS)
+def test_up_in_8_bits(mk, strict, name, rows):
+    T.check_up(mk, T.Case("e4m3", T.DIMS[name], T.routed(T.DIMS[name], rows), rows))
+
+
+@pytest.mark.parametrize("rows", [1, 3, 37, 150])
+def test_up_in_8_bits_full_size(mk, strict, rows):
+    D = (2048, 12, 8, 768)
+    T.check_up(mk, T.Case("e4m3", D, T.routed(D, rows), rows))
+
+
+@pytest.mark.parametrize("name,rows", [("odd", 77), ("odd", 600), ("odd", 601), ("tail", 300)])
+def test_up_in_8_bits_between_alignments(mk, strict, name, rows):
+    # a scale that is none (255) lies right behind the last one, and right before the first
+    T.test_products_between_alignments(mk, name, rows, "e4m3")
+
+
+@pytest.mark.parametrize("before,behind", [(1, 2), (3, 1), (2, 3), (0, 1)])
+@pytest.mark.parametrize("hidden", [32, 96, 160, 1056])
+@pytest.mark.parametrize("rows", [1, 5, 130])
+def test_scales_beside_others_that_are_none(mk, strict, before, behind, hidden, rows):
+    # bytes of 255 (a NaN as a scale) on both sides of every buffer of scales, in the words that its ends share
+    c = T.Case("e4m3", (hidden, 3, 1, 96), T.routed((hidden, 3, 1, 96), rows), 61)
+
+    def among(t):
+        whole = torch.full((4 + before + t.numel() + behind + 4,), 255, dtype=U8, device="cuda")
+        part = whole[4 + before:4 + before + t.numel()].view(t.shape)
+        part.copy_(t.cuda())
+        return part
+
+    (x, w, hh, d), (xs, ws, hs, ds) = ([p[i].cuda() if i == 0 else among(p[i]) for p in (c.x, c.gu, c.h, c.dn)] for i in (0, 1))
+    m = c.experts_of(mk)
+    first, order, gates = c.first.cuda(), c.order.cuda(), c.gates.cuda()
+    h, s = torch.empty(c.pairs, c.ffn, dtype=E4M3, device="cuda"), among(torch.zeros(c.pairs, c.ffn // 32, dtype=U8))
+    y = torch.empty(c.rows, 1, c.hidden, dtype=BF16, device="cuda")
+    m.up(x, w, first, order, h, x_scales=xs, w_scales=ws, h_scales=s)
+    m.down(hh, d, first, order, gates, y, h_scales=hs, w_scales=ds)
+    assert m.sync() == mk.MK_OK
+    mu.check_eights(h.cpu(), s.cpu(), *mu.up(c.vx, c.vgu, c.first, c.order, 1))
+    mu.within(y.cpu().flatten(0, 1), *mu.down(c.vh, c.vdn, c.first, c.order, c.gates))
