@@ -143,3 +143,54 @@ def test_scales_beside_others_that_are_none(mk, strict, before, behind, hidden, 
     assert m.sync() == mk.MK_OK
     mu.check_eights(h.cpu(), s.cpu(), *mu.up(c.vx, c.vgu, c.first, c.order, 1))
     mu.within(y.cpu().flatten(0, 1), *mu.down(c.vh, c.vdn, c.first, c.order, c.gates))
+
+
+# ---- lists of tiles ----
+
+def tiles_a_block(D, first, up, sms, group):
+    """The largest number of tiles that a block gets of the products with tiles of 32 rows and up to 192 columns: the
+    rule of set_width (the width with the fewest rounds times columns and 32 beside them, the widest of equal ones)."""
+    hidden, experts, _, ffn = D
+    n = 2 * ffn if up else hidden
+    rows = (first[1:] - first[:-1]).tolist()
+    row_tiles = sum((r + 31) // 32 for r in rows)
+    cost = {w: -(-row_tiles * -(-n // w) // sms) * (w + 32) for w in range(group, 193, group)}
+    width = max(w for w in cost if cost[w] == min(cost.values()))
+    return -(-row_tiles * -(-n // width) // sms)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("up", [True, False])
+def test_lists_of_several_parts(mk, strict, kind, up):
+    # a block's list is planned 32 tiles at a time, in two places in turn: more than 96 tiles use each place twice, so the
+    # planning warp waits for its readers
+    D = (32, 256, 8, 5120) if up else (10240, 256, 8, 32)
+    c = T.Case(kind, D, T.routed(D, 512), 71)
+    assert 32 < c.pairs <= 16 * c.experts           # tiles of 32 rows
+    group = {(True, "bf16"): 16, (True, "e4m3"): 64, (False, "bf16"): 64, (False, "e4m3"): 16}[up, kind]
+    assert tiles_a_block(D, c.first, up, torch.cuda.get_device_properties(0).multi_processor_count, group) > 96
+    (T.check_up if up else T.check_down)(mk, c)
+
+
+@pytest.mark.parametrize("up", [True, False])
+def test_lists_of_several_parts_in_two_sms(mk, up):
+    D = (64, 2, 1, 16384) if up else (32768, 2, 1, 64)
+    rows = 16000
+    c = T.Case("bf16", D, torch.randint(0, 2, (rows, 1), generator=torch.Generator().manual_seed(2)).int(), 72)
+    n, sms = 32768, torch.cuda.get_device_properties(0).multi_processor_count
+    assert sum(-(-int(r) // 256) for r in c.first[1:] - c.first[:-1]) * (n // 256) > 96 * (sms // 2)
+    m = c.experts_of(mk)
+    some = torch.arange(3, rows, 397)               # pairs, in the sorted order
+    one = torch.stack([torch.zeros(()), (some < c.first[1]).sum(), torch.tensor(len(some))]).int()
+    if up:
+        w_h, h = T.cuda_empty((rows, c.ffn), BF16)
+        m.up(c.x[0].cuda(), c.gu[0].cuda(), c.first.cuda(), c.order.cuda(), h)
+        got, (ref, slack) = h[some.cuda()], mu.up(c.vx[c.order[some].long()], c.vgu, one, torch.arange(len(some)), 1)
+    else:
+        w_h, y = T.cuda_empty((rows, 1, c.hidden), BF16)
+        m.down(c.h[0].cuda(), c.dn[0].cuda(), c.first.cuda(), c.order.cuda(), c.gates.cuda(), y)
+        at = c.order[some].long()
+        got = y[at.cuda(), 0]
+        ref, slack = mu.down(c.vh[some], c.vdn, one, torch.arange(len(some)), c.gates[at])
+    assert m.sync() == mk.MK_OK and T.behind(w_h)
+    mu.within(got.cpu(), ref, slack)
