@@ -21,6 +21,7 @@ void set_last_error(const char* msg);
 
 using mk::AppendPage;
 using mk::AttnTask;
+using mk::BesideCaptures;
 using mk::ChunkReq;
 using mk::JoinTask;
 
@@ -285,14 +286,6 @@ struct mk_chunk {
 };
 
 namespace {
-
-// Allocations of this thread while it captures some other stream: without it
-// they would fail, and end that capture.
-struct BesideCaptures {
-  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-  BesideCaptures() { cudaThreadExchangeStreamCaptureMode(&mode); }
-  ~BesideCaptures() { cudaThreadExchangeStreamCaptureMode(&mode); }
-};
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 

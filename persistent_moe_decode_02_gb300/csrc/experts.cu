@@ -697,6 +697,7 @@ int mk_experts_sync(mk_experts* m, mk_stream stream) {
 
 void mk_experts_destroy(mk_experts* m) {
   if (!m) return;
+  mk::BesideCaptures relaxed;
   cudaFree(m->status);
   delete m;
 }

@@ -45,6 +45,14 @@ cudaError_t launch_kernel(void (*k)(A...), dim3 grid, dim3 block, size_t smem, i
   return cudaLaunchKernelEx(&cfg, k, static_cast<A>(args)...);
 }
 
+// Allocations and releases of this thread while it captures some other stream: without it
+// they would fail, and end that capture.
+struct BesideCaptures {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  BesideCaptures() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~BesideCaptures() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 // Kernels' attributes that this thread of the host has asked for already (asking
 // takes as long as a fifth of a launch).  Forgotten after any error, so that a
 // device whose context was made anew is asked again.

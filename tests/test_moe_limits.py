@@ -167,3 +167,19 @@ def test_every_stream_hears_of_it_once(mk):
     torch.cuda.synchronize()
     assert r.m.sync(b) == mk.MK_ERR_DEP_TIMEOUT and r.m.sync(a) == mk.MK_ERR_DEP_TIMEOUT
     assert r.m.sync(a) == r.m.sync(b) == mk.MK_OK
+
+
+@pytest.mark.gpu
+def test_an_object_dies_beside_a_capture(mk):
+    # the garbage collector may take an object at any time, while the thread captures a graph too
+    r = Run(mk, "bf16", (64, 4, 2, 64), T.routed((64, 4, 2, 64), 20))
+    other = mk.Experts(mu.dims(64, 4, 2, 32), "e4m3")
+    r.up()
+    want = r.h.clone()
+    r.h.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        other.close()
+        r.m.up(r.x, r.w, r.first, r.order, r.h)
+    g.replay()
+    assert r.m.sync() == mk.MK_OK and torch.equal(r.h, want)
