@@ -407,6 +407,7 @@ extern "C" {
 
 void mk_chunk_destroy(mk_chunk* c) {
   if (!c) return;
+  BesideCaptures relaxed;
   for (Stage& s : c->stage) {
     if (s.sent) {
       cudaEventSynchronize(s.sent);

@@ -15,6 +15,7 @@
 #include <thread>
 #include <vector>
 
+#include "launch.cuh"
 #include "mk.h"
 #include "mk_internal.h"
 
@@ -1477,6 +1478,7 @@ int mk_plan_info(const mk_plan* p, int* out, int n) {
 
 void mk_plan_destroy(mk_plan* p) {
   if (!p) return;
+  mk::BesideCaptures relaxed;
   if (p->subs.empty()) destroy_one(p);
   else destroy_group(p);
 }

@@ -183,3 +183,27 @@ def test_an_object_dies_beside_a_capture(mk):
         r.m.up(r.x, r.w, r.first, r.order, r.h)
     g.replay()
     assert r.m.sync() == mk.MK_OK and torch.equal(r.h, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["plan", "chunk"])
+def test_plans_and_chunks_die_beside_a_capture(mk, what):
+    import synth
+    from synth.device import DeviceModel
+    D = synth.TINY
+    pools = [torch.zeros(4, D.n_kv_heads, 2, D.head_dim, 16, dtype=BF16, device="cuda") for _ in range(D.n_layers)]
+    if what == "plan":
+        gone = mk.Plan(D, DeviceModel(D, 1).weights(), pools, [0], [0, 1, 2], 3)
+        nxt = torch.zeros(1, dtype=torch.int32, device="cuda")
+        assert gone.step(nxt, nxt) == mk.MK_OK and gone.sync() == mk.MK_OK
+    else:
+        gone = mk.Chunk(D, "bf16", 4, [0], [3], [0, 1, 2], 3)
+        gone.update([0], [5], [0, 1, 2], 3)         # (an upload, whose buffer is released too)
+    x = torch.zeros(8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gone.close()
+        x += 1
+    g.replay()
+    assert (x.cpu() == 1).all()
