@@ -51,12 +51,9 @@ __device__ __forceinline__ void tma_3d(void* dst, const void* map, int x, int y,
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
-// 16 (or 4) bytes of this thread on their way to shared memory; zeros where `there` is false.
+// 16 bytes of this thread on their way to shared memory; zeros where `there` is false.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // One of the barrier's counted arrivals, once this thread's copies have landed.
