@@ -636,7 +636,9 @@ int mk_verify(int batch, int max_draft, int vocab, const float* target, const fl
  * n a multiple of 8 (E4M3: of 32), at most 16384 (MK_ERR_UNSUPPORTED); x_stride
  * times the element's size a multiple of 16; buffers 16-byte aligned (scales:
  * any).  A NaN in a row makes the row's out NaN; so does eps 0 for a row of
- * zeros. */
+ * zeros.  Squares and their sum are fp32: where they overflow (|t| of 1.8e19 / sqrt(n)
+ * and more) out is 0, and with eps 0 rows below 1e-18 lose precision, rows whose
+ * squares vanish (below 2.6e-23) give infinities. */
 int mk_norm(int rows, int n, const void* x, int x_type, long long x_stride, const void* add, int add_type, int terms,
             const void* gamma, float eps, void* total, void* out, int out_type, uint8_t* scales, mk_stream stream);
 
@@ -677,7 +679,8 @@ int mk_experts_create(const mk_model_dims* dims, int rows_type, mk_experts** out
 
 /* h[i] = silu(g) * u for each pair in the sorted order, (g, u) = the gate and up
  * products of row order[i] / top_k of x with the weights of the expert that has i
- * in first[e] .. first[e + 1] - 1.  Sums are fp32, h is rounded once.
+ * in first[e] .. first[e + 1] - 1.  Sums are fp32, silu is formed from them within
+ * (15 + 1.5 |g|) 2^-24 of itself, h is rounded once.
  *   x     device [rows, hidden] of rows_type (8 bits: x_scales)
  *   w     device [n_experts, 2 * expert_ffn, hidden] of rows_type, rows
  *         interleaved as w_gate_up of mk_weights (8 bits: w_scales)
@@ -685,8 +688,8 @@ int mk_experts_create(const mk_model_dims* dims, int rows_type, mk_experts** out
  *   h     device [rows * top_k, expert_ffn] of rows_type (8 bits: h_scales);
  *         rows from first[n_experts] on are left as they were
  * Buffers 16-byte aligned (scales: any; the products read them by aligned words
- * of 4 bytes or more that hold a byte of theirs, so up to 3 bytes before
- * and behind them too, which change nothing).  first and order may hold
+ * that hold a byte of theirs, so up to 3 bytes before and behind them too, which
+ * change nothing).  first and order may hold
  * anything: an entry out of range is read as none. */
 int mk_experts_up(mk_experts* m, int rows, const void* x, const uint8_t* x_scales, const void* w, const uint8_t* w_scales,
                   const int* first, const int* order, void* h, uint8_t* h_scales, mk_stream stream);

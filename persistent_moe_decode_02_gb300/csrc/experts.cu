@@ -15,11 +15,15 @@
 // hundred rows the weights' bytes: 37 rows of up 96 us, 6.6 TB/s of what comes
 // from device memory (0.81 of its cycles), 300 rows of down 64 us.  One row is a
 // chain of latencies (lists, first weights, one tile of 96 columns a block of
-// 128) and takes 12.8 us for 50 MB, down 7.5 us for 25 MB.  Thousands of rows
-// are bound by the way from L2 to the SMs: a step of 128 bytes of K takes 48 KB
-// (8 bits: 40 KB of 192 columns) and an SM got 118 GB/s (103): 8143 rows in 8
-// bits take up 198 us (2.1 PFLOP/s) and down 118; in bf16 the tiles of two SMs
-// take over (experts_two.cu).
+// 128) and takes 12.8 us for 50 MB, down 7.5 us for 25 MB.  Of thousands of rows
+// in bf16 a step of 128 bytes of K takes 48 KB and 416 ns, 118 GB/s an SM, which
+// is what L2 gives it; the tiles of two SMs take over (experts_two.cu).  In 8 bits
+// it takes 40 KB (192 columns) and some 400 ns, where the products need 246 at
+// twice bf16's measured rate: 8143 rows take up 198 us (2.1 PFLOP/s) and down 118.
+// Neither the scales, nor the gather, nor the results bound up by themselves: each
+// left out gives about a twelfth, all three a fifth.  Down is bound by its
+// results (88 us without).  (Times in short bursts; call after call for tenths of
+// a second the clock falls, and up of 8143 rows takes 223 us.)
 //
 // 8 bits: codes and scales are what the block-scaled matrix instructions take.
 // The scales pass through shared memory to tensor memory; up's epilogue has a
@@ -534,9 +538,9 @@ cudaError_t launch(const Args& a, const void* rows, const void* w, cudaStream_t 
   int sms = 0;
   const cudaError_t e = multiprocessors(&sms);
   if (e != cudaSuccess) return e;
-  // bf16 with 128 rows an expert: tiles of two SMs (8143 rows of the full model:
-  // up 295 us, 311 with one; down 156 and 175; 2500 rows: 144 and 150, 82 and 85;
-  // 1200, 75 an expert: 135 and 130), where they are enough for four rounds of
+  // bf16 with 128 rows an expert: tiles of two SMs (8143 rows of the full model, in
+  // short bursts: up 284 us, 311 with one; down 155 and 175; 2500 rows: 144 and 150,
+  // 82 and 85; 1200, 75 an expert: 135 and 130), where they are enough for four rounds of
   // the SMs and little of their 256 columns is lost (hidden 1056: 28.6 us with
   // one, 32.6).
   const long long cols = (a.n + 255) / 256;

@@ -4,8 +4,12 @@
 // each block of a pair), the expert's rows are B, up to 256 of them, half in each
 // block.  A tile of 128 rows by 256 columns in one SM takes 48 KB for each 128
 // bytes of K, and its products wait for them (8143 rows of up: 416 ns a step,
-// 118 GB/s an SM, as much as L2 gives it; the products need 270); a pair's blocks
-// take 32 KB each for the same products.  And an expert's rows are cut into tiles
+// 118 GB/s an SM, as much as L2 gives it; the products need 270 at the rated
+// clock, 328 at the rate that large library products reach); a pair's blocks take
+// 32 KB each for the same products.  (A step of theirs takes some 335 ns on the
+// average, though the mean tile has 212 of 256 tokens: why a narrower step is
+// hardly shorter was not found.  Without the gather up is a tenth faster, without
+// the results a sixteenth.)  And an expert's rows are cut into tiles
 // of any multiple of 32 instead of 128: of 8143 tokens' 65144 pairs 3 in 100 rows
 // are padding, not 13.
 //

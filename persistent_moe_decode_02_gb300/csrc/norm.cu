@@ -92,7 +92,9 @@ struct NormArgs {
 // A row is the work of blockDim.x threads (a multiple of 32; blockDim.y rows a
 // block), 8 elements a thread and pass, AHEAD terms in flight at a time.  Few
 // terms: 32 registers and all 2048 threads of an SM (8143 rows of 2048 with one
-// term to 8 bits take 32.8 us so, 36.8 with 46 registers).
+// term to 8 bits take 32.8 us so, 36.8 with 46 registers).  With fp32 terms and
+// blocks of 1024 threads a register is spilled, which is no reason for fewer of
+// them: 2000 rows of 8192 with one fp32 term 44.0 us, 52.3 with half the threads.
 template <class X, class A, int OUT, int PASSES, int AHEAD, int MAX_NT>
 __global__ void __launch_bounds__(MAX_NT, PASSES > 1 ? 1 : (AHEAD == 1 ? 2048 : sizeof(A) == 4 ? 1024 : 1280) / MAX_NT)
     k_norm(const __grid_constant__ NormArgs a) {
